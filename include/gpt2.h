@@ -87,7 +87,9 @@ typedef enum gpt2_wdtype {
     GPT2_F32  = 0,
     GPT2_F16  = 1,
     GPT2_INT4 = 2,
-    GPT2_BF16 = 3     /* batched models only (gpt2_create_batch)          */
+    GPT2_BF16 = 3,    /* batched models only (gpt2_create_batch)          */
+    GPT2_INT8 = 4,    /* element types of a gpt2_kv cache only (the cache */
+    GPT2_E4M3 = 5     /* operations below), never of weights              */
 } gpt2_wdtype;
 
 /* One block's tensors, DEVICE pointers to fp32, in the checkpoint's HF
@@ -446,6 +448,137 @@ int gpt2_sync_batch(gpt2_batch *m);
 size_t gpt2_op_linear_bf16_workspace(int32_t M, int32_t n, int32_t K);
 int gpt2_op_linear_bf16(const void *W, const float *X, int32_t M, int32_t n, int32_t K,
                         float *Y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- speculative decoding on caller buffers ------------------------------- */
+
+/* A step that decodes several drafted tokens of a sequence at once keeps
+ * attention's cache ("Let's make GPT-2 in assembly", Step 6) and the final
+ * choice (Step 7) but asks more of both: the drafted tokens form a tree, each
+ * attends to the cached prefix and to its own ancestors, and the choice walks
+ * the tree.  The operations below are those parts, on caller buffers, for one
+ * layer's cache of any element type.  Conventions they share:
+ *   - The drafted nodes of n_seqs sequences are packed: rows first[b] ..
+ *     first[b+1]-1 (DEVICE int32 [n_seqs+1], non-decreasing, first[n_seqs] <=
+ *     n_rows) are sequence b's nodes, at most max_nodes of them, in an order in
+ *     which a parent comes before its children.  Node 0 is the sequence's last
+ *     chosen token, which is not in the cache yet.  A sequence may have no
+ *     nodes.  Rows from first[n_seqs] on are left as they were.
+ *   - Sequence b owns cache slot slot[b] and has cached[b] cached rows; its
+ *     node j's key and value are cache row cached[b] + j.
+ *   - slot, pos, cached, first, path and the like are DEVICE int32 arrays: their
+ *     values are not known to the host, so an entry outside its range is not
+ *     reported; what it names is skipped, as each operation says, and no access
+ *     leaves the buffers.
+ *   - Every call is asynchronous on `stream`, allocates nothing, may be captured
+ *     into a graph, and keeps nothing between calls.  Two calls may be in
+ *     flight together if neither writes what the other uses (a workspace
+ *     included).
+ *   - Errors: INVALID_ARG (NULL, bad shape or type, misaligned), CUDA,
+ *     UNSUPPORTED_DEVICE. */
+
+/* One layer's cache.  k and v are DEVICE [n_slots][n_head][n_positions]
+ * [head_dim] of `dtype`: GPT2_F32, GPT2_F16, GPT2_BF16, GPT2_INT8 or GPT2_E4M3,
+ * 16-byte aligned, head_dim 32, 64 or 128.  For the two 8-bit types k_scale and
+ * v_scale are DEVICE fp32 [n_slots][n_head][n_positions]: one scale per head
+ * and cache row, value = code * scale; NULL for the others.
+ *   GPT2_INT8: codes in [-127, 127], scale = max|x| / 127 rounded to fp32 (at
+ *     least 2^-126), code = the integer nearest x / scale, ties to even.
+ *   GPT2_E4M3: 8-bit floats (4 exponent, 3 fraction bits, largest 448), scale =
+ *     the smallest power of two (at least 2^-126) with max|x| / scale <= 448,
+ *     code = x / scale rounded to nearest even.
+ *   A head's row that holds an infinity or a NaN gets the scale NaN and codes
+ *   0, so that it reads back as NaN. */
+typedef struct gpt2_kv {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int32_t dtype;
+    int32_t n_slots, n_head, n_positions, head_dim;
+} gpt2_kv;
+
+/* Writes n_rows rows of k and v (DEVICE, src_dtype GPT2_F32, GPT2_F16 or
+ * GPT2_BF16; row i's heads [n_head][head_dim] start at element i * row_stride,
+ * row_stride >= n_head * head_dim, so the rows may lie inside fused QKV rows)
+ * into the cache at (slot[i], pos[i]), rounded (nearest even) or quantised to
+ * the cache's type.  A row whose slot or pos is outside the cache (-1, say) is
+ * skipped.  No two rows of a call may name the same (slot, pos): such a cache
+ * row's codes and scale would mix.  k and v must not overlap the cache. */
+int gpt2_op_kv_store(const gpt2_kv *kv, const void *k, const void *v, int32_t src_dtype, int64_t row_stride,
+                     const int32_t *slot, const int32_t *pos, int32_t n_rows, void *stream);
+
+/* Reads cache rows (slot[i], pos[i]) back into rows of k and v (dst_dtype
+ * GPT2_F32, GPT2_F16 or GPT2_BF16, layout as gpt2_op_kv_store's): widened, or
+ * code * scale in fp32, rounded to nearest even.  A row outside the cache reads
+ * as zeros. */
+int gpt2_op_kv_load(const gpt2_kv *kv, const int32_t *slot, const int32_t *pos, int32_t n_rows, void *k, void *v,
+                    int32_t dst_dtype, int64_t row_stride, void *stream);
+
+#define GPT2_MAX_NODES 64
+/* Attention of the packed nodes over the cache ("Let's make GPT-2 in assembly",
+ * Step 6: score q.k * scale, softmax, weighted sum), scale 1/sqrt(head_dim) for
+ * GPT-2.  mask: DEVICE uint64 [n_rows]; bit j of a node's mask lets it see node
+ * j of its own sequence (a tree: itself and its ancestors); it always sees rows
+ * 0..cached[b]-1.  One node per sequence with mask 1 is a decode step.  What a
+ * node does not see does not enter its result, infinities and NaN included; a
+ * node that sees nothing gets zeros.  slot[b] outside the cache: zeros; nodes
+ * whose cache row would be n_positions or more are not seen.
+ *   q: DEVICE, q_dtype, row i's n_head heads of head_dim at element i *
+ *   q_stride; out: the same type, row i at i * out_stride.  n_head is a multiple
+ *   of kv->n_head: query head h reads cache head h / (n_head / kv->n_head).
+ *   Types: q_dtype GPT2_F32 with any cache; GPT2_F16 and GPT2_BF16 with a cache
+ *   of the same type, GPT2_INT8 or GPT2_E4M3.  Scores, softmax and sums are
+ *   fp32.  q and out 16-byte aligned, strides multiples of 8 elements and >=
+ *   n_head * head_dim; max_nodes in [1, GPT2_MAX_NODES] (of a sequence with
+ *   more, the rows from max_nodes on are left as they were). */
+int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, int64_t q_stride, int32_t n_head,
+                           const int32_t *slot, const int32_t *cached, const int32_t *first, const uint64_t *mask,
+                           int32_t n_seqs, int32_t n_rows, int32_t max_nodes, float scale, void *out,
+                           int64_t out_stride, void *stream);
+
+/* Which drafted nodes the target model accepts, and the token after them, from
+ * given random numbers.  logits: DEVICE fp32 [n_rows][vocab], row i the target's
+ * after node i; tokens, parents: DEVICE int32 [n_rows], a node's token and its
+ * parent's index within the sequence (ignored for node 0; a node whose parent
+ * does not come before it is never reached).  Per sequence, from node 0 on:
+ *   temperature 0: the choice is the highest logit (exact ties to the lowest
+ *     id, "Let's make GPT-2 in assembly", Step 7); the first child whose token
+ *     it is is accepted, otherwise the walk ends.
+ *   temperature > 0: r = softmax(logits / temperature) of the current node.  Its
+ *     children are tried in order: child i with token x is accepted if u_accept[i]
+ *     * q(x) < r(x), and the walk goes on from it; otherwise r becomes max(r -
+ *     q, 0) / its sum.  q is the draft's distribution at the node (row of
+ *     draft_probs, DEVICE fp32 [n_rows][vocab], from which its children were
+ *     drawn) or, with draft_probs NULL, all of q is on x.  The walk ends where
+ *     no child is accepted, and the next token is drawn from r in the Gumbel-max
+ *     form of gpt2_set_sampling: the id v with the highest r(v) / -log(u_draw[b]
+ *     [v]) (ties to the lowest id).  Where r is zero everywhere, the node's own
+ *     distribution is used.  u_accept: DEVICE fp32 [n_rows], u_draw: DEVICE fp32
+ *     [n_seqs][vocab], uniform in (0, 1).  So the accepted tokens and the next
+ *     one are distributed as the target's own.
+ * Logits of -infinity have probability zero; NaN logits are never chosen as the
+ * greedy token.  A row without a logit above -infinity, or with a NaN or
+ * +infinity at temperature > 0, ends the walk at its node with next token -1.  A
+ * node whose token is outside [0, vocab) is passed over.
+ * Outputs (DEVICE int32): path [n_seqs][max_nodes], the accepted nodes in order
+ * (node 0 first), -1 behind them; n_path [n_seqs], how many; next_token
+ * [n_seqs].  A sequence without nodes gets 0 and -1.  draft_probs, u_accept and
+ * u_draw may be NULL at temperature 0.  workspace: 16-byte aligned DEVICE
+ * memory of gpt2_op_verify_tree_workspace bytes. */
+size_t gpt2_op_verify_tree_workspace(int32_t n_rows, int32_t vocab);
+int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *tokens, const int32_t *parents,
+                        const int32_t *first, int32_t n_seqs, int32_t n_rows, int32_t max_nodes, float temperature,
+                        const float *draft_probs, const float *u_accept, const float *u_draw, int32_t *path,
+                        int32_t *n_path, int32_t *next_token, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Keeps an accepted path in the cache: for every layer and sequence, cache row
+ * cached[b] + path[b][i] moves to row cached[b] + i, i < n_path[b] (codes and
+ * scales as they are).  kv describes layer 0; the n_layer layers' k, v (and
+ * scales) follow one another without gaps.  path [n_seqs][max_nodes] and n_path
+ * are gpt2_op_verify_tree's: strictly increasing nodes; a path is kept only up
+ * to its first entry that breaks this, is max_nodes or more, or whose row is
+ * outside the cache.  A slot outside the cache, or the same slot twice (then
+ * undefined for that slot), see above. */
+int gpt2_op_kv_commit(const gpt2_kv *kv, int32_t n_layer, const int32_t *slot, const int32_t *cached,
+                      const int32_t *path, const int32_t *n_path, int32_t n_seqs, int32_t max_nodes, void *stream);
 
 /* ---- errors ------------------------------------------------------------- */
 const char *gpt2_strerror(int status);

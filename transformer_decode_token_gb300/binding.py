@@ -14,7 +14,8 @@ import numpy as np
 
 from . import build as _build
 
-GPT2_F32, GPT2_F16, GPT2_INT4, GPT2_BF16 = 0, 1, 2, 3
+GPT2_F32, GPT2_F16, GPT2_INT4, GPT2_BF16, GPT2_INT8, GPT2_E4M3 = 0, 1, 2, 3, 4, 5
+MAX_NODES = 64                 # GPT2_MAX_NODES
 WDTYPES = {"f32": GPT2_F32, "f16": GPT2_F16, "int4": GPT2_INT4, "bf16": GPT2_BF16}
 MAT_ATTN, MAT_PROJ, MAT_FC, MAT_MLP_PROJ = 0, 1, 2, 3
 MATRIX_KEYS = ("attn_w", "proj_w", "fc_w", "mlp_proj_w")   # index = MAT_*
@@ -31,7 +32,8 @@ EXPORTED = ("gpt2_create", "gpt2_create_ex", "gpt2_path", "gpt2_launch_count", "
             "gpt2_create_batch", "gpt2_create_batch_ex", "gpt2_destroy_batch", "gpt2_decode_batch", "gpt2_prefill_batch",
             "gpt2_decode_batch_greedy", "gpt2_argmax_batch", "gpt2_batch_ids", "gpt2_copy_logits_batch",
             "gpt2_export_kv_batch", "gpt2_batch_info", "gpt2_sync_batch", "gpt2_op_linear_bf16_workspace",
-            "gpt2_op_linear_bf16", "gpt2_strerror")
+            "gpt2_op_linear_bf16", "gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit",
+            "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree", "gpt2_strerror")
 
 
 class GPT2Error(RuntimeError):
@@ -58,6 +60,13 @@ class LayerWeights(ctypes.Structure):
 class Weights(ctypes.Structure):
     _fields_ = [("wte", ctypes.c_void_p), ("wpe", ctypes.c_void_p), ("ln_f_w", ctypes.c_void_p),
                 ("ln_f_b", ctypes.c_void_p), ("layers", ctypes.POINTER(LayerWeights))]
+
+
+class KV(ctypes.Structure):
+    """gpt2_kv: one layer's cache (include/gpt2.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("n_head", ctypes.c_int32), ("n_positions", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -137,11 +146,20 @@ def lib(build_if_stale: bool = True, path: str = None):
             L.gpt2_op_linear_bf16_workspace.argtypes = [i32, i32, i32]
             L.gpt2_op_linear_bf16_workspace.restype = sz
             L.gpt2_op_linear_bf16.argtypes = [vp, vp, i32, i32, i32, vp, vp, sz, vp]
+            i64, kv = ctypes.c_int64, ctypes.POINTER(KV)
+            L.gpt2_op_kv_store.argtypes = [kv, vp, vp, i32, i64, vp, vp, i32, vp]
+            L.gpt2_op_kv_load.argtypes = [kv, vp, vp, i32, vp, vp, i32, i64, vp]
+            L.gpt2_op_kv_commit.argtypes = [kv, i32, vp, vp, vp, vp, i32, i32, vp]
+            L.gpt2_op_tree_attention.argtypes = [kv, vp, i32, i64, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, i64, vp]
+            L.gpt2_op_verify_tree_workspace.argtypes = [i32, i32]
+            L.gpt2_op_verify_tree_workspace.restype = sz
+            L.gpt2_op_verify_tree.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz,
+                                              vp]
             L.gpt2_strerror.argtypes = [ctypes.c_int]
             L.gpt2_strerror.restype = ctypes.c_char_p
             for n in EXPORTED:
                 if n not in ("gpt2_destroy", "gpt2_destroy_batch", "gpt2_op_head_argmax_workspace",
-                             "gpt2_op_linear_bf16_workspace", "gpt2_strerror"):
+                             "gpt2_op_linear_bf16_workspace", "gpt2_op_verify_tree_workspace", "gpt2_strerror"):
                     getattr(L, n).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -459,3 +477,265 @@ def op_linear_bf16(W_bf16, X, stream=None):
     check(lib().gpt2_op_linear_bf16(_ptr(W_bf16), _ptr(X), M, n, K, _ptr(Y), _ptr(ws), ws_bytes,
                                     _stream_handle(stream)), "gpt2_op_linear_bf16")
     return Y
+
+
+# ---- speculative decoding on caller tensors -----------------------------------------
+#
+# Caches are CUDA tensors [slots][heads][positions][head_dim] of torch.float32,
+# float16, bfloat16, int8 or float8_e4m3fn; the two 8-bit types come with fp32
+# scales [slots][heads][positions].  Index tensors are int32 (the masks int64,
+# taken as 64 bits).  Every tensor lives on the current device; tensors that a
+# call makes are made on its stream.  See the gpt2_op_* calls of include/gpt2.h.
+
+_row_types = None
+
+
+def _dtypes():
+    """torch dtypes of rows and of caches -> GPT2_*."""
+    global _row_types, _cache_types
+    if _row_types is None:
+        import torch
+        _cache_types = {torch.float32: GPT2_F32, torch.float16: GPT2_F16, torch.bfloat16: GPT2_BF16,
+                        torch.int8: GPT2_INT8, torch.float8_e4m3fn: GPT2_E4M3}
+        _row_types = {torch.float32: GPT2_F32, torch.float16: GPT2_F16, torch.bfloat16: GPT2_BF16}
+    return _row_types, _cache_types
+
+
+def _on_device(**tensors):
+    """Raises unless every tensor is on the current CUDA device."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and (t.device.type != "cuda" or t.device.index != dev):
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
+
+
+def _whole(name, t, dtype, shape):
+    """Raises unless t is a contiguous tensor of this type and shape."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+
+
+def _kv(k_cache, v_cache, k_scale, v_scale, layers=False):
+    """(gpt2_kv, layers) of a layer's cache, or of [layers][slots]... caches."""
+    import torch
+    types = _dtypes()[1]
+    nd = k_cache.dim()
+    if nd != 4 and not (layers and nd == 5):
+        raise ValueError(f"a cache is [slots][heads][positions][head_dim], not {tuple(k_cache.shape)}")
+    if k_cache.dtype not in types:
+        raise ValueError(f"unsupported cache type {k_cache.dtype}")
+    if not k_cache.is_contiguous():
+        raise ValueError("k_cache must be contiguous")
+    _whole("v_cache", v_cache, k_cache.dtype, k_cache.shape)
+    t = types[k_cache.dtype]
+    if t >= GPT2_INT8:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an 8-bit cache needs k_scale and v_scale")
+        _whole("k_scale", k_scale, torch.float32, k_cache.shape[:-1])
+        _whole("v_scale", v_scale, torch.float32, k_cache.shape[:-1])
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError(f"a {k_cache.dtype} cache has no scales")
+    S, H, P, D = k_cache.shape[-4:]
+    kv = KV(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+            v_scale.data_ptr() if v_scale is not None else None, t, S, H, P, D)
+    return kv, (k_cache.shape[0] if nd == 5 else 1)
+
+
+def _rows(name, t, H, D):
+    """The row stride of a [rows][H][D] tensor whose rows are contiguous."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (H, D):
+        raise ValueError(f"{name} must be [rows][{H}][{D}], not {tuple(t.shape)}")
+    if t.dtype not in _dtypes()[0]:
+        raise ValueError(f"unsupported {name} type {t.dtype}")
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else H * D
+
+
+class _OnStream:
+    """The call's stream: allocations inside belong to it."""
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        import torch
+        self.ctx = torch.cuda.stream(self.stream) if self.stream is not None else None
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return (self.stream if self.stream is not None else torch.cuda.current_stream()).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def op_kv_store(k, v, k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, stream=None):
+    """Writes rows of k and v ([rows][heads][head_dim], possibly views into
+    fused QKV rows) into the cache at (slot[i], pos[i]), quantised or rounded
+    to its type; rows outside the cache are skipped."""
+    import torch
+    _on_device(k=k, v=v, k_cache=k_cache, v_cache=v_cache, slot=slot, pos=pos, k_scale=k_scale, v_scale=v_scale)
+    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale)
+    n = k.shape[0]
+    stride = _rows("k", k, kv.n_head, kv.head_dim)
+    if v.dtype != k.dtype or v.shape != k.shape or _rows("v", v, kv.n_head, kv.head_dim) != stride:
+        raise ValueError("k and v must have the same type, shape and row stride")
+    _whole("slot", slot, torch.int32, (n,))
+    _whole("pos", pos, torch.int32, (n,))
+    with _OnStream(stream) as s:
+        if n > 0:
+            check(lib().gpt2_op_kv_store(kv, k.data_ptr(), v.data_ptr(), _row_types[k.dtype], stride,
+                                         slot.data_ptr(), pos.data_ptr(), n, s), "gpt2_op_kv_store")
+
+
+def op_kv_load(k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, dtype=None, k=None, v=None, stream=None):
+    """Reads cache rows (slot[i], pos[i]) back as (k, v), each [rows][heads]
+    [head_dim] of `dtype` (float32 unless given, or the given k's); rows
+    outside the cache are zeros."""
+    import torch
+    _on_device(k=k, v=v, k_cache=k_cache, v_cache=v_cache, slot=slot, pos=pos, k_scale=k_scale, v_scale=v_scale)
+    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale)
+    n = slot.numel()
+    _whole("slot", slot, torch.int32, (n,))
+    _whole("pos", pos, torch.int32, (n,))
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    with _OnStream(stream) as s:
+        if k is None:
+            k = torch.empty((n, kv.n_head, kv.head_dim), dtype=dtype or torch.float32, device=k_cache.device)
+            v = torch.empty_like(k)
+        elif dtype is not None and dtype != k.dtype:
+            raise ValueError(f"k is {k.dtype}, not {dtype}")
+        stride = _rows("k", k, kv.n_head, kv.head_dim)
+        if k.shape[0] != n or v.dtype != k.dtype or v.shape != k.shape or \
+                _rows("v", v, kv.n_head, kv.head_dim) != stride:
+            raise ValueError("k and v must be [rows][heads][head_dim] of the same type and row stride")
+        if n > 0:
+            check(lib().gpt2_op_kv_load(kv, slot.data_ptr(), pos.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                        _row_types[k.dtype], stride, s), "gpt2_op_kv_load")
+    return k, v
+
+
+def op_kv_commit(k_cache, v_cache, slot, cached, path, n_path, k_scale=None, v_scale=None, stream=None):
+    """Moves the accepted nodes' cache rows into place, in every layer of a
+    [layers][slots][heads][positions][head_dim] cache (or of one layer's)."""
+    import torch
+    _on_device(k_cache=k_cache, v_cache=v_cache, slot=slot, cached=cached, path=path, n_path=n_path,
+               k_scale=k_scale, v_scale=v_scale)
+    kv, layers = _kv(k_cache, v_cache, k_scale, v_scale, layers=True)
+    B = slot.numel()
+    if path.dim() != 2 or not 1 <= path.shape[1] <= MAX_NODES:
+        raise ValueError(f"path must be [sequences][nodes], at most {MAX_NODES} nodes")
+    _whole("slot", slot, torch.int32, (B,))
+    _whole("cached", cached, torch.int32, (B,))
+    _whole("path", path, torch.int32, (B, path.shape[1]))
+    _whole("n_path", n_path, torch.int32, (B,))
+    with _OnStream(stream) as s:
+        if B > 0:
+            check(lib().gpt2_op_kv_commit(kv, layers, slot.data_ptr(), cached.data_ptr(), path.data_ptr(),
+                                          n_path.data_ptr(), B, path.shape[1], s), "gpt2_op_kv_commit")
+
+
+def tree_masks(parents) -> np.ndarray:
+    """Masks of one sequence's nodes (bit j: node j is the node itself or an
+    ancestor) from its parents (node 0's is ignored; a parent comes before its
+    children), as int64 with the same 64 bits."""
+    p = np.asarray(parents, np.int64)
+    if p.ndim != 1 or not 1 <= p.size <= MAX_NODES:
+        raise ValueError(f"a sequence has 1 to {MAX_NODES} nodes")
+    out = np.zeros(p.size, np.uint64)
+    for i in range(p.size):
+        if i and not 0 <= p[i] < i:
+            raise ValueError(f"node {i}'s parent {p[i]} does not come before it")
+        out[i] = np.uint64(1 << i) | (out[p[i]] if i else np.uint64(0))
+    return out.view(np.int64)
+
+
+def op_tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale=None, v_scale=None,
+                      scale=None, out=None, stream=None):
+    """Attention of packed drafted nodes q [rows][query heads][head_dim] over
+    the cached prefix and the nodes of their masks; scale 1/sqrt(head_dim)
+    unless given.  Returns out, like q."""
+    import torch
+    _on_device(q=q, k_cache=k_cache, v_cache=v_cache, slot=slot, cached=cached, first=first, mask=mask,
+               k_scale=k_scale, v_scale=v_scale, out=out)
+    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3 or q.shape[2] != kv.head_dim:
+        raise ValueError(f"q must be [rows][heads][{kv.head_dim}], not {tuple(q.shape)}")
+    n, H, D = q.shape
+    B = slot.numel()
+    stride = _rows("q", q, H, D)
+    _whole("slot", slot, torch.int32, (B,))
+    _whole("cached", cached, torch.int32, (B,))
+    _whole("first", first, torch.int32, (B + 1,))
+    _whole("mask", mask, torch.int64, (n,))
+    with _OnStream(stream) as s:
+        if out is None:
+            out = torch.empty((n, H, D), dtype=q.dtype, device=q.device)
+        elif out.dtype != q.dtype or out.shape != q.shape:
+            raise ValueError("out must have q's type and shape")
+        if n > 0 and B > 0:
+            check(lib().gpt2_op_tree_attention(
+                kv, q.data_ptr(), _row_types[q.dtype], stride, H, slot.data_ptr(), cached.data_ptr(),
+                first.data_ptr(), mask.data_ptr(), B, n, int(max_nodes),
+                1.0 / D ** 0.5 if scale is None else float(scale), out.data_ptr(), _rows("out", out, H, D), s),
+                "gpt2_op_tree_attention")
+    return out
+
+
+def op_verify_tree_workspace(n_rows: int, vocab: int) -> int:
+    return int(lib().gpt2_op_verify_tree_workspace(n_rows, vocab))
+
+
+def op_verify_tree(logits, tokens, parents, first, max_nodes, temperature=0.0, draft_probs=None, u_accept=None,
+                   u_draw=None, path=None, n_path=None, next_token=None, workspace=None, stream=None):
+    """Which drafted nodes the target accepts, and the token after them:
+    (path [sequences][max_nodes], n_path, next_token), int32."""
+    import torch
+    _on_device(logits=logits, tokens=tokens, parents=parents, first=first, draft_probs=draft_probs,
+               u_accept=u_accept, u_draw=u_draw, path=path, n_path=n_path, next_token=next_token,
+               workspace=workspace)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows][vocab]")
+    n, V = logits.shape
+    B, T = first.numel() - 1, int(max_nodes)
+    _whole("logits", logits, torch.float32, (n, V))
+    _whole("tokens", tokens, torch.int32, (n,))
+    _whole("parents", parents, torch.int32, (n,))
+    _whole("first", first, torch.int32, (B + 1,))
+    if draft_probs is not None:
+        _whole("draft_probs", draft_probs, torch.float32, (n, V))
+    if temperature != 0:
+        if u_accept is None or u_draw is None:
+            raise ValueError("temperature > 0 needs u_accept and u_draw")
+        _whole("u_accept", u_accept, torch.float32, (n,))
+        _whole("u_draw", u_draw, torch.float32, (B, V))
+    with _OnStream(stream) as s:
+        dev = logits.device
+        if path is None:
+            path = torch.empty((B, T), dtype=torch.int32, device=dev)
+        if n_path is None:
+            n_path = torch.empty(B, dtype=torch.int32, device=dev)
+        if next_token is None:
+            next_token = torch.empty(B, dtype=torch.int32, device=dev)
+        _whole("path", path, torch.int32, (B, T))
+        _whole("n_path", n_path, torch.int32, (B,))
+        _whole("next_token", next_token, torch.int32, (B,))
+        L = lib()
+        if workspace is None:
+            workspace = torch.empty(L.gpt2_op_verify_tree_workspace(n, V), dtype=torch.uint8, device=dev)
+        p = lambda t: t.data_ptr() if t is not None else None
+        if B > 0 and n > 0:
+            check(L.gpt2_op_verify_tree(
+                logits.data_ptr(), V, tokens.data_ptr(), parents.data_ptr(), first.data_ptr(), B, n, T,
+                float(temperature), p(draft_probs), p(u_accept), p(u_draw), path.data_ptr(), n_path.data_ptr(),
+                next_token.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s),
+                "gpt2_op_verify_tree")
+        elif B > 0:
+            path.fill_(-1)
+            n_path.zero_()
+            next_token.fill_(-1)
+    return path, n_path, next_token

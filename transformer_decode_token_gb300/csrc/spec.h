@@ -1,0 +1,40 @@
+// Internal interface of the speculative-decoding operations: what the C entry
+// points (kv_ops.cu, tree_attn.cu, verify.cu) and the batched engine share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gpt2.h"
+
+namespace gpt2 {
+
+inline int spec_rc(cudaError_t e)
+{
+    if (e == cudaSuccess) return GPT2_OK;
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? GPT2_ERR_OUT_OF_MEMORY : GPT2_ERR_CUDA;
+}
+
+inline bool is_row_type(int t) { return t == GPT2_F32 || t == GPT2_F16 || t == GPT2_BF16; }
+inline bool is_scaled(int t) { return t == GPT2_INT8 || t == GPT2_E4M3; }
+inline int elem_size(int t) { return t == GPT2_F32 ? 4 : is_scaled(t) ? 1 : 2; }
+inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+inline bool kv_ok(const gpt2_kv *kv)
+{
+    if (!kv || !kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v)) return false;
+    if (!is_row_type(kv->dtype) && !is_scaled(kv->dtype)) return false;
+    if (is_scaled(kv->dtype) && (!kv->k_scale || !kv->v_scale)) return false;
+    if (kv->n_slots < 1 || kv->n_head < 1 || kv->n_positions < 1) return false;
+    if (kv->head_dim != 32 && kv->head_dim != 64 && kv->head_dim != 128) return false;
+    // (slot, head, position) rows are counted in 64 bits; heads x positions of
+    // a slot in 32
+    return (long long)kv->n_head * kv->n_positions < (1ll << 31);
+}
+
+// Multiprocessors of the current device (0 and *rc on failure, also where it
+// is not of compute capability 10.3).  Looked up once per device.
+int spec_sms(int *rc);
+
+}  // namespace gpt2

@@ -1,0 +1,780 @@
+// Attention of a tree of drafted tokens over a cache: the kernel.
+//
+// For a sequence's nodes i and the cache rows j that node i sees (the cached
+// prefix, and the nodes of its mask),
+//   s_ij = scale * q_i . k_j,   o_i = sum_j 2^(s'_ij - m_i) v_j / sum_j 2^(s'_ij - m_i),
+// s' = s log2(e), m_i the maximum so far, in one pass over the cache rows: a
+// new maximum scales what has been summed.
+//
+// Work split.  The rows of a (sequence, cache head) are its nodes times the
+// query heads that share the head; 16 * MT of them are the M side of the
+// matrix instructions, so every cache row is read once for all of them.  A
+// warp takes tiles of KS cache rows; the kNW warps of a CTA and the CTAs of a
+// cluster take different tiles (long caches and few sequences still fill the
+// GPU) and join their (m, sum, o) in shared memory, then over the cluster's
+// distributed shared memory, in a fixed order: one launch, no workspace, and
+// every run gives the same bits.
+//
+// Cache rows go straight from global memory to registers, in the order the
+// matrix instructions want them.  In mma.m16n8k* the thread with g = lane / 4,
+// c = lane % 4 supplies B's column g at the k indices of c.  Which head
+// dimension (or cache row) a k index stands for is free as long as A agrees,
+// so for the scores thread (g, c) loads 16-byte pieces c, c + 4, .. of cache
+// row g of eight, and for the weighted sum pieces g, g + 8, .. of the values
+// of the rows 2c, 2c + 1, whose weights it holds already.  Every access of a
+// warp covers whole lines, nothing is staged or transposed in shared memory,
+// and the next tile's keys are loaded while this one's weights are formed.
+//
+// Types (struct Tr): the fp32 cache uses tf32 products with q, k, p and v as
+// two parts each (three products, 22 bits); 16-bit caches the products of
+// their own type; 8-bit codes are exact in fp16.  q and the weights p are split
+// into kNQ and kNP parts, so that results keep about 22 bits for fp32 rows,
+// and for 16-bit rows at least 16 bits of every weight: only the final
+// rounding to the row type is visible.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "spec.h"
+
+namespace gpt2 {
+
+struct TreeArgs {
+    gpt2_kv kv;
+    const void *q;
+    void *out;
+    int64_t q_stride, out_stride;
+    const int32_t *slot, *cached, *first;
+    const uint64_t *mask;
+    int32_t n_seqs, n_rows, max_nodes, group, row_tiles, splits, q_dtype;
+    float scale_log2;               // scale * log2(e)
+};
+
+cudaError_t tree_attn_f32(const TreeArgs &a, int mt, cudaStream_t s);
+cudaError_t tree_attn_16(const TreeArgs &a, int mt, cudaStream_t s);
+cudaError_t tree_attn_8(const TreeArgs &a, int mt, cudaStream_t s);
+
+namespace tree {
+
+constexpr int kNW = 4;              // warps of a CTA
+constexpr float kShift = 13.f;      // fp16 weights are 2^(s' - m + 13): small ones stay normal numbers
+
+enum Mma { kTf32, kF16, kBf16 };
+
+template <Mma M, int ES, int NQ, int NP, bool E4M3 = false>
+struct Traits {
+    static constexpr Mma kMma = M;
+    static constexpr int kES = ES;          // bytes of a cache element
+    static constexpr int kNQ = NQ, kNP = NP;
+    static constexpr bool kE4M3 = E4M3;
+    static constexpr bool kScaled = ES == 1;
+    static constexpr bool kNorm = M == kF16 && (NQ > 1 || ES == 1);   // q brought into fp16's range by a power of two
+};
+
+// Shape of a warp's tile.
+template <class Tr, int D, int MT>
+struct Tile {
+    static constexpr int kRowB = D * Tr::kES;
+    static constexpr int kKLd = kRowB / 4 < 16 ? kRowB / 4 : 16;     // bytes per key access of a thread
+    static constexpr int kNK = kRowB / (4 * kKLd);                   // key accesses per row
+    static constexpr int kVLd = kRowB / 8 < 16 ? kRowB / 8 : 16;     // bytes per value access
+    static constexpr int kNV = kRowB / (8 * kVLd);
+    static constexpr int kEK = kKLd / Tr::kES, kEV = kVLd / Tr::kES; // elements of an access
+    static constexpr int kMost = MT * D >= 256 ? 16 : 32;
+    static constexpr int KS = 4096 / kRowB > kMost ? kMost : 4096 / kRowB;   // cache rows per tile: 4 KB of keys, or fewer
+    static constexpr int kT8 = KS / 8;                               // score tiles of 8 cache rows
+    static constexpr int kSteps = Tr::kMma == kTf32 ? D / 8 : D / 16;   // k steps of the score product
+    static constexpr int kKR = kT8 * kRowB / 16;                     // 32-bit registers of the keys
+    static constexpr int kVR = kT8 * 2 * kRowB / 32;                 // ... of the values
+    static constexpr int kNT = D / 8;                                // output tiles of 8 dimensions
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool bf)
+{
+    if (bf)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// B bytes at p (zeros where !there) into B / 4 registers.
+template <int B>
+__device__ __forceinline__ void load_piece(uint32_t *r, const uint8_t *p, bool there)
+{
+    const int t = there;
+    if constexpr (B == 16)
+        asm volatile(
+            "{.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+            "mov.b32 %3, 0;\n\t@p ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];}"
+            : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3])
+            : "l"(p), "r"(t));
+    else if constexpr (B == 8)
+        asm volatile(
+            "{.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+            "@p ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];}"
+            : "=&r"(r[0]), "=&r"(r[1])
+            : "l"(p), "r"(t));
+    else
+        asm volatile(
+            "{.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+            "@p ld.global.nc.L1::no_allocate.b32 %0, [%1];}"
+            : "=&r"(r[0])
+            : "l"(p), "r"(t));
+}
+__device__ __forceinline__ float load_scale(const float *p, bool there)
+{
+    float v;
+    const int t = there;
+    asm volatile("{.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@p ld.global.nc.f32 %0, [%1];}"
+                 : "=&f"(v)
+                 : "l"(p), "r"(t));
+    return v;
+}
+
+// Two codes in the low half of `x` (one per byte) as an fp16 pair.
+// int8 (already offset by 128): 0x64uu is 1024 + u, minus 1152 is the code.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t x, uint32_t sel)
+{
+    if constexpr (E4M3) {
+        const uint16_t two = uint16_t(sel == 0x4140u ? x & 0xffffu : x >> 16);
+        uint32_t r;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+        return r;
+    } else {
+        uint32_t h = __byte_perm(x, 0x64646464u, sel);
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        __half2 v = __hsub2(*reinterpret_cast<__half2 *>(&h), off);
+        return *reinterpret_cast<uint32_t *>(&v);
+    }
+}
+
+// B operands of the score product, k step s, from a row's registers.
+template <class Tr>
+__device__ __forceinline__ void key_operand(const uint32_t *r, int s, uint32_t &b0, uint32_t &b1)
+{
+    if constexpr (Tr::kES == 1) {
+        const uint32_t x = Tr::kE4M3 ? r[s] : r[s] ^ 0x80808080u;
+        b0 = codes_to_half2<Tr::kE4M3>(x, 0x4140u);
+        b1 = codes_to_half2<Tr::kE4M3>(x, 0x4342u);
+    } else {
+        b0 = r[2 * s];
+        b1 = r[2 * s + 1];
+    }
+}
+
+// B operand of the weighted sum: the values of element j of two rows (registers
+// a, b of the rows' accesses) as a 16-bit pair.
+template <class Tr>
+__device__ __forceinline__ uint32_t value_pair(const uint32_t *a, const uint32_t *b, int j)
+{
+    if constexpr (Tr::kES == 1) {
+        uint32_t x = a[j / 4], y = b[j / 4];
+        if (!Tr::kE4M3) {
+            x ^= 0x80808080u;
+            y ^= 0x80808080u;
+        }
+        const uint32_t z = __byte_perm(x, y, j % 4 < 2 ? 0x5140u : 0x7362u);   // a0 b0 a1 b1
+        return codes_to_half2<Tr::kE4M3>(z, j % 2 == 0 ? 0x4140u : 0x4342u);
+    } else {
+        return __byte_perm(a[j / 2], b[j / 2], j % 2 == 0 ? 0x5410u : 0x7632u);
+    }
+}
+
+// x as NP parts of the 16-bit type, each the rounding of what the parts before
+// it leave (pairs: x0 in the low half).
+template <Mma M, int N>
+__device__ __forceinline__ void split16(float x0, float x1, uint32_t (&part)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr (M == kBf16) {
+            __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+            part[i] = *reinterpret_cast<uint32_t *>(&h);
+            x0 -= __uint_as_float(part[i] << 16);
+            x1 -= __uint_as_float(part[i] & 0xffff0000u);
+        } else {
+            __half2 h = __floats2half2_rn(x0, x1);
+            part[i] = *reinterpret_cast<uint32_t *>(&h);
+            const float2 f = __half22float2(h);
+            x0 -= f.x;
+            x1 -= f.y;
+        }
+    }
+}
+
+// Which halves of a 16-bit pair are not finite, as a mask of whole halves.
+template <Mma M>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x)
+{
+    constexpr uint32_t e = M == kBf16 ? 0x7f80u : 0x7c00u;
+    return ((x & e) == e ? 0xffffu : 0u) | ((x >> 16 & e) == e ? 0xffff0000u : 0u);
+}
+
+__device__ __forceinline__ float load_row(const void *p, size_t i, int dtype)
+{
+    if (dtype == GPT2_F32) return static_cast<const float *>(p)[i];
+    if (dtype == GPT2_F16) return __half2float(static_cast<const __half *>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+
+// Element d of a cache row, as fp32 (a code without its scale).
+template <class Tr>
+__device__ __forceinline__ float element(const uint8_t *row, int d)
+{
+    if constexpr (Tr::kMma == kTf32) return reinterpret_cast<const float *>(row)[d];
+    else if constexpr (Tr::kES == 2 && Tr::kMma == kBf16)
+        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[d]);
+    else if constexpr (Tr::kES == 2) return __half2float(reinterpret_cast<const __half *>(row)[d]);
+    else if constexpr (Tr::kE4M3) {
+        const uint32_t h = codes_to_half2<true>(row[d], 0x4140u);
+        return __half2float(__ushort_as_half(uint16_t(h)));
+    } else return float(reinterpret_cast<const int8_t *>(row)[d]);
+}
+
+template <class Tr, int D, int MT>
+struct Smem {
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kParts = Tr::kMma == kTf32 ? 2 : Tr::kNQ;
+    static constexpr size_t kQ = size_t(MT) * Tile<Tr, D, MT>::kSteps * kParts * 32 * 16;
+    static constexpr size_t kO = size_t(kNW) * kRows * D * 4;
+    static constexpr size_t kBytes = kQ > kO ? kQ : kO;   // q's operands, then the warps' sums
+};
+
+template <class Tr, int D, int MT>
+__global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(const TreeArgs a)
+{
+    using T = Tile<Tr, D, MT>;
+    using S = Smem<Tr, D, MT>;
+    constexpr int KS = T::KS, R = S::kRows, kQP = S::kParts;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float sm_m[kNW][R], sm_l[kNW][R];   // [0] then holds the CTA's
+    __shared__ float sm_rs[R];                     // score factor of each row
+    __shared__ int sm_bad;
+
+    const int rank = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
+    const int rt = unit % a.row_tiles, bh = unit / a.row_tiles;
+    const int kvh = bh % a.kv.n_head, b = bh / a.kv.n_head;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int P = a.kv.n_positions, G = a.group;
+
+    const int f0 = min(max(a.first[b], 0), a.n_rows), f1 = min(max(a.first[b + 1], f0), a.n_rows);
+    const int nodes = min(f1 - f0, a.max_nodes);
+    const int row0 = rt * R, rows = min(nodes * G - row0, R);
+    if (rows <= 0) return;                         // the whole cluster leaves
+    const int slot = a.slot[b];
+    const bool there = slot >= 0 && slot < a.kv.n_slots;
+    const int pre = there ? min(max(a.cached[b], 0), P) : 0;
+    const int total = there ? min(pre + nodes, P) : 0;
+
+    const size_t row_base = (size_t(there ? slot : 0) * a.kv.n_head + kvh) * P;
+    const uint8_t *kbase = static_cast<const uint8_t *>(a.kv.k) + row_base * T::kRowB;
+    const uint8_t *vbase = static_cast<const uint8_t *>(a.kv.v) + row_base * T::kRowB;
+    const float *kscale = Tr::kScaled ? a.kv.k_scale + row_base : nullptr;
+    const float *vscale = Tr::kScaled ? a.kv.v_scale + row_base : nullptr;
+
+    // this warp's tiles: t0, t0 + kNW, ... < t1
+    const int tiles = (total + KS - 1) / KS, per = (tiles + a.splits - 1) / a.splits;
+    const int t0 = rank * per + warp, t1 = min(tiles, (rank + 1) * per);
+
+    uint32_t kr[T::kKR];
+    auto load_keys = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < T::kT8; ++u) {
+            const int j = t * KS + u * 8 + g;
+            const uint8_t *p = kbase + size_t(j) * T::kRowB + c * T::kKLd;
+#pragma unroll
+            for (int i = 0; i < T::kNK; ++i)
+                load_piece<T::kKLd>(kr + (u * T::kNK + i) * (T::kKLd / 4), p + i * 4 * T::kKLd, j < total);
+        }
+    };
+    if (t0 < t1) load_keys(t0);
+
+    // ---- q as the A operand, in the order the threads take it ----
+    uint32_t *qop = reinterpret_cast<uint32_t *>(dyn);   // [MT][kSteps][kQP][32][4]
+    for (int mt = warp; mt < MT; mt += kNW) {
+        constexpr int kE = Tr::kMma == kTf32 ? 2 : 4;    // elements of a thread per k step
+        float x[2][T::kSteps * kE];
+        float top[2] = {0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = mt * 16 + half * 8 + g;
+            const bool ok = r < rows;
+            const int node = (row0 + (ok ? r : 0)) / G, h = kvh * G + (row0 + (ok ? r : 0)) % G;
+            const size_t base = size_t(f0 + node) * a.q_stride + size_t(h) * D;
+#pragma unroll
+            for (int e = 0; e < T::kSteps * kE; ++e) {
+                const int d = (4 * (e / T::kEK) + c) * T::kEK + e % T::kEK;
+                x[half][e] = ok ? load_row(a.q, base + d, a.q_dtype) : 0.f;
+                top[half] = fmaxf(top[half], fabsf(x[half][e]));
+            }
+            float f = 1.f;
+            if constexpr (Tr::kNorm) {
+                // bring the row's largest value into [2^13, 2^14)
+                top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
+                top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
+                const int ex = int(__float_as_uint(top[half]) >> 23);           // biased exponent
+                const int up = min(max(127 + 13 - ex, -100), 100);
+                f = __uint_as_float(uint32_t(127 + up) << 23);
+#pragma unroll
+                for (int e = 0; e < T::kSteps * kE; ++e) x[half][e] *= f;
+            }
+            if (c == 0) sm_rs[r] = a.scale_log2 / f;     // (f is a power of two)
+        }
+#pragma unroll
+        for (int s = 0; s < T::kSteps; ++s) {
+            uint32_t w[kQP][4];
+            if constexpr (Tr::kMma == kTf32) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float v = x[half][2 * s + e];
+                        uint32_t hi, lo;
+                        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
+                        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(v - __uint_as_float(hi)));
+                        w[0][e * 2 + half] = hi;
+                        w[1][e * 2 + half] = lo;
+                    }
+            } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t part[kQP];
+                        split16<Tr::kMma, kQP>(x[half][4 * s + 2 * e], x[half][4 * s + 2 * e + 1], part);
+#pragma unroll
+                        for (int i = 0; i < kQP; ++i) w[i][e * 2 + half] = part[i];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < kQP; ++i)
+                reinterpret_cast<uint4 *>(qop)[((mt * T::kSteps + s) * kQP + i) * 32 + lane] =
+                    make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        }
+    }
+    __syncthreads();
+
+    // this thread's rows (g and g + 8 of each 16): masks, factors, softmax state
+    uint64_t see[MT][2];
+    float rs[MT][2], m[MT][2], l[MT][2];
+    uint64_t all = ~0ull;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = mt * 16 + half * 8 + g;
+            see[mt][half] = r < rows ? a.mask[f0 + (row0 + r) / G] : ~0ull;
+            all &= see[mt][half];
+            rs[mt][half] = sm_rs[r];
+            m[mt][half] = -INFINITY;
+            l[mt][half] = 0.f;
+        }
+    // some row does not see some node: a value that is not finite must not
+    // reach it through a weight of zero
+    const uint64_t present = nodes >= 64 ? ~0ull : (1ull << nodes) - 1;
+    const bool partial = __any_sync(0xffffffffu, (all & present) != present);
+
+    float o[MT][T::kNT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < T::kNT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
+    float gv = 0x1p-126f;            // scaled caches: o counts in units of gv, a power of two >= the value scales so far
+
+    uint32_t vr[T::kVR];
+    auto visible = [&](int mt, int half, int j) {
+        return j < pre || (j < total && (see[mt][half] >> (j - pre) & 1));
+    };
+
+    bool bad = false;                // a value that some row does not see is not finite
+    for (int t = t0; t < t1; t += kNW) {
+        const bool tail = (t + 1) * KS > pre;      // the tile holds nodes, or ends inside
+        // values of rows 2c, 2c + 1 of each eight
+#pragma unroll
+        for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = t * KS + u * 8 + 2 * c + e;
+                const uint8_t *p = vbase + size_t(j) * T::kRowB + g * T::kVLd;
+#pragma unroll
+                for (int i = 0; i < T::kNV; ++i)
+                    load_piece<T::kVLd>(vr + ((u * 2 + e) * T::kNV + i) * (T::kVLd / 4), p + i * 8 * T::kVLd,
+                                        j < total);
+            }
+        float ks[T::kT8][2], vs[T::kT8][2];
+        if constexpr (Tr::kScaled) {
+#pragma unroll
+            for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = t * KS + u * 8 + 2 * c + e;
+                    ks[u][e] = load_scale(kscale + j, j < total);
+                    vs[u][e] = load_scale(vscale + j, j < total);
+                }
+        }
+        // scores
+        float sc[MT][T::kT8][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[mt][u][i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < T::kSteps; ++s) {
+            uint32_t qa[MT][kQP][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < kQP; ++i) {
+                    const uint4 w = reinterpret_cast<const uint4 *>(qop)[((mt * T::kSteps + s) * kQP + i) * 32 + lane];
+                    qa[mt][i][0] = w.x, qa[mt][i][1] = w.y, qa[mt][i][2] = w.z, qa[mt][i][3] = w.w;
+                }
+#pragma unroll
+            for (int u = 0; u < T::kT8; ++u) {
+                const uint32_t *r = kr + u * T::kNK * (T::kKLd / 4);
+                if constexpr (Tr::kMma == kTf32) {
+                    const uint32_t h0 = r[2 * s] & 0xffffe000u, h1 = r[2 * s + 1] & 0xffffe000u;
+                    const uint32_t l0 = __float_as_uint(__uint_as_float(r[2 * s]) - __uint_as_float(h0));
+                    const uint32_t l1 = __float_as_uint(__uint_as_float(r[2 * s + 1]) - __uint_as_float(h1));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma1688(sc[mt][u], qa[mt][0], l0, l1);
+                        mma1688(sc[mt][u], qa[mt][1], h0, h1);
+                        mma1688(sc[mt][u], qa[mt][0], h0, h1);
+                    }
+                } else {
+                    uint32_t b0, b1;
+                    key_operand<Tr>(r, s, b0, b1);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = kQP - 1; i >= 0; --i) mma16816(sc[mt][u], qa[mt][i], b0, b1, Tr::kMma == kBf16);
+                }
+            }
+        }
+        if (t + kNW < t1) load_keys(t + kNW);
+
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sc[mt][u][i] *= rs[mt][i >> 1];
+                    if constexpr (Tr::kScaled) sc[mt][u][i] *= ks[u][i & 1];
+                }
+        if (tail) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!visible(mt, i >> 1, t * KS + u * 8 + 2 * c + (i & 1))) sc[mt][u][i] = -INFINITY;
+            if (partial) {
+                // a value that is not finite must not meet the weight zero of a
+                // row that does not see it: it is taken out here and added at the end
+                if constexpr (Tr::kScaled) {
+#pragma unroll
+                    for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = t * KS + u * 8 + 2 * c + e;
+                            if (j >= pre && !(fabsf(vs[u][e]) <= 3.0e38f)) vs[u][e] = 0.f, bad = true;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < T::kVR; ++i) {
+                    const uint32_t x = vr[i];
+                    uint32_t gone = 0;
+                    if constexpr (Tr::kMma == kTf32) gone = (x & 0x7f800000u) == 0x7f800000u ? ~0u : 0u;
+                    else if constexpr (Tr::kES == 2) gone = not_finite<Tr::kMma>(x);
+                    else if constexpr (Tr::kE4M3) gone = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    vr[i] = x & ~gone;
+                    bad = bad || gone != 0;
+                }
+            }
+        }
+
+        // weights, in place of the scores
+        float inv_gv = 1.f;
+        if constexpr (Tr::kScaled) {
+            float top = 0.f;
+#pragma unroll
+            for (int u = 0; u < T::kT8; ++u) top = fmaxf(top, fmaxf(vs[u][0], vs[u][1]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (top > gv) {      // (the same in every thread: rows 2c, 2c + 1 of all c)
+                const uint32_t up = min((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u, 253u << 23);
+                const float f = gv * __uint_as_float((254u << 23) - up);
+                gv = __uint_as_float(up);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < T::kNT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[mt][j][i] *= f;
+            }
+            inv_gv = __uint_as_float((254u << 23) - __float_as_uint(gv));
+#pragma unroll
+            for (int u = 0; u < T::kT8; ++u) vs[u][0] *= inv_gv, vs[u][1] *= inv_gv;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < T::kT8; ++u)
+                    top = fmaxf(top, fmaxf(sc[mt][u][half * 2], sc[mt][u][half * 2 + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float mn = fmaxf(m[mt][half], top), safe = mn == -INFINITY ? 0.f : mn;
+                const float ref = safe - (Tr::kMma == kF16 ? kShift : 0.f);
+                const float old = exp2_approx(m[mt][half] - safe);
+                m[mt][half] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = sc[mt][u][half * 2 + e];
+                        x = exp2_approx(x - ref);
+                        sum += x;
+                        if constexpr (Tr::kScaled) x *= vs[u][e];
+                    }
+                l[mt][half] = l[mt][half] * old + sum;
+#pragma unroll
+                for (int j = 0; j < T::kNT; ++j) {
+                    o[mt][j][half * 2] *= old;
+                    o[mt][j][half * 2 + 1] *= old;
+                }
+            }
+
+        // weighted sum
+        auto value = [&](int row, int j) {   // registers of a row's access (row: 0 .. 2 kT8 - 1) that holds element j
+            return vr + (row * T::kNV + j / T::kEV) * (T::kVLd / 4);
+        };
+        if constexpr (Tr::kMma == kTf32) {
+#pragma unroll
+            for (int u = 0; u < T::kT8; ++u) {
+                uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // a0 (g, row 2c), a1 (g + 8, 2c), a2 (g, 2c + 1), a3 (g + 8, 2c + 1)
+                        const float p = sc[mt][u][(i & 1) * 2 + (i >> 1)];
+                        ph[mt][i] = __float_as_uint(p) & 0xffffe000u;
+                        pl[mt][i] = __float_as_uint(p - __uint_as_float(ph[mt][i]));
+                    }
+#pragma unroll
+                for (int j = 0; j < T::kNT; ++j) {
+                    const uint32_t x0 = value(2 * u, j)[j % T::kEV], x1 = value(2 * u + 1, j)[j % T::kEV];
+                    const uint32_t h0 = x0 & 0xffffe000u, h1 = x1 & 0xffffe000u;
+                    const uint32_t l0 = __float_as_uint(__uint_as_float(x0) - __uint_as_float(h0));
+                    const uint32_t l1 = __float_as_uint(__uint_as_float(x1) - __uint_as_float(h1));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma1688(o[mt][j], ph[mt], l0, l1);
+                        mma1688(o[mt][j], pl[mt], h0, h1);
+                        mma1688(o[mt][j], ph[mt], h0, h1);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < T::kT8; u += 2) {
+                uint32_t pw[MT][Tr::kNP][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // a0 (g, rows 2c, 2c + 1), a1 (g + 8), a2 (g, the next eight's), a3 (g + 8)
+                        const int uu = u + (k >> 1), half = k & 1;
+                        uint32_t part[Tr::kNP];
+                        split16<Tr::kMma, Tr::kNP>(sc[mt][uu][half * 2], sc[mt][uu][half * 2 + 1], part);
+#pragma unroll
+                        for (int i = 0; i < Tr::kNP; ++i) pw[mt][i][k] = part[i];
+                    }
+#pragma unroll
+                for (int j = 0; j < T::kNT; ++j) {
+                    const uint32_t b0 = value_pair<Tr>(value(2 * u, j), value(2 * u + 1, j), j % T::kEV);
+                    const uint32_t b1 = value_pair<Tr>(value(2 * u + 2, j), value(2 * u + 3, j), j % T::kEV);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = Tr::kNP - 1; i >= 0; --i) mma16816(o[mt][j], pw[mt][i], b0, b1, Tr::kMma == kBf16);
+                }
+            }
+        }
+    }
+
+    // ---- join the warps, then the cluster ----
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float &x = l[mt][half];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            if (c == 0) {
+                sm_m[warp][mt * 16 + half * 8 + g] = m[mt][half];
+                sm_l[warp][mt * 16 + half * 8 + g] = x;
+            }
+        }
+    const bool cta_bad = __syncthreads_or(bad);   // (also: every warp is done with q's operands)
+    if (tid == 0) sm_bad = cta_bad;
+    float *so = reinterpret_cast<float *>(dyn);          // [kNW][R][D]
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = mt * 16 + half * 8 + g;
+            float top = sm_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kNW; ++w) top = fmaxf(top, sm_m[w][r]);
+            const float f = (top == -INFINITY ? 0.f : exp2_approx(m[mt][half] - top)) * (Tr::kScaled ? gv : 1.f);
+            float *dst = so + (size_t(warp) * R + r) * D;
+#pragma unroll
+            for (int j = 0; j < T::kNT; ++j) {
+                const int piece = j / T::kEV, w = j % T::kEV;
+                dst[(8 * piece + 2 * c) * T::kEV + w] = o[mt][j][half * 2] * f;
+                dst[(8 * piece + 2 * c + 1) * T::kEV + w] = o[mt][j][half * 2 + 1] * f;
+            }
+        }
+    __syncthreads();
+    float cta_m = 0.f, cta_l = 0.f;
+    if (tid < R) {
+        float top = sm_m[0][tid];
+        for (int w = 1; w < kNW; ++w) top = fmaxf(top, sm_m[w][tid]);
+        for (int w = 0; w < kNW; ++w)
+            cta_l += top == -INFINITY ? 0.f : sm_l[w][tid] * exp2_approx(sm_m[w][tid] - top);
+        cta_m = top;
+    }
+    for (int e = tid; e < rows * D; e += kNW * 32) {
+        float v = so[e];
+#pragma unroll
+        for (int w = 1; w < kNW; ++w) v += so[w * R * D + e];
+        so[e] = v;
+    }
+    __syncthreads();
+    if (tid < R) {
+        sm_m[0][tid] = cta_m;
+        sm_l[0][tid] = cta_l;
+    }
+    auto store = [&](int e, float v) {
+        const int r = e / D, d = e % D;
+        const size_t at = size_t(f0 + (row0 + r) / G) * a.out_stride + size_t(kvh * G + (row0 + r) % G) * D + d;
+        if (a.q_dtype == GPT2_F32) static_cast<float *>(a.out)[at] = v;
+        else if (a.q_dtype == GPT2_F16) static_cast<__half *>(a.out)[at] = __float2half_rn(v);
+        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+    };
+    // the infinities and NaNs that were taken out, for the rows that see them
+    auto bad_sum = [&](int e) {
+        const int r = e / D, d = e % D;
+        const uint64_t sees = a.mask[f0 + (row0 + r) / G];
+        float x = 0.f;
+        for (int j = pre; j < total; ++j) {
+            if (!(sees >> (j - pre) & 1)) continue;
+            const float v = element<Tr>(vbase + size_t(j) * T::kRowB, d) * (Tr::kScaled ? vscale[j] : 1.f);
+            if (!(fabsf(v) <= 3.0e38f)) x += v;
+        }
+        return x;
+    };
+    if (a.splits == 1) {
+        __syncthreads();
+        for (int e = tid; e < rows * D; e += kNW * 32) {
+            const float sum = sm_l[0][e / D];
+            float v = sum == 0.f ? 0.f : so[e] / sum;
+            if (cta_bad) v += bad_sum(e);
+            store(e, v);
+        }
+    } else {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        bool any_bad = false;
+        for (int k = 0; k < a.splits; ++k) any_bad = any_bad || *cl.map_shared_rank(&sm_bad, k) != 0;
+        // every CTA finishes its share of the elements from all CTAs' sums
+        for (int e = rank * kNW * 32 + tid; e < rows * D; e += a.splits * kNW * 32) {
+            const int r = e / D;
+            float top = -INFINITY;
+            for (int k = 0; k < a.splits; ++k) top = fmaxf(top, *cl.map_shared_rank(&sm_m[0][r], k));
+            float sum = 0.f, v = 0.f;
+            for (int k = 0; k < a.splits; ++k) {
+                const float mk = *cl.map_shared_rank(&sm_m[0][r], k);
+                const float f = top == -INFINITY ? 0.f : exp2_approx(mk - top);
+                sum += *cl.map_shared_rank(&sm_l[0][r], k) * f;
+                v += *cl.map_shared_rank(so + e, k) * f;
+            }
+            v = sum == 0.f ? 0.f : v / sum;
+            if (any_bad) v += bad_sum(e);
+            store(e, v);
+        }
+        cl.sync();          // nobody leaves while its sums are read
+    }
+}
+
+template <class Tr, int D, int MT>
+cudaError_t launch(const TreeArgs &a, cudaStream_t s)
+{
+    auto fn = k_tree_attn<Tr, D, MT>;
+    constexpr size_t smem = Smem<Tr, D, MT>::kBytes;
+    cudaError_t e = cudaSuccess;
+    if (smem > 40 * 1024)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e == cudaSuccess && a.splits > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(a.n_seqs) * a.kv.n_head * a.row_tiles * a.splits);
+    cfg.blockDim = dim3(kNW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = unsigned(a.splits);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+template <class Tr>
+cudaError_t launch_shape(const TreeArgs &a, int mt, cudaStream_t s)
+{
+    switch (a.kv.head_dim) {
+    case 32: return mt == 1 ? launch<Tr, 32, 1>(a, s) : launch<Tr, 32, 2>(a, s);
+    case 64: return mt == 1 ? launch<Tr, 64, 1>(a, s) : launch<Tr, 64, 2>(a, s);
+    default: return mt == 1 ? launch<Tr, 128, 1>(a, s) : launch<Tr, 128, 2>(a, s);
+    }
+}
+
+}  // namespace tree
+}  // namespace gpt2

@@ -1,0 +1,450 @@
+// gpt2_op_verify_tree: which drafted nodes the target accepts, and the token
+// after them.
+//
+// Two kernels.  k_row_stats reads every logit once and leaves, per chunk of a
+// row, the maximum and the sum of exp((l - max) / temperature) (or the argmax
+// key): it is bound by HBM.  k_verify, one cluster of CTAs per sequence, joins
+// the chunks, looks up every node's probability at its parent, walks the tree
+// in one thread, and draws the next token with all threads: of the rows, only
+// the last node's is read again (and its draft distribution and the sequence's
+// random numbers once).  A rejected child that has a sibling behind it costs
+// one more pass over the row, for the sum that makes the rest a distribution.
+//
+// Rounding: probabilities of single tokens, the residual's scale and every
+// comparison are in 64 bits; the sums over the vocabulary are fp32 per thread
+// (at most a few dozen terms) and 64 bits across threads; the race over the
+// vocabulary compares fp32 values.
+#include <cooperative_groups.h>
+
+#include <cfloat>
+#include <cmath>
+
+#include "common.cuh"
+#include "spec.h"
+
+namespace gpt2 {
+namespace {
+
+constexpr int kChunk = 8192;       // logits per CTA of k_row_stats
+constexpr int kStatThreads = 256;
+constexpr int kVec = kChunk / 4 / kStatThreads;   // 16-byte loads in flight per thread
+constexpr int kVThreads = 512;
+constexpr int kMaxCluster = 8;
+
+struct Stat {
+    float m, z;                    // maximum, sum of exp((l - m) / T)
+    unsigned long long key;        // temperature 0: argmax key
+};
+
+struct VerifyArgs {
+    const float *logits, *draft, *u_accept, *u_draw;
+    const int32_t *tokens, *parents, *first;
+    int32_t *path, *n_path, *next_token;
+    Stat *stats;                   // [n_rows][chunks]
+    int32_t V, n_seqs, n_rows, max_nodes, chunks, cluster;
+    float c_hi, c_lo;              // log2(e) / temperature as two fp32 parts; 0: greedy
+    double inv_t;
+};
+
+// exp(d / temperature) for d <= 0, 0 for -infinity (the two parts keep the
+// exponent's scale to 48 bits; the exponent itself is rounded once).
+__device__ __forceinline__ float weight(const VerifyArgs &a, float d)
+{
+    return d == -INFINITY ? 0.f : exp2f(fmaf(d, a.c_hi, d * a.c_lo));
+}
+
+__global__ void __launch_bounds__(kStatThreads) k_row_stats(const VerifyArgs a)
+{
+    __shared__ float red[kStatThreads / 32];
+    __shared__ unsigned long long keys[kStatThreads / 32];
+    pdl_launch_dependents();
+    const int row = blockIdx.x, chunk = blockIdx.y, tid = threadIdx.x;
+    if (row >= min(max(a.first[a.n_seqs], 0), a.n_rows)) return;
+    // chunks of a row: equal shares, a multiple of 4
+    const int per = ((a.V + a.chunks - 1) / a.chunks + 3) / 4 * 4;
+    const int lo = min(chunk * per, a.V), hi = min(lo + per, a.V);
+    const float *p = a.logits + size_t(row) * a.V + lo;
+    const int n = hi - lo;
+    // up to three values before a 16-byte boundary, then whole vectors, then the rest
+    const int head = min(n, int((16 - reinterpret_cast<uintptr_t>(p) % 16) / 4 % 4));
+    const int n4 = (n - head) / 4, rest = head + n4 * 4;
+    const float4 *p4 = reinterpret_cast<const float4 *>(p + head);
+    float v[kVec + 1][4];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int k = tid + i * kStatThreads;
+        float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (k < n4) x = __ldcs(p4 + k);
+        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+    }
+    v[kVec][0] = tid < head ? p[tid] : -INFINITY;
+    v[kVec][1] = tid < n - rest ? p[rest + tid] : -INFINITY;
+    v[kVec][2] = v[kVec][3] = -INFINITY;
+    Stat *out = a.stats + size_t(row) * a.chunks + chunk;
+    if (a.c_hi == 0.f) {
+        // (a NaN or -infinity gets no key)
+        unsigned long long best = 0;
+        auto take = [&](float x, int i) {
+            if (x > -INFINITY) {
+                const unsigned long long k = argmax_key(x, uint32_t(lo + i));
+                best = k > best ? k : best;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) take(v[i][j], head + (tid + i * kStatThreads) * 4 + j);
+        take(v[kVec][0], tid);
+        take(v[kVec][1], rest + tid);
+        best = warp_max_u64(best);
+        if ((tid & 31) == 0) keys[tid >> 5] = best;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 1; w < kStatThreads / 32; ++w) best = keys[w] > best ? keys[w] : best;
+            *out = Stat{0.f, 0.f, best};
+        }
+        return;
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i <= kVec; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i][j]);
+    m = warp_max(m);
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+    for (int w = 0; w < kStatThreads / 32; ++w) m = fmaxf(m, red[w]);
+    __syncthreads();
+    float z = 0.f;
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i <= kVec; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z += weight(a, v[i][j] - ref);   // (NaN and +infinity leave a NaN)
+    z = warp_sum(z);
+    if ((tid & 31) == 0) red[tid >> 5] = z;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kStatThreads / 32; ++w) z += red[w];
+        *out = Stat{m, z, 0};
+    }
+}
+
+// What the walk of a sequence has come to; thread 0 of every CTA of the
+// cluster computes the same.
+struct Walk {
+    unsigned long long children[GPT2_MAX_NODES];
+    double prob[GPT2_MAX_NODES];       // p(token) at the parent
+    float q[GPT2_MAX_NODES], u[GPT2_MAX_NODES];
+    float m[GPT2_MAX_NODES], inv_z[GPT2_MAX_NODES];
+    double z[GPT2_MAX_NODES];
+    int choice[GPT2_MAX_NODES];        // temperature 0
+    int token[GPT2_MAX_NODES];
+    bool valid[GPT2_MAX_NODES];
+    // children of `cur` rejected so far: their tokens (draft on one token), or
+    // the sums that bring what is left back to a distribution
+    int rejected[GPT2_MAX_NODES];
+    double mass[GPT2_MAX_NODES];
+    float inv_mass[GPT2_MAX_NODES];    // (0 where nothing is left)
+    int n_rejected, cur, length, path[GPT2_MAX_NODES];
+    double scale;                      // draft on one token: 1 / what is left
+    unsigned long long left;           // children of cur not tried yet
+    bool need_mass, dead;
+};
+
+// Goes on until the walk ends (need_mass false) or a sum over the vocabulary
+// is needed (need_mass true; mass[n_rejected - 1] is then to be set).
+__device__ void walk_on(const VerifyArgs &a, Walk &w)
+{
+    w.need_mass = false;
+    while (w.left) {
+        const int i = __ffsll((long long)w.left) - 1;
+        w.left &= w.left - 1;
+        const int x = w.token[i];
+        if (x < 0 || x >= a.V || !w.valid[w.cur]) continue;
+        bool yes;
+        double r = 0.0;
+        if (a.c_hi == 0.f) {
+            yes = w.choice[w.cur] == x;
+        } else {
+            r = w.prob[i];
+            if (a.draft) {
+                for (int k = 0; k < w.n_rejected; ++k) {
+                    r -= double(w.q[i]);
+                    r = r > 0.0 && w.mass[k] > 0.0 ? r / w.mass[k] : 0.0;
+                }
+            } else {
+                r = w.dead ? 0.0 : r * w.scale;
+                for (int k = 0; k < w.n_rejected; ++k)
+                    if (w.rejected[k] == x) r = 0.0;
+            }
+            yes = double(w.u[i]) * double(w.q[i]) < r;
+        }
+        if (yes) {
+            w.path[w.length++] = i;
+            w.cur = i;
+            w.left = w.children[i];
+            w.n_rejected = 0;
+            w.scale = 1.0;
+            w.dead = false;
+        } else if (a.c_hi != 0.f) {
+            w.rejected[w.n_rejected] = x;
+            w.inv_mass[w.n_rejected] = 1.f;
+            w.mass[w.n_rejected++] = 1.0;
+            if (!a.draft) {
+                const double rest = 1.0 - r;
+                if (rest > 0.0) w.scale /= rest;
+                else w.dead = true;
+            } else if (w.left) {
+                w.need_mass = true;
+                return;
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
+{
+    namespace cg = cooperative_groups;
+    __shared__ Walk w;
+    __shared__ double red[kVThreads / 32];
+    __shared__ unsigned long long keys[kVThreads / 32];
+    __shared__ double part_sum[2];                 // this CTA's share, for the cluster (two rounds in flight)
+    __shared__ unsigned long long part_key[2];
+    const int b = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+    const int tid = threadIdx.x;
+    const int f0 = min(max(a.first[b], 0), a.n_rows), f1 = min(max(a.first[b + 1], f0), a.n_rows);
+    const int nodes = min(f1 - f0, a.max_nodes);
+    int parent = -1;
+    if (tid < GPT2_MAX_NODES) {
+        w.children[tid] = 0;
+        if (tid > 0 && tid < nodes) parent = a.parents[f0 + tid];
+        if (tid < nodes) w.token[tid] = a.tokens[f0 + tid];
+    }
+    __syncthreads();
+    if (parent >= 0 && parent < tid) atomicOr(&w.children[parent], 1ull << tid);
+    pdl_wait();                                    // k_row_stats' sums
+    if (tid < nodes) {
+        const Stat *st = a.stats + size_t(f0 + tid) * a.chunks;
+        float m = -INFINITY;
+        unsigned long long key = 0;
+        for (int k = 0; k < a.chunks; ++k) {
+            m = fmaxf(m, st[k].m);
+            key = st[k].key > key ? st[k].key : key;
+        }
+        if (a.c_hi == 0.f) {
+            w.valid[tid] = key != 0;
+            w.choice[tid] = key != 0 ? argmax_key_index(key) : -1;
+        } else {
+            double z = 0.0;
+            for (int k = 0; k < a.chunks; ++k)
+                if (st[k].z != 0.f) z += double(st[k].z) * double(weight(a, st[k].m - m));
+            w.m[tid] = m;
+            w.z[tid] = z;
+            w.inv_z[tid] = float(1.0 / z);
+            w.valid[tid] = z > 0.0 && fabsf(m) <= FLT_MAX;   // (false for NaN sums)
+        }
+    }
+    __syncthreads();
+    if (a.c_hi != 0.f && parent >= 0 && parent < tid) {
+        const int x = w.token[tid];
+        w.u[tid] = a.u_accept[f0 + tid];
+        w.q[tid] = 1.f;
+        w.prob[tid] = 0.0;
+        if (x >= 0 && x < a.V) {
+            const size_t at = size_t(f0 + parent) * a.V + x;
+            w.prob[tid] = exp((double(a.logits[at]) - double(w.m[parent])) * a.inv_t) / w.z[parent];
+            if (a.draft) w.q[tid] = a.draft[at];
+        }
+    }
+    if (tid == 0) {
+        w.cur = 0;
+        w.length = nodes > 0 ? 1 : 0;
+        w.path[0] = 0;
+        w.left = nodes > 0 ? w.children[0] : 0;
+        w.n_rejected = 0;
+        w.scale = 1.0;
+        w.dead = false;
+    }
+    __syncthreads();
+
+    const cg::cluster_group cl = cg::this_cluster();
+    const int per = (a.V + a.cluster - 1) / a.cluster, v0 = rank * per, v1 = min(a.V, v0 + per);
+    int round = 0;
+    // what is left of p at id v after the rejected children (scaled by any factor)
+    auto residual = [&](float p, float q, int v, int n) {
+        if (a.draft) {
+            for (int k = 0; k < n; ++k) p = fmaxf(p - q, 0.f) * w.inv_mass[k];
+        } else {
+            if (w.dead) return 0.f;
+            for (int k = 0; k < n; ++k)
+                if (w.rejected[k] == v) p = 0.f;
+        }
+        return p;
+    };
+    for (;;) {
+        if (tid == 0) walk_on(a, w);
+        __syncthreads();
+        if (!w.need_mass) break;                   // (the same in every CTA of the cluster)
+        const size_t row = size_t(f0 + w.cur) * a.V;
+        const float m = w.m[w.cur], iz = w.inv_z[w.cur];
+        const int n = w.n_rejected;
+        float s = 0.f;
+        for (int v = v0 + tid; v < v1; v += kVThreads)
+            s += residual(weight(a, a.logits[row + v] - m) * iz, a.draft[row + v], v, n);
+        s = warp_sum(s);
+        if ((tid & 31) == 0) red[tid >> 5] = double(s);
+        __syncthreads();
+        if (tid == 0) {
+            double t = 0.0;
+            for (int k = 0; k < kVThreads / 32; ++k) t += red[k];
+            part_sum[round & 1] = t;
+        }
+        cl.sync();
+        if (tid == 0) {
+            double t = 0.0;
+            for (int k = 0; k < a.cluster; ++k) t += *cl.map_shared_rank(&part_sum[round & 1], k);
+            w.mass[n - 1] = t;
+            w.inv_mass[n - 1] = t > 0.0 ? float(1.0 / t) : 0.f;
+        }
+        ++round;
+        __syncthreads();
+    }
+
+    int token = -1;
+    if (nodes > 0 && w.valid[w.cur]) {             // (the same in every CTA of the cluster)
+        if (a.c_hi == 0.f) {
+            token = w.choice[w.cur];
+        } else {
+            const size_t row = size_t(f0 + w.cur) * a.V;
+            const float m = w.m[w.cur], iz = w.inv_z[w.cur];
+            const float *u = a.u_draw + size_t(b) * a.V;
+            // the race over what is left; where nothing is, over the node's own distribution
+            for (int pass = 0; pass < 2; ++pass) {
+                const int n = pass == 0 ? w.n_rejected : 0;
+                const bool dense = a.draft && n > 0;
+                unsigned long long best = 0;
+                for (int v = v0 + tid; v < v1; v += kVThreads) {
+                    const float p = weight(a, a.logits[row + v] - m) * iz;
+                    const float r = n > 0 ? residual(p, dense ? a.draft[row + v] : 0.f, v, n) : p;
+                    if (r > 0.f) {
+                        const unsigned long long k = argmax_key(r / -logf(u[v]), uint32_t(v));
+                        best = k > best ? k : best;
+                    }
+                }
+                best = warp_max_u64(best);
+                if ((tid & 31) == 0) keys[tid >> 5] = best;
+                __syncthreads();
+                if (tid == 0) {
+                    for (int k = 0; k < kVThreads / 32; ++k) best = keys[k] > best ? keys[k] : best;
+                    part_key[round & 1] = best;
+                }
+                cl.sync();
+                best = 0;
+                for (int k = 0; k < a.cluster; ++k) {
+                    const unsigned long long o = *cl.map_shared_rank(&part_key[round & 1], k);
+                    best = o > best ? o : best;
+                }
+                ++round;
+                if (best != 0) {
+                    token = argmax_key_index(best);
+                    break;
+                }
+                if (n == 0) break;
+            }
+        }
+    }
+    if (rank == 0) {
+        if (tid < a.max_nodes) a.path[size_t(b) * a.max_nodes + tid] = tid < w.length ? w.path[tid] : -1;
+        if (tid == 0) {
+            a.n_path[b] = w.length;
+            a.next_token[b] = token;
+        }
+    }
+    cl.sync();                                     // nobody leaves while its shares are read
+}
+
+int chunks_of(int32_t vocab) { return (vocab + kChunk - 1) / kChunk; }
+
+}  // namespace
+}  // namespace gpt2
+
+using namespace gpt2;
+
+extern "C" {
+
+size_t gpt2_op_verify_tree_workspace(int32_t n_rows, int32_t vocab)
+{
+    if (n_rows < 1 || vocab < 1) return 16;
+    return size_t(n_rows) * chunks_of(vocab) * sizeof(Stat);
+}
+
+int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *tokens, const int32_t *parents,
+                        const int32_t *first, int32_t n_seqs, int32_t n_rows, int32_t max_nodes, float temperature,
+                        const float *draft_probs, const float *u_accept, const float *u_draw, int32_t *path,
+                        int32_t *n_path, int32_t *next_token, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!logits || !tokens || !parents || !first || !path || !n_path || !next_token || !workspace)
+        return GPT2_ERR_INVALID_ARG;
+    if (vocab < 1 || n_seqs < 0 || n_rows < 0 || max_nodes < 1 || max_nodes > GPT2_MAX_NODES)
+        return GPT2_ERR_INVALID_ARG;
+    if (!(temperature >= 0.f) || !std::isfinite(temperature)) return GPT2_ERR_INVALID_ARG;
+    const double c = temperature > 0.f ? 1.4426950408889634 / double(temperature) : 0.0;
+    if (c > double(FLT_MAX)) return GPT2_ERR_INVALID_ARG;
+    if (temperature > 0.f && (!u_accept || !u_draw)) return GPT2_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % 4 || !aligned16(workspace)) return GPT2_ERR_INVALID_ARG;
+    if (workspace_bytes < gpt2_op_verify_tree_workspace(n_rows, vocab)) return GPT2_ERR_INVALID_ARG;
+    if (chunks_of(vocab) > 65535 || (long long)n_seqs * kMaxCluster >= (1ll << 31)) return GPT2_ERR_INVALID_ARG;
+    if (n_seqs == 0) return GPT2_OK;
+    int rc;
+    const int sms = spec_sms(&rc);
+    if (!sms) return rc;
+    VerifyArgs a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.parents = parents;
+    a.first = first;
+    a.path = path;
+    a.n_path = n_path;
+    a.next_token = next_token;
+    a.stats = static_cast<Stat *>(workspace);
+    a.V = vocab;
+    a.n_seqs = n_seqs;
+    a.n_rows = n_rows;
+    a.max_nodes = max_nodes;
+    a.chunks = chunks_of(vocab);
+    a.cluster = 1;
+    if (temperature > 0.f) {
+        a.draft = draft_probs;
+        a.u_accept = u_accept;
+        a.u_draw = u_draw;
+        a.c_hi = float(c);
+        a.c_lo = float(c - double(a.c_hi));
+        a.inv_t = 1.0 / double(temperature);
+        // the final draw reads a row with the CTAs of a cluster: as many as
+        // keep 2048 ids or more each, while all sequences' fit the GPU together
+        while (a.cluster < kMaxCluster && vocab >= 4096 * a.cluster && n_seqs * a.cluster * 2ll <= 4ll * sms)
+            a.cluster *= 2;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n_rows > 0) {
+        k_row_stats<<<dim3(n_rows, a.chunks), kStatThreads, 0, s>>>(a);
+        rc = spec_rc(cudaGetLastError());
+        if (rc != GPT2_OK) return rc;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(n_seqs) * a.cluster);
+    cfg.blockDim = dim3(kVThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = unsigned(a.cluster);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = n_rows > 0 ? 1 : 0;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return spec_rc(cudaLaunchKernelEx(&cfg, k_verify, a));
+}
+
+}  // extern "C"
