@@ -484,159 +484,157 @@ def op_linear_bf16(W_bf16, X, stream=None):
 # Caches are CUDA tensors [slots][heads][positions][head_dim] of torch.float32,
 # float16, bfloat16, int8 or float8_e4m3fn; the two 8-bit types come with fp32
 # scales [slots][heads][positions].  Index tensors are int32 (the masks int64,
-# taken as 64 bits).  Every tensor lives on the current device; tensors that a
-# call makes are made on its stream.  See the gpt2_op_* calls of include/gpt2.h.
+# taken as 64 bits).  Every tensor lives on the current device; a call with
+# `stream` runs, and makes the tensors that it makes, on that stream.  See the
+# gpt2_op_* calls of include/gpt2.h.
 
-_row_types = None
+_types = None
 
 
-def _dtypes():
-    """torch dtypes of rows and of caches -> GPT2_*."""
-    global _row_types, _cache_types
-    if _row_types is None:
+class _Types:
+    """torch's types (torch is not imported with this module)."""
+
+    def __init__(self):
         import torch
-        _cache_types = {torch.float32: GPT2_F32, torch.float16: GPT2_F16, torch.bfloat16: GPT2_BF16,
-                        torch.int8: GPT2_INT8, torch.float8_e4m3fn: GPT2_E4M3}
-        _row_types = {torch.float32: GPT2_F32, torch.float16: GPT2_F16, torch.bfloat16: GPT2_BF16}
-    return _row_types, _cache_types
+        self.torch = torch
+        self.rows = {torch.float32: GPT2_F32, torch.float16: GPT2_F16, torch.bfloat16: GPT2_BF16}
+        self.caches = {**self.rows, torch.int8: GPT2_INT8, torch.float8_e4m3fn: GPT2_E4M3}
+        self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.device = torch.cuda.current_device
 
 
-def _on_device(**tensors):
-    """Raises unless every tensor is on the current CUDA device."""
-    import torch
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and (t.device.type != "cuda" or t.device.index != dev):
-            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
+def _call():
+    """(types, library, current device)."""
+    global _types
+    if _types is None:
+        lib()
+        _types = _Types()
+    return _types, _lib, _types.device()
 
 
-def _whole(name, t, dtype, shape):
-    """Raises unless t is a contiguous tensor of this type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
+def _whole(name, t, dtype, shape, dev):
+    """Raises unless t is a contiguous tensor of this type and shape on the
+    current device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current device "
+                         f"cuda:{dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _kv(k_cache, v_cache, k_scale, v_scale, layers=False):
+def _kv(k_cache, v_cache, k_scale, v_scale, ty, dev, layers=False):
     """(gpt2_kv, layers) of a layer's cache, or of [layers][slots]... caches."""
-    import torch
-    types = _dtypes()[1]
-    nd = k_cache.dim()
+    shape, dtype = k_cache.shape, k_cache.dtype
+    nd = len(shape)
     if nd != 4 and not (layers and nd == 5):
-        raise ValueError(f"a cache is [slots][heads][positions][head_dim], not {tuple(k_cache.shape)}")
-    if k_cache.dtype not in types:
-        raise ValueError(f"unsupported cache type {k_cache.dtype}")
-    if not k_cache.is_contiguous():
-        raise ValueError("k_cache must be contiguous")
-    _whole("v_cache", v_cache, k_cache.dtype, k_cache.shape)
-    t = types[k_cache.dtype]
+        raise ValueError(f"a cache is [slots][heads][positions][head_dim], not {tuple(shape)}")
+    t = ty.caches.get(dtype)
+    if t is None:
+        raise ValueError(f"unsupported cache type {dtype}")
+    _whole("k_cache", k_cache, dtype, shape, dev)
+    _whole("v_cache", v_cache, dtype, shape, dev)
+    ks = vs = None
     if t >= GPT2_INT8:
         if k_scale is None or v_scale is None:
             raise ValueError("an 8-bit cache needs k_scale and v_scale")
-        _whole("k_scale", k_scale, torch.float32, k_cache.shape[:-1])
-        _whole("v_scale", v_scale, torch.float32, k_cache.shape[:-1])
+        _whole("k_scale", k_scale, ty.f32, shape[:-1], dev)
+        _whole("v_scale", v_scale, ty.f32, shape[:-1], dev)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
-        raise ValueError(f"a {k_cache.dtype} cache has no scales")
-    S, H, P, D = k_cache.shape[-4:]
-    kv = KV(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
-            v_scale.data_ptr() if v_scale is not None else None, t, S, H, P, D)
-    return kv, (k_cache.shape[0] if nd == 5 else 1)
+        raise ValueError(f"a {dtype} cache has no scales")
+    L = 1
+    if nd == 5:
+        L, S, H, P, D = shape
+    else:
+        S, H, P, D = shape
+    return KV(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, t, S, H, P, D), L
 
 
-def _rows(name, t, H, D):
+def _rows(name, t, H, D, ty, dev):
     """The row stride of a [rows][H][D] tensor whose rows are contiguous."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (H, D):
+    n, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
+    if h != H or d != D:
         raise ValueError(f"{name} must be [rows][{H}][{D}], not {tuple(t.shape)}")
-    if t.dtype not in _dtypes()[0]:
-        raise ValueError(f"unsupported {name} type {t.dtype}")
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    if t.dtype not in ty.rows or t.get_device() != dev:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16 on the current device cuda:{dev}, "
+                         f"not {t.dtype} on {t.device}")
+    r, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else H * D
-
-
-class _OnStream:
-    """The call's stream: allocations inside belong to it."""
-
-    def __init__(self, stream):
-        self.stream = stream
-
-    def __enter__(self):
-        import torch
-        self.ctx = torch.cuda.stream(self.stream) if self.stream is not None else None
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return (self.stream if self.stream is not None else torch.cuda.current_stream()).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+    return r if n > 1 else H * D
 
 
 def op_kv_store(k, v, k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, stream=None):
     """Writes rows of k and v ([rows][heads][head_dim], possibly views into
     fused QKV rows) into the cache at (slot[i], pos[i]), quantised or rounded
     to its type; rows outside the cache are skipped."""
-    import torch
-    _on_device(k=k, v=v, k_cache=k_cache, v_cache=v_cache, slot=slot, pos=pos, k_scale=k_scale, v_scale=v_scale)
-    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale)
+    ty, L, dev = _call()
+    if stream is not None:
+        with ty.torch.cuda.stream(stream):
+            return op_kv_store(k, v, k_cache, v_cache, slot, pos, k_scale, v_scale)
+    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev)
+    stride = _rows("k", k, kv.n_head, kv.head_dim, ty, dev)
     n = k.shape[0]
-    stride = _rows("k", k, kv.n_head, kv.head_dim)
-    if v.dtype != k.dtype or v.shape != k.shape or _rows("v", v, kv.n_head, kv.head_dim) != stride:
+    if v.dtype is not k.dtype or v.shape != k.shape or _rows("v", v, kv.n_head, kv.head_dim, ty, dev) != stride:
         raise ValueError("k and v must have the same type, shape and row stride")
-    _whole("slot", slot, torch.int32, (n,))
-    _whole("pos", pos, torch.int32, (n,))
-    with _OnStream(stream) as s:
-        if n > 0:
-            check(lib().gpt2_op_kv_store(kv, k.data_ptr(), v.data_ptr(), _row_types[k.dtype], stride,
-                                         slot.data_ptr(), pos.data_ptr(), n, s), "gpt2_op_kv_store")
+    _whole("slot", slot, ty.i32, (n,), dev)
+    _whole("pos", pos, ty.i32, (n,), dev)
+    if n > 0:
+        check(L.gpt2_op_kv_store(kv, k.data_ptr(), v.data_ptr(), ty.rows[k.dtype], stride, slot.data_ptr(),
+                                 pos.data_ptr(), n, ty.raw_stream(dev)), "gpt2_op_kv_store")
 
 
 def op_kv_load(k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, dtype=None, k=None, v=None, stream=None):
     """Reads cache rows (slot[i], pos[i]) back as (k, v), each [rows][heads]
     [head_dim] of `dtype` (float32 unless given, or the given k's); rows
     outside the cache are zeros."""
-    import torch
-    _on_device(k=k, v=v, k_cache=k_cache, v_cache=v_cache, slot=slot, pos=pos, k_scale=k_scale, v_scale=v_scale)
-    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale)
-    n = slot.numel()
-    _whole("slot", slot, torch.int32, (n,))
-    _whole("pos", pos, torch.int32, (n,))
+    ty, L, dev = _call()
+    if stream is not None:
+        with ty.torch.cuda.stream(stream):
+            return op_kv_load(k_cache, v_cache, slot, pos, k_scale, v_scale, dtype, k, v)
+    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev)
+    H, D, n = kv.n_head, kv.head_dim, slot.shape[0] if slot.dim() == 1 else -1
+    _whole("slot", slot, ty.i32, (n,), dev)
+    _whole("pos", pos, ty.i32, (n,), dev)
     if (k is None) != (v is None):
         raise ValueError("give both k and v, or neither")
-    with _OnStream(stream) as s:
-        if k is None:
-            k = torch.empty((n, kv.n_head, kv.head_dim), dtype=dtype or torch.float32, device=k_cache.device)
-            v = torch.empty_like(k)
-        elif dtype is not None and dtype != k.dtype:
+    if k is None:
+        dtype = dtype or ty.f32
+        if dtype not in ty.rows:
+            raise ValueError(f"unsupported row type {dtype}")
+        k = ty.torch.empty((n, H, D), dtype=dtype, device=k_cache.device)
+        v = ty.torch.empty_like(k)
+        stride = H * D
+    else:
+        stride = _rows("k", k, H, D, ty, dev)
+        if dtype is not None and dtype is not k.dtype:
             raise ValueError(f"k is {k.dtype}, not {dtype}")
-        stride = _rows("k", k, kv.n_head, kv.head_dim)
-        if k.shape[0] != n or v.dtype != k.dtype or v.shape != k.shape or \
-                _rows("v", v, kv.n_head, kv.head_dim) != stride:
+        if k.shape[0] != n or v.dtype is not k.dtype or v.shape != k.shape or \
+                _rows("v", v, H, D, ty, dev) != stride:
             raise ValueError("k and v must be [rows][heads][head_dim] of the same type and row stride")
-        if n > 0:
-            check(lib().gpt2_op_kv_load(kv, slot.data_ptr(), pos.data_ptr(), n, k.data_ptr(), v.data_ptr(),
-                                        _row_types[k.dtype], stride, s), "gpt2_op_kv_load")
+    if n > 0:
+        check(L.gpt2_op_kv_load(kv, slot.data_ptr(), pos.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                ty.rows[k.dtype], stride, ty.raw_stream(dev)), "gpt2_op_kv_load")
     return k, v
 
 
 def op_kv_commit(k_cache, v_cache, slot, cached, path, n_path, k_scale=None, v_scale=None, stream=None):
     """Moves the accepted nodes' cache rows into place, in every layer of a
     [layers][slots][heads][positions][head_dim] cache (or of one layer's)."""
-    import torch
-    _on_device(k_cache=k_cache, v_cache=v_cache, slot=slot, cached=cached, path=path, n_path=n_path,
-               k_scale=k_scale, v_scale=v_scale)
-    kv, layers = _kv(k_cache, v_cache, k_scale, v_scale, layers=True)
-    B = slot.numel()
-    if path.dim() != 2 or not 1 <= path.shape[1] <= MAX_NODES:
+    ty, L, dev = _call()
+    if stream is not None:
+        with ty.torch.cuda.stream(stream):
+            return op_kv_commit(k_cache, v_cache, slot, cached, path, n_path, k_scale, v_scale)
+    kv, layers = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev, layers=True)
+    B, T = path.shape if path.dim() == 2 else (0, 0)
+    if not 1 <= T <= MAX_NODES:
         raise ValueError(f"path must be [sequences][nodes], at most {MAX_NODES} nodes")
-    _whole("slot", slot, torch.int32, (B,))
-    _whole("cached", cached, torch.int32, (B,))
-    _whole("path", path, torch.int32, (B, path.shape[1]))
-    _whole("n_path", n_path, torch.int32, (B,))
-    with _OnStream(stream) as s:
-        if B > 0:
-            check(lib().gpt2_op_kv_commit(kv, layers, slot.data_ptr(), cached.data_ptr(), path.data_ptr(),
-                                          n_path.data_ptr(), B, path.shape[1], s), "gpt2_op_kv_commit")
+    _whole("slot", slot, ty.i32, (B,), dev)
+    _whole("cached", cached, ty.i32, (B,), dev)
+    _whole("path", path, ty.i32, (B, T), dev)
+    _whole("n_path", n_path, ty.i32, (B,), dev)
+    if B > 0:
+        check(L.gpt2_op_kv_commit(kv, layers, slot.data_ptr(), cached.data_ptr(), path.data_ptr(), n_path.data_ptr(),
+                                  B, T, ty.raw_stream(dev)), "gpt2_op_kv_commit")
 
 
 def tree_masks(parents) -> np.ndarray:
@@ -659,30 +657,32 @@ def op_tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes,
     """Attention of packed drafted nodes q [rows][query heads][head_dim] over
     the cached prefix and the nodes of their masks; scale 1/sqrt(head_dim)
     unless given.  Returns out, like q."""
-    import torch
-    _on_device(q=q, k_cache=k_cache, v_cache=v_cache, slot=slot, cached=cached, first=first, mask=mask,
-               k_scale=k_scale, v_scale=v_scale, out=out)
-    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3 or q.shape[2] != kv.head_dim:
-        raise ValueError(f"q must be [rows][heads][{kv.head_dim}], not {tuple(q.shape)}")
-    n, H, D = q.shape
-    B = slot.numel()
-    stride = _rows("q", q, H, D)
-    _whole("slot", slot, torch.int32, (B,))
-    _whole("cached", cached, torch.int32, (B,))
-    _whole("first", first, torch.int32, (B + 1,))
-    _whole("mask", mask, torch.int64, (n,))
-    with _OnStream(stream) as s:
-        if out is None:
-            out = torch.empty((n, H, D), dtype=q.dtype, device=q.device)
-        elif out.dtype != q.dtype or out.shape != q.shape:
+    ty, L, dev = _call()
+    if stream is not None:
+        with ty.torch.cuda.stream(stream):
+            return op_tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale, v_scale,
+                                     scale, out)
+    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev)
+    D = kv.head_dim
+    n, H, _ = q.shape if q.dim() == 3 else (0, 0, 0)
+    stride = _rows("q", q, H, D, ty, dev)
+    B = slot.shape[0] if slot.dim() == 1 else -1
+    _whole("slot", slot, ty.i32, (B,), dev)
+    _whole("cached", cached, ty.i32, (B,), dev)
+    _whole("first", first, ty.i32, (B + 1,), dev)
+    _whole("mask", mask, ty.i64, (n,), dev)
+    if out is None:
+        out = ty.torch.empty((n, H, D), dtype=q.dtype, device=q.device)
+        out_stride = H * D
+    else:
+        if out.dtype is not q.dtype or out.shape != q.shape:
             raise ValueError("out must have q's type and shape")
-        if n > 0 and B > 0:
-            check(lib().gpt2_op_tree_attention(
-                kv, q.data_ptr(), _row_types[q.dtype], stride, H, slot.data_ptr(), cached.data_ptr(),
-                first.data_ptr(), mask.data_ptr(), B, n, int(max_nodes),
-                1.0 / D ** 0.5 if scale is None else float(scale), out.data_ptr(), _rows("out", out, H, D), s),
-                "gpt2_op_tree_attention")
+        out_stride = _rows("out", out, H, D, ty, dev)
+    if n > 0 and B > 0:
+        check(L.gpt2_op_tree_attention(kv, q.data_ptr(), ty.rows[q.dtype], stride, H, slot.data_ptr(),
+                                       cached.data_ptr(), first.data_ptr(), mask.data_ptr(), B, n, max_nodes,
+                                       D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride,
+                                       ty.raw_stream(dev)), "gpt2_op_tree_attention")
     return out
 
 
@@ -694,48 +694,51 @@ def op_verify_tree(logits, tokens, parents, first, max_nodes, temperature=0.0, d
                    u_draw=None, path=None, n_path=None, next_token=None, workspace=None, stream=None):
     """Which drafted nodes the target accepts, and the token after them:
     (path [sequences][max_nodes], n_path, next_token), int32."""
-    import torch
-    _on_device(logits=logits, tokens=tokens, parents=parents, first=first, draft_probs=draft_probs,
-               u_accept=u_accept, u_draw=u_draw, path=path, n_path=n_path, next_token=next_token,
-               workspace=workspace)
-    if logits.dim() != 2:
-        raise ValueError("logits must be [rows][vocab]")
-    n, V = logits.shape
-    B, T = first.numel() - 1, int(max_nodes)
-    _whole("logits", logits, torch.float32, (n, V))
-    _whole("tokens", tokens, torch.int32, (n,))
-    _whole("parents", parents, torch.int32, (n,))
-    _whole("first", first, torch.int32, (B + 1,))
+    ty, L, dev = _call()
+    if stream is not None:
+        with ty.torch.cuda.stream(stream):
+            return op_verify_tree(logits, tokens, parents, first, max_nodes, temperature, draft_probs, u_accept,
+                                  u_draw, path, n_path, next_token, workspace)
+    n, V = logits.shape if logits.dim() == 2 else (-1, -1)
+    B, T = first.shape[0] - 1 if first.dim() == 1 else -1, int(max_nodes)
+    if not 1 <= T <= MAX_NODES:
+        raise ValueError(f"max_nodes must be 1 to {MAX_NODES}, not {max_nodes}")
+    _whole("logits", logits, ty.f32, (n, V), dev)
+    _whole("tokens", tokens, ty.i32, (n,), dev)
+    _whole("parents", parents, ty.i32, (n,), dev)
+    _whole("first", first, ty.i32, (B + 1,), dev)
+    pd = pa = pu = None
     if draft_probs is not None:
-        _whole("draft_probs", draft_probs, torch.float32, (n, V))
+        _whole("draft_probs", draft_probs, ty.f32, (n, V), dev)
+        pd = draft_probs.data_ptr()
     if temperature != 0:
         if u_accept is None or u_draw is None:
             raise ValueError("temperature > 0 needs u_accept and u_draw")
-        _whole("u_accept", u_accept, torch.float32, (n,))
-        _whole("u_draw", u_draw, torch.float32, (B, V))
-    with _OnStream(stream) as s:
-        dev = logits.device
-        if path is None:
-            path = torch.empty((B, T), dtype=torch.int32, device=dev)
-        if n_path is None:
-            n_path = torch.empty(B, dtype=torch.int32, device=dev)
-        if next_token is None:
-            next_token = torch.empty(B, dtype=torch.int32, device=dev)
-        _whole("path", path, torch.int32, (B, T))
-        _whole("n_path", n_path, torch.int32, (B,))
-        _whole("next_token", next_token, torch.int32, (B,))
-        L = lib()
-        if workspace is None:
-            workspace = torch.empty(L.gpt2_op_verify_tree_workspace(n, V), dtype=torch.uint8, device=dev)
-        p = lambda t: t.data_ptr() if t is not None else None
-        if B > 0 and n > 0:
-            check(L.gpt2_op_verify_tree(
-                logits.data_ptr(), V, tokens.data_ptr(), parents.data_ptr(), first.data_ptr(), B, n, T,
-                float(temperature), p(draft_probs), p(u_accept), p(u_draw), path.data_ptr(), n_path.data_ptr(),
-                next_token.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s),
-                "gpt2_op_verify_tree")
-        elif B > 0:
-            path.fill_(-1)
-            n_path.zero_()
-            next_token.fill_(-1)
+        _whole("u_accept", u_accept, ty.f32, (n,), dev)
+        _whole("u_draw", u_draw, ty.f32, (B, V), dev)
+        pa, pu = u_accept.data_ptr(), u_draw.data_ptr()
+    empty, where = ty.torch.empty, logits.device
+    if path is None:
+        path = empty((B, T), dtype=ty.i32, device=where)
+    if n_path is None:
+        n_path = empty(B, dtype=ty.i32, device=where)
+    if next_token is None:
+        next_token = empty(B, dtype=ty.i32, device=where)
+    _whole("path", path, ty.i32, (B, T), dev)
+    _whole("n_path", n_path, ty.i32, (B,), dev)
+    _whole("next_token", next_token, ty.i32, (B,), dev)
+    size = L.gpt2_op_verify_tree_workspace(n, V)
+    if workspace is None:
+        workspace = empty((size + 3) // 4, dtype=ty.i32, device=where)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be contiguous and on the current device cuda:{dev}")
+    if B > 0 and V > 0:
+        if n == 0:
+            path.fill_(-1), n_path.zero_(), next_token.fill_(-1)
+        else:
+            check(L.gpt2_op_verify_tree(logits.data_ptr(), V, tokens.data_ptr(), parents.data_ptr(), first.data_ptr(),
+                                        B, n, T, temperature, pd, pa, pu, path.data_ptr(), n_path.data_ptr(),
+                                        next_token.data_ptr(), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), ty.raw_stream(dev)),
+                  "gpt2_op_verify_tree")
     return path, n_path, next_token

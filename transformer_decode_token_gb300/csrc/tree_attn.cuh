@@ -26,7 +26,7 @@
 // and the next tile's keys are loaded while this one's weights are formed.
 //
 // Types (struct Tr): the fp32 cache uses tf32 products with q, k, p and v as
-// two parts each (three products, 22 bits); 16-bit caches the products of
+// two parts each (three products, all but the two second parts'); 16-bit caches the products of
 // their own type; 8-bit codes are exact in fp16.  q and the weights p are split
 // into kNQ and kNP parts, so that results keep about 22 bits for fp32 rows,
 // and for 16-bit rows at least 16 bits of every weight: only the final
@@ -94,22 +94,30 @@ struct Tile {
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool bf)
 {
     if (bf)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x as a tf32 number (rounded to nearest) and what that leaves, which tf32
+// holds exactly.
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo)
+{
+    hi = (x + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
 }
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -353,8 +361,7 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
                     for (int e = 0; e < 2; ++e) {
                         const float v = x[half][2 * s + e];
                         uint32_t hi, lo;
-                        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
-                        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(v - __uint_as_float(hi)));
+                        split_tf32(__float_as_uint(v), hi, lo);
                         w[0][e * 2 + half] = hi;
                         w[1][e * 2 + half] = lo;
                     }
@@ -438,13 +445,16 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
                 }
         }
         // scores
-        float sc[MT][T::kT8][4];
+        float sc[MT][T::kT8][4], lo[kQP > 1 ? MT : 1][T::kT8][4];   // the first parts' products, the others'
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int u = 0; u < T::kT8; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[mt][u][i] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    sc[mt][u][i] = 0.f;
+                    if (kQP > 1) lo[mt][u][i] = 0.f;
+                }
 #pragma unroll
         for (int s = 0; s < T::kSteps; ++s) {
             uint32_t qa[MT][kQP][4];
@@ -459,13 +469,13 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
             for (int u = 0; u < T::kT8; ++u) {
                 const uint32_t *r = kr + u * T::kNK * (T::kKLd / 4);
                 if constexpr (Tr::kMma == kTf32) {
-                    const uint32_t h0 = r[2 * s] & 0xffffe000u, h1 = r[2 * s + 1] & 0xffffe000u;
-                    const uint32_t l0 = __float_as_uint(__uint_as_float(r[2 * s]) - __uint_as_float(h0));
-                    const uint32_t l1 = __float_as_uint(__uint_as_float(r[2 * s + 1]) - __uint_as_float(h1));
+                    uint32_t h0, h1, l0, l1;
+                    split_tf32(r[2 * s], h0, l0);
+                    split_tf32(r[2 * s + 1], h1, l1);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        mma1688(sc[mt][u], qa[mt][0], l0, l1);
-                        mma1688(sc[mt][u], qa[mt][1], h0, h1);
+                        mma1688(lo[mt][u], qa[mt][0], l0, l1);
+                        mma1688(lo[mt][u], qa[mt][1], h0, h1);
                         mma1688(sc[mt][u], qa[mt][0], h0, h1);
                     }
                 } else {
@@ -474,7 +484,8 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int i = kQP - 1; i >= 0; --i) mma16816(sc[mt][u], qa[mt][i], b0, b1, Tr::kMma == kBf16);
+                        for (int i = kQP - 1; i >= 0; --i)
+                            mma16816(i ? lo[mt][u] : sc[mt][u], qa[mt][i], b0, b1, Tr::kMma == kBf16);
                 }
             }
         }
@@ -486,6 +497,7 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
             for (int u = 0; u < T::kT8; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    if (kQP > 1) sc[mt][u][i] += lo[mt][u][i];
                     sc[mt][u][i] *= rs[mt][i >> 1];
                     if constexpr (Tr::kScaled) sc[mt][u][i] *= ks[u][i & 1];
                 }
@@ -545,6 +557,7 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
 #pragma unroll
             for (int u = 0; u < T::kT8; ++u) vs[u][0] *= inv_gv, vs[u][1] *= inv_gv;
         }
+        float keep[MT][2];           // what a new maximum leaves of the sums so far
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -570,69 +583,80 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
                         if constexpr (Tr::kScaled) x *= vs[u][e];
                     }
                 l[mt][half] = l[mt][half] * old + sum;
-#pragma unroll
-                for (int j = 0; j < T::kNT; ++j) {
-                    o[mt][j][half * 2] *= old;
-                    o[mt][j][half * 2 + 1] *= old;
-                }
+                keep[mt][half] = old;
             }
 
-        // weighted sum
-        auto value = [&](int row, int j) {   // registers of a row's access (row: 0 .. 2 kT8 - 1) that holds element j
-            return vr + (row * T::kNV + j / T::kEV) * (T::kVLd / 4);
-        };
-        if constexpr (Tr::kMma == kTf32) {
+        // weighted sum: the tile's own in fresh accumulators (the matrix units
+        // cut each sum off, so the running sums are kept by fp32 additions),
+        // the small parts first
+        uint32_t pw[MT][Tr::kMma == kTf32 ? T::kT8 : T::kT8 / 2][Tr::kNP][4];
 #pragma unroll
-            for (int u = 0; u < T::kT8; ++u) {
-                uint32_t ph[MT][4], pl[MT][4];
+        for (int mt = 0; mt < MT; ++mt)
+            if constexpr (Tr::kMma == kTf32) {
+                // a0 (g, row 2c), a1 (g + 8, 2c), a2 (g, 2c + 1), a3 (g + 8, 2c + 1)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int u = 0; u < T::kT8; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // a0 (g, row 2c), a1 (g + 8, 2c), a2 (g, 2c + 1), a3 (g + 8, 2c + 1)
-                        const float p = sc[mt][u][(i & 1) * 2 + (i >> 1)];
-                        ph[mt][i] = __float_as_uint(p) & 0xffffe000u;
-                        pl[mt][i] = __float_as_uint(p - __uint_as_float(ph[mt][i]));
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        split_tf32(__float_as_uint(sc[mt][u][(i & 1) * 2 + (i >> 1)]), pw[mt][u][0][i], pw[mt][u][1][i]);
+            } else {
+                // a0 (g, rows 2c, 2c + 1), a1 (g + 8), a2 (g, the next eight's), a3 (g + 8)
 #pragma unroll
-                for (int j = 0; j < T::kNT; ++j) {
-                    const uint32_t x0 = value(2 * u, j)[j % T::kEV], x1 = value(2 * u + 1, j)[j % T::kEV];
-                    const uint32_t h0 = x0 & 0xffffe000u, h1 = x1 & 0xffffe000u;
-                    const uint32_t l0 = __float_as_uint(__uint_as_float(x0) - __uint_as_float(h0));
-                    const uint32_t l1 = __float_as_uint(__uint_as_float(x1) - __uint_as_float(h1));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma1688(o[mt][j], ph[mt], l0, l1);
-                        mma1688(o[mt][j], pl[mt], h0, h1);
-                        mma1688(o[mt][j], ph[mt], h0, h1);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < T::kT8; u += 2) {
-                uint32_t pw[MT][Tr::kNP][4];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int u = 0; u < T::kT8; u += 2)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        // a0 (g, rows 2c, 2c + 1), a1 (g + 8), a2 (g, the next eight's), a3 (g + 8)
                         const int uu = u + (k >> 1), half = k & 1;
                         uint32_t part[Tr::kNP];
                         split16<Tr::kMma, Tr::kNP>(sc[mt][uu][half * 2], sc[mt][uu][half * 2 + 1], part);
 #pragma unroll
-                        for (int i = 0; i < Tr::kNP; ++i) pw[mt][i][k] = part[i];
+                        for (int i = 0; i < Tr::kNP; ++i) pw[mt][u / 2][i][k] = part[i];
+                    }
+            }
+        auto value = [&](int row, int j) {   // registers of a row's access (row: 0 .. 2 kT8 - 1) that holds element j
+            return vr + (row * T::kNV + j / T::kEV) * (T::kVLd / 4);
+        };
+#pragma unroll
+        for (int j = 0; j < T::kNT; ++j) {
+            float sum[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[mt][i] = 0.f;
+            if constexpr (Tr::kMma == kTf32) {
+                uint32_t h[T::kT8][2], l_[T::kT8][2];
+#pragma unroll
+                for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) split_tf32(value(2 * u + e, j)[j % T::kEV], h[u][e], l_[u][e]);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                    for (int u = 0; u < T::kT8; ++u) {
+                        mma1688(sum[mt], pw[mt][u][0], l_[u][0], l_[u][1]);
+                        mma1688(sum[mt], pw[mt][u][1], h[u][0], h[u][1]);
                     }
 #pragma unroll
-                for (int j = 0; j < T::kNT; ++j) {
-                    const uint32_t b0 = value_pair<Tr>(value(2 * u, j), value(2 * u + 1, j), j % T::kEV);
-                    const uint32_t b1 = value_pair<Tr>(value(2 * u + 2, j), value(2 * u + 3, j), j % T::kEV);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int i = Tr::kNP - 1; i >= 0; --i) mma16816(o[mt][j], pw[mt][i], b0, b1, Tr::kMma == kBf16);
+                    for (int u = 0; u < T::kT8; ++u) mma1688(sum[mt], pw[mt][u][0], h[u][0], h[u][1]);
                 }
+            } else {
+                uint32_t b[T::kT8 / 2][2];
+#pragma unroll
+                for (int u = 0; u < T::kT8 / 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        b[u][e] = value_pair<Tr>(value(4 * u + 2 * e, j), value(4 * u + 2 * e + 1, j), j % T::kEV);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = Tr::kNP - 1; i >= 0; --i)
+#pragma unroll
+                        for (int u = 0; u < T::kT8 / 2; ++u)
+                            mma16816(sum[mt], pw[mt][u][i], b[u][0], b[u][1], Tr::kMma == kBf16);
             }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[mt][j][i] = fmaf(o[mt][j][i], keep[mt][i >> 1], sum[mt][i]);
         }
     }
 
