@@ -10,10 +10,10 @@
 // random numbers once).  A rejected child that has a sibling behind it costs
 // one more pass over the row, for the sum that makes the rest a distribution.
 //
-// Rounding: probabilities of single tokens, the residual's scale and every
-// comparison are in 64 bits; the sums over the vocabulary are fp32 per thread
-// (at most a few dozen terms) and 64 bits across threads; the race over the
-// vocabulary compares fp32 values.
+// Rounding: everything is fp32 (a few units in the last place; the sums over
+// the vocabulary are of a few dozen terms per thread, then pairwise or in 64
+// bits), so a decision can differ from the exact one where a random number
+// falls within about 1e-6 of its border.
 #include <cooperative_groups.h>
 
 #include <cfloat>
@@ -30,6 +30,7 @@ constexpr int kStatThreads = 256;
 constexpr int kVec = kChunk / 4 / kStatThreads;   // 16-byte loads in flight per thread
 constexpr int kVThreads = 512;
 constexpr int kMaxCluster = 8;
+constexpr int kBatch = 8;          // ids whose loads a thread has in flight together
 
 struct Stat {
     float m, z;                    // maximum, sum of exp((l - m) / T)
@@ -43,14 +44,22 @@ struct VerifyArgs {
     Stat *stats;                   // [n_rows][chunks]
     int32_t V, n_seqs, n_rows, max_nodes, chunks, cluster;
     float c_hi, c_lo;              // log2(e) / temperature as two fp32 parts; 0: greedy
-    double inv_t;
 };
 
-// exp(d / temperature) for d <= 0, 0 for -infinity (the two parts keep the
-// exponent's scale to 48 bits; the exponent itself is rounded once).
+// exp(d / temperature) for d <= 0, 0 for -infinity (the two parts, both
+// positive, keep the exponent's scale to 47 bits; the exponent itself is
+// rounded once).
 __device__ __forceinline__ float weight(const VerifyArgs &a, float d)
 {
-    return d == -INFINITY ? 0.f : exp2f(fmaf(d, a.c_hi, d * a.c_lo));
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(d, a.c_hi, d * a.c_lo)));
+    return y;
+}
+__device__ __forceinline__ float weight(const VerifyArgs &a, float d, float rest)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(d, a.c_hi, fmaf(rest, a.c_hi, d * a.c_lo))));
+    return y;
 }
 
 __global__ void __launch_bounds__(kStatThreads) k_row_stats(const VerifyArgs a)
@@ -134,26 +143,24 @@ __global__ void __launch_bounds__(kStatThreads) k_row_stats(const VerifyArgs a)
 // cluster computes the same.
 struct Walk {
     unsigned long long children[GPT2_MAX_NODES];
-    double prob[GPT2_MAX_NODES];       // p(token) at the parent
+    float prob[GPT2_MAX_NODES];        // p(token) at the parent
     float q[GPT2_MAX_NODES], u[GPT2_MAX_NODES];
     float m[GPT2_MAX_NODES], inv_z[GPT2_MAX_NODES];
-    double z[GPT2_MAX_NODES];
     int choice[GPT2_MAX_NODES];        // temperature 0
     int token[GPT2_MAX_NODES];
     bool valid[GPT2_MAX_NODES];
     // children of `cur` rejected so far: their tokens (draft on one token), or
-    // the sums that bring what is left back to a distribution
+    // 1 / the sums that bring what is left back to a distribution
     int rejected[GPT2_MAX_NODES];
-    double mass[GPT2_MAX_NODES];
     float inv_mass[GPT2_MAX_NODES];    // (0 where nothing is left)
     int n_rejected, cur, length, path[GPT2_MAX_NODES];
-    double scale;                      // draft on one token: 1 / what is left
+    float scale;                       // draft on one token: 1 / what is left
     unsigned long long left;           // children of cur not tried yet
     bool need_mass, dead;
 };
 
 // Goes on until the walk ends (need_mass false) or a sum over the vocabulary
-// is needed (need_mass true; mass[n_rejected - 1] is then to be set).
+// is needed (need_mass true; inv_mass[n_rejected - 1] is then to be set).
 __device__ void walk_on(const VerifyArgs &a, Walk &w)
 {
     w.need_mass = false;
@@ -163,37 +170,35 @@ __device__ void walk_on(const VerifyArgs &a, Walk &w)
         const int x = w.token[i];
         if (x < 0 || x >= a.V || !w.valid[w.cur]) continue;
         bool yes;
-        double r = 0.0;
+        float r = 0.f;
         if (a.c_hi == 0.f) {
             yes = w.choice[w.cur] == x;
         } else {
             r = w.prob[i];
             if (a.draft) {
                 for (int k = 0; k < w.n_rejected; ++k) {
-                    r -= double(w.q[i]);
-                    r = r > 0.0 && w.mass[k] > 0.0 ? r / w.mass[k] : 0.0;
+                    r = fmaxf(r - w.q[i], 0.f) * w.inv_mass[k];
                 }
             } else {
-                r = w.dead ? 0.0 : r * w.scale;
+                r = w.dead ? 0.f : r * w.scale;
                 for (int k = 0; k < w.n_rejected; ++k)
-                    if (w.rejected[k] == x) r = 0.0;
+                    if (w.rejected[k] == x) r = 0.f;
             }
-            yes = double(w.u[i]) * double(w.q[i]) < r;
+            yes = w.u[i] * w.q[i] < r;
         }
         if (yes) {
             w.path[w.length++] = i;
             w.cur = i;
             w.left = w.children[i];
             w.n_rejected = 0;
-            w.scale = 1.0;
+            w.scale = 1.f;
             w.dead = false;
         } else if (a.c_hi != 0.f) {
             w.rejected[w.n_rejected] = x;
-            w.inv_mass[w.n_rejected] = 1.f;
-            w.mass[w.n_rejected++] = 1.0;
+            w.inv_mass[w.n_rejected++] = 1.f;
             if (!a.draft) {
-                const double rest = 1.0 - r;
-                if (rest > 0.0) w.scale /= rest;
+                const float rest = 1.f - r;
+                if (rest > 0.f) w.scale *= __frcp_rn(rest);
                 else w.dead = true;
             } else if (w.left) {
                 w.need_mass = true;
@@ -222,40 +227,61 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
         if (tid < nodes) w.token[tid] = a.tokens[f0 + tid];
     }
     __syncthreads();
-    if (parent >= 0 && parent < tid) atomicOr(&w.children[parent], 1ull << tid);
+    // (k_row_stats writes none of what is read before the wait)
+    float lx = 0.f, qx = 1.f, ux = 0.f;            // of this thread's node: target's logit at its parent, draft's, random number
+    if (parent >= 0 && parent < tid) {
+        atomicOr(&w.children[parent], 1ull << tid);
+        const int x = w.token[tid];
+        if (a.c_hi != 0.f && x >= 0 && x < a.V) {
+            const size_t at = size_t(f0 + parent) * a.V + x;
+            lx = a.logits[at];
+            ux = a.u_accept[f0 + tid];
+            if (a.draft) qx = a.draft[at];
+        }
+    }
     pdl_wait();                                    // k_row_stats' sums
-    if (tid < nodes) {
-        const Stat *st = a.stats + size_t(f0 + tid) * a.chunks;
+    // eight threads per node join its chunks
+    for (int i0 = 0; i0 < nodes; i0 += kVThreads / 8) {
+        const int i = i0 + tid / 8, l = tid % 8;
+        const Stat *st = a.stats + size_t(f0 + min(i, nodes - 1)) * a.chunks;
         float m = -INFINITY;
         unsigned long long key = 0;
-        for (int k = 0; k < a.chunks; ++k) {
-            m = fmaxf(m, st[k].m);
-            key = st[k].key > key ? st[k].key : key;
+        float z = 0.f;
+        for (int k0 = 0; k0 < a.chunks; k0 += 8) {
+            const Stat v = k0 + l < a.chunks ? st[k0 + l] : Stat{-INFINITY, 0.f, 0};
+            float mk = v.m;
+            key = v.key > key ? v.key : key;
+            for (int o = 4; o > 0; o >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            const float mn = fmaxf(m, mk);         // the same in all eight threads
+            if (mn > -INFINITY) {
+                if (m > -INFINITY) z *= weight(a, m - mn);
+                if (v.z != 0.f) z += v.z * weight(a, v.m - mn);
+            }
+            m = mn;
         }
-        if (a.c_hi == 0.f) {
-            w.valid[tid] = key != 0;
-            w.choice[tid] = key != 0 ? argmax_key_index(key) : -1;
-        } else {
-            double z = 0.0;
-            for (int k = 0; k < a.chunks; ++k)
-                if (st[k].z != 0.f) z += double(st[k].z) * double(weight(a, st[k].m - m));
-            w.m[tid] = m;
-            w.z[tid] = z;
-            w.inv_z[tid] = float(1.0 / z);
-            w.valid[tid] = z > 0.0 && fabsf(m) <= FLT_MAX;   // (false for NaN sums)
+        for (int o = 4; o > 0; o >>= 1) {
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+            const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
+            key = other > key ? other : key;
+        }
+        if (l == 0 && i < nodes) {
+            if (a.c_hi == 0.f) {
+                w.valid[i] = key != 0;
+                w.choice[i] = key != 0 ? argmax_key_index(key) : -1;
+            } else {
+                w.m[i] = m;
+                w.inv_z[i] = __frcp_rn(z);
+                w.valid[i] = z > 0.f && fabsf(m) <= FLT_MAX;   // (false for NaN sums)
+            }
         }
     }
     __syncthreads();
-    if (a.c_hi != 0.f && parent >= 0 && parent < tid) {
-        const int x = w.token[tid];
-        w.u[tid] = a.u_accept[f0 + tid];
-        w.q[tid] = 1.f;
-        w.prob[tid] = 0.0;
-        if (x >= 0 && x < a.V) {
-            const size_t at = size_t(f0 + parent) * a.V + x;
-            w.prob[tid] = exp((double(a.logits[at]) - double(w.m[parent])) * a.inv_t) / w.z[parent];
-            if (a.draft) w.q[tid] = a.draft[at];
-        }
+    if (parent >= 0 && parent < tid) {
+        w.u[tid] = ux;
+        w.q[tid] = qx;
+        // lx - m in two parts, so that its rounding does not show
+        const float m = w.m[parent], d = lx - m, t = d + m, rest = (lx - t) + (m - (t - d));
+        w.prob[tid] = weight(a, d, rest) * w.inv_z[parent];
     }
     if (tid == 0) {
         w.cur = 0;
@@ -263,7 +289,7 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
         w.path[0] = 0;
         w.left = nodes > 0 ? w.children[0] : 0;
         w.n_rejected = 0;
-        w.scale = 1.0;
+        w.scale = 1.f;
         w.dead = false;
     }
     __syncthreads();
@@ -290,8 +316,17 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
         const float m = w.m[w.cur], iz = w.inv_z[w.cur];
         const int n = w.n_rejected;
         float s = 0.f;
-        for (int v = v0 + tid; v < v1; v += kVThreads)
-            s += residual(weight(a, a.logits[row + v] - m) * iz, a.draft[row + v], v, n);
+        for (int b0 = v0 + tid; b0 < v1; b0 += kBatch * kVThreads) {
+            float x[kBatch], q[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int v = b0 + i * kVThreads;
+                x[i] = v < v1 ? a.logits[row + v] : -INFINITY;
+                q[i] = v < v1 ? a.draft[row + v] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) s += residual(weight(a, x[i] - m) * iz, q[i], 0, n);
+        }
         s = warp_sum(s);
         if ((tid & 31) == 0) red[tid >> 5] = double(s);
         __syncthreads();
@@ -304,8 +339,7 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
         if (tid == 0) {
             double t = 0.0;
             for (int k = 0; k < a.cluster; ++k) t += *cl.map_shared_rank(&part_sum[round & 1], k);
-            w.mass[n - 1] = t;
-            w.inv_mass[n - 1] = t > 0.0 ? float(1.0 / t) : 0.f;
+            w.inv_mass[n - 1] = t > 0.0 ? __frcp_rn(float(t)) : 0.f;
         }
         ++round;
         __syncthreads();
@@ -324,12 +358,24 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
                 const int n = pass == 0 ? w.n_rejected : 0;
                 const bool dense = a.draft && n > 0;
                 unsigned long long best = 0;
-                for (int v = v0 + tid; v < v1; v += kVThreads) {
-                    const float p = weight(a, a.logits[row + v] - m) * iz;
-                    const float r = n > 0 ? residual(p, dense ? a.draft[row + v] : 0.f, v, n) : p;
-                    if (r > 0.f) {
-                        const unsigned long long k = argmax_key(r / -logf(u[v]), uint32_t(v));
-                        best = k > best ? k : best;
+                for (int b0 = v0 + tid; b0 < v1; b0 += kBatch * kVThreads) {
+                    float x[kBatch], q[kBatch], e[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int v = b0 + i * kVThreads;
+                        x[i] = v < v1 ? a.logits[row + v] : -INFINITY;
+                        e[i] = v < v1 ? u[v] : 0.5f;
+                        q[i] = dense && v < v1 ? a.draft[row + v] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int v = b0 + i * kVThreads;
+                        const float p = weight(a, x[i] - m) * iz;
+                        const float r = n > 0 ? residual(p, q[i], v, n) : p;
+                        if (r > 0.f) {
+                            const unsigned long long k = argmax_key(__fdividef(r, -logf(e[i])), uint32_t(v));
+                            best = k > best ? k : best;
+                        }
                     }
                 }
                 best = warp_max_u64(best);
@@ -418,12 +464,11 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
         a.draft = draft_probs;
         a.u_accept = u_accept;
         a.u_draw = u_draw;
-        a.c_hi = float(c);
+        a.c_hi = std::nextafterf(float(c), 0.f);    // below c, so that the rest is positive
         a.c_lo = float(c - double(a.c_hi));
-        a.inv_t = 1.0 / double(temperature);
         // the final draw reads a row with the CTAs of a cluster: as many as
-        // keep 2048 ids or more each, while all sequences' fit the GPU together
-        while (a.cluster < kMaxCluster && vocab >= 4096 * a.cluster && n_seqs * a.cluster * 2ll <= 4ll * sms)
+        // keep 2048 ids or more each, while all sequences' fit the GPU together (two per SM)
+        while (a.cluster < kMaxCluster && vocab >= 4096 * a.cluster && n_seqs * a.cluster * 2ll <= 2ll * sms)
             a.cluster *= 2;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
