@@ -488,153 +488,61 @@ def op_linear_bf16(W_bf16, X, stream=None):
 # `stream` runs, and makes the tensors that it makes, on that stream.  See the
 # gpt2_op_* calls of include/gpt2.h.
 
-_types = None
+_torch_ops = None
 
 
-class _Types:
-    """torch's types (torch is not imported with this module)."""
+def _native():
+    """The compiled marshalling of torch tensors (csrc/torch_ops.cpp), built if
+    it is missing or older than its source, bound to the loaded library."""
+    global _torch_ops
+    if _torch_ops is None:
+        import importlib.machinery
+        import importlib.util
 
-    def __init__(self):
-        import torch
-        self.torch = torch
-        self.rows = {torch.float32: GPT2_F32, torch.float16: GPT2_F16, torch.bfloat16: GPT2_BF16}
-        self.caches = {**self.rows, torch.int8: GPT2_INT8, torch.float8_e4m3fn: GPT2_E4M3}
-        self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
-        self.device = torch.cuda.current_device
-
-
-def _call():
-    """(types, library, current device)."""
-    global _types
-    if _types is None:
-        lib()
-        _types = _Types()
-    return _types, _lib, _types.device()
+        import torch  # noqa: F401  (its libraries come first)
+        L = lib()
+        loader = importlib.machinery.ExtensionFileLoader("_torch_ops", _build.build_torch_ops())
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_torch_ops", loader))
+        loader.exec_module(m)
+        m.bind(GPT2Error, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
+                            ("gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit", "gpt2_op_tree_attention",
+                             "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree")))
+        _torch_ops = m
+    return _torch_ops
 
 
-def _whole(name, t, dtype, shape, dev):
-    """Raises unless t is a contiguous tensor of this type and shape on the
-    current device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current device "
-                         f"cuda:{dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _kv(k_cache, v_cache, k_scale, v_scale, ty, dev, layers=False):
-    """(gpt2_kv, layers) of a layer's cache, or of [layers][slots]... caches."""
-    shape, dtype = k_cache.shape, k_cache.dtype
-    nd = len(shape)
-    if nd != 4 and not (layers and nd == 5):
-        raise ValueError(f"a cache is [slots][heads][positions][head_dim], not {tuple(shape)}")
-    t = ty.caches.get(dtype)
-    if t is None:
-        raise ValueError(f"unsupported cache type {dtype}")
-    _whole("k_cache", k_cache, dtype, shape, dev)
-    _whole("v_cache", v_cache, dtype, shape, dev)
-    ks = vs = None
-    if t >= GPT2_INT8:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an 8-bit cache needs k_scale and v_scale")
-        _whole("k_scale", k_scale, ty.f32, shape[:-1], dev)
-        _whole("v_scale", v_scale, ty.f32, shape[:-1], dev)
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError(f"a {dtype} cache has no scales")
-    L = 1
-    if nd == 5:
-        L, S, H, P, D = shape
-    else:
-        S, H, P, D = shape
-    return KV(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, t, S, H, P, D), L
-
-
-def _rows(name, t, H, D, ty, dev):
-    """The row stride of a [rows][H][D] tensor whose rows are contiguous."""
-    n, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
-    if h != H or d != D:
-        raise ValueError(f"{name} must be [rows][{H}][{D}], not {tuple(t.shape)}")
-    if t.dtype not in ty.rows or t.get_device() != dev:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16 on the current device cuda:{dev}, "
-                         f"not {t.dtype} on {t.device}")
-    r, sh, sd = t.stride()
-    if sd != 1 or (H > 1 and sh != D):
-        raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return r if n > 1 else H * D
+def _on(stream):
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def op_kv_store(k, v, k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, stream=None):
     """Writes rows of k and v ([rows][heads][head_dim], possibly views into
     fused QKV rows) into the cache at (slot[i], pos[i]), quantised or rounded
     to its type; rows outside the cache are skipped."""
-    ty, L, dev = _call()
     if stream is not None:
-        with ty.torch.cuda.stream(stream):
+        with _on(stream):
             return op_kv_store(k, v, k_cache, v_cache, slot, pos, k_scale, v_scale)
-    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev)
-    stride = _rows("k", k, kv.n_head, kv.head_dim, ty, dev)
-    n = k.shape[0]
-    if v.dtype is not k.dtype or v.shape != k.shape or _rows("v", v, kv.n_head, kv.head_dim, ty, dev) != stride:
-        raise ValueError("k and v must have the same type, shape and row stride")
-    _whole("slot", slot, ty.i32, (n,), dev)
-    _whole("pos", pos, ty.i32, (n,), dev)
-    if n > 0:
-        check(L.gpt2_op_kv_store(kv, k.data_ptr(), v.data_ptr(), ty.rows[k.dtype], stride, slot.data_ptr(),
-                                 pos.data_ptr(), n, ty.raw_stream(dev)), "gpt2_op_kv_store")
+    return (_torch_ops or _native()).kv_store(k, v, k_cache, v_cache, slot, pos, k_scale, v_scale)
 
 
 def op_kv_load(k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, dtype=None, k=None, v=None, stream=None):
     """Reads cache rows (slot[i], pos[i]) back as (k, v), each [rows][heads]
     [head_dim] of `dtype` (float32 unless given, or the given k's); rows
     outside the cache are zeros."""
-    ty, L, dev = _call()
     if stream is not None:
-        with ty.torch.cuda.stream(stream):
+        with _on(stream):
             return op_kv_load(k_cache, v_cache, slot, pos, k_scale, v_scale, dtype, k, v)
-    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev)
-    H, D, n = kv.n_head, kv.head_dim, slot.shape[0] if slot.dim() == 1 else -1
-    _whole("slot", slot, ty.i32, (n,), dev)
-    _whole("pos", pos, ty.i32, (n,), dev)
-    if (k is None) != (v is None):
-        raise ValueError("give both k and v, or neither")
-    if k is None:
-        dtype = dtype or ty.f32
-        if dtype not in ty.rows:
-            raise ValueError(f"unsupported row type {dtype}")
-        k = ty.torch.empty((n, H, D), dtype=dtype, device=k_cache.device)
-        v = ty.torch.empty_like(k)
-        stride = H * D
-    else:
-        stride = _rows("k", k, H, D, ty, dev)
-        if dtype is not None and dtype is not k.dtype:
-            raise ValueError(f"k is {k.dtype}, not {dtype}")
-        if k.shape[0] != n or v.dtype is not k.dtype or v.shape != k.shape or \
-                _rows("v", v, H, D, ty, dev) != stride:
-            raise ValueError("k and v must be [rows][heads][head_dim] of the same type and row stride")
-    if n > 0:
-        check(L.gpt2_op_kv_load(kv, slot.data_ptr(), pos.data_ptr(), n, k.data_ptr(), v.data_ptr(),
-                                ty.rows[k.dtype], stride, ty.raw_stream(dev)), "gpt2_op_kv_load")
-    return k, v
+    return (_torch_ops or _native()).kv_load(k_cache, v_cache, slot, pos, k_scale, v_scale, dtype, k, v)
 
 
 def op_kv_commit(k_cache, v_cache, slot, cached, path, n_path, k_scale=None, v_scale=None, stream=None):
     """Moves the accepted nodes' cache rows into place, in every layer of a
     [layers][slots][heads][positions][head_dim] cache (or of one layer's)."""
-    ty, L, dev = _call()
     if stream is not None:
-        with ty.torch.cuda.stream(stream):
+        with _on(stream):
             return op_kv_commit(k_cache, v_cache, slot, cached, path, n_path, k_scale, v_scale)
-    kv, layers = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev, layers=True)
-    B, T = path.shape if path.dim() == 2 else (0, 0)
-    if not 1 <= T <= MAX_NODES:
-        raise ValueError(f"path must be [sequences][nodes], at most {MAX_NODES} nodes")
-    _whole("slot", slot, ty.i32, (B,), dev)
-    _whole("cached", cached, ty.i32, (B,), dev)
-    _whole("path", path, ty.i32, (B, T), dev)
-    _whole("n_path", n_path, ty.i32, (B,), dev)
-    if B > 0:
-        check(L.gpt2_op_kv_commit(kv, layers, slot.data_ptr(), cached.data_ptr(), path.data_ptr(), n_path.data_ptr(),
-                                  B, T, ty.raw_stream(dev)), "gpt2_op_kv_commit")
+    return (_torch_ops or _native()).kv_commit(k_cache, v_cache, slot, cached, path, n_path, k_scale, v_scale)
 
 
 def tree_masks(parents) -> np.ndarray:
@@ -657,33 +565,12 @@ def op_tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes,
     """Attention of packed drafted nodes q [rows][query heads][head_dim] over
     the cached prefix and the nodes of their masks; scale 1/sqrt(head_dim)
     unless given.  Returns out, like q."""
-    ty, L, dev = _call()
     if stream is not None:
-        with ty.torch.cuda.stream(stream):
+        with _on(stream):
             return op_tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale, v_scale,
                                      scale, out)
-    kv, _ = _kv(k_cache, v_cache, k_scale, v_scale, ty, dev)
-    D = kv.head_dim
-    n, H, _ = q.shape if q.dim() == 3 else (0, 0, 0)
-    stride = _rows("q", q, H, D, ty, dev)
-    B = slot.shape[0] if slot.dim() == 1 else -1
-    _whole("slot", slot, ty.i32, (B,), dev)
-    _whole("cached", cached, ty.i32, (B,), dev)
-    _whole("first", first, ty.i32, (B + 1,), dev)
-    _whole("mask", mask, ty.i64, (n,), dev)
-    if out is None:
-        out = ty.torch.empty((n, H, D), dtype=q.dtype, device=q.device)
-        out_stride = H * D
-    else:
-        if out.dtype is not q.dtype or out.shape != q.shape:
-            raise ValueError("out must have q's type and shape")
-        out_stride = _rows("out", out, H, D, ty, dev)
-    if n > 0 and B > 0:
-        check(L.gpt2_op_tree_attention(kv, q.data_ptr(), ty.rows[q.dtype], stride, H, slot.data_ptr(),
-                                       cached.data_ptr(), first.data_ptr(), mask.data_ptr(), B, n, max_nodes,
-                                       D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride,
-                                       ty.raw_stream(dev)), "gpt2_op_tree_attention")
-    return out
+    return (_torch_ops or _native()).tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale,
+                                                    v_scale, scale, out)
 
 
 def op_verify_tree_workspace(n_rows: int, vocab: int) -> int:
@@ -694,51 +581,9 @@ def op_verify_tree(logits, tokens, parents, first, max_nodes, temperature=0.0, d
                    u_draw=None, path=None, n_path=None, next_token=None, workspace=None, stream=None):
     """Which drafted nodes the target accepts, and the token after them:
     (path [sequences][max_nodes], n_path, next_token), int32."""
-    ty, L, dev = _call()
     if stream is not None:
-        with ty.torch.cuda.stream(stream):
+        with _on(stream):
             return op_verify_tree(logits, tokens, parents, first, max_nodes, temperature, draft_probs, u_accept,
                                   u_draw, path, n_path, next_token, workspace)
-    n, V = logits.shape if logits.dim() == 2 else (-1, -1)
-    B, T = first.shape[0] - 1 if first.dim() == 1 else -1, int(max_nodes)
-    if not 1 <= T <= MAX_NODES:
-        raise ValueError(f"max_nodes must be 1 to {MAX_NODES}, not {max_nodes}")
-    _whole("logits", logits, ty.f32, (n, V), dev)
-    _whole("tokens", tokens, ty.i32, (n,), dev)
-    _whole("parents", parents, ty.i32, (n,), dev)
-    _whole("first", first, ty.i32, (B + 1,), dev)
-    pd = pa = pu = None
-    if draft_probs is not None:
-        _whole("draft_probs", draft_probs, ty.f32, (n, V), dev)
-        pd = draft_probs.data_ptr()
-    if temperature != 0:
-        if u_accept is None or u_draw is None:
-            raise ValueError("temperature > 0 needs u_accept and u_draw")
-        _whole("u_accept", u_accept, ty.f32, (n,), dev)
-        _whole("u_draw", u_draw, ty.f32, (B, V), dev)
-        pa, pu = u_accept.data_ptr(), u_draw.data_ptr()
-    empty, where = ty.torch.empty, logits.device
-    if path is None:
-        path = empty((B, T), dtype=ty.i32, device=where)
-    if n_path is None:
-        n_path = empty(B, dtype=ty.i32, device=where)
-    if next_token is None:
-        next_token = empty(B, dtype=ty.i32, device=where)
-    _whole("path", path, ty.i32, (B, T), dev)
-    _whole("n_path", n_path, ty.i32, (B,), dev)
-    _whole("next_token", next_token, ty.i32, (B,), dev)
-    size = L.gpt2_op_verify_tree_workspace(n, V)
-    if workspace is None:
-        workspace = empty((size + 3) // 4, dtype=ty.i32, device=where)
-    elif not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError(f"workspace must be contiguous and on the current device cuda:{dev}")
-    if B > 0 and V > 0:
-        if n == 0:
-            path.fill_(-1), n_path.zero_(), next_token.fill_(-1)
-        else:
-            check(L.gpt2_op_verify_tree(logits.data_ptr(), V, tokens.data_ptr(), parents.data_ptr(), first.data_ptr(),
-                                        B, n, T, temperature, pd, pa, pu, path.data_ptr(), n_path.data_ptr(),
-                                        next_token.data_ptr(), workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), ty.raw_stream(dev)),
-                  "gpt2_op_verify_tree")
-    return path, n_path, next_token
+    return (_torch_ops or _native()).verify_tree(logits, tokens, parents, first, max_nodes, temperature, draft_probs,
+                                                 u_accept, u_draw, path, n_path, next_token, workspace)

@@ -16,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libgpt2.so")
+TORCH_OPS = os.path.join(HERE, "_torch_ops.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -76,6 +77,33 @@ def build(force: bool = False, verbose: bool = False, extra=(), lib: str = None,
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
     return lib
+
+
+def torch_ops_stale() -> bool:
+    deps = (os.path.join(CSRC, "torch_ops.cpp"), os.path.join(INCLUDE, "gpt2.h"), os.path.abspath(__file__))
+    return not os.path.exists(TORCH_OPS) or any(os.path.getmtime(p) > os.path.getmtime(TORCH_OPS) for p in deps)
+
+
+def build_torch_ops(force: bool = False) -> str:
+    """Compiles the marshalling of torch tensors (torch_ops.cpp) against the
+    installed torch; its calls into libgpt2.so are bound when it is loaded."""
+    if not force and not torch_ops_stale():
+        return TORCH_OPS
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = TORCH_OPS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
+           f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "torch_ops.cpp"), "-o", tmp, f"-L{root}/lib",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{root}/lib"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_ops.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_OPS)
+    return TORCH_OPS
 
 
 if __name__ == "__main__":
