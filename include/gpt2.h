@@ -528,11 +528,15 @@ int gpt2_op_kv_load(const gpt2_kv *kv, const int32_t *slot, const int32_t *pos, 
  *   of the same type, GPT2_INT8 or GPT2_E4M3.  Scores, softmax and sums are
  *   fp32.  q and out 16-byte aligned, strides multiples of 8 elements and >=
  *   n_head * head_dim; max_nodes in [1, GPT2_MAX_NODES] (of a sequence with
- *   more, the rows from max_nodes on are left as they were). */
+ *   more, the rows from max_nodes on are left as they were).  workspace: 16-byte
+ *   aligned DEVICE memory of gpt2_op_tree_attention_workspace bytes (which depends
+ *   on the current device; 0, and NULL then, for the shapes that need none:
+ *   max_nodes * n_head / kv->n_head <= 16, or a cache type other than q's). */
+size_t gpt2_op_tree_attention_workspace(const gpt2_kv *kv, int32_t q_dtype, int32_t n_head, int32_t max_nodes);
 int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, int64_t q_stride, int32_t n_head,
                            const int32_t *slot, const int32_t *cached, const int32_t *first, const uint64_t *mask,
                            int32_t n_seqs, int32_t n_rows, int32_t max_nodes, float scale, void *out,
-                           int64_t out_stride, void *stream);
+                           int64_t out_stride, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Which drafted nodes the target model accepts, and the token after them, from
  * given random numbers.  logits: DEVICE fp32 [n_rows][vocab], row i the target's

@@ -289,6 +289,21 @@ def test_tree_attention_many_rows(qt, ct, counts, G, D):
     run_attention(rng, qt, ct, D, 2, G, 500, [int(x) for x in rng.integers(0, 430, len(counts))], counts)
 
 
+@pytest.mark.parametrize("counts,G,D", [(17, 1, 64), (33, 1, 128), (5, 4, 128), (40, 2, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_tree_attention_many_units(dtype, counts, G, D):
+    """Many more (sequence, cache head, row tile) units than SMs, of ragged
+    lengths from no cached row to several tiles: a CTA works through several
+    units, and units are shared between CTAs."""
+    rng = np.random.default_rng(counts + D)
+    B, K = 30, 9
+    cached = [int(x) for x in rng.integers(0, 700, B)]
+    cached[3] = cached[17] = 0
+    n = [int(x) for x in rng.integers(1, counts + 1, B)]
+    n[0], n[5], n[20] = counts, 0, 0
+    run_attention(rng, dtype, dtype, D, K, G, 760, cached, n)
+
+
 @pytest.mark.parametrize("qt,ct", COMBOS)
 def test_single_tokens_long_and_short(qt, ct):
     """The decode form (one node per sequence), from no cached row to long

@@ -37,9 +37,10 @@ def commit(c, layers=1, slot=P, cached=P, path=P, n_path=P, seqs=1, nodes=4):
 
 
 def attend(c, q=P, dtype=0, q_stride=192, heads=3, slot=P, cached=P, first=P, mask=P, seqs=1, rows=1, nodes=1,
-           scale=0.125, out=P, out_stride=192):
+           scale=0.125, out=P, out_stride=192, ws=None, size=0):
     return binding.lib().gpt2_op_tree_attention(ctypes.byref(c) if c else None, q, dtype, q_stride, heads, slot,
-                                                cached, first, mask, seqs, rows, nodes, scale, out, out_stride, None)
+                                                cached, first, mask, seqs, rows, nodes, scale, out, out_stride, ws, size,
+                                                None)
 
 
 def verify(logits=P, vocab=100, tokens=P, parents=P, first=P, seqs=1, rows=4, nodes=4, temperature=1.0, draft=None,

@@ -33,7 +33,7 @@ EXPORTED = ("gpt2_create", "gpt2_create_ex", "gpt2_path", "gpt2_launch_count", "
             "gpt2_decode_batch_greedy", "gpt2_argmax_batch", "gpt2_batch_ids", "gpt2_copy_logits_batch",
             "gpt2_export_kv_batch", "gpt2_batch_info", "gpt2_sync_batch", "gpt2_op_linear_bf16_workspace",
             "gpt2_op_linear_bf16", "gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit",
-            "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree", "gpt2_strerror")
+            "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree", "gpt2_strerror")
 
 
 class GPT2Error(RuntimeError):
@@ -150,7 +150,10 @@ def lib(build_if_stale: bool = True, path: str = None):
             L.gpt2_op_kv_store.argtypes = [kv, vp, vp, i32, i64, vp, vp, i32, vp]
             L.gpt2_op_kv_load.argtypes = [kv, vp, vp, i32, vp, vp, i32, i64, vp]
             L.gpt2_op_kv_commit.argtypes = [kv, i32, vp, vp, vp, vp, i32, i32, vp]
-            L.gpt2_op_tree_attention.argtypes = [kv, vp, i32, i64, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, i64, vp]
+            L.gpt2_op_tree_attention_workspace.argtypes = [kv, i32, i32, i32]
+            L.gpt2_op_tree_attention_workspace.restype = sz
+            L.gpt2_op_tree_attention.argtypes = [kv, vp, i32, i64, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, i64, vp,
+                                                 sz, vp]
             L.gpt2_op_verify_tree_workspace.argtypes = [i32, i32]
             L.gpt2_op_verify_tree_workspace.restype = sz
             L.gpt2_op_verify_tree.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz,
@@ -159,7 +162,8 @@ def lib(build_if_stale: bool = True, path: str = None):
             L.gpt2_strerror.restype = ctypes.c_char_p
             for n in EXPORTED:
                 if n not in ("gpt2_destroy", "gpt2_destroy_batch", "gpt2_op_head_argmax_workspace",
-                             "gpt2_op_linear_bf16_workspace", "gpt2_op_verify_tree_workspace", "gpt2_strerror"):
+                             "gpt2_op_linear_bf16_workspace", "gpt2_op_tree_attention_workspace",
+                             "gpt2_op_verify_tree_workspace", "gpt2_strerror"):
                     getattr(L, n).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -505,8 +509,8 @@ def _native():
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_torch_ops", loader))
         loader.exec_module(m)
         m.bind(GPT2Error, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
-                            ("gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit", "gpt2_op_tree_attention",
-                             "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree")))
+                            ("gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit",
+                             "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree")))
         _torch_ops = m
     return _torch_ops
 
@@ -561,16 +565,16 @@ def tree_masks(parents) -> np.ndarray:
 
 
 def op_tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale=None, v_scale=None,
-                      scale=None, out=None, stream=None):
+                      scale=None, out=None, workspace=None, stream=None):
     """Attention of packed drafted nodes q [rows][query heads][head_dim] over
     the cached prefix and the nodes of their masks; scale 1/sqrt(head_dim)
     unless given.  Returns out, like q."""
     if stream is not None:
         with _on(stream):
             return op_tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale, v_scale,
-                                     scale, out)
+                                     scale, out, workspace)
     return (_torch_ops or _native()).tree_attention(q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale,
-                                                    v_scale, scale, out)
+                                                    v_scale, scale, out, workspace)
 
 
 def op_verify_tree_workspace(n_rows: int, vocab: int) -> int:

@@ -25,6 +25,7 @@ struct {
     decltype(&gpt2_op_kv_store) kv_store;
     decltype(&gpt2_op_kv_load) kv_load;
     decltype(&gpt2_op_kv_commit) kv_commit;
+    decltype(&gpt2_op_tree_attention_workspace) tree_attention_workspace;
     decltype(&gpt2_op_tree_attention) tree_attention;
     decltype(&gpt2_op_verify_tree_workspace) verify_tree_workspace;
     decltype(&gpt2_op_verify_tree) verify_tree;
@@ -278,10 +279,11 @@ PyObject *kv_commit(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale, v_scale, scale (or None), out (or None)
+// q, k_cache, v_cache, slot, cached, first, mask, max_nodes, k_scale, v_scale, scale, out, workspace (the
+// last three may be None)
 PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return guarded("tree_attention", 12, n, [&]() -> PyObject * {
+    return guarded("tree_attention", 13, n, [&]() -> PyObject * {
         const Call c;
         const Cache cache(a[1], a[2], a[8], a[9], c.dev);
         const at::Tensor &q = tensor(a[0], "q");
@@ -306,11 +308,23 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
                 throw Bad{"out must have q's type and shape"};
             out_stride = row_stride(out, "out", H, D, c.dev);
         }
-        if (rows > 0 && B > 0)
-            check(g_lib.tree_attention(&cache.kv, q.data_ptr(), row_type(q.scalar_type()), stride, int32_t(H), slot,
-                                         cached, first, mask, int32_t(B), int32_t(rows), nodes, scale, out.data_ptr(),
-                                         out_stride, c.stream),
+        if (rows > 0 && B > 0) {
+            const int type = row_type(q.scalar_type());
+            const size_t need = g_lib.tree_attention_workspace(&cache.kv, type, int32_t(H), nodes);
+            at::Tensor ws;
+            if (a[12] != Py_None) {
+                ws = tensor(a[12], "workspace");
+                if (!ws.is_contiguous() || !ws.is_cuda() || ws.get_device() != c.dev)
+                    throw Bad{"workspace must be contiguous and on the current device"};
+            } else if (need) {
+                ws = at::empty({int64_t(need)}, q.options().dtype(at::kByte));
+            }
+            check(g_lib.tree_attention(&cache.kv, q.data_ptr(), type, stride, int32_t(H), slot, cached, first, mask,
+                                       int32_t(B), int32_t(rows), nodes, scale, out.data_ptr(), out_stride,
+                                       ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? size_t(ws.nbytes()) : 0,
+                                       c.stream),
                   "gpt2_op_tree_attention");
+        }
         if (a[11] != Py_None) return Py_NewRef(a[11]);
         return THPVariable_Wrap(out);
     });
@@ -376,14 +390,15 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyObject *bind(PyObject *, PyObject *args)
 {
     PyObject *cls;
-    unsigned long long f[6];
-    if (!PyArg_ParseTuple(args, "OKKKKKK", &cls, f, f + 1, f + 2, f + 3, f + 4, f + 5)) return nullptr;
+    unsigned long long f[7];
+    if (!PyArg_ParseTuple(args, "OKKKKKKK", &cls, f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6)) return nullptr;
     g_lib.kv_store = reinterpret_cast<decltype(g_lib.kv_store)>(f[0]);
     g_lib.kv_load = reinterpret_cast<decltype(g_lib.kv_load)>(f[1]);
     g_lib.kv_commit = reinterpret_cast<decltype(g_lib.kv_commit)>(f[2]);
-    g_lib.tree_attention = reinterpret_cast<decltype(g_lib.tree_attention)>(f[3]);
-    g_lib.verify_tree_workspace = reinterpret_cast<decltype(g_lib.verify_tree_workspace)>(f[4]);
-    g_lib.verify_tree = reinterpret_cast<decltype(g_lib.verify_tree)>(f[5]);
+    g_lib.tree_attention_workspace = reinterpret_cast<decltype(g_lib.tree_attention_workspace)>(f[3]);
+    g_lib.tree_attention = reinterpret_cast<decltype(g_lib.tree_attention)>(f[4]);
+    g_lib.verify_tree_workspace = reinterpret_cast<decltype(g_lib.verify_tree_workspace)>(f[5]);
+    g_lib.verify_tree = reinterpret_cast<decltype(g_lib.verify_tree)>(f[6]);
     Py_XSETREF(g_error, Py_NewRef(cls));
     Py_RETURN_NONE;
 }

@@ -6,16 +6,48 @@
 
 using namespace gpt2;
 
+namespace {
+
+// More than 16 query rows on a cache head over a 16-bit cache of the rows' own
+// type: the 5th-generation tensor cores, in tiles of 32 or 64 query rows (0:
+// not).
+int tensor_tile(const gpt2_kv &kv, int q_dtype, int rows)
+{
+    if (rows <= 16 || q_dtype != kv.dtype || q_dtype == GPT2_F32 || kv.head_dim < 64) return 0;
+    if ((long long)kv.n_slots * kv.n_head * kv.n_positions >= (1ll << 31) - 128) return 0;   // TMA's row coordinates
+    return rows <= 32 ? 32 : 64;
+}
+
+bool shape_ok(const gpt2_kv *kv, int q_dtype, int n_head, int max_nodes)
+{
+    if (!kv_ok(kv) || !is_row_type(q_dtype)) return false;
+    if (q_dtype != GPT2_F32 && q_dtype != kv->dtype && !is_scaled(kv->dtype)) return false;
+    if (max_nodes < 1 || max_nodes > GPT2_MAX_NODES) return false;
+    return n_head >= 1 && n_head % kv->n_head == 0 && n_head <= (1 << 16);
+}
+
+}  // namespace
+
+extern "C" size_t gpt2_op_tree_attention_workspace(const gpt2_kv *kv, int32_t q_dtype, int32_t n_head,
+                                                   int32_t max_nodes)
+{
+    if (!shape_ok(kv, q_dtype, n_head, max_nodes)) return 0;
+    const int tile = tensor_tile(*kv, q_dtype, max_nodes * (n_head / kv->n_head));
+    if (!tile) return 0;
+    int rc;
+    const int sms = spec_sms(&rc);
+    return sms ? tree_attn_tc_workspace(kv->head_dim, tile, sms) : 0;
+}
+
 extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, int64_t q_stride,
                                       int32_t n_head, const int32_t *slot, const int32_t *cached, const int32_t *first,
                                       const uint64_t *mask, int32_t n_seqs, int32_t n_rows, int32_t max_nodes,
-                                      float scale, void *out, int64_t out_stride, void *stream)
+                                      float scale, void *out, int64_t out_stride, void *workspace,
+                                      size_t workspace_bytes, void *stream)
 {
-    if (!kv_ok(kv) || !q || !slot || !cached || !first || !mask || !out) return GPT2_ERR_INVALID_ARG;
-    if (!is_row_type(q_dtype) || n_seqs < 0 || n_rows < 0 || !std::isfinite(scale)) return GPT2_ERR_INVALID_ARG;
-    if (q_dtype != GPT2_F32 && q_dtype != kv->dtype && !is_scaled(kv->dtype)) return GPT2_ERR_INVALID_ARG;
-    if (max_nodes < 1 || max_nodes > GPT2_MAX_NODES) return GPT2_ERR_INVALID_ARG;
-    if (n_head < 1 || n_head % kv->n_head || n_head > (1 << 16)) return GPT2_ERR_INVALID_ARG;
+    if (!shape_ok(kv, q_dtype, n_head, max_nodes)) return GPT2_ERR_INVALID_ARG;
+    if (!q || !slot || !cached || !first || !mask || !out) return GPT2_ERR_INVALID_ARG;
+    if (n_seqs < 0 || n_rows < 0 || !std::isfinite(scale)) return GPT2_ERR_INVALID_ARG;
     const int64_t E = int64_t(n_head) * kv->head_dim;
     if (q_stride < E || out_stride < E || q_stride % 8 || out_stride % 8) return GPT2_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out)) return GPT2_ERR_INVALID_ARG;
@@ -36,20 +68,27 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     a.q_dtype = q_dtype;
     a.group = n_head / kv->n_head;
     a.scale_log2 = scale * 1.4426950408889634f;
-    // 16 rows of a (sequence, cache head) per warp, or 32 where there are more
-    const int rows = max_nodes * a.group, mt = rows <= 16 ? 1 : 2;
-    a.row_tiles = (rows + 16 * mt - 1) / (16 * mt);
+    const int rows = max_nodes * a.group, tc = tensor_tile(*kv, q_dtype, rows);
+    const int tile = tc ? tc : rows <= 16 ? 16 : 32;   // (else 16 query rows per warp, or 32)
+    a.row_tiles = (rows + tile - 1) / tile;
     const long long units = (long long)n_seqs * kv->n_head * a.row_tiles;
     if (units * 16 >= (1ll << 31)) return GPT2_ERR_INVALID_ARG;
     if (units == 0 || n_rows == 0) return GPT2_OK;
     int rc;
     const int sms = spec_sms(&rc);
     if (!sms) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tc) {
+        if (!workspace || !aligned16(workspace) ||
+            workspace_bytes < tree_attn_tc_workspace(kv->head_dim, tile, sms))
+            return GPT2_ERR_INVALID_ARG;
+        return spec_rc(tree_attn_tc(a, tile, sms, workspace, s));
+    }
     // split the cache between up to 16 CTAs (a cluster) until there are about
     // four per SM, as long as each has 128 positions or more
     a.splits = 1;
     while (a.splits < 16 && units * a.splits < 2ll * sms && kv->n_positions >= 256 * a.splits) a.splits *= 2;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int mt = tile / 16;
     if (kv->dtype == GPT2_F32) return spec_rc(tree_attn_f32(a, mt, s));
     if (is_scaled(kv->dtype)) return spec_rc(tree_attn_8(a, mt, s));
     return spec_rc(tree_attn_16(a, mt, s));

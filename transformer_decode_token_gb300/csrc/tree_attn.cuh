@@ -55,6 +55,9 @@ struct TreeArgs {
 cudaError_t tree_attn_f32(const TreeArgs &a, int mt, cudaStream_t s);
 cudaError_t tree_attn_16(const TreeArgs &a, int mt, cudaStream_t s);
 cudaError_t tree_attn_8(const TreeArgs &a, int mt, cudaStream_t s);
+// n: query rows of a tile, 32 or 64
+cudaError_t tree_attn_tc(const TreeArgs &a, int n, int sms, void *workspace, cudaStream_t s);
+size_t tree_attn_tc_workspace(int head_dim, int n, int sms);
 
 namespace tree {
 
