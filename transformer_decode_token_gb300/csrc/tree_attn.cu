@@ -87,7 +87,7 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     // split the cache between up to 16 CTAs (a cluster) until there are about
     // four per SM, as long as each has 128 positions or more
     a.splits = 1;
-    while (a.splits < 16 && units * a.splits < 2ll * sms && kv->n_positions >= 256 * a.splits) a.splits *= 2;
+    while (a.splits < tree::kMaxSplits && units * a.splits < 2ll * sms && kv->n_positions >= 256 * a.splits) a.splits *= 2;
     const int mt = tile / 16;
     if (kv->dtype == GPT2_F32) return spec_rc(tree_attn_f32(a, mt, s));
     if (is_scaled(kv->dtype)) return spec_rc(tree_attn_8(a, mt, s));

@@ -62,6 +62,7 @@ size_t tree_attn_tc_workspace(int head_dim, int n, int sms);
 namespace tree {
 
 constexpr int kNW = 4;              // warps of a CTA
+constexpr int kMaxSplits = 16;      // CTAs of a cluster
 constexpr float kShift = 13.f;      // fp16 weights are 2^(s' - m + 13): small ones stay normal numbers
 
 enum Mma { kTf32, kF16, kBf16 };
@@ -244,11 +245,17 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x)
     return ((x & e) == e ? 0xffffu : 0u) | ((x >> 16 & e) == e ? 0xffff0000u : 0u);
 }
 
-__device__ __forceinline__ float load_row(const void *p, size_t i, int dtype)
+// Four elements of a query row (aligned to their size) as fp32.
+__device__ __forceinline__ float4 load_row4(const void *p, size_t i, int dtype)
 {
-    if (dtype == GPT2_F32) return static_cast<const float *>(p)[i];
-    if (dtype == GPT2_F16) return __half2float(static_cast<const __half *>(p)[i]);
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+    if (dtype == GPT2_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    if (dtype == GPT2_BF16)
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                           __uint_as_float(u.y & 0xffff0000u));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // Element d of a cache row, as fp32 (a code without its scale).
@@ -275,7 +282,7 @@ struct Smem {
 };
 
 template <class Tr, int D, int MT>
-__global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(const TreeArgs a)
+__global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_attn(const TreeArgs a)
 {
     using T = Tile<Tr, D, MT>;
     using S = Smem<Tr, D, MT>;
@@ -284,6 +291,7 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
     __shared__ float sm_m[kNW][R], sm_l[kNW][R];   // [0] then holds the CTA's
     __shared__ float sm_rs[R];                     // score factor of each row
     __shared__ int sm_bad;
+    __shared__ float sm_f[kMaxSplits][R];
 
     const int rank = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
     const int rt = unit % a.row_tiles, bh = unit / a.row_tiles;
@@ -321,7 +329,41 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
                 load_piece<T::kKLd>(kr + (u * T::kNK + i) * (T::kKLd / 4), p + i * 4 * T::kKLd, j < total);
         }
     };
-    if (t0 < t1) load_keys(t0);
+    // values (and scales) of rows 2c, 2c + 1 of each eight
+    uint32_t vr[T::kVR];
+    float ks[T::kT8][2], vs[T::kT8][2];
+    auto load_values = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < T::kT8; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = t * KS + u * 8 + 2 * c + e;
+                const uint8_t *p = vbase + size_t(j) * T::kRowB + g * T::kVLd;
+#pragma unroll
+                for (int i = 0; i < T::kNV; ++i)
+                    load_piece<T::kVLd>(vr + ((u * 2 + e) * T::kNV + i) * (T::kVLd / 4), p + i * 8 * T::kVLd,
+                                        j < total);
+                if constexpr (Tr::kScaled) {
+                    ks[u][e] = load_scale(kscale + j, j < total);
+                    vs[u][e] = load_scale(vscale + j, j < total);
+                }
+            }
+    };
+    // what the first tile needs is on its way while q is made ready
+    if (t0 < t1) {
+        load_keys(t0);
+        load_values(t0);
+    }
+    // masks of this thread's rows (g and g + 8 of each 16)
+    uint64_t see[MT][2], all = ~0ull;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = mt * 16 + half * 8 + g;
+            see[mt][half] = r < rows ? a.mask[f0 + (row0 + r) / G] : ~0ull;
+            all &= see[mt][half];
+        }
 
     // ---- q as the A operand, in the order the threads take it ----
     uint32_t *qop = reinterpret_cast<uint32_t *>(dyn);   // [MT][kSteps][kQP][32][4]
@@ -336,11 +378,13 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
             const int node = (row0 + (ok ? r : 0)) / G, h = kvh * G + (row0 + (ok ? r : 0)) % G;
             const size_t base = size_t(f0 + node) * a.q_stride + size_t(h) * D;
 #pragma unroll
-            for (int e = 0; e < T::kSteps * kE; ++e) {
+            for (int e = 0; e < T::kSteps * kE; e += 4) {
                 const int d = (4 * (e / T::kEK) + c) * T::kEK + e % T::kEK;
-                x[half][e] = ok ? load_row(a.q, base + d, a.q_dtype) : 0.f;
-                top[half] = fmaxf(top[half], fabsf(x[half][e]));
+                const float4 v = ok ? load_row4(a.q, base + d, a.q_dtype) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[half][e] = v.x, x[half][e + 1] = v.y, x[half][e + 2] = v.z, x[half][e + 3] = v.w;
             }
+#pragma unroll
+            for (int e = 0; e < T::kSteps * kE; ++e) top[half] = fmaxf(top[half], fabsf(x[half][e]));
             float f = 1.f;
             if constexpr (Tr::kNorm) {
                 // bring the row's largest value into [2^13, 2^14)
@@ -387,18 +431,13 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
     }
     __syncthreads();
 
-    // this thread's rows (g and g + 8 of each 16): masks, factors, softmax state
-    uint64_t see[MT][2];
+    // this thread's rows: factors, softmax state
     float rs[MT][2], m[MT][2], l[MT][2];
-    uint64_t all = ~0ull;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int r = mt * 16 + half * 8 + g;
-            see[mt][half] = r < rows ? a.mask[f0 + (row0 + r) / G] : ~0ull;
-            all &= see[mt][half];
-            rs[mt][half] = sm_rs[r];
+            rs[mt][half] = sm_rs[mt * 16 + half * 8 + g];
             m[mt][half] = -INFINITY;
             l[mt][half] = 0.f;
         }
@@ -416,7 +455,6 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
             for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
     float gv = 0x1p-126f;            // scaled caches: o counts in units of gv, a power of two >= the value scales so far
 
-    uint32_t vr[T::kVR];
     auto visible = [&](int mt, int half, int j) {
         return j < pre || (j < total && (see[mt][half] >> (j - pre) & 1));
     };
@@ -424,29 +462,7 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
     bool bad = false;                // a value that some row does not see is not finite
     for (int t = t0; t < t1; t += kNW) {
         const bool tail = (t + 1) * KS > pre;      // the tile holds nodes, or ends inside
-        // values of rows 2c, 2c + 1 of each eight
-#pragma unroll
-        for (int u = 0; u < T::kT8; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = t * KS + u * 8 + 2 * c + e;
-                const uint8_t *p = vbase + size_t(j) * T::kRowB + g * T::kVLd;
-#pragma unroll
-                for (int i = 0; i < T::kNV; ++i)
-                    load_piece<T::kVLd>(vr + ((u * 2 + e) * T::kNV + i) * (T::kVLd / 4), p + i * 8 * T::kVLd,
-                                        j < total);
-            }
-        float ks[T::kT8][2], vs[T::kT8][2];
-        if constexpr (Tr::kScaled) {
-#pragma unroll
-            for (int u = 0; u < T::kT8; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = t * KS + u * 8 + 2 * c + e;
-                    ks[u][e] = load_scale(kscale + j, j < total);
-                    vs[u][e] = load_scale(vscale + j, j < total);
-                }
-        }
+        if (t > t0) load_values(t);
         // scores
         float sc[MT][T::kT8][4], lo[kQP > 1 ? MT : 1][T::kT8][4];   // the first parts' products, the others'
 #pragma unroll
@@ -689,6 +705,7 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
             for (int w = 1; w < kNW; ++w) top = fmaxf(top, sm_m[w][r]);
             const float f = (top == -INFINITY ? 0.f : exp2_approx(m[mt][half] - top)) * (Tr::kScaled ? gv : 1.f);
             float *dst = so + (size_t(warp) * R + r) * D;
+            if (r < rows)
 #pragma unroll
             for (int j = 0; j < T::kNT; ++j) {
                 const int piece = j / T::kEV, w = j % T::kEV;
@@ -705,23 +722,37 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
             cta_l += top == -INFINITY ? 0.f : sm_l[w][tid] * exp2_approx(sm_m[w][tid] - top);
         cta_m = top;
     }
-    for (int e = tid; e < rows * D; e += kNW * 32) {
-        float v = so[e];
+    for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
+        float4 v = *reinterpret_cast<const float4 *>(so + e);
 #pragma unroll
-        for (int w = 1; w < kNW; ++w) v += so[w * R * D + e];
-        so[e] = v;
+        for (int w = 1; w < kNW; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(so + w * R * D + e);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        *reinterpret_cast<float4 *>(so + e) = v;
     }
     __syncthreads();
     if (tid < R) {
         sm_m[0][tid] = cta_m;
         sm_l[0][tid] = cta_l;
     }
-    auto store = [&](int e, float v) {
+    // four elements of a row, from element e = row * D + dim on
+    auto store4 = [&](int e, const float (&v)[4]) {
         const int r = e / D, d = e % D;
         const size_t at = size_t(f0 + (row0 + r) / G) * a.out_stride + size_t(kvh * G + (row0 + r) % G) * D + d;
-        if (a.q_dtype == GPT2_F32) static_cast<float *>(a.out)[at] = v;
-        else if (a.q_dtype == GPT2_F16) static_cast<__half *>(a.out)[at] = __float2half_rn(v);
-        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+        if (a.q_dtype == GPT2_F32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = a.q_dtype == GPT2_F16 ? *reinterpret_cast<const uint32_t *>(&h)
+                                             : *reinterpret_cast<const uint32_t *>(&x);
+            }
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(w[0], w[1]);
+        }
     };
     // the infinities and NaNs that were taken out, for the rows that see them
     auto bad_sum = [&](int e) {
@@ -737,33 +768,55 @@ __global__ void __launch_bounds__(kNW * 32, MT * D <= 64 ? 3 : 2) k_tree_attn(co
     };
     if (a.splits == 1) {
         __syncthreads();
-        for (int e = tid; e < rows * D; e += kNW * 32) {
-            const float sum = sm_l[0][e / D];
-            float v = sum == 0.f ? 0.f : so[e] / sum;
-            if (cta_bad) v += bad_sum(e);
-            store(e, v);
+        for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
+            const float sum = sm_l[0][e / D], inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float4 o4 = *reinterpret_cast<const float4 *>(so + e);
+            float v[4] = {o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv};
+            if (cta_bad)
+                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
+            store4(e, v);
         }
     } else {
         namespace cg = cooperative_groups;
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();
-        bool any_bad = false;
-        for (int k = 0; k < a.splits; ++k) any_bad = any_bad || *cl.map_shared_rank(&sm_bad, k) != 0;
-        // every CTA finishes its share of the elements from all CTAs' sums
-        for (int e = rank * kNW * 32 + tid; e < rows * D; e += a.splits * kNW * 32) {
-            const int r = e / D;
-            float top = -INFINITY;
-            for (int k = 0; k < a.splits; ++k) top = fmaxf(top, *cl.map_shared_rank(&sm_m[0][r], k));
-            float sum = 0.f, v = 0.f;
-            for (int k = 0; k < a.splits; ++k) {
-                const float mk = *cl.map_shared_rank(&sm_m[0][r], k);
-                const float f = top == -INFINITY ? 0.f : exp2_approx(mk - top);
-                sum += *cl.map_shared_rank(&sm_l[0][r], k) * f;
-                v += *cl.map_shared_rank(so + e, k) * f;
+        // every CTA finishes its share of the elements from all CTAs' sums: first
+        // each CTA's factor for each row (2^(its m - the largest) / the sum)
+        for (int r = tid; r < rows; r += kNW * 32) {
+            float mk[kMaxSplits], lk[kMaxSplits], top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                mk[k] = k < a.splits ? *cl.map_shared_rank(&sm_m[0][r], k) : -INFINITY;
+                lk[k] = k < a.splits ? *cl.map_shared_rank(&sm_l[0][r], k) : 0.f;
             }
-            v = sum == 0.f ? 0.f : v / sum;
-            if (any_bad) v += bad_sum(e);
-            store(e, v);
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) top = fmaxf(top, mk[k]);
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                mk[k] = mk[k] == -INFINITY ? 0.f : exp2_approx(mk[k] - top);
+                sum += lk[k] * mk[k];
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) sm_f[k][r] = mk[k] * inv;
+        }
+        const bool any_bad = __syncthreads_or(tid < a.splits ? *cl.map_shared_rank(&sm_bad, tid) : 0);
+        for (int e = (rank * kNW * 32 + tid) * 4; e < rows * D; e += a.splits * kNW * 32 * 4) {
+            float4 x[kMaxSplits];
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k)
+                x[k] = k < a.splits ? *reinterpret_cast<const float4 *>(cl.map_shared_rank(so + e, k))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                const float f = sm_f[k][e / D];
+                v[0] = fmaf(x[k].x, f, v[0]), v[1] = fmaf(x[k].y, f, v[1]);
+                v[2] = fmaf(x[k].z, f, v[2]), v[3] = fmaf(x[k].w, f, v[3]);
+            }
+            if (any_bad)
+                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
+            store4(e, v);
         }
         cl.sync();          // nobody leaves while its sums are read
     }
