@@ -584,6 +584,40 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
 int gpt2_op_kv_commit(const gpt2_kv *kv, int32_t n_layer, const int32_t *slot, const int32_t *cached,
                       const int32_t *path, const int32_t *n_path, int32_t n_seqs, int32_t max_nodes, void *stream);
 
+/* Speculative decoding on a batched model: one step runs several drafted tokens
+ * of a sequence as rows of the batch (a step costs nearly the same for 1 row as
+ * for 64), and the target's own logits decide how many of them stand.
+ *
+ * gpt2_decode_tree_batch: sequence b (b < n) has n_nodes[b] nodes (0: it sits the
+ * step out), host tokens and parents packed one sequence after another; node 0 is
+ * the token the sequence is to consume next (its last choice), every other node a
+ * drafted token after its parent, which comes before it (parents: index within
+ * the sequence; node 0's is ignored).  At most GPT2_MAX_NODES nodes per sequence
+ * and max_batch in all.  Node i stands at position cached length + its depth; its
+ * k and v go to cache row cached length + i, which must be < n_positions.  The
+ * attention is gpt2_op_tree_attention.  If dev_logits is not NULL it receives the
+ * device buffer of the packed nodes' [rows][vocab_size] logits, valid until the
+ * next step.  The cached lengths stay; any other step discards the nodes.  The
+ * first call allocates the step's buffers and captures its graph.
+ * Errors: INVALID_ARG (no nodes, too many, a parent that does not come before its
+ * child), TOKEN_RANGE, POSITION_RANGE, OUT_OF_MEMORY, CUDA.
+ *
+ * gpt2_accept_tree_batch: verifies the nodes of the last such step against its
+ * logits (gpt2_op_verify_tree with these arguments; DEVICE pointers, NULL where
+ * that allows it; u_draw [n][vocab_size]), keeps the accepted path of each
+ * sequence in every layer's cache (gpt2_op_kv_commit), and advances its cached
+ * length over it.  host_tokens [n][GPT2_MAX_NODES] receives the tokens that each
+ * sequence gained (the accepted drafts, then the next token, which the caller
+ * feeds as node 0 or with gpt2_decode_batch, or gpt2_decode_batch_greedy does),
+ * host_counts [n] how many (0 for a sequence that sat out).  Synchronises.
+ * gpt2_batch_ids does not record these tokens.  Errors: NOT_READY (no such step
+ * before), INVALID_ARG, DEVICE_STATE (logits without a choice: that sequence gains
+ * its accepted drafts only), CUDA. */
+int gpt2_decode_tree_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *parents, const int32_t *n_nodes,
+                           int32_t n, const float **dev_logits);
+int gpt2_accept_tree_batch(gpt2_batch *m, float temperature, const float *draft_probs, const float *u_accept,
+                           const float *u_draw, int32_t *host_tokens, int32_t *host_counts);
+
 /* ---- errors ------------------------------------------------------------- */
 const char *gpt2_strerror(int status);
 

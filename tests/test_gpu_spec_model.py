@@ -1,0 +1,194 @@
+"""Speculative decoding on the batched model: tree steps and their acceptance
+against the CPU oracle, through the C ABI.
+
+As in test_gpu_batch.py the oracle runs each sequence on its own with the
+weights as the model stores them, and logits agree within 2e-3 abs.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import oracle as orc
+from transformer_decode_token_gb300 import binding, synth
+
+from gpu_util import max_abs, top2_margin
+
+ATOL = 2e-3
+
+
+def oracle_ids(cfg, w, prompt, steps, kv):
+    sw = orc.stored_weights(w, "bf16", head="bf16")
+    return orc.greedy(cfg, sw, prompt, steps, omp=True, kv=kv)
+
+
+def test_tree_calls_are_refused_on_the_host():
+    L = binding.lib()
+    one = (ctypes.c_int32 * 1)(1)
+    assert L.gpt2_decode_tree_batch(None, one, one, one, 1, None) == -1
+    assert L.gpt2_accept_tree_batch(None, 0.0, None, None, None, one, one) == -1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["f32", "bf16"])
+@pytest.mark.parametrize("deep", [False, True])
+def test_greedy_trees_give_the_greedy_tokens(kv, deep):
+    """Ragged sequences, each step a tree that holds the oracle's own
+    continuation for a few tokens, wrong siblings before and after it, and a
+    wrong child at its end: exactly the right branch is accepted, its logits
+    are the oracle's, and the tokens are those of plain greedy decoding.  deep:
+    one sequence with trees of up to 30 nodes."""
+    cfg = synth.TINY
+    w = synth.make_weights(cfg, 0)
+    prompts = synth.make_batch_prompts(cfg, 1 if deep else 5, 4, 20, seed=4)
+    B, V = len(prompts), cfg.vocab_size
+    ref = [oracle_ids(cfg, w, p, 40, kv) for p in prompts]
+    rng = np.random.default_rng(1)
+    m = binding.BatchModel(cfg, binding.upload_weights(w), 40, kv=kv)
+    try:
+        m.prefill(prompts)
+        gained = [[t] for t in m.argmax(B)]              # ids after the prompt, the first by the prefill
+        for step in range(5):
+            trees, right = [], []
+            for b in range(B):
+                ids = ref[b][0]
+                at = len(gained[b]) - 1                  # the last gained id is consumed next
+                if step == 2 and b == 1:
+                    trees.append(None)
+                    right.append([])
+                    continue
+                take = int(rng.integers(0, 6 if deep else 3))
+                tok, par, path = [gained[b][-1]], [-1], [0]
+                for k in range(take):
+                    for wrong in range(int(rng.integers(0, 3))):   # siblings tried before the right one
+                        tok.append((ids[at + 1 + k] + 1 + wrong) % V)
+                        par.append(path[-1])
+                    tok.append(ids[at + 1 + k])
+                    par.append(path[-1])
+                    path.append(len(tok) - 1)
+                tok.append((ids[at + 1 + take] + 7) % V)
+                par.append(path[-1])
+                while deep and len(tok) < 30 and step % 2:
+                    tok.append(int(rng.integers(0, V)))
+                    par.append(0)
+                trees.append((tok, par))
+                right.append(path)
+            addr = m.decode_tree(trees)
+            rows = sum(len(t[0]) for t in trees if t)
+            assert addr
+            lg = m.logits(rows)
+            r0 = 0
+            for b in range(B):
+                if trees[b] is None:
+                    continue
+                for depth, node in enumerate(right[b]):
+                    row = ref[b][1][len(prompts[b]) + len(gained[b]) - 1 + depth]
+                    d = max_abs(lg[r0 + node], row)
+                    assert d <= ATOL, f"sequence {b} node {node}: {d:.3g}"
+                r0 += len(trees[b][0])
+            new = m.accept_tree()
+            for b in range(B):
+                if trees[b] is None:
+                    assert new[b] == []
+                    continue
+                at = len(gained[b]) - 1
+                want = ref[b][0][at + 1:at + 1 + len(right[b])]
+                rows_ = ref[b][1][len(prompts[b]) + at:len(prompts[b]) + at + len(right[b])]
+                assert min(top2_margin(x) for x in rows_) > 1e-3, "the seed gives near ties"
+                assert new[b] == want, f"sequence {b} step {step}"
+                gained[b] += new[b]
+        # the cache holds what plain decoding leaves: the next plain steps agree
+        lens = [len(p) + len(g) - 1 for p, g in zip(prompts, gained)]
+        m.decode([g[-1] for g in gained], lens)
+        lg = m.logits(B)
+        for b in range(B):
+            assert max_abs(lg[b], ref[b][1][lens[b]]) <= ATOL
+        m.decode_greedy(2)
+        m.sync()
+    finally:
+        m.close()
+
+
+@pytest.mark.gpu
+def test_next_tokens_feed_the_greedy_steps():
+    """After an acceptance gpt2_decode_batch_greedy goes on from the next token."""
+    cfg = synth.TINY
+    w = synth.make_weights(cfg, 0)
+    prompts = synth.make_batch_prompts(cfg, 3, 5, 9, seed=6)
+    ref = [oracle_ids(cfg, w, p, 12, "f32")[0] for p in prompts]
+    m = binding.BatchModel(cfg, binding.upload_weights(w), 16)
+    try:
+        m.prefill(prompts)
+        m.decode_tree([([r[0], r[1], r[2]], [-1, 0, 1]) for r in ref])
+        assert m.accept_tree() == [r[1:4] for r in ref]
+        m.decode_greedy(3)
+        assert m.argmax(3) == [r[6] for r in ref]
+        with pytest.raises(binding.GPT2Error) as e:      # the nodes are gone
+            m.accept_tree()
+        assert e.value.name == "NOT_READY"
+    finally:
+        m.close()
+
+
+@pytest.mark.gpu
+def test_sampled_acceptance_is_the_operation():
+    """temperature > 0: path, tokens and cache are those of gpt2_op_verify_tree
+    on the step's logits; a chain whose u_accept are 0 is accepted whole, with
+    u_accept just below 1 and improbable drafts none of it."""
+    import torch
+    cfg = synth.TINY
+    w = synth.make_weights(cfg, 0)
+    prompts = synth.make_batch_prompts(cfg, 2, 5, 9, seed=6)
+    m = binding.BatchModel(cfg, binding.upload_weights(w), 16)
+    rng = np.random.default_rng(2)
+    try:
+        m.prefill(prompts)
+        first = m.argmax(2)
+        trees = [([first[0], 5, 9], [-1, 0, 1]), ([first[1], 7, 8, 7], [-1, 0, 0, 2])]
+        m.decode_tree(trees)
+        lg = torch.from_numpy(m.logits(7)).cuda()
+        ud = torch.from_numpy(((rng.integers(0, 1 << 23, (2, cfg.vocab_size)) + 0.5) * 2.0 ** -23).astype(np.float32)).cuda()
+        for ua, lens in ((1e-9, [3, 2]), (1 - 2.0 ** -24, [1, 1])):
+            u = torch.full((7,), ua, device="cuda")
+            i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+            path, n_path, nxt = binding.op_verify_tree(lg, i32([first[0], 5, 9, first[1], 7, 8, 7]),
+                                                       i32([-1, 0, 1, -1, 0, 0, 2]), i32([0, 3, 7]), 64, 0.9, None, u, ud)
+            assert n_path.tolist() == lens
+            if ua > 0.5:
+                got = m.accept_tree(0.9, None, u, ud)
+                assert got == [[nxt[0].item()], [nxt[1].item()]]
+    finally:
+        m.close()
+
+
+@pytest.mark.gpu
+def test_tree_steps_refuse():
+    cfg = synth.TINY                                     # 64 positions
+    w = synth.make_weights(cfg, 0)
+    m = binding.BatchModel(cfg, binding.upload_weights(w), 8)
+    try:
+        def status(*trees):
+            with pytest.raises(binding.GPT2Error) as e:
+                m.decode_tree(list(trees))
+            return e.value.name
+        m.prefill([[1, 2, 3], list(range(60))])
+        assert status(None, None) == "INVALID_ARG"
+        assert status(([1] * 9, list(range(-1, 8)))) == "INVALID_ARG"            # more than max_batch rows
+        assert status(([1, 2], [-1, 1])) == "INVALID_ARG"
+        assert status(([1, 2], [-1, -1])) == "INVALID_ARG"
+        assert status(([cfg.vocab_size], [-1])) == "TOKEN_RANGE"
+        assert status(([-1], [-1])) == "TOKEN_RANGE"
+        assert status(None, ([1] * 5, list(range(-1, 4)))) == "POSITION_RANGE"
+        with pytest.raises(binding.GPT2Error) as e:
+            m.accept_tree()
+        assert e.value.name == "NOT_READY"
+        m.decode_tree([None, ([1] * 4, list(range(-1, 3)))])                      # to the last position
+        assert len(m.accept_tree()[1]) >= 1
+        m.decode_tree([([1, 2], [-1, 0])])
+        with pytest.raises(binding.GPT2Error):
+            m.accept_tree(-1.0)
+        with pytest.raises(binding.GPT2Error):
+            m.accept_tree(1.0)
+        assert len(m.accept_tree()[0]) >= 1
+    finally:
+        m.close()

@@ -33,7 +33,8 @@ EXPORTED = ("gpt2_create", "gpt2_create_ex", "gpt2_path", "gpt2_launch_count", "
             "gpt2_decode_batch_greedy", "gpt2_argmax_batch", "gpt2_batch_ids", "gpt2_copy_logits_batch",
             "gpt2_export_kv_batch", "gpt2_batch_info", "gpt2_sync_batch", "gpt2_op_linear_bf16_workspace",
             "gpt2_op_linear_bf16", "gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit",
-            "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree", "gpt2_strerror")
+            "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree", "gpt2_decode_tree_batch",
+            "gpt2_accept_tree_batch", "gpt2_strerror")
 
 
 class GPT2Error(RuntimeError):
@@ -158,6 +159,8 @@ def lib(build_if_stale: bool = True, path: str = None):
             L.gpt2_op_verify_tree_workspace.restype = sz
             L.gpt2_op_verify_tree.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz,
                                               vp]
+            L.gpt2_decode_tree_batch.argtypes = [vp, pi32, pi32, pi32, i32, ctypes.POINTER(vp)]
+            L.gpt2_accept_tree_batch.argtypes = [vp, f32, vp, vp, vp, pi32, pi32]
             L.gpt2_strerror.argtypes = [ctypes.c_int]
             L.gpt2_strerror.restype = ctypes.c_char_p
             for n in EXPORTED:
@@ -424,6 +427,43 @@ class BatchModel:
 
     def decode_greedy(self, n_steps: int):
         check(lib().gpt2_decode_batch_greedy(self._h, int(n_steps)), "gpt2_decode_batch_greedy")
+
+    def decode_tree(self, trees) -> int:
+        """One step over drafted tokens: trees[b] is (tokens, parents) of
+        sequence b's nodes, node 0 the token it consumes next, or None where it
+        sits out; see gpt2_decode_tree_batch.  Returns the device address of the
+        packed nodes' logits."""
+        trees = [q if q is not None else ((), ()) for q in trees]
+        if any(len(t) != len(p) for t, p in trees):
+            raise ValueError("a tree needs one parent per token")
+        counts, cp = _i32([len(t) for t, _ in trees])
+        tok, tp = _i32([x for t, _ in trees for x in t])
+        par, pp = _i32([x for _, p in trees for x in p])
+        d = ctypes.c_void_p()
+        check(lib().gpt2_decode_tree_batch(self._h, tp, pp, cp, counts.size, ctypes.byref(d)),
+              "gpt2_decode_tree_batch")
+        self._tree_counts = counts.tolist()
+        return d.value
+
+    def accept_tree(self, temperature: float = 0.0, draft_probs=None, u_accept=None, u_draw=None) -> list:
+        """Verifies the last tree step's nodes, keeps each sequence's accepted
+        path and returns the tokens it gained (its accepted drafts, then its
+        next token); see gpt2_accept_tree_batch.  CUDA fp32 tensors:
+        draft_probs [nodes][vocab], u_accept [nodes], u_draw
+        [sequences][vocab]."""
+        import torch
+        counts = getattr(self, "_tree_counts", [0])
+        n, rows, V = len(counts), sum(counts), self.cfg.vocab_size
+        for name, t, shape in (("draft_probs", draft_probs, (rows, V)), ("u_accept", u_accept, (rows,)),
+                               ("u_draw", u_draw, (n, V))):
+            if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or
+                                  t.device.type != "cuda"):
+                raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape {shape}")
+        out, op = _i32(np.zeros((n, MAX_NODES)))
+        got, gp = _i32(np.zeros(n))
+        check(lib().gpt2_accept_tree_batch(self._h, float(temperature), _ptr(draft_probs), _ptr(u_accept),
+                                           _ptr(u_draw), op, gp), "gpt2_accept_tree_batch")
+        return [out[b, :got[b]].tolist() for b in range(n)]
 
     def argmax(self, n: int) -> list:
         out = np.zeros(n, np.int32)

@@ -450,6 +450,53 @@ __global__ void __launch_bounds__(kBT) k_b_append(const BAttnArgs a, int D)
     }
 }
 
+struct BTreeArgs {
+    const float *parts;             // [splits][rows][3E] QKV shares
+    int32_t splits;
+    const float *bias;              // [3E]
+    void *kc, *vc;                  // this layer's cache: [slots][H][P][D], fp32 or bf16
+    const int32_t *pos;             // [rows]; -1: no node
+    const int32_t *slot, *crow;     // [rows] a node's cache slot and row
+    int32_t E, H, P, rows;
+    float *q;                       // [rows][E]
+};
+
+// q, k and v of every node (QKV shares + bias): q as the tree attention reads
+// it, k and v into the cache at the node's row.
+template <typename KT>
+__global__ void __launch_bounds__(kBT) k_b_tree_qkv(const BTreeArgs a, int D)
+{
+    const int b = blockIdx.x, E = a.E;
+    pdl_wait();
+    pdl_launch_dependents();   // the next kernel's CTAs may start and park on their wait
+    if (a.pos[b] < 0) return;
+    const int slot = a.slot[b], crow = a.crow[b];
+    for (int j = blockIdx.y * kBT + threadIdx.x; j < 3 * E; j += gridDim.y * kBT) {
+        const float v = sum_shares(a.parts, a.splits, a.rows, 3 * E, b, j) + a.bias[j];
+        const int part = j / E, hd = j % E, h = hd / D, d = hd % D;
+        if (part == 0) a.q[size_t(b) * E + hd] = v;
+        else kv_put(static_cast<KT *>(part == 1 ? a.kc : a.vc) + ((size_t(slot) * a.H + h) * a.P + crow) * D + d, v);
+    }
+}
+
+// The attention's rows as the B operand of the output projection (rows without
+// a node: zero).
+__global__ void __launch_bounds__(kBT) k_b_tree_out(const float *x, const int32_t *pos, int E, __nv_bfloat16 *out)
+{
+    const int b = blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();   // the next kernel's CTAs may start and park on their wait
+    const bool node = pos[b] >= 0;
+    for (int i = threadIdx.x; i < E; i += kBT) put_hi_lo(out, b, E, i, node ? x[size_t(b) * E + i] : 0.f);
+}
+
+// The next tokens of the sequences that took part in a tree step.
+__global__ void k_b_set_next(int32_t *next_tok, const int32_t *next, const int32_t *n_path, int n)
+{
+    const int b = threadIdx.x;
+    if (b < n && n_path[b] > 0 && next[b] >= 0) next_tok[b] = next[b];
+}
+
 struct BArgmaxArgs {
     const float *logits;            // [rows][V]
     int32_t V, rows, P;
@@ -606,6 +653,21 @@ struct gpt2_batch {
     int kernels_per_prompt_step = 0;
     int32_t *slot_of = nullptr;     // [kTcMaxRows] cache slot of each row in a prompt step
     int32_t *order = nullptr;       // [kTcMaxRows] rows by decreasing position (the attention's CTA order)
+    // tree steps (allocated and captured by the first)
+    struct Tree {
+        uint8_t *mem = nullptr;
+        float *q = nullptr, *out = nullptr;                    // [64][E]
+        int32_t *first = nullptr, *cached = nullptr, *ident = nullptr, *crow = nullptr;   // [65], [64] each
+        int32_t *tokens = nullptr, *parents = nullptr;         // [64], packed nodes
+        int32_t *path = nullptr, *n_path = nullptr, *next = nullptr;   // [64][64], [64], [64]
+        uint64_t *mask = nullptr;                              // [64]
+        void *ws = nullptr;                                    // verification
+        size_t ws_bytes = 0;
+        cudaGraph_t graph[2] = {};                             // up to 16 nodes per sequence, up to 64
+        cudaGraphExec_t exec[2] = {};
+        int kernels = 0;
+        std::vector<int32_t> h_first, h_tokens;                // the last step's nodes (empty: none pending)
+    } tree;
     std::vector<int> cached;        // host view: cached length of each sequence
     bool has_step = false;
     unsigned long long launches = 0;
@@ -670,7 +732,10 @@ const void *attn_kernel(int D, bool bf16)
 // packed: a prompt step of the batched model: rows are (sequence, position)
 // pairs (slot_of), every row's k, v appended first; only the blocks run (the
 // cache is what a prompt step is for: no head, no choice).
-int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false)
+// tree_nodes > 0: a step whose rows are the drafted nodes of trees of at most
+// that many nodes (gpt2_decode_tree_batch): the attention is the tree attention,
+// and the step ends with the logits.
+int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false, int tree_nodes = 0)
 {
     const gpt2_config &c = m->cfg;
     const int E = c.n_embd, H = c.n_head, D = E / H, F = 4 * E, R = m->max_batch, P = c.n_positions;
@@ -724,6 +789,47 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false)
         at.P = P;
         at.rows = R;
         at.slots = slots;
+        if (tree_nodes > 0) {
+            const gpt2_batch::Tree &tr = m->tree;
+            BTreeArgs tq{};
+            tq.parts = m->p_qkv;
+            tq.splits = Ly.lin[0].splits;
+            tq.bias = Ly.attn_b;
+            tq.kc = at.kc;
+            tq.vc = at.vc;
+            tq.pos = m->pos;
+            tq.slot = m->slot_of;
+            tq.crow = tr.crow;
+            tq.E = E;
+            tq.H = H;
+            tq.P = P;
+            tq.rows = R;
+            tq.q = tr.q;
+            int dd = D;
+            void *ap[] = {&tq, &dd};
+            const void *fn = m->kv_bf16 ? reinterpret_cast<const void *>(k_b_tree_qkv<__nv_bfloat16>)
+                                        : reinterpret_cast<const void *>(k_b_tree_qkv<float>);
+            BTRY(launch_pdl(fn, dim3(R, 3), dim3(kBT), 0, s, pdl(), ap));
+            gpt2_kv kv{};
+            kv.k = at.kc;
+            kv.v = at.vc;
+            kv.dtype = m->kv_bf16 ? GPT2_BF16 : GPT2_F32;
+            kv.n_slots = slots;
+            kv.n_head = H;
+            kv.n_positions = P;
+            kv.head_dim = D;
+            const int rc = gpt2_op_tree_attention(&kv, tr.q, GPT2_F32, E, H, tr.ident, tr.cached, tr.first, tr.mask, R,
+                                                  R, tree_nodes, float(1.0 / std::sqrt(double(D))), tr.out, E, nullptr,
+                                                  0, s);
+            if (rc != GPT2_OK) return rc;
+            const float *xo = tr.out;
+            const int32_t *ps = m->pos;
+            int ee = E;
+            __nv_bfloat16 *bo = m->b_a;
+            void *ao[] = {&xo, &ps, &ee, &bo};
+            BTRY(launch_pdl(reinterpret_cast<const void *>(k_b_tree_out), dim3(R), dim3(kBT), 0, s, pdl(), ao));
+            kernels += 2;
+        }
         const bool pre = slots == 1 || packed;   // rows of prompts: every row's k, v first (k_b_append)
         at.append = pre ? 0 : 1;
         at.slot_of = packed ? m->slot_of : nullptr;
@@ -731,7 +837,7 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false)
         at.scale = float(1.0 / std::sqrt(double(D)));
         at.out = m->b_a;
         at.st = m->st;
-        if (pre) {
+        if (pre && tree_nodes == 0) {
             int dd = D;
             void *ap[] = {&at, &dd};
             const void *fn = m->kv_bf16 ? reinterpret_cast<const void *>(k_b_append<__nv_bfloat16>)
@@ -740,8 +846,9 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false)
             ++kernels;
         }
         void *a2[] = {&at};
-        BTRY(launch_pdl(attn_kernel(D, m->kv_bf16), dim3(R, H), dim3(kBT), attn_smem(D, P, m->kv_bf16 ? 2 : 4), s,
-                        pdl(), a2));
+        if (tree_nodes == 0)
+            BTRY(launch_pdl(attn_kernel(D, m->kv_bf16), dim3(R, H), dim3(kBT), attn_smem(D, P, m->kv_bf16 ? 2 : 4),
+                            s, pdl(), a2));
         BTRY(run_linear(m, Ly.lin[1], m->map_a, m->p_o, s, pdl()));
         ln.mode = 1;
         ln.parts = m->p_o;
@@ -787,6 +894,10 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false)
     void *a5[] = {&ln};
     BTRY(launch_pdl(reinterpret_cast<const void *>(k_b_ln), dim3(R), dim3(kBT), ln_smem, s, pdl(), a5));
     BTRY(run_linear(m, m->head_lin, m->map_e, m->logits, s, pdl()));
+    if (tree_nodes > 0) {
+        m->tree.kernels = kernels + 2;
+        return GPT2_OK;
+    }
     BArgmaxArgs am{};
     am.logits = m->logits;
     am.V = V;
@@ -807,7 +918,7 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false)
     return GPT2_OK;
 }
 
-int capture_step(gpt2_batch *m, bool packed, cudaGraph_t *graph, cudaGraphExec_t *exec)
+int capture_step(gpt2_batch *m, bool packed, cudaGraph_t *graph, cudaGraphExec_t *exec, int tree_nodes = 0)
 {
     cudaStream_t cs;
     BTRY(cudaStreamCreateWithFlags(&cs, cudaStreamNonBlocking));
@@ -816,7 +927,7 @@ int capture_step(gpt2_batch *m, bool packed, cudaGraph_t *graph, cudaGraphExec_t
         cudaStreamDestroy(cs);
         return cuda_rc(e);
     }
-    const int rc = record_step(m, cs, packed);
+    const int rc = record_step(m, cs, packed, tree_nodes);
     cudaGraph_t g = nullptr;
     e = cudaStreamEndCapture(cs, &g);
     cudaStreamDestroy(cs);
@@ -846,6 +957,11 @@ void free_batch(gpt2_batch *m)
     if (m->graph) cudaGraphDestroy(m->graph);
     if (m->exec_p) cudaGraphExecDestroy(m->exec_p);
     if (m->graph_p) cudaGraphDestroy(m->graph_p);
+    for (int k = 0; k < 2; ++k) {
+        if (m->tree.exec[k]) cudaGraphExecDestroy(m->tree.exec[k]);
+        if (m->tree.graph[k]) cudaGraphDestroy(m->tree.graph[k]);
+    }
+    if (m->tree.mem) cudaFree(m->tree.mem);
     if (m->arena) cudaFree(m->arena);
     if (m->work) cudaFree(m->work);
     delete m;
@@ -1275,6 +1391,7 @@ int gpt2_decode_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *posit
     BTRY(upload_order(m, p.data(), m->stream));
     BTRY(cudaGraphLaunch(m->exec, m->stream));
     m->launches += m->kernels_per_step;
+    m->tree.h_first.clear();                       // a tree step's nodes, if any, are gone
     for (int b = 0; b < n; ++b)
         if (p[b] >= 0) m->cached[b] = p[b] + 1;
     m->has_step = true;
@@ -1293,6 +1410,7 @@ int gpt2_prefill_batch(gpt2_batch *m, const int32_t *ids, const int32_t *lens, i
     for (size_t i = 0; i < total; ++i)
         if (ids[i] < 0 || ids[i] >= m->cfg.vocab_size) return GPT2_ERR_TOKEN_RANGE;
     std::fill(m->cached.begin(), m->cached.end(), 0);
+    m->tree.h_first.clear();
     std::vector<size_t> start(n, 0);
     for (int b = 1; b < n; ++b) start[b] = start[b - 1] + size_t(lens[b - 1]);
     // prompt steps: every position but each sequence's last, max_batch rows
@@ -1358,6 +1476,7 @@ int gpt2_decode_batch_greedy(gpt2_batch *m, int32_t n_steps)
     for (int b = 0; b < m->max_batch; ++b)
         if (m->cached[b] > 0 && m->cached[b] + n_steps > m->cfg.n_positions) return GPT2_ERR_POSITION_RANGE;
     if (n_steps == 0) return GPT2_OK;
+    m->tree.h_first.clear();
     // every sequence with a cached prefix continues from its own length with
     // its last choice
     std::vector<int32_t> p(kTcMaxRows, -1);
@@ -1371,6 +1490,142 @@ int gpt2_decode_batch_greedy(gpt2_batch *m, int32_t n_steps)
     for (int b = 0; b < m->max_batch; ++b)
         if (m->cached[b] > 0) m->cached[b] += n_steps;
     return GPT2_OK;
+}
+
+int gpt2_decode_tree_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *parents, const int32_t *n_nodes,
+                           int32_t n, const float **dev_logits)
+{
+    if (!m || !tokens || !parents || !n_nodes || n < 1 || n > m->max_batch) return GPT2_ERR_INVALID_ARG;
+    const gpt2_config &c = m->cfg;
+    const int R = kTcMaxRows;
+    std::vector<int32_t> t(R, 0), par(R, 0), p(R, -1), sl(R, 0), crow(R, 0), first(R + 1, 0), cached(R, 0);
+    std::vector<uint64_t> mask(R, 0);
+    int r = 0, most = 0;
+    for (int b = 0; b < n; ++b) {
+        const int k = n_nodes[b], r0 = r;
+        if (k < 0 || k > GPT2_MAX_NODES || r + k > m->max_batch) return GPT2_ERR_INVALID_ARG;
+        if (k > 0 && m->cached[b] + k > c.n_positions) return GPT2_ERR_POSITION_RANGE;
+        for (int i = 0; i < k; ++i, ++r) {
+            const int q = i == 0 ? -1 : parents[r];
+            if (i > 0 && (q < 0 || q >= i)) return GPT2_ERR_INVALID_ARG;
+            if (tokens[r] < 0 || tokens[r] >= c.vocab_size) return GPT2_ERR_TOKEN_RANGE;
+            t[r] = tokens[r];
+            par[r] = q;
+            p[r] = i == 0 ? m->cached[b] : p[r0 + q] + 1;
+            sl[r] = b;
+            crow[r] = m->cached[b] + i;
+            mask[r] = (uint64_t(1) << i) | (i > 0 ? mask[r0 + q] : 0);
+        }
+        first[b + 1] = r;
+        cached[b] = m->cached[b];
+        most = std::max(most, k);
+    }
+    if (r == 0) return GPT2_ERR_INVALID_ARG;
+    for (int b = n; b < R; ++b) first[b + 1] = r;
+    gpt2_batch::Tree &tr = m->tree;
+    if (!tr.mem) {
+        const int E = c.n_embd;
+        size_t off = 0;
+        auto take = [&](size_t bytes) {
+            const size_t o = off;
+            off += a256(bytes);
+            return o;
+        };
+        tr.ws_bytes = gpt2_op_verify_tree_workspace(m->max_batch, c.vocab_size);
+        const size_t oq = take(size_t(R) * E * 4), oo = take(size_t(R) * E * 4), of = take((R + 1) * 4), oc = take(R * 4);
+        const size_t oi = take(R * 4), ow = take(R * 4), ot = take(R * 4), op = take(R * 4), om = take(R * 8);
+        const size_t oh = take(size_t(R) * GPT2_MAX_NODES * 4), on = take(R * 4), ox = take(R * 4), os = take(tr.ws_bytes);
+        uint8_t *mem = nullptr;
+        BTRY(cudaMalloc(&mem, off));
+        std::vector<int32_t> ident(R);
+        for (int b = 0; b < R; ++b) ident[b] = b;
+        cudaError_t e = cudaMemset(mem, 0, off);
+        if (e == cudaSuccess) e = cudaMemcpy(mem + oi, ident.data(), R * 4, cudaMemcpyHostToDevice);
+        if (e != cudaSuccess) {
+            cudaFree(mem);
+            return cuda_rc(e);
+        }
+        tr.mem = mem;
+        tr.q = reinterpret_cast<float *>(mem + oq);
+        tr.out = reinterpret_cast<float *>(mem + oo);
+        tr.first = reinterpret_cast<int32_t *>(mem + of);
+        tr.cached = reinterpret_cast<int32_t *>(mem + oc);
+        tr.ident = reinterpret_cast<int32_t *>(mem + oi);
+        tr.crow = reinterpret_cast<int32_t *>(mem + ow);
+        tr.tokens = reinterpret_cast<int32_t *>(mem + ot);
+        tr.parents = reinterpret_cast<int32_t *>(mem + op);
+        tr.mask = reinterpret_cast<uint64_t *>(mem + om);
+        tr.path = reinterpret_cast<int32_t *>(mem + oh);
+        tr.n_path = reinterpret_cast<int32_t *>(mem + on);
+        tr.next = reinterpret_cast<int32_t *>(mem + ox);
+        tr.ws = mem + os;
+    }
+    const int k = most <= 16 ? 0 : 1;
+    if (!tr.exec[k]) {
+        const int rc = capture_step(m, false, &tr.graph[k], &tr.exec[k], k == 0 ? 16 : GPT2_MAX_NODES);
+        if (rc != GPT2_OK) return rc;
+    }
+    const std::pair<void *, const std::vector<int32_t> *> up[] = {{m->tok, &t},          {m->pos, &p},
+                                                                  {m->slot_of, &sl},     {tr.crow, &crow},
+                                                                  {tr.first, &first},    {tr.cached, &cached},
+                                                                  {tr.tokens, &t},       {tr.parents, &par}};
+    for (const auto &u : up)
+        BTRY(cudaMemcpyAsync(u.first, u.second->data(), u.second->size() * 4, cudaMemcpyHostToDevice, m->stream));
+    BTRY(cudaMemcpyAsync(tr.mask, mask.data(), mask.size() * 8, cudaMemcpyHostToDevice, m->stream));
+    BTRY(cudaGraphLaunch(tr.exec[k], m->stream));
+    m->launches += tr.kernels;
+    m->has_step = true;
+    tr.h_first.assign(first.begin(), first.begin() + n + 1);
+    tr.h_tokens.assign(t.begin(), t.begin() + r);
+    if (dev_logits) *dev_logits = m->logits;
+    return GPT2_OK;
+}
+
+int gpt2_accept_tree_batch(gpt2_batch *m, float temperature, const float *draft_probs, const float *u_accept,
+                           const float *u_draw, int32_t *host_tokens, int32_t *host_counts)
+{
+    if (!m || !host_tokens || !host_counts) return GPT2_ERR_INVALID_ARG;
+    gpt2_batch::Tree &tr = m->tree;
+    if (tr.h_first.empty()) return GPT2_ERR_NOT_READY;
+    const gpt2_config &c = m->cfg;
+    const int n = int(tr.h_first.size()) - 1, rows = tr.h_first[n];
+    int rc = gpt2_op_verify_tree(m->logits, c.vocab_size, tr.tokens, tr.parents, tr.first, n, rows, GPT2_MAX_NODES,
+                                 temperature, draft_probs, u_accept, u_draw, tr.path, tr.n_path, tr.next, tr.ws,
+                                 tr.ws_bytes, m->stream);
+    if (rc != GPT2_OK) return rc;
+    gpt2_kv kv{};
+    kv.k = m->kc;
+    kv.v = m->vc;
+    kv.dtype = m->kv_bf16 ? GPT2_BF16 : GPT2_F32;
+    kv.n_slots = m->slots;
+    kv.n_head = c.n_head;
+    kv.n_positions = c.n_positions;
+    kv.head_dim = c.n_embd / c.n_head;
+    rc = gpt2_op_kv_commit(&kv, c.n_layer, tr.ident, tr.cached, tr.path, tr.n_path, n, GPT2_MAX_NODES, m->stream);
+    if (rc != GPT2_OK) return rc;
+    k_b_set_next<<<1, kTcMaxRows, 0, m->stream>>>(m->next_tok, tr.next, tr.n_path, n);
+    BTRY(cudaGetLastError());
+    m->launches += 4;
+    std::vector<int32_t> path(size_t(n) * GPT2_MAX_NODES), n_path(n), next(n);
+    BTRY(cudaMemcpyAsync(path.data(), tr.path, path.size() * 4, cudaMemcpyDeviceToHost, m->stream));
+    BTRY(cudaMemcpyAsync(n_path.data(), tr.n_path, size_t(n) * 4, cudaMemcpyDeviceToHost, m->stream));
+    BTRY(cudaMemcpyAsync(next.data(), tr.next, size_t(n) * 4, cudaMemcpyDeviceToHost, m->stream));
+    rc = read_batch_state(m);
+    if (rc != GPT2_OK) return rc;
+    const std::vector<int32_t> first = std::move(tr.h_first);
+    tr.h_first.clear();
+    for (int b = 0; b < n; ++b) {
+        int k = 0;
+        for (int i = 1; i < n_path[b]; ++i)
+            host_tokens[size_t(b) * GPT2_MAX_NODES + k++] = tr.h_tokens[first[b] + path[size_t(b) * GPT2_MAX_NODES + i]];
+        if (n_path[b] > 0) {
+            if (next[b] >= 0) host_tokens[size_t(b) * GPT2_MAX_NODES + k++] = next[b];
+            else rc = GPT2_ERR_DEVICE_STATE;
+        }
+        host_counts[b] = k;
+        m->cached[b] += n_path[b];
+    }
+    return rc;
 }
 
 int gpt2_argmax_batch(gpt2_batch *m, int32_t *host_ids, int32_t n)
