@@ -192,3 +192,130 @@ def test_tree_steps_refuse():
         assert len(m.accept_tree()[0]) >= 1
     finally:
         m.close()
+
+
+# ---- the int8 cache -----------------------------------------------------------------
+
+def quantise(x):
+    """Rows [..][D] as an int8 cache holds them, by the definition in gpt2.h, and
+    the steps (scales)."""
+    s = np.maximum(np.abs(x).max(-1, keepdims=True).astype(np.float32) / np.float32(127), np.float32(2.0 ** -126))
+    return np.rint(x / s.astype(np.float64)) * s.astype(np.float64), s.astype(np.float64)
+
+
+def forward64(cfg, w, tokens, kv=quantise):
+    """Float64 GPT-2 forward (logits of every position) whose keys and values
+    pass through the int8 cache's rounding, per head and row."""
+    d = lambda a: np.asarray(a, np.float64)
+    E, H, D, n = cfg.n_embd, cfg.n_head, cfg.head_dim, len(tokens)
+
+    def norm(x, g, b):
+        x = x - x.mean(-1, keepdims=True)
+        return x / np.sqrt((x * x).mean(-1, keepdims=True) + cfg.ln_eps) * d(g) + d(b)
+
+    x = d(w["wte"])[tokens] + d(w["wpe"])[:n]
+    rows = []
+    for L in w["layers"]:
+        q, k, v = np.split(norm(x, L["ln1_w"], L["ln1_b"]) @ d(L["attn_w"]) + d(L["attn_b"]), 3, -1)
+        q, k, v = (a.reshape(n, H, D).transpose(1, 0, 2) for a in (q, k, v))
+        k, v = (kv(a)[0] for a in (k, v))
+        rows.append((k, v))
+        s = q @ k.transpose(0, 2, 1) / np.sqrt(D)
+        s[:, np.triu(np.ones((n, n), bool), 1)] = -np.inf
+        p = np.exp(s - s.max(-1, keepdims=True))
+        a = (p / p.sum(-1, keepdims=True)) @ v
+        x = x + a.transpose(1, 0, 2).reshape(n, E) @ d(L["proj_w"]) + d(L["proj_b"])
+        h = norm(x, L["ln2_w"], L["ln2_b"]) @ d(L["fc_w"]) + d(L["fc_b"])
+        h = h / (1 + np.exp(-2 * np.sqrt(2 / np.pi) * (h + 0.044715 * h ** 3)))
+        x = x + h @ d(L["mlp_proj_w"]) + d(L["mlp_proj_b"])
+    return norm(x, w["ln_f_w"], w["ln_f_b"]) @ d(w.get("head", w["wte"])).T, rows
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [7, 1])
+def test_int8_cache_model(batch):
+    """Ragged prompts (packed prompt steps; one sequence: a step per position)
+    and decode steps against the float64 forward with the same rounding of the
+    keys and values.  The model's own k and v are off from exact ones by about
+    2^-17 (bf16 hi + lo products), so a code differs where a value lies that
+    near to a rounding border, for about one in a thousand, by one step (1/127
+    of its row's largest): far below the tolerance of 2e-3 in the logits.
+    Layer 0's exported rows are within half a step, and that error, of the
+    exact rows."""
+    cfg = synth.TINY
+    w = synth.make_weights(cfg, 0)
+    sw = orc.stored_weights(w, "bf16", head="bf16")
+    prompts = synth.make_batch_prompts(cfg, batch, 3, 30, seed=8)
+    m = binding.BatchModel(cfg, binding.upload_weights(w), batch, kv="int8")
+    rng = np.random.default_rng(3)
+    try:
+        m.prefill(prompts)
+        lg = m.logits(batch)
+        seqs = [list(p) for p in prompts]
+        for step in range(4):
+            for b in range(batch):
+                want, _ = forward64(cfg, sw, np.array(seqs[b]))
+                d = max_abs(lg[b], want[-1])
+                assert d <= ATOL, f"sequence {b} step {step}: {d:.3g}"
+            if step == 3:
+                break
+            nxt = [int(x) for x in rng.integers(0, cfg.vocab_size, batch)]
+            m.decode(nxt, [len(q) for q in seqs])
+            for q, t in zip(seqs, nxt):
+                q.append(t)
+            lg = m.logits(batch)
+        b = batch - 1
+        k, v = m.export_kv(0, b, len(seqs[b]))
+        for got, exact in zip((k, v), forward64(cfg, sw, np.array(seqs[b]), kv=lambda a: (a, None))[1][0]):
+            _, step_size = quantise(exact)
+            assert np.all(np.abs(got - exact) <= 0.5 * step_size + 2.0 ** -15 * (1 + np.abs(exact)))
+        m.decode_greedy(2)
+        m.sync()
+    finally:
+        m.close()
+
+
+@pytest.mark.gpu
+def test_int8_cache_tree_steps():
+    """A tree step over the int8 cache: every node's logits are those of its own
+    path run through the float64 forward, and after the acceptance plain steps go
+    on from the kept path."""
+    cfg = synth.TINY
+    w = synth.make_weights(cfg, 0)
+    sw = orc.stored_weights(w, "bf16", head="bf16")
+    prompts = synth.make_batch_prompts(cfg, 3, 5, 20, seed=9)
+    m = binding.BatchModel(cfg, binding.upload_weights(w), 24, kv="int8")
+    try:
+        m.prefill(prompts)
+        first = m.argmax(3)
+        follow = []
+        for p, t in zip(prompts, first):                 # two exact greedy tokens after the first
+            ids = list(p) + [t]
+            for _ in range(2):
+                ids.append(int(np.argmax(forward64(cfg, sw, np.array(ids))[0][-1])))
+            follow.append(ids[-2:])
+        trees = [([t, 3, f[0], 9, f[1], 8], [-1, 0, 0, 1, 2, 4]) for t, f in zip(first, follow)]
+        m.decode_tree(trees)
+        lg = m.logits(18)
+        margins = []
+        for b, (tok, par) in enumerate(trees):
+            for i in range(6):
+                path, j = [], i
+                while j >= 0:
+                    path.append(tok[j])
+                    j = par[j]
+                want = forward64(cfg, sw, np.array(list(prompts[b]) + path[::-1]))[0][-1]
+                assert max_abs(lg[6 * b + i], want) <= ATOL, (b, i)
+                if i in (0, 2, 4):
+                    margins.append(top2_margin(want))
+        assert min(margins) > 4e-3, "the seed gives near ties"
+        got = m.accept_tree()
+        for b in range(3):
+            assert got[b][:2] == follow[b] and len(got[b]) == (4 if got[b][2] == 8 else 3)
+        m.decode([g[-1] for g in got], [len(p) + len(g) for p, g in zip(prompts, got)])
+        lg = m.logits(3)
+        for b in range(3):
+            ids = list(prompts[b]) + [first[b]] + got[b]
+            assert max_abs(lg[b], forward64(cfg, sw, np.array(ids))[0][-1]) <= ATOL
+    finally:
+        m.close()

@@ -382,17 +382,18 @@ def _i32(a):
     return a, a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
 
 
-BATCH_KV_BF16 = 1
+BATCH_KV_BF16, BATCH_KV_INT8 = 1, 4
 
 
 class BatchModel:
     """Up to max_batch independent sequences decoded together (bf16 weights,
     tensor-core linears); see gpt2_create_batch in include/gpt2.h.  kv:
-    the cache's element type, "f32" or "bf16" (GPT2_BATCH_KV_BF16)."""
+    the cache's element type, "f32", "bf16" (GPT2_BATCH_KV_BF16) or "int8"
+    (GPT2_BATCH_KV_INT8)."""
 
     def __init__(self, cfg, dev_weights: dict, max_batch: int, wdtype: str = "bf16", stream=None,
                  kv: str = "f32"):
-        if kv not in ("f32", "bf16"):
+        if kv not in ("f32", "bf16", "int8"):
             raise ValueError(f"unknown KV cache type {kv!r}")
         L = lib()
         self.cfg = cfg
@@ -407,7 +408,7 @@ class BatchModel:
                     ctypes.cast(layers, ctypes.POINTER(LayerWeights)))
         h = ctypes.c_void_p()
         check(L.gpt2_create_batch_ex(ctypes.byref(c), ctypes.byref(w), WDTYPES[wdtype], int(max_batch),
-                                     BATCH_KV_BF16 if kv == "bf16" else 0, _stream_handle(stream), ctypes.byref(h)),
+                                     {"f32": 0, "bf16": BATCH_KV_BF16, "int8": BATCH_KV_INT8}[kv], _stream_handle(stream), ctypes.byref(h)),
               "gpt2_create_batch_ex")
         self.kv = kv
         self._h = h

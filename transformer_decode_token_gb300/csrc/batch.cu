@@ -459,10 +459,11 @@ struct BTreeArgs {
     const int32_t *slot, *crow;     // [rows] a node's cache slot and row
     int32_t E, H, P, rows;
     float *q;                       // [rows][E]
+    float *k, *v;                   // [rows][E] rows to be quantised into the cache, or null: written here
 };
 
 // q, k and v of every node (QKV shares + bias): q as the tree attention reads
-// it, k and v into the cache at the node's row.
+// it, k and v into the cache at the node's row (or as rows, for an int8 cache).
 template <typename KT>
 __global__ void __launch_bounds__(kBT) k_b_tree_qkv(const BTreeArgs a, int D)
 {
@@ -475,6 +476,7 @@ __global__ void __launch_bounds__(kBT) k_b_tree_qkv(const BTreeArgs a, int D)
         const float v = sum_shares(a.parts, a.splits, a.rows, 3 * E, b, j) + a.bias[j];
         const int part = j / E, hd = j % E, h = hd / D, d = hd % D;
         if (part == 0) a.q[size_t(b) * E + hd] = v;
+        else if (a.k) (part == 1 ? a.k : a.v)[size_t(b) * E + hd] = v;
         else kv_put(static_cast<KT *>(part == 1 ? a.kc : a.vc) + ((size_t(slot) * a.H + h) * a.P + crow) * D + d, v);
     }
 }
@@ -638,6 +640,8 @@ struct gpt2_batch {
     // work
     void *kc = nullptr, *vc = nullptr;                    // [L][slots][H][P][D] fp32, or bf16 (kv_bf16)
     bool kv_bf16 = false;
+    bool kv_int8 = false;                                 // int8 codes, and their scales [L][slots][H][P]:
+    float *kscale = nullptr, *vscale = nullptr;
     float *x = nullptr;                                   // [64][E]
     __nv_bfloat16 *b_e = nullptr, *b_a = nullptr, *b_f = nullptr;   // [128][E], [128][E], [128][F]
     CUtensorMap map_e{}, map_a{}, map_f{};
@@ -657,10 +661,13 @@ struct gpt2_batch {
     struct Tree {
         uint8_t *mem = nullptr;
         float *q = nullptr, *out = nullptr;                    // [64][E]
-        int32_t *first = nullptr, *cached = nullptr, *ident = nullptr, *crow = nullptr;   // [65], [64] each
+        int32_t *first = nullptr, *cached = nullptr, *crow = nullptr;                    // [65], [64] each
         int32_t *tokens = nullptr, *parents = nullptr;         // [64], packed nodes
         int32_t *path = nullptr, *n_path = nullptr, *next = nullptr;   // [64][64], [64], [64]
         uint64_t *mask = nullptr;                              // [64]
+        float *k = nullptr, *v = nullptr;                      // [64][E] rows on their way into an int8 cache
+        int32_t *each = nullptr;                               // [65] 0, 1, ..: every row a sequence of its own
+        uint64_t *one = nullptr;                               // [64] masks of single nodes
         void *ws = nullptr;                                    // verification
         size_t ws_bytes = 0;
         cudaGraph_t graph[2] = {};                             // up to 16 nodes per sequence, up to 64
@@ -728,6 +735,26 @@ const void *attn_kernel(int D, bool bf16)
                      : reinterpret_cast<const void *>(k_b_attn<128, float>);
 }
 
+// The cache of layer l as the cache operations see it.
+gpt2_kv layer_kv(const gpt2_batch *m, int l)
+{
+    const gpt2_config &c = m->cfg;
+    gpt2_kv kv{};
+    kv.dtype = m->kv_int8 ? GPT2_INT8 : m->kv_bf16 ? GPT2_BF16 : GPT2_F32;
+    kv.n_slots = m->slots;
+    kv.n_head = c.n_head;
+    kv.n_positions = c.n_positions;
+    kv.head_dim = c.n_embd / c.n_head;
+    const size_t rows = size_t(m->slots) * c.n_head * c.n_positions, es = m->kv_int8 ? 1 : m->kv_bf16 ? 2 : 4;
+    kv.k = static_cast<uint8_t *>(m->kc) + l * rows * kv.head_dim * es;
+    kv.v = static_cast<uint8_t *>(m->vc) + l * rows * kv.head_dim * es;
+    if (m->kv_int8) {
+        kv.k_scale = m->kscale + l * rows;
+        kv.v_scale = m->vscale + l * rows;
+    }
+    return kv;
+}
+
 // Records one batched step on stream s (under capture).
 // packed: a prompt step of the batched model: rows are (sequence, position)
 // pairs (slot_of), every row's k, v appended first; only the blocks run (the
@@ -789,38 +816,45 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false, int tree_nod
         at.P = P;
         at.rows = R;
         at.slots = slots;
-        if (tree_nodes > 0) {
+        // the rows as nodes: drafted ones; or, for an int8 cache, a prompt's
+        // consecutive positions (a chain per sequence), or single tokens
+        const bool as_nodes = tree_nodes > 0 || m->kv_int8;
+        if (as_nodes) {
             const gpt2_batch::Tree &tr = m->tree;
+            const gpt2_kv kv = layer_kv(m, l);
+            const bool chain = packed, single = tree_nodes == 0 && !packed;
+            const int nodes = single ? 1 : chain ? GPT2_MAX_NODES : tree_nodes;
+            const int32_t *row_slot = single ? tr.each : m->slot_of, *row_at = tree_nodes > 0 ? tr.crow : m->pos;
             BTreeArgs tq{};
             tq.parts = m->p_qkv;
             tq.splits = Ly.lin[0].splits;
             tq.bias = Ly.attn_b;
-            tq.kc = at.kc;
-            tq.vc = at.vc;
+            tq.kc = kv.k;
+            tq.vc = kv.v;
             tq.pos = m->pos;
-            tq.slot = m->slot_of;
-            tq.crow = tr.crow;
+            tq.slot = row_slot;
+            tq.crow = row_at;
             tq.E = E;
             tq.H = H;
             tq.P = P;
             tq.rows = R;
             tq.q = tr.q;
+            tq.k = m->kv_int8 ? tr.k : nullptr;
+            tq.v = m->kv_int8 ? tr.v : nullptr;
             int dd = D;
             void *ap[] = {&tq, &dd};
             const void *fn = m->kv_bf16 ? reinterpret_cast<const void *>(k_b_tree_qkv<__nv_bfloat16>)
                                         : reinterpret_cast<const void *>(k_b_tree_qkv<float>);
             BTRY(launch_pdl(fn, dim3(R, 3), dim3(kBT), 0, s, pdl(), ap));
-            gpt2_kv kv{};
-            kv.k = at.kc;
-            kv.v = at.vc;
-            kv.dtype = m->kv_bf16 ? GPT2_BF16 : GPT2_F32;
-            kv.n_slots = slots;
-            kv.n_head = H;
-            kv.n_positions = P;
-            kv.head_dim = D;
-            const int rc = gpt2_op_tree_attention(&kv, tr.q, GPT2_F32, E, H, tr.ident, tr.cached, tr.first, tr.mask, R,
-                                                  R, tree_nodes, float(1.0 / std::sqrt(double(D))), tr.out, E, nullptr,
-                                                  0, s);
+            int rc = GPT2_OK;
+            if (m->kv_int8) {   // (rows without a node have no cache row: skipped)
+                rc = gpt2_op_kv_store(&kv, tr.k, tr.v, GPT2_F32, E, row_slot, row_at, R, s);
+                ++kernels;
+            }
+            if (rc == GPT2_OK)
+                rc = gpt2_op_tree_attention(&kv, tr.q, GPT2_F32, E, H, tr.each, single ? m->pos : tr.cached,
+                                            single ? tr.each : tr.first, single ? tr.one : tr.mask, R, R, nodes,
+                                            float(1.0 / std::sqrt(double(D))), tr.out, E, nullptr, 0, s);
             if (rc != GPT2_OK) return rc;
             const float *xo = tr.out;
             const int32_t *ps = m->pos;
@@ -837,7 +871,7 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false, int tree_nod
         at.scale = float(1.0 / std::sqrt(double(D)));
         at.out = m->b_a;
         at.st = m->st;
-        if (pre && tree_nodes == 0) {
+        if (pre && !as_nodes) {
             int dd = D;
             void *ap[] = {&at, &dd};
             const void *fn = m->kv_bf16 ? reinterpret_cast<const void *>(k_b_append<__nv_bfloat16>)
@@ -846,7 +880,7 @@ int record_step(gpt2_batch *m, cudaStream_t s, bool packed = false, int tree_nod
             ++kernels;
         }
         void *a2[] = {&at};
-        if (tree_nodes == 0)
+        if (!as_nodes)
             BTRY(launch_pdl(attn_kernel(D, m->kv_bf16), dim3(R, H), dim3(kBT), attn_smem(D, P, m->kv_bf16 ? 2 : 4),
                             s, pdl(), a2));
         BTRY(run_linear(m, Ly.lin[1], m->map_a, m->p_o, s, pdl()));
@@ -941,6 +975,54 @@ int capture_step(gpt2_batch *m, bool packed, cudaGraph_t *graph, cudaGraphExec_t
     return GPT2_OK;
 }
 
+// The buffers of steps whose rows are nodes.
+int tree_alloc(gpt2_batch *m)
+{
+    gpt2_batch::Tree &tr = m->tree;
+    const int E = m->cfg.n_embd, R = kTcMaxRows;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += a256(bytes);
+        return o;
+    };
+    tr.ws_bytes = gpt2_op_verify_tree_workspace(m->max_batch, m->cfg.vocab_size);
+    const size_t oq = take(size_t(R) * E * 4), oo = take(size_t(R) * E * 4), of = take((R + 1) * 4), oc = take(R * 4);
+    const size_t oe = take((R + 1) * 4), ow = take(R * 4), ot = take(R * 4), op = take(R * 4), om = take(R * 8);
+    const size_t o1 = take(R * 8), oh = take(size_t(R) * GPT2_MAX_NODES * 4), on = take(R * 4), ox = take(R * 4);
+    const size_t os = take(tr.ws_bytes), kv = m->kv_int8 ? size_t(R) * E * 4 : 0, ok = take(kv), ov = take(kv);
+    uint8_t *mem = nullptr;
+    BTRY(cudaMalloc(&mem, off));
+    std::vector<int32_t> each(R + 1);
+    std::vector<uint64_t> one(R, 1);
+    for (int b = 0; b <= R; ++b) each[b] = b;
+    cudaError_t e = cudaMemset(mem, 0, off);
+    if (e == cudaSuccess) e = cudaMemcpy(mem + oe, each.data(), each.size() * 4, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaMemcpy(mem + o1, one.data(), one.size() * 8, cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) {
+        cudaFree(mem);
+        return cuda_rc(e);
+    }
+    tr.mem = mem;
+    tr.q = reinterpret_cast<float *>(mem + oq);
+    tr.out = reinterpret_cast<float *>(mem + oo);
+    tr.first = reinterpret_cast<int32_t *>(mem + of);
+    tr.cached = reinterpret_cast<int32_t *>(mem + oc);
+    tr.each = reinterpret_cast<int32_t *>(mem + oe);
+    tr.crow = reinterpret_cast<int32_t *>(mem + ow);
+    tr.tokens = reinterpret_cast<int32_t *>(mem + ot);
+    tr.parents = reinterpret_cast<int32_t *>(mem + op);
+    tr.mask = reinterpret_cast<uint64_t *>(mem + om);
+    tr.one = reinterpret_cast<uint64_t *>(mem + o1);
+    tr.path = reinterpret_cast<int32_t *>(mem + oh);
+    tr.n_path = reinterpret_cast<int32_t *>(mem + on);
+    tr.next = reinterpret_cast<int32_t *>(mem + ox);
+    tr.ws = mem + os;
+    tr.k = m->kv_int8 ? reinterpret_cast<float *>(mem + ok) : nullptr;
+    tr.v = m->kv_int8 ? reinterpret_cast<float *>(mem + ov) : nullptr;
+    return GPT2_OK;
+}
+
 // The decode step's graph, and for a batched model (one cache slot per
 // sequence) the prompt step's.
 int build_step_graph(gpt2_batch *m)
@@ -1004,6 +1086,7 @@ struct EngineSrc {
     bool borrow = false;
     float *kc = nullptr, *vc = nullptr;   // an fp32 cache of the caller's
     bool kv_bf16 = false;                 // an own cache of bf16 k, v (RNE)
+    bool kv_int8 = false;                 // an own cache of int8 k, v and scales
     int planes = 1, slots = 1, rows = kTcMaxRows;
     // in place of w[] / head: write the fp32 [out][in] matrix (or the [V][E]
     // head) into dst
@@ -1038,6 +1121,7 @@ int engine_build(gpt2_batch *m, const gpt2_config &cfg, const EngineSrc &src, cu
     m->slots = src.slots;
     m->own_cache = src.kc == nullptr;
     m->kv_bf16 = src.kv_bf16 && m->own_cache;
+    m->kv_int8 = src.kv_int8 && m->own_cache;
     m->stream = stream;
     m->num_sms = sms;
     m->cached.assign(src.rows, 0);
@@ -1069,8 +1153,9 @@ int engine_build(gpt2_batch *m, const gpt2_config &cfg, const EngineSrc &src, cu
     const size_t arena_bytes = off;
     // ---- work ----
     off = 0;
-    const size_t kv = m->own_cache ? size_t(L) * src.slots * H * P * D * (m->kv_bf16 ? 2 : 4) : 0;
+    const size_t kv = m->own_cache ? size_t(L) * src.slots * H * P * D * (m->kv_int8 ? 1 : m->kv_bf16 ? 2 : 4) : 0;
     const size_t o_k = m->own_cache ? take(kv) : 0, o_v = m->own_cache ? take(kv) : 0;
+    const size_t sc = m->kv_int8 ? size_t(L) * src.slots * H * P * 4 : 0, o_ks = take(sc), o_vs = take(sc);
     const size_t o_x = take(size_t(kTcMaxRows) * E * 4);
     const size_t o_be = take(size_t(2 * kTcMaxRows) * E * 2), o_ba = take(size_t(2 * kTcMaxRows) * E * 2);
     const size_t o_bf = take(size_t(2 * kTcMaxRows) * F * 2);
@@ -1167,6 +1252,12 @@ int engine_build(gpt2_batch *m, const gpt2_config &cfg, const EngineSrc &src, cu
     m->head_lin.cps = E / kTcK;
     m->kc = m->own_cache ? static_cast<void *>(W + o_k) : static_cast<void *>(src.kc);
     m->vc = m->own_cache ? static_cast<void *>(W + o_v) : static_cast<void *>(src.vc);
+    if (m->kv_int8) {
+        m->kscale = reinterpret_cast<float *>(W + o_ks);
+        m->vscale = reinterpret_cast<float *>(W + o_vs);
+        rc = tree_alloc(m);
+        if (rc != GPT2_OK) goto done;
+    }
     m->x = reinterpret_cast<float *>(W + o_x);
     m->b_e = reinterpret_cast<__nv_bfloat16 *>(W + o_be);
     m->b_a = reinterpret_cast<__nv_bfloat16 *>(W + o_ba);
@@ -1314,7 +1405,7 @@ int gpt2_create_batch_ex(const gpt2_config *cfg, const gpt2_weights *w, int32_t 
 {
     if (!out) return GPT2_ERR_INVALID_ARG;
     *out = nullptr;
-    if (flags & ~uint32_t(GPT2_BATCH_KV_BF16)) return GPT2_ERR_INVALID_ARG;
+    if (flags != 0 && flags != GPT2_BATCH_KV_BF16 && flags != GPT2_BATCH_KV_INT8) return GPT2_ERR_INVALID_ARG;
     if (!cfg || !w || !w->layers) return GPT2_ERR_INVALID_ARG;
     if (wdtype != GPT2_BF16) return GPT2_ERR_INVALID_ARG;
     if (max_batch < 1 || max_batch > kTcMaxRows) return GPT2_ERR_INVALID_ARG;
@@ -1353,7 +1444,8 @@ int gpt2_create_batch_ex(const gpt2_config *cfg, const gpt2_weights *w, int32_t 
     src.planes = 1;
     src.slots = max_batch;
     src.rows = max_batch;
-    src.kv_bf16 = (flags & GPT2_BATCH_KV_BF16) != 0;
+    src.kv_bf16 = flags == GPT2_BATCH_KV_BF16;
+    src.kv_int8 = flags == GPT2_BATCH_KV_INT8;
     gpt2_batch *m = new (std::nothrow) gpt2_batch();
     if (!m) return GPT2_ERR_OUT_OF_MEMORY;
     rc = engine_build(m, *cfg, src, static_cast<cudaStream_t>(stream), prop.multiProcessorCount);
@@ -1431,6 +1523,18 @@ int gpt2_prefill_batch(gpt2_batch *m, const int32_t *ids, const int32_t *lens, i
         BTRY(cudaMemcpyAsync(m->pos, p.data(), p.size() * 4, cudaMemcpyHostToDevice, m->stream));
         BTRY(cudaMemcpyAsync(m->slot_of, sl.data(), sl.size() * 4, cudaMemcpyHostToDevice, m->stream));
         BTRY(upload_order(m, p.data(), m->stream));
+        if (m->kv_int8) {   // the rows as chains of nodes, one per sequence
+            std::vector<int32_t> first(kTcMaxRows + 1, 0), from(kTcMaxRows, 0);
+            std::vector<uint64_t> mask(kTcMaxRows, 0);
+            for (int i = r - 1; i >= 0; --i) from[sl[i]] = p[i];
+            for (int i = 0; i < r; ++i) {
+                mask[i] = ~uint64_t(0) >> (63 - (p[i] - from[sl[i]]));
+                for (int b = sl[i] + 1; b <= kTcMaxRows; ++b) first[b] = i + 1;
+            }
+            BTRY(cudaMemcpyAsync(m->tree.first, first.data(), first.size() * 4, cudaMemcpyHostToDevice, m->stream));
+            BTRY(cudaMemcpyAsync(m->tree.cached, from.data(), from.size() * 4, cudaMemcpyHostToDevice, m->stream));
+            BTRY(cudaMemcpyAsync(m->tree.mask, mask.data(), mask.size() * 8, cudaMemcpyHostToDevice, m->stream));
+        }
         BTRY(cudaGraphLaunch(m->exec_p, m->stream));
         m->launches += m->kernels_per_prompt_step;
         r = 0;
@@ -1498,7 +1602,7 @@ int gpt2_decode_tree_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *
     if (!m || !tokens || !parents || !n_nodes || n < 1 || n > m->max_batch) return GPT2_ERR_INVALID_ARG;
     const gpt2_config &c = m->cfg;
     const int R = kTcMaxRows;
-    std::vector<int32_t> t(R, 0), par(R, 0), p(R, -1), sl(R, 0), crow(R, 0), first(R + 1, 0), cached(R, 0);
+    std::vector<int32_t> t(R, 0), par(R, 0), p(R, -1), sl(R, 0), crow(R, -1), first(R + 1, 0), cached(R, 0);
     std::vector<uint64_t> mask(R, 0);
     int r = 0, most = 0;
     for (int b = 0; b < n; ++b) {
@@ -1524,41 +1628,8 @@ int gpt2_decode_tree_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *
     for (int b = n; b < R; ++b) first[b + 1] = r;
     gpt2_batch::Tree &tr = m->tree;
     if (!tr.mem) {
-        const int E = c.n_embd;
-        size_t off = 0;
-        auto take = [&](size_t bytes) {
-            const size_t o = off;
-            off += a256(bytes);
-            return o;
-        };
-        tr.ws_bytes = gpt2_op_verify_tree_workspace(m->max_batch, c.vocab_size);
-        const size_t oq = take(size_t(R) * E * 4), oo = take(size_t(R) * E * 4), of = take((R + 1) * 4), oc = take(R * 4);
-        const size_t oi = take(R * 4), ow = take(R * 4), ot = take(R * 4), op = take(R * 4), om = take(R * 8);
-        const size_t oh = take(size_t(R) * GPT2_MAX_NODES * 4), on = take(R * 4), ox = take(R * 4), os = take(tr.ws_bytes);
-        uint8_t *mem = nullptr;
-        BTRY(cudaMalloc(&mem, off));
-        std::vector<int32_t> ident(R);
-        for (int b = 0; b < R; ++b) ident[b] = b;
-        cudaError_t e = cudaMemset(mem, 0, off);
-        if (e == cudaSuccess) e = cudaMemcpy(mem + oi, ident.data(), R * 4, cudaMemcpyHostToDevice);
-        if (e != cudaSuccess) {
-            cudaFree(mem);
-            return cuda_rc(e);
-        }
-        tr.mem = mem;
-        tr.q = reinterpret_cast<float *>(mem + oq);
-        tr.out = reinterpret_cast<float *>(mem + oo);
-        tr.first = reinterpret_cast<int32_t *>(mem + of);
-        tr.cached = reinterpret_cast<int32_t *>(mem + oc);
-        tr.ident = reinterpret_cast<int32_t *>(mem + oi);
-        tr.crow = reinterpret_cast<int32_t *>(mem + ow);
-        tr.tokens = reinterpret_cast<int32_t *>(mem + ot);
-        tr.parents = reinterpret_cast<int32_t *>(mem + op);
-        tr.mask = reinterpret_cast<uint64_t *>(mem + om);
-        tr.path = reinterpret_cast<int32_t *>(mem + oh);
-        tr.n_path = reinterpret_cast<int32_t *>(mem + on);
-        tr.next = reinterpret_cast<int32_t *>(mem + ox);
-        tr.ws = mem + os;
+        const int rc = tree_alloc(m);
+        if (rc != GPT2_OK) return rc;
     }
     const int k = most <= 16 ? 0 : 1;
     if (!tr.exec[k]) {
@@ -1593,15 +1664,8 @@ int gpt2_accept_tree_batch(gpt2_batch *m, float temperature, const float *draft_
                                  temperature, draft_probs, u_accept, u_draw, tr.path, tr.n_path, tr.next, tr.ws,
                                  tr.ws_bytes, m->stream);
     if (rc != GPT2_OK) return rc;
-    gpt2_kv kv{};
-    kv.k = m->kc;
-    kv.v = m->vc;
-    kv.dtype = m->kv_bf16 ? GPT2_BF16 : GPT2_F32;
-    kv.n_slots = m->slots;
-    kv.n_head = c.n_head;
-    kv.n_positions = c.n_positions;
-    kv.head_dim = c.n_embd / c.n_head;
-    rc = gpt2_op_kv_commit(&kv, c.n_layer, tr.ident, tr.cached, tr.path, tr.n_path, n, GPT2_MAX_NODES, m->stream);
+    const gpt2_kv kv = layer_kv(m, 0);
+    rc = gpt2_op_kv_commit(&kv, c.n_layer, tr.each, tr.cached, tr.path, tr.n_path, n, GPT2_MAX_NODES, m->stream);
     if (rc != GPT2_OK) return rc;
     k_b_set_next<<<1, kTcMaxRows, 0, m->stream>>>(m->next_tok, tr.next, tr.n_path, n);
     BTRY(cudaGetLastError());
@@ -1662,10 +1726,12 @@ int gpt2_export_kv_batch(gpt2_batch *m, int32_t layer, int32_t seq, int32_t n_ro
     if (!m || layer < 0 || layer >= m->cfg.n_layer || seq < 0 || seq >= m->max_batch) return GPT2_ERR_INVALID_ARG;
     const int H = m->cfg.n_head, D = m->cfg.n_embd / H, P = m->cfg.n_positions;
     if (n_rows < 0 || n_rows > P) return GPT2_ERR_INVALID_ARG;
-    const size_t es = m->kv_bf16 ? 2 : 4, row_elems = size_t(n_rows) * D;
+    const size_t es = m->kv_int8 ? 1 : m->kv_bf16 ? 2 : 4, row_elems = size_t(n_rows) * D;
     // bf16 rows are widened to fp32 on the host on their way out
     std::vector<uint16_t> tmp16(m->kv_bf16 ? row_elems : 0);
-    std::vector<float> tmp32(m->kv_bf16 ? row_elems : 0);
+    std::vector<float> tmp32(m->kv_bf16 || m->kv_int8 ? row_elems : 0);
+    std::vector<int8_t> tmp8(m->kv_int8 ? row_elems : 0);
+    std::vector<float> scale(m->kv_int8 ? n_rows : 0);
     for (int h = 0; h < H; ++h) {
         const size_t src = ((size_t(layer) * m->max_batch + seq) * H + h) * P * D * es;
         for (int part = 0; part < 2; ++part) {
@@ -1673,6 +1739,15 @@ int gpt2_export_kv_batch(gpt2_batch *m, int32_t layer, int32_t seq, int32_t n_ro
             if (!dst) continue;
             const uint8_t *from = static_cast<const uint8_t *>(part == 0 ? m->kc : m->vc) + src;
             dst += size_t(h) * row_elems;
+            if (m->kv_int8) {
+                const float *sc = (part == 0 ? m->kscale : m->vscale) + src / D;
+                BTRY(cudaMemcpyAsync(tmp8.data(), from, row_elems, cudaMemcpyDeviceToHost, m->stream));
+                BTRY(cudaMemcpyAsync(scale.data(), sc, size_t(n_rows) * 4, cudaMemcpyDeviceToHost, m->stream));
+                BTRY(cudaStreamSynchronize(m->stream));
+                for (size_t i = 0; i < row_elems; ++i) tmp32[i] = float(tmp8[i]) * scale[i / D];
+                BTRY(cudaMemcpy(dst, tmp32.data(), row_elems * 4, cudaMemcpyDefault));
+                continue;
+            }
             if (!m->kv_bf16) {
                 BTRY(cudaMemcpyAsync(dst, from, row_elems * 4, cudaMemcpyDefault, m->stream));
                 continue;
