@@ -386,6 +386,44 @@ def test_what_is_not_seen_does_not_enter(qt, ct):
         assert not torch.isfinite(hit.float()).any()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("c,n,K", [(60, 24, 200), (1500, 24, 2), (1020, 40, 1)])
+def test_what_is_not_seen_does_not_enter_many_rows(dtype, D, c, n, K):
+    """The same with more than 16 query rows: units within one CTA's share
+    (200 heads of one tile) and units that many CTAs share."""
+    import torch
+    rng = np.random.default_rng(c + n)
+    P = c + n + 30
+    kc, _ = make_cache(rng, dtype, 1, K, P, D)
+    vc, _ = make_cache(rng, dtype, 1, K, P, D)
+    mask = binding.tree_masks(random_tree(rng, n, 6))
+    q = torch.from_numpy(rng.standard_normal((n, K, D)).astype(np.float32)).to(dt(dtype)).cuda()
+    args = (i32([0]), i32([c]), i32([0, n]), torch.from_numpy(mask).cuda(), n)
+    h = K - 1                                     # (heads alike: the reference for the poisoned one)
+    want, tol = attend64(q[:, h:], kc[:, h:], vc[:, h:], None, None, [0], [c], [0, n], mask, 1 / math.sqrt(D))
+    kc[:, :, c + n:] = math.nan
+    vc[:, :, c + n:] = math.inf
+    base = binding.op_tree_attention(q, kc, vc, *args)
+    check_attention(base[:, h:], want, tol)
+    node = 4
+    sees = np.array([(int(m) >> node) & 1 for m in mask], bool)
+    assert sees.any() and not sees.all()
+    for t, x in [(vc, math.nan), (vc, math.inf), (vc, -math.inf), (kc, math.nan)]:
+        at = (0, h, c + node, 17)
+        old = t[at].clone()
+        t[at] = x
+        got = binding.op_tree_attention(q, kc, vc, *args)
+        t[at] = old
+        assert torch.equal(got[:, :h], base[:, :h])
+        check_attention(got[~sees][:, h:], want[~sees], tol[~sees])
+        hit = got[sees][:, h] if t is kc else got[sees][:, h, 17]
+        assert not torch.isfinite(hit.float()).any()
+        if t is vc:
+            rest = [d for d in range(D) if d != 17]
+            check_attention(got[sees][:, h:][..., rest], want[sees][..., rest], tol[sees][..., rest])
+
+
 def test_wide_value_scales():
     """int8 value scales that differ by 2^40 within a sequence, rising and
     falling over the tiles, zero among them."""

@@ -46,27 +46,40 @@ constexpr uint32_t kBoxB = kRowsT * 128;         // one TMA box: 128 rows of 64 
 constexpr float kRaise = 8.f;                    // log2 of the weight that raises a maximum
 constexpr float kNone = -1e30f;                  // the maximum of a row that has seen nothing
 
-constexpr int kC = 16;                           // query rows of a softmax thread
 
+// 64 dimensions: two CTAs per SM, which overlap one another's softmax, products
+// and changes of unit (one CTA of 16 softmax warps took 2,400 cycles a tile, two
+// of 8 take about 1,700 together); the sums of the weights come from the matrix
+// units as well (see kOnes).  128 dimensions: one CTA, a tile's loads are twice
+// as long.
 template <int D, int N>
 struct Shape {
+    static constexpr int kPerSM = D == 64 ? 2 : 1;
+    static constexpr int kC = D == 64 ? N / 2 : 16;              // query rows of a softmax thread
     static constexpr int kSoft = 4 * N / kC;                     // softmax warps: 128 cache rows x N / kC
-    static constexpr int kThreads = (kSoft + 3) * 32;
+    static constexpr int kMmaWarps = D == 64 ? 1 : 2;
+    static constexpr int kThreads = (kSoft + 1 + kMmaWarps) * 32;
     static constexpr int kBoxes = D / 64;
     static constexpr uint32_t kTileB = kBoxes * kBoxB;           // K or V of a tile
-    static constexpr int kPBufs = D == 128 && N == 64 ? 1 : 2;   // buffers of weights
+    static constexpr int kPBufs = D == 128 && N == 32 ? 2 : 1;   // buffers of weights
+    static constexpr int kQBufs = D == 64 ? 1 : 2;               // of query rows: the next unit's come early
+    // 64 dimensions leave half of the weighted sum's 128 rows free: there V's tile
+    // is followed by a block of ones, and those rows are the sums of the weights.
+    static constexpr bool kOnes = D == 64;
     // Rings of K and of V tiles.  Two, because a barrier may only be waited on by
     // who has seen its every phase (a wait names a phase by its parity): in one
     // ring of an odd size a place holds K and V in turn, and the warp that runs
     // ahead mistakes the phase before last for its own.
-    static constexpr int kKRing = D == 128 ? 2 : N == 64 ? 4 : 5, kVRing = kKRing + 1, kStages = kKRing + kVRing;
+    static constexpr int kKRing = 2, kVRing = N == 64 ? 2 : 3;
+    static constexpr int kStages = kKRing + kVRing;
     static_assert(kVRing >= kPBufs, "the softmax warps wait for V too");
     static constexpr uint32_t kPB = kRowsT * N * 2;              // one part of the weights
     static constexpr uint32_t kQB = N * 128 * kBoxes;
     static constexpr uint32_t kOffP = kStages * kTileB, kOffQ = kOffP + kPBufs * 2 * kPB;
-    static constexpr uint32_t kBytes = kOffQ + kQB + 1024;       // + alignment
+    static constexpr uint32_t kOffOnes = kOffQ + kQBufs * kQB;   // 16 rows of 64 ones
+    static constexpr uint32_t kBytes = kOffOnes + (kOnes ? 2048 : 0) + 1024;   // + alignment
     static constexpr uint32_t kCols = 4 * N;                     // TMEM: S twice, O of the first parts, of the second
-    static_assert(kBytes <= 222 * 1024, "shared memory of an SM");
+    static_assert(kBytes <= (kPerSM == 2 ? 108 : 220) * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity)
@@ -214,6 +227,17 @@ __device__ __forceinline__ void split_pair(float2 p, uint32_t &hi, uint32_t &lo)
     }
 }
 
+// Asynchronous copies into shared memory; bytes past `have` are zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t have)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Barrier of the softmax warps, alone (1) and with a vote (2).
 template <int THREADS>
 __device__ __forceinline__ void soft_sync()
@@ -353,19 +377,21 @@ __device__ __forceinline__ int64_t out_row(const TreeArgs &a, const Sequence &s,
 }
 
 template <bool BF, int D, int N>
-__global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
     k_tree_tc(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
               const __grid_constant__ TreeArgs a, Part<D, N> *parts, Head *heads)
 {
     using S = Shape<D, N>;
     using T16 = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-    constexpr int kSt = S::kStages, kKR = S::kKRing, kVR = S::kVRing, kPB = S::kPBufs, kSoft = S::kSoft, kSync = kSoft * 32, C = kC;
+    constexpr int kPair = 1;                        // tiles of a softmax step
+    constexpr int kSt = S::kStages, kKR = S::kKRing, kVR = S::kVRing, kPB = S::kPBufs, kSoft = S::kSoft, kSync = kSoft * 32, C = S::kC;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full[kSt], empty[kSt], sfull[2], sfree[2], pfull[kPB], pfree[kPB], qfull, odone;
     __shared__ uint32_t tmem_slot;
     __shared__ __align__(16) float sm_m[N], sm_alpha[N];   // minus the maxima (log2); what a raise leaves of the sums
     __shared__ float sm_inv[N], sm_part[4][N];
     __shared__ int64_t sm_out[N];
+    __shared__ uint64_t sm_mask[2][N];           // the unit's query rows' masks, and the next unit's
     __shared__ uint64_t sm_see[GPT2_MAX_NODES];  // which query rows see a node
     __shared__ long long red[S::kThreads / 32];
     __shared__ int start_b, start_u, start_t;
@@ -380,7 +406,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1), mbar_init(&sfree[i], kSoft);
         for (int i = 0; i < kPB; ++i) mbar_init(&pfull[i], kSoft), mbar_init(&pfree[i], 1);
         mbar_init(&qfull, kSoft);
-        mbar_init(&odone, 2);
+        mbar_init(&odone, S::kMmaWarps);
         mbar_init_fence();
         sm_bad = 0;
         sm_fail = 0;
@@ -390,6 +416,12 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
                      "r"(S::kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if constexpr (S::kOnes) {
+        constexpr uint32_t one = BF ? 0x3f803f80u : 0x3c003c00u;
+        for (int i = tid; i < 2048 / 16; i += S::kThreads)
+            *reinterpret_cast<uint4 *>(sm + S::kOffOnes + i * 16) = make_uint4(one, one, one, one);
+        fence_async();
     }
     // this CTA's run of the list
     const long long all = tiles_before(a, a.n_seqs, N, red);
@@ -469,49 +501,66 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
             }
         }
     } else if (warp > kSoft) {
-        // one warp for the scores, one for the weighted sums: a warp issues an
-        // MMA in about 85 cycles and tests a barrier in 100 to 200, so that one
-        // warp for both took 2,800 cycles a tile
-        const bool scores = warp == kSoft + 1, leader = lane == 0;
+        // A warp issues an MMA in about 85 cycles and tests a barrier in 100 to
+        // 200, whatever the MMA's size: with a tile in 1,400 cycles or more, one
+        // warp per CTA of two, or one for the scores and one for the weighted sums.
+        const bool leader = lane == 0;
         constexpr uint32_t kIS = instruction(N, BF, false), kIO = instruction(2 * N, BF, true);
         constexpr uint32_t kHiK = desc_hi(1024, 2), kHiP = desc_hi(kRowsT * 16, 0);
         auto wait = [&](uint64_t *bar, uint32_t phase) {
             if (ok) ok = __all_sync(0xffffffffu, wait_phase(bar, phase));
         };
-        const int first_place = scores ? 0 : kKR, end_place = scores ? kKR : kSt;
-        int st = first_place;                    // ring place of the next K or V, and how often it was used
-        uint32_t use = 0, unit = 0;
+        int kst = 0, vst = kKR;                  // ring places of the next K and V, and how often they were used
+        uint32_t kuse = 0, vuse = 0, unit = 0;
+        auto scores = [&](int g) {
+            wait(&full[kst], kuse);
+            if (g >= 2) wait(&sfree[g & 1], uint32_t(g / 2 - 1));
+            if (!ok) return;
+            fence_after();
+            const uint32_t k = desc_lo(base + kst * S::kTileB, 16);
+            const uint32_t qd = desc_lo(base + S::kOffQ + ((unit - 1) % S::kQBufs) * S::kQB, 16);
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+                mma(tmem + (g & 1) * N, k + (s / 4) * (kBoxB >> 4) + (s % 4) * 2, kHiK,
+                    qd + (s / 4) * (N * 128 >> 4) + (s % 4) * 2, kHiK, kIS, s > 0, leader);
+            commit(&empty[kst], leader);
+            commit(&sfull[g & 1], leader);
+            if (++kst == kKR) kst = 0, ++kuse;
+        };
+        auto weighted = [&](int g, bool first) {   // (the first of a unit starts O anew)
+            const int pb = g % kPB;
+            wait(&full[vst], vuse);
+            wait(&pfull[pb], uint32_t(g / kPB));
+            if (!ok) return;
+            fence_after();
+            const uint32_t at = base + vst * S::kTileB, v = desc_lo(at, S::kOnes ? base + S::kOffOnes - at : kBoxB);
+            const uint32_t p = desc_lo(base + S::kOffP + pb * 2 * S::kPB, 128);
+            // (the second parts follow the first, as further columns; the block of
+            // ones stays where it is: its distance shrinks with every step)
+#pragma unroll
+            for (int s = 0; s < kRowsT / 16; ++s)
+                mma(t_o, v + s * (2048 >> 4) - (S::kOnes ? uint32_t(s * (2048 >> 4)) << 16 : 0u), kHiK,
+                    p + s * (256 >> 4), kHiP, kIO, !first || s > 0, leader);
+            commit(&empty[vst], leader);
+            commit(&pfree[pb], leader);
+            if (++vst == kSt) vst = kKR, ++vuse;
+        };
+        const bool do_scores = S::kMmaWarps == 1 || warp == kSoft + 1;
         if (some) do {
             const int n = __shfl_sync(0xffffffffu, w.n, 0);
-            if (scores) wait(&qfull, unit);
+            if (do_scores) wait(&qfull, unit);
             ++unit;
-            for (int t = 0; t < n && ok; ++t, ++g) {
-                wait(&full[st], use);
-                if (scores) {
-                    if (g >= 2) wait(&sfree[g & 1], uint32_t(g / 2 - 1));
-                    if (!ok) break;
-                    fence_after();
-                    const uint32_t k = desc_lo(base + st * S::kTileB, 16), qd = desc_lo(base + S::kOffQ, 16);
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma(tmem + (g & 1) * N, k + (s / 4) * (kBoxB >> 4) + (s % 4) * 2, kHiK,
-                            qd + (s / 4) * (N * 128 >> 4) + (s % 4) * 2, kHiK, kIS, s > 0, leader);
-                    commit(&empty[st], leader);
-                    commit(&sfull[g & 1], leader);
-                } else {
-                    const int pb = g % kPB;
-                    wait(&pfull[pb], uint32_t(g / kPB));
-                    if (!ok) break;
-                    fence_after();
-                    const uint32_t v = desc_lo(base + st * S::kTileB, D == 64 ? 0 : kBoxB);
-                    const uint32_t p = desc_lo(base + S::kOffP + pb * 2 * S::kPB, 128);
-#pragma unroll
-                    for (int s = 0; s < kRowsT / 16; ++s)   // (the second parts follow the first, as further columns)
-                        mma(t_o, v + s * (2048 >> 4), kHiK, p + s * (256 >> 4), kHiP, kIO, t > 0 || s > 0, leader);
-                    commit(&empty[st], leader);
-                    commit(&pfree[pb], leader);
+            if constexpr (S::kMmaWarps == 1) {
+                for (int t = 0; t < n && ok; ++t, ++g) {
+                    scores(g);
+                    if (t > 0) weighted(g - 1, t == 1);
                 }
-                if (++st == end_place) st = first_place, ++use;
+                weighted(g - 1, n == 1);
+            } else {
+                for (int t = 0; t < n && ok; ++t, ++g) {
+                    if (do_scores) scores(g);
+                    else weighted(g, t == 0);
+                }
             }
         } while (ok && w.next(a, N));
         if (!ok && leader) sm_fail = 1;
@@ -525,44 +574,48 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
         auto wait = [&](uint64_t *bar, int phase) {
             if (ok) ok = __all_sync(0xffffffffu, wait_phase(bar, uint32_t(phase)));
         };
-        // a unit's query rows as the B operand: K-major, 128-byte swizzle; rows
-        // past the last are zero (the products that read the last unit's are
-        // complete when its scores have been read)
-        auto load_q = [&](const Walk &w) {
+        // a unit's query rows as the B operand (K-major, 128-byte swizzle; rows
+        // past the last are zero) and their masks, on their way
+        auto fetch_q = [&](const Walk &w, int buf) {
             const int kvh = w.u % a.kv.n_head, row0 = w.u / a.kv.n_head * N;
             for (int i = tid; i < N * (D / 8); i += kSync) {
                 const int r = i / (D / 8), piece = i % (D / 8);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (row0 + r < w.s.rows) {
-                    const int node = (row0 + r) / a.group, h = kvh * a.group + (row0 + r) % a.group;
-                    x = *reinterpret_cast<const uint4 *>(static_cast<const T16 *>(a.q) +
-                                                         size_t(w.s.f0 + node) * a.q_stride + size_t(h) * D + piece * 8);
-                }
-                *reinterpret_cast<uint4 *>(sm + S::kOffQ + (piece / 8) * (N * 128) + r * 128 +
-                                           ((piece % 8) ^ (r & 7)) * 16) = x;
+                const bool ok = row0 + r < w.s.rows;
+                const int rr = ok ? row0 + r : 0, node = rr / a.group, h = kvh * a.group + rr % a.group;
+                copy16(base + S::kOffQ + buf * S::kQB + (piece / 8) * (N * 128) + r * 128 + ((piece % 8) ^ (r & 7)) * 16,
+                       static_cast<const T16 *>(a.q) + size_t(w.s.f0 + node) * a.q_stride + size_t(h) * D + piece * 8,
+                       ok ? 16 : 0);
             }
+            if (tid < N) {
+                const bool ok = row0 + tid < w.s.rows;
+                copy8(smem_addr(&sm_mask[buf][tid]), a.mask + w.s.f0 + (ok ? (row0 + tid) / a.group : 0), ok ? 8 : 0);
+            }
+        };
+        auto have_q = [&]() {                    // fetched rows are there: the scores may begin
+            copies_landed();
             fence_async();
             __syncwarp();
             if (lane == 0) arrive(&qfull);
         };
-        bool more = some, first_unit = true;
         if (tid < 2) heads[2 * blockIdx.x + tid].n = 0;
-        if (some) load_q(w);
-        while (more) {
+        bool more = some, first_unit = true;
+        int buf = 0;
+        if (some) {
+            fetch_q(w, 0);
+            have_q();
+        }
+        for (; more; buf = (buf + 1) % S::kQBufs) {
             const Sequence sq = w.s;
             const int unit = w.u, t0 = w.t0, n = w.n, w_b = w.b;
             const int kvh = unit % a.kv.n_head, row0 = unit / a.kv.n_head * N, rows = min(sq.rows - row0, N);
             // who sees node j: a lane per query row
             const uint64_t valid = rows >= 64 ? ~0ull : (1ull << rows) - 1;
             bool partial = false;
-            soft_sync<kSync>();                  // the last unit's masks, maxima and sums are no longer read
+            soft_sync<kSync>();                  // masks are there; the last unit's maxima and sums are no longer read
             if ((t0 + n) * kRowsT > sq.pre) {
                 uint64_t mask[N / 32];
 #pragma unroll
-                for (int k = 0; k < N / 32; ++k) {
-                    const int r = k * 32 + lane;
-                    mask[k] = r < rows ? a.mask[sq.f0 + (row0 + r) / a.group] : 0ull;
-                }
+                for (int k = 0; k < N / 32; ++k) mask[k] = sm_mask[buf][k * 32 + lane];
                 for (int j = warp; j < sq.nodes; j += kSoft) {
                     uint64_t see = 0;
 #pragma unroll
@@ -575,46 +628,65 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
             if (tid < N) sm_m[tid] = -kNone;
             if (tid == 0) sm_bad = 0;
             partial = soft_any<kSync>(partial);
-            float2 l[C / 2];
+            float2 l[C / 2];                     // (not where the matrix units sum the weights)
 #pragma unroll
             for (int i = 0; i < C / 2; ++i) l[i] = make_float2(0.f, 0.f);
 
-            for (int t = 0; t < n; ++t, ++g) {
-                const int j = (t0 + t) * kRowsT + key;                 // this thread's cache row
-                const bool tail = (t0 + t + 1) * kRowsT > sq.pre;
-                const uint64_t see = !tail || j < sq.pre ? ~0ull : j < sq.total ? sm_see[j - sq.pre] >> c0 : 0ull;
-                const uint32_t t_s = tmem + (g & 1) * N + lanes + c0;
-                wait(&sfull[g & 1], g / 2);
+            for (int t = 0; t < n; t += kPair) {
+                const int np = min(kPair, n - t);                      // tiles of this step
+                // this thread's cache rows, and which of its 16 query rows see them
+                uint32_t see[kPair];
+                float d[kPair][C];                                     // scores less their rows' maxima, in log2
+#pragma unroll
+                for (int x = 0; x < kPair; ++x) {
+                    const int j = (t0 + t + x) * kRowsT + key;
+                    see[x] = x >= np ? 0u : j < sq.pre ? ~0u : j < sq.total ? uint32_t(sm_see[j - sq.pre] >> c0) : 0u;
+                    if (x < np) wait(&sfull[(g + x) & 1], (g + x) / 2);
+                }
                 fence_after();
-                float d[C];                                            // scores less their rows' maxima, in log2
+                const bool tail = (t0 + t + np) * kRowsT > sq.pre;
+                auto t_s = [&](int x) { return tmem + ((g + x) & 1) * N + lanes + c0; };
                 auto distances = [&]() {
                     float most = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < C; i += 16) tmem_load16(t_s + i, d + i);
+                    for (int x = 0; x < kPair; ++x) {
+                        if (x < np) {
 #pragma unroll
-                    for (int i = 0; i < C; i += 4) {
-                        const float4 m = *reinterpret_cast<const float4 *>(&sm_m[c0 + i]);
-                        const float2 x = fma2(make_float2(d[i], d[i + 1]), scale, make_float2(m.x, m.y));
-                        const float2 y = fma2(make_float2(d[i + 2], d[i + 3]), scale, make_float2(m.z, m.w));
-                        d[i] = x.x, d[i + 1] = x.y, d[i + 2] = y.x, d[i + 3] = y.y;
+                            for (int i = 0; i < C; i += 16) tmem_load16(t_s(x) + i, d[x] + i);
+#pragma unroll
+                            for (int i = 0; i < C; i += 4) {
+                                const float4 m = *reinterpret_cast<const float4 *>(&sm_m[c0 + i]);
+                                const float2 p = fma2(make_float2(d[x][i], d[x][i + 1]), scale, make_float2(m.x, m.y));
+                                const float2 q = fma2(make_float2(d[x][i + 2], d[x][i + 3]), scale, make_float2(m.z, m.w));
+                                d[x][i] = p.x, d[x][i + 1] = p.y, d[x][i + 2] = q.x, d[x][i + 3] = q.y;
+                            }
+                            if (see[x] != ~0u) {
+#pragma unroll
+                                for (int i = 0; i < C; ++i)
+                                    if (!(see[x] >> i & 1)) d[x][i] = -INFINITY;
+                            }
+#pragma unroll
+                            for (int i = 0; i < C; ++i) most = fmaxf(most, d[x][i]);
+                        }
                     }
-                    if (see != ~0ull) {
-#pragma unroll
-                        for (int i = 0; i < C; ++i)
-                            if (!(see >> i & 1)) d[i] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int i = 0; i < C; ++i) most = fmaxf(most, d[i]);
                     return most;
                 };
                 if (soft_any<kSync>(distances() > kRaise)) {
-                    // raise the maxima: this tile's per query row, over the warp's
+                    // raise the maxima: these tiles' per query row, over the warp's
                     // cache rows and then the warps
+                    float top[C];
 #pragma unroll
-                    for (int i = 0; i < C; i += 16) tmem_load16(t_s + i, d + i);
+                    for (int i = 0; i < C; ++i) top[i] = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < C; ++i) d[i] = see >> i & 1 ? d[i] * a.scale_log2 : -INFINITY;
-                    const float mx = warp_columns(d, lane, [](float x, float y) { return fmaxf(x, y); });
+                    for (int x = 0; x < kPair; ++x)
+                        if (x < np) {
+#pragma unroll
+                            for (int i = 0; i < C; i += 16) tmem_load16(t_s(x) + i, d[x] + i);
+#pragma unroll
+                            for (int i = 0; i < C; ++i)
+                                if (see[x] >> i & 1) top[i] = fmaxf(top[i], d[x][i] * a.scale_log2);
+                        }
+                    const float mx = warp_columns(top, lane, [](float x, float y) { return fmaxf(x, y); });
                     if (lane % (32 / C) == 0) sm_part[q][c0 + lane / (32 / C)] = mx;
                     soft_sync<kSync>();
                     if (tid < N) {
@@ -628,118 +700,162 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1)
                     soft_sync<kSync>();
                     fence_after();
 #pragma unroll
-                    for (int i = 0; i < C / 2; ++i) l[i].x *= sm_alpha[c0 + 2 * i], l[i].y *= sm_alpha[c0 + 2 * i + 1];
+                    for (int i = 0; i < (S::kOnes ? 0 : C / 2); ++i) l[i].x *= sm_alpha[c0 + 2 * i], l[i].y *= sm_alpha[c0 + 2 * i + 1];
                     if (t > 0) {
+#pragma unroll 1
+                        for (int i = 0; i < 2 * C; i += 16) {
+                            const int col = i % C;
+                            const uint32_t at = t_o + (i / C) * N + lanes + c0 + col;
+                            float x[16];
+                            tmem_load16(at, x);
 #pragma unroll
-                        for (int i = 0; i < C; i += 16)
-                            for (int k = 0; k < 2; ++k) {
-                                float x[16];
-                                tmem_load16(t_o + k * N + lanes + c0 + i, x);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) x[e] *= sm_alpha[c0 + i + e];
-                                tmem_store16(t_o + k * N + lanes + c0 + i, x);
-                            }
+                            for (int e = 0; e < 16; ++e) x[e] *= sm_alpha[c0 + col + e];
+                            tmem_store16(at, x);
+                        }
                         tmem_wait_store();
                     }
                     distances();
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(&sfree[g & 1]);
-                if (g >= kPB) wait(&pfree[g % kPB], g / kPB - 1);
-                uint8_t *ph = sm + S::kOffP + (g % kPB) * 2 * S::kPB + key * 16 + c0 / 8 * (kRowsT * 16);
+                if (lane == 0)
+                    for (int x = 0; x < np; ++x) arrive(&sfree[(g + x) & 1]);
 #pragma unroll
-                for (int i = 0; i < C; i += 8) {
-                    uint32_t hi[4], lo[4];
+                for (int x = 0; x < kPair; ++x) {
+                    if (x >= np) break;
+                    const int gx = g + x, j = (t0 + t + x) * kRowsT + key;
+                    if (gx >= kPB) wait(&pfree[gx % kPB], gx / kPB - 1);
+                    uint8_t *ph = sm + S::kOffP + (gx % kPB) * 2 * S::kPB + key * 16 + c0 / 8 * (kRowsT * 16);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 p = make_float2(tree::exp2_approx(d[i + 2 * k]), tree::exp2_approx(d[i + 2 * k + 1]));
-                        l[i / 2 + k] = add2(l[i / 2 + k], p);
-                        split_pair<BF>(p, hi[k], lo[k]);
-                    }
-                    *reinterpret_cast<uint4 *>(ph + i / 8 * (kRowsT * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(ph + S::kPB + i / 8 * (kRowsT * 16)) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                // rows past the end hold anything, and a value that is not finite must
-                // not meet the weight zero of a row that does not see it: taken out
-                // here (by the first warps), the latter added at the end
-                if (tail && warp < 4 && (partial || (t0 + t + 1) * kRowsT > sq.total)) {
-                    const int st = kKR + g % kVR;
-                    wait(&full[st], g / kVR);
-                    if (j >= sq.total || (partial && j >= sq.pre)) {
-                        bool bad = false;
-                        for (int x = 0; x < S::kBoxes; ++x) {
-                            uint4 *v = reinterpret_cast<uint4 *>(sm + st * S::kTileB + x * kBoxB + key * 128);
-                            for (int k = 0; k < 8; ++k) {
-                                uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, gone = 0;
+                    for (int i = 0; i < C; i += 8) {
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t x16 =
-                                        j >= sq.total ? ~0u : tree::not_finite<BF ? tree::kBf16 : tree::kF16>(w[e]);
-                                    gone |= x16;
-                                    w[e] &= ~x16;
-                                }
-                                if (gone) v[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                                bad = bad || (gone && j < sq.total);
-                            }
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 p =
+                                make_float2(tree::exp2_approx(d[x][i + 2 * k]), tree::exp2_approx(d[x][i + 2 * k + 1]));
+                            if constexpr (!S::kOnes) l[i / 2 + k] = add2(l[i / 2 + k], p);
+                            split_pair<BF>(p, hi[k], lo[k]);
                         }
-                        if (bad) sm_bad = 1;
+                        *reinterpret_cast<uint4 *>(ph + i / 8 * (kRowsT * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(ph + S::kPB + i / 8 * (kRowsT * 16)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
+                    // rows past the end hold anything, and a value that is not finite must
+                    // not meet the weight zero of a row that does not see it: taken out
+                    // here (by the first warps), the latter added at the end
+                    if (tail && warp < 4 && (partial || (t0 + t + x + 1) * kRowsT > sq.total)) {
+                        const int st = kKR + gx % kVR;
+                        wait(&full[st], gx / kVR);
+                        if (j >= sq.total || (partial && j >= sq.pre)) {
+                            bool bad = false;
+                            for (int y = 0; y < S::kBoxes; ++y) {
+                                uint4 *v = reinterpret_cast<uint4 *>(sm + st * S::kTileB + y * kBoxB + key * 128);
+                                for (int k = 0; k < 8; ++k) {
+                                    uint32_t w4[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, gone = 0;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const uint32_t x16 =
+                                            j >= sq.total ? ~0u : tree::not_finite<BF ? tree::kBf16 : tree::kF16>(w4[e]);
+                                        gone |= x16;
+                                        w4[e] &= ~x16;
+                                    }
+                                    if (gone) v[k] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                                    bad = bad || (gone && j < sq.total);
+                                }
+                            }
+                            if (bad) sm_bad = 1;
+                        }
+                    }
+                    fence_async();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&pfull[gx % kPB]);
                 }
-                fence_async();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(&pfull[g % kPB]);
+                g += np;
+                // the next unit's query rows are fetched during this one, and its
+                // scores begin as soon as this one's have been computed
+                if (S::kQBufs == 2 && t == 0) {
+                    more = w.next(a, N);
+                    if (more) fetch_q(w, buf ^ 1);
+                } else if (S::kQBufs == 2 && t == kPair && more) {
+                    have_q();
+                }
+            }
+            if (S::kQBufs == 1) {                // (every product that reads this unit's is complete)
+                more = w.next(a, N);
+                if (more) fetch_q(w, 0);
+            } else if (n <= kPair && more) {
+                have_q();
             }
 
-            // ---- the unit's sums: sum over the tile's rows of l, O from TMEM
-            float sum[C];
-#pragma unroll
-            for (int i = 0; i < C / 2; ++i) sum[2 * i] = l[i].x, sum[2 * i + 1] = l[i].y;
-            const float x = warp_columns(sum, lane, [](float p, float y) { return p + y; });
-            if (lane % (32 / C) == 0) sm_part[q][c0 + lane / (32 / C)] = x;
+            // ---- the unit's sums: of the weights (over the tile's rows, or from the
+            // rows of O that the ones gave), then O from TMEM
             if (!ok) sm_fail = 1;
-            more = w.next(a, N);
-            if (more) load_q(w);                 // (the next unit's scores are computed meanwhile)
+            if constexpr (S::kOnes) {
+                wait(&pfree[(g - 1) % kPB], (g - 1) / kPB);
+                fence_after();
+                if (q == 2) {
+                    float x[C];
+#pragma unroll
+                    for (int i = 0; i < C; i += 16) tmem_sum16<2, N>(t_o + lanes + c0 + i, x + i);
+#pragma unroll
+                    for (int i = 0; i < C; ++i)
+                        if (lane == i) sm_part[0][c0 + i] = x[i];   // (every lane holds the same)
+                }
+            } else {
+                float sum[C];
+#pragma unroll
+                for (int i = 0; i < C / 2; ++i) sum[2 * i] = l[i].x, sum[2 * i + 1] = l[i].y;
+                const float x = warp_columns(sum, lane, [](float p, float y) { return p + y; });
+                if (lane % (32 / C) == 0) sm_part[q][c0 + lane / (32 / C)] = x;
+            }
             soft_sync<kSync>();
             const bool whole = n == sq.tiles, bad = sm_bad != 0;
             const int place = 2 * blockIdx.x + (first_unit ? 0 : 1);
             const float nan = __int_as_float(0x7fc00000);
             if (tid < N) {
-                const float sum = sm_part[0][tid] + sm_part[1][tid] + sm_part[2][tid] + sm_part[3][tid];
+                float sum = sm_part[0][tid];
+                if constexpr (!S::kOnes) sum += sm_part[1][tid] + sm_part[2][tid] + sm_part[3][tid];
                 // (what a wait that ran out leaves is NaN)
                 sm_inv[tid] = sm_fail ? nan : sum == 0.f ? 0.f : 1.f / sum;
                 if (tid < rows) sm_out[tid] = out_row(a, sq, D, kvh, row0 + tid);
                 if (!whole) parts[place].m[tid] = sm_m[tid], parts[place].l[tid] = sm_fail ? nan : sum;
                 if (!whole && tid == 0) heads[place] = Head{w_b, unit, t0, n, sq.tiles, bad};
             }
-            wait(&pfree[(g - 1) % kPB], (g - 1) / kPB);
-            fence_after();
+            if constexpr (!S::kOnes) {
+                wait(&pfree[(g - 1) % kPB], (g - 1) / kPB);
+                fence_after();
+            }
             soft_sync<kSync>();
             if (q * 32 < D) {
                 const int dim = q * 32 + lane;
-                float o[C];
-                tmem_sum16<2, N>(t_o + lanes + c0, o);
-                if (whole) {
-                    T16 *out = static_cast<T16 *>(a.out) + dim;
+                T16 *out = static_cast<T16 *>(a.out) + dim;
+                // (in a loop: what is run once per unit should be short, its
+                // instructions come from memory)
+#pragma unroll 1
+                for (int i0 = 0; i0 < C; i0 += 16) {
+                    float o[16];
+                    tmem_sum16<2, N>(t_o + lanes + c0 + i0, o);
+                    const int r0 = c0 + i0;
+                    if (whole) {
 #pragma unroll
-                    for (int i = 0; i < C; ++i)
-                        if (c0 + i < rows) {
-                            float v = o[i] * sm_inv[c0 + i];
-                            if (bad)
-                                v += not_finite_seen<T16>(a.kv.v, sq.row_base + int64_t(kvh) * a.kv.n_positions,
-                                                          a.mask[sq.f0 + (row0 + c0 + i) / a.group], sq.pre, sq.total,
-                                                          D, dim);
-                            out[sm_out[c0 + i]] = T16(v);
-                        }
-                } else {
+                        for (int i = 0; i < 16; ++i)
+                            if (r0 + i < rows) out[sm_out[r0 + i]] = T16(o[i] * sm_inv[r0 + i]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < C; ++i)
-                        if (c0 + i < rows) parts[place].o[c0 + i][dim] = o[i];
+                        for (int i = 0; i < 16; ++i)
+                            if (r0 + i < rows) parts[place].o[r0 + i][dim] = o[i];
+                    }
                 }
+                if (bad && whole)
+                    for (int r = c0; r < min(c0 + C, rows); ++r)
+                        out[sm_out[r]] = T16(float(out[sm_out[r]]) +
+                                             not_finite_seen<T16>(a.kv.v, sq.row_base + int64_t(kvh) * a.kv.n_positions,
+                                                                  a.mask[sq.f0 + (row0 + r) / a.group], sq.pre, sq.total,
+                                                                  D, dim));
                 fence_before();
             }
+            if (S::kQBufs == 1 && more) have_q();
             first_unit = false;
         }
         if (!ok) sm_fail = 1;
@@ -837,7 +953,7 @@ cudaError_t launch_tc(const TreeArgs &a, int sms, void *workspace, cudaStream_t 
     if (!encoder() || !cache_map(&km, a.kv.k, a.kv) || !cache_map(&vm, a.kv.v, a.kv)) return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<D, N>::kBytes));
     if (e != cudaSuccess) return e;
-    const int runs = sms;
+    const int runs = sms * Shape<D, N>::kPerSM;
     Part<D, N> *parts = static_cast<Part<D, N> *>(workspace);
     Head *heads = reinterpret_cast<Head *>(parts + 2 * runs);
     fn<<<runs, Shape<D, N>::kThreads, Shape<D, N>::kBytes, s>>>(km, vm, a, parts, heads);
@@ -859,7 +975,7 @@ cudaError_t launch_tc(const TreeArgs &a, int sms, void *workspace, cudaStream_t 
 template <int D, int N>
 constexpr size_t parts_bytes(int sms)
 {
-    return size_t(2) * sms * (sizeof(Part<D, N>) + sizeof(Head));
+    return size_t(2) * sms * Shape<D, N>::kPerSM * (sizeof(Part<D, N>) + sizeof(Head));
 }
 
 }  // namespace
