@@ -488,8 +488,9 @@ int gpt2_op_linear_bf16(const void *W, const float *X, int32_t M, int32_t n, int
  * 16-byte aligned, head_dim 32, 64 or 128.  For the two 8-bit types k_scale and
  * v_scale are DEVICE fp32 [n_slots][n_head][n_positions]: one scale per head
  * and cache row, value = code * scale; NULL for the others.
- *   GPT2_INT8: codes in [-127, 127], scale = max|x| / 127 rounded to fp32 (at
- *     least 2^-126), code = the integer nearest x / scale, ties to even.
+ *   GPT2_INT8: codes in [-127, 127], scale = max|x| * (1/127) (both factors and
+ *     the product rounded to fp32; at least 2^-126), code = the integer nearest x /
+ *     scale, ties to even.
  *   GPT2_E4M3: 8-bit floats (4 exponent, 3 fraction bits, largest 448), scale =
  *     the smallest power of two (at least 2^-126) with max|x| / scale <= 448,
  *     code = x / scale rounded to nearest even.
@@ -537,8 +538,7 @@ int gpt2_op_kv_load(const gpt2_kv *kv, const int32_t *slot, const int32_t *pos, 
  *   n_head * head_dim; max_nodes in [1, GPT2_MAX_NODES] (of a sequence with
  *   more, the rows from max_nodes on are left as they were).  workspace: 16-byte
  *   aligned DEVICE memory of gpt2_op_tree_attention_workspace bytes (which depends
- *   on the current device; 0, and NULL then, for the shapes that need none:
- *   max_nodes * n_head / kv->n_head <= 16, or a cache type other than q's). */
+ *   on the current device; 0, and NULL will do, for the shapes that need none). */
 size_t gpt2_op_tree_attention_workspace(const gpt2_kv *kv, int32_t q_dtype, int32_t n_head, int32_t max_nodes);
 int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, int64_t q_stride, int32_t n_head,
                            const int32_t *slot, const int32_t *cached, const int32_t *first, const uint64_t *mask,

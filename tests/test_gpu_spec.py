@@ -50,7 +50,8 @@ def quantise64(x, kind):
     fine = np.isfinite(x).all(-1)
     with np.errstate(all="ignore"):
         if kind == "int8":
-            s = np.maximum(top.astype(np.float32) / np.float32(127), np.float32(2.0 ** -126)).astype(np.float64)
+            s = np.maximum(top.astype(np.float32) * (np.float32(1) / np.float32(127)),
+                           np.float32(2.0 ** -126)).astype(np.float64)
             y = np.rint(np.where(fine[..., None], x, 0) / np.where(fine, s, 1)[..., None])
         else:
             e = np.array([max(-126, next(k for k in range(-200, 130) if t <= 448 * 2.0 ** k)) if f else 0
@@ -289,6 +290,17 @@ def test_tree_attention_many_rows(qt, ct, counts, G, D):
     run_attention(rng, qt, ct, D, 2, G, 500, [int(x) for x in rng.integers(0, 430, len(counts))], counts)
 
 
+@pytest.mark.parametrize("counts,G,D", [([64, 33, 17], 1, 64), ([20, 3], 3, 64), ([40, 1], 1, 128), ([9], 8, 128),
+                                        ([17], 1, 128), ([21, 0, 32], 1, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_tree_attention_many_rows_long_caches(dtype, counts, G, D):
+    """The same over caches of many positions (of which few are used), where the
+    tensor cores' kernel takes over: fewer tiles than SMs, parts of units."""
+    rng = np.random.default_rng(sum(counts) + G + D)
+    cached = [int(x) for x in rng.integers(0, 3000, len(counts))]
+    run_attention(rng, dtype, dtype, D, 2, G, 36000 // len(counts), cached, counts)
+
+
 @pytest.mark.parametrize("counts,G,D", [(17, 1, 64), (33, 1, 128), (5, 4, 128), (40, 2, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_tree_attention_many_units(dtype, counts, G, D):
@@ -301,7 +313,7 @@ def test_tree_attention_many_units(dtype, counts, G, D):
     cached[3] = cached[17] = 0
     n = [int(x) for x in rng.integers(1, counts + 1, B)]
     n[0], n[5], n[20] = counts, 0, 0
-    run_attention(rng, dtype, dtype, D, K, G, 760, cached, n)
+    run_attention(rng, dtype, dtype, D, K, G, 1600, cached, n)
 
 
 @pytest.mark.parametrize("qt,ct", COMBOS)
@@ -388,13 +400,13 @@ def test_what_is_not_seen_does_not_enter(qt, ct):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("c,n,K", [(60, 24, 200), (1500, 24, 2), (1020, 40, 1)])
-def test_what_is_not_seen_does_not_enter_many_rows(dtype, D, c, n, K):
+@pytest.mark.parametrize("c,n,K,P", [(60, 24, 200, 1600), (1500, 24, 2, 40000), (1020, 40, 1, 70000),
+                                     (60, 24, 3, 200)])
+def test_what_is_not_seen_does_not_enter_many_rows(dtype, D, c, n, K, P):
     """The same with more than 16 query rows: units within one CTA's share
-    (200 heads of one tile) and units that many CTAs share."""
+    (200 heads of one tile), units that many CTAs share, and a short cache."""
     import torch
     rng = np.random.default_rng(c + n)
-    P = c + n + 30
     kc, _ = make_cache(rng, dtype, 1, K, P, D)
     vc, _ = make_cache(rng, dtype, 1, K, P, D)
     mask = binding.tree_masks(random_tree(rng, n, 6))

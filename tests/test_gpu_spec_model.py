@@ -199,7 +199,8 @@ def test_tree_steps_refuse():
 def quantise(x):
     """Rows [..][D] as an int8 cache holds them, by the definition in gpt2.h, and
     the steps (scales)."""
-    s = np.maximum(np.abs(x).max(-1, keepdims=True).astype(np.float32) / np.float32(127), np.float32(2.0 ** -126))
+    s = np.maximum(np.abs(x).max(-1, keepdims=True).astype(np.float32) * (np.float32(1) / np.float32(127)),
+                   np.float32(2.0 ** -126))
     return np.rint(x / s.astype(np.float64)) * s.astype(np.float64), s.astype(np.float64)
 
 

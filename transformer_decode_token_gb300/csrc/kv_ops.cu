@@ -160,7 +160,7 @@ __device__ __forceinline__ void put_vals(T *p, uint32_t step, const float (&x)[k
     }
 }
 
-// Codes of kVals values, the integers nearest x / s (|x| <= 127 s (1 + 2^-23)),
+// Codes of kVals values, the integers nearest x / s (|x| <= 127 s (1 + 2^-22)),
 // ties to even, of the exact quotient and not of a rounded one.  Adding 1.5 *
 // 2^23 to x * (1/s) rounds it to an integer q, whose two's complement is then
 // the low byte of the sum; q is at most one off.  The remainder x - q s is
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(256) k_kv_store(const RowArgs a)
             float s;
             Words<CT> codes;
             if constexpr (std::is_same<CT, int8_t>::value) {
-                s = fmaxf(__fdiv_rn(top, 127.f), FLT_MIN);
+                s = fmaxf(top * (1.f / 127.f), FLT_MIN);
                 quant_int8(x[u], s, __frcp_rn(s), codes.w);
             } else {
                 s = e4m3_scale(top);

@@ -8,14 +8,26 @@ using namespace gpt2;
 
 namespace {
 
-// More than 16 query rows on a cache head over a 16-bit cache of the rows' own
-// type: the 5th-generation tensor cores, in tiles of 32 or 64 query rows (0:
-// not).
+// The 5th-generation tensor cores (tree_attn_tc.cu), in tiles of 32 or 64 query
+// rows (0: not): for more than 16 query rows on a cache head over a 16-bit cache
+// of the rows' own type.
 int tensor_tile(const gpt2_kv &kv, int q_dtype, int rows)
 {
     if (rows <= 16 || q_dtype != kv.dtype || q_dtype == GPT2_F32 || kv.head_dim < 64) return 0;
+    if (kv.n_positions < 1536) return 0;
     if ((long long)kv.n_slots * kv.n_head * kv.n_positions >= (1ll << 31) - 128) return 0;   // TMA's row coordinates
     return rows <= 32 ? 32 : 64;
+}
+
+// They pay for their second kernel and for the change from one unit to the next
+// where caches are long and there is much of them.  Measured in us against the
+// other kernel (query rows x cache heads x sequences, positions, dimensions):
+// 64 x 12 x 32, 4,000, 64: 86 / 155; 64 x 12 x 4, 2,000, 64: 27 / 31; 32 x 8 x 2,
+// 8,000, 128: 27 / 53; 32 x 8 x 2, 2,000, 128: 16 / 18; but 32 x 12, 4,000, 64:
+// 18 / 11; 24 x 12 x 64, 540, 64: 56 / 35.
+bool tensor_pays(const gpt2_kv &kv, int n_seqs)
+{
+    return (long long)n_seqs * kv.n_head * kv.n_positions * kv.head_dim >= 4000000;
 }
 
 bool shape_ok(const gpt2_kv *kv, int q_dtype, int n_head, int max_nodes)
@@ -68,7 +80,8 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     a.q_dtype = q_dtype;
     a.group = n_head / kv->n_head;
     a.scale_log2 = scale * 1.4426950408889634f;
-    const int rows = max_nodes * a.group, tc = tensor_tile(*kv, q_dtype, rows);
+    const int rows = max_nodes * a.group, can = tensor_tile(*kv, q_dtype, rows);
+    const int tc = can && tensor_pays(*kv, n_seqs) ? can : 0;
     const int tile = tc ? tc : rows <= 16 ? 16 : 32;   // (else 16 query rows per warp, or 32)
     a.row_tiles = (rows + tile - 1) / tile;
     const long long units = (long long)n_seqs * kv->n_head * a.row_tiles;
@@ -78,12 +91,10 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     const int sms = spec_sms(&rc);
     if (!sms) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (tc) {
-        if (!workspace || !aligned16(workspace) ||
-            workspace_bytes < tree_attn_tc_workspace(kv->head_dim, tile, sms))
-            return GPT2_ERR_INVALID_ARG;
-        return spec_rc(tree_attn_tc(a, tile, sms, workspace, s));
-    }
+    if (can && (!workspace || !aligned16(workspace) ||
+                workspace_bytes < tree_attn_tc_workspace(kv->head_dim, can, sms)))
+        return GPT2_ERR_INVALID_ARG;
+    if (tc) return spec_rc(tree_attn_tc(a, tile, sms, workspace, s));
     // split the cache between up to 16 CTAs (a cluster) until there are about
     // four per SM, as long as each has 128 positions or more
     a.splits = 1;

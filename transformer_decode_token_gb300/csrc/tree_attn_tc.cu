@@ -313,8 +313,14 @@ __device__ __forceinline__ long long tiles_before(const TreeArgs &a, int end, in
     return x;
 }
 
-// First tile of run i of `runs` over `all` tiles.
-__device__ __forceinline__ long long run_begin(long long all, int i, int runs) { return all * i / runs; }
+// First tile of run i of `runs` over `all` tiles.  Runs have two tiles or more
+// (kLeast), so that few tiles do not leave many parts to add up.
+constexpr int kLeast = 2;
+__device__ __forceinline__ long long run_begin(long long all, int i, int runs)
+{
+    const long long n = min((long long)runs, max(1ll, all / kLeast));
+    return i >= n ? all : all * i / n;
+}
 
 // The units of a run in order: unit u of sequence s from tile t0, n tiles.
 struct Walk {
@@ -870,7 +876,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
 
 // Adds up the parts of a unit that several runs share, in the runs' order: a
 // row of CTAs for the run that holds the unit's first tile.
-constexpr int kJoinThreads = 256, kJoinCut = 8;
+constexpr int kJoinThreads = 256, kJoinCut = 8, kJoinAhead = 8;
 template <bool BF, int D, int N>
 __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, const Part<D, N> *parts, const Head *heads)
 {
@@ -898,13 +904,24 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, co
     for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * D; e += kJoinCut * kJoinThreads) {
         const int r = e / D, d = e % D;
         float m = -parts[first].m[r], sum = parts[first].l[r], v = parts[first].o[r][d];
-        for (int i = blockIdx.x + 1; i <= last; ++i) {
-            if (heads[2 * i].n == 0) continue;    // (more runs than tiles)
-            const Part<D, N> &p = parts[2 * i];
-            const float mi = -p.m[r], top = fmaxf(m, mi), f = tree::exp2_approx(m - top), fi = tree::exp2_approx(mi - top);
-            sum = sum * f + p.l[r] * fi;
-            v = v * f + p.o[r][d] * fi;
-            m = top;
+        // (the runs between hold one unit each, in their first place)
+        for (int i0 = blockIdx.x + 1; i0 <= last; i0 += kJoinAhead) {
+            float mi[kJoinAhead], li[kJoinAhead], vi[kJoinAhead];
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const Part<D, N> &p = parts[2 * min(i0 + k, last)];
+                mi[k] = -p.m[r];
+                li[k] = p.l[r];
+                vi[k] = p.o[r][d];
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k)
+                if (i0 + k <= last) {
+                    const float top = fmaxf(m, mi[k]), f = tree::exp2_approx(m - top), fi = tree::exp2_approx(mi[k] - top);
+                    sum = sum * f + li[k] * fi;
+                    v = v * f + vi[k] * fi;
+                    m = top;
+                }
         }
         v = sum == 0.f ? 0.f : v / sum;
         if (bad)
