@@ -163,6 +163,51 @@ def test_load_reads_back(cache, dst, D):
     assert (out[:, H * D] == 9).all() and (out[:, 2 * H * D + 1:] == 9).all()
 
 
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cache", ["int8", "e4m3", "f32", "f16", "bf16"])
+def test_prompts_through_the_cache(src, cache, D):
+    """Prompt-sized calls (several rows per thread; a last block that is not
+    full): the codes and scales of 13,003 rows against the definition in 64 bits
+    on the GPU, and the same rows read back as each row type."""
+    import torch
+    n, H, S, P = 13003, 5, 40, 400
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    x, y = ((torch.randn((n, H, D), generator=g, device="cuda") *
+             torch.exp(torch.randn((n, H, 1), generator=g, device="cuda"))).to(dt(src)) for _ in range(2))
+    at = torch.randperm(S * P, generator=g, device="cuda")[:n]
+    slot, pos = (at // P).int(), (at % P).int()
+    kc, vc = (torch.zeros((S, H, P, D), device="cuda").to(dt(cache)) for _ in range(2))
+    scaled = cache in ("int8", "e4m3")
+    ks, vs = (torch.zeros((S, H, P), device="cuda") for _ in range(2)) if scaled else (None, None)
+    binding.op_kv_store(x, y, kc, vc, slot, pos, ks, vs)
+    for rows, c, sc in ((x, kc, ks), (y, vc, vs)):
+        d = rows.double()
+        if cache == "int8":
+            want_s = (rows.float().abs().amax(-1) * torch.full((), 1.0 / 127, device="cuda")).clamp(min=2.0 ** -126)
+            want = torch.round(d / want_s.double().unsqueeze(-1))
+        elif cache == "e4m3":
+            m, e = torch.frexp(d.abs().amax(-1) / 448)      # (exact; a logarithm is not, at a power of two)
+            want_s = torch.exp2(torch.where(m == 0.5, e - 1, e).clamp(min=-126).float())
+            want = (d / want_s.double().unsqueeze(-1)).float().to(torch.float8_e4m3fn).double()
+        else:
+            want, want_s = rows.to(dt(cache)).double(), None
+        got = c[slot.long(), :, pos.long()] if cache != "e4m3" else \
+            c.view(torch.uint8)[slot.long(), :, pos.long()].view(c.dtype)
+        assert torch.equal(got.double(), want)
+        if scaled:
+            assert torch.equal(sc[slot.long(), :, pos.long()], want_s)
+    for dst in ("f32", "f16", "bf16"):
+        k, v = binding.op_kv_load(kc, vc, slot, pos, ks, vs, dtype=dt(dst))
+        for got, c, sc in ((k, kc, ks), (v, vc, vs)):
+            w = c.view(torch.uint8)[slot.long(), :, pos.long()].view(c.dtype).float() if cache == "e4m3" else \
+                c[slot.long(), :, pos.long()].float()
+            if scaled:
+                w = w * sc[slot.long(), :, pos.long()].unsqueeze(-1)
+            assert torch.equal(got, w.to(dt(dst)))
+
+
 # ---- tree attention ---------------------------------------------------------------------
 
 COMBOS = [("f32", "f32"), ("f32", "bf16"), ("f32", "f16"), ("f32", "int8"), ("f32", "e4m3"), ("bf16", "bf16"),

@@ -389,7 +389,6 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
 {
     using S = Shape<D, N>;
     using T16 = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-    constexpr int kPair = 1;                        // tiles of a softmax step
     constexpr int kSt = S::kStages, kKR = S::kKRing, kVR = S::kVRing, kPB = S::kPBufs, kSoft = S::kSoft, kSync = kSoft * 32, C = S::kC;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full[kSt], empty[kSt], sfull[2], sfree[2], pfull[kPB], pfree[kPB], qfull, odone;
@@ -638,61 +637,43 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
 #pragma unroll
             for (int i = 0; i < C / 2; ++i) l[i] = make_float2(0.f, 0.f);
 
-            for (int t = 0; t < n; t += kPair) {
-                const int np = min(kPair, n - t);                      // tiles of this step
-                // this thread's cache rows, and which of its 16 query rows see them
-                uint32_t see[kPair];
-                float d[kPair][C];                                     // scores less their rows' maxima, in log2
-#pragma unroll
-                for (int x = 0; x < kPair; ++x) {
-                    const int j = (t0 + t + x) * kRowsT + key;
-                    see[x] = x >= np ? 0u : j < sq.pre ? ~0u : j < sq.total ? uint32_t(sm_see[j - sq.pre] >> c0) : 0u;
-                    if (x < np) wait(&sfull[(g + x) & 1], (g + x) / 2);
-                }
+            for (int t = 0; t < n; ++t, ++g) {
+                // this thread's cache row, and which of its query rows see it
+                const int j = (t0 + t) * kRowsT + key;
+                const uint32_t see = j < sq.pre ? ~0u : j < sq.total ? uint32_t(sm_see[j - sq.pre] >> c0) : 0u;
+                const bool tail = (t0 + t + 1) * kRowsT > sq.pre;
+                const uint32_t t_s = tmem + (g & 1) * N + lanes + c0;
+                wait(&sfull[g & 1], g / 2);
                 fence_after();
-                const bool tail = (t0 + t + np) * kRowsT > sq.pre;
-                auto t_s = [&](int x) { return tmem + ((g + x) & 1) * N + lanes + c0; };
+                float d[C];                                            // scores less their rows' maxima, in log2
                 auto distances = [&]() {
                     float most = -INFINITY;
 #pragma unroll
-                    for (int x = 0; x < kPair; ++x) {
-                        if (x < np) {
+                    for (int i = 0; i < C; i += 16) tmem_load16(t_s + i, d + i);
 #pragma unroll
-                            for (int i = 0; i < C; i += 16) tmem_load16(t_s(x) + i, d[x] + i);
-#pragma unroll
-                            for (int i = 0; i < C; i += 4) {
-                                const float4 m = *reinterpret_cast<const float4 *>(&sm_m[c0 + i]);
-                                const float2 p = fma2(make_float2(d[x][i], d[x][i + 1]), scale, make_float2(m.x, m.y));
-                                const float2 q = fma2(make_float2(d[x][i + 2], d[x][i + 3]), scale, make_float2(m.z, m.w));
-                                d[x][i] = p.x, d[x][i + 1] = p.y, d[x][i + 2] = q.x, d[x][i + 3] = q.y;
-                            }
-                            if (see[x] != ~0u) {
-#pragma unroll
-                                for (int i = 0; i < C; ++i)
-                                    if (!(see[x] >> i & 1)) d[x][i] = -INFINITY;
-                            }
-#pragma unroll
-                            for (int i = 0; i < C; ++i) most = fmaxf(most, d[x][i]);
-                        }
+                    for (int i = 0; i < C; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(&sm_m[c0 + i]);
+                        const float2 x = fma2(make_float2(d[i], d[i + 1]), scale, make_float2(m.x, m.y));
+                        const float2 y = fma2(make_float2(d[i + 2], d[i + 3]), scale, make_float2(m.z, m.w));
+                        d[i] = x.x, d[i + 1] = x.y, d[i + 2] = y.x, d[i + 3] = y.y;
                     }
+                    if (see != ~0u) {
+#pragma unroll
+                        for (int i = 0; i < C; ++i)
+                            if (!(see >> i & 1)) d[i] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int i = 0; i < C; ++i) most = fmaxf(most, d[i]);
                     return most;
                 };
                 if (soft_any<kSync>(distances() > kRaise)) {
-                    // raise the maxima: these tiles' per query row, over the warp's
+                    // raise the maxima: this tile's per query row, over the warp's
                     // cache rows and then the warps
-                    float top[C];
 #pragma unroll
-                    for (int i = 0; i < C; ++i) top[i] = -INFINITY;
+                    for (int i = 0; i < C; i += 16) tmem_load16(t_s + i, d + i);
 #pragma unroll
-                    for (int x = 0; x < kPair; ++x)
-                        if (x < np) {
-#pragma unroll
-                            for (int i = 0; i < C; i += 16) tmem_load16(t_s(x) + i, d[x] + i);
-#pragma unroll
-                            for (int i = 0; i < C; ++i)
-                                if (see[x] >> i & 1) top[i] = fmaxf(top[i], d[x][i] * a.scale_log2);
-                        }
-                    const float mx = warp_columns(top, lane, [](float x, float y) { return fmaxf(x, y); });
+                    for (int i = 0; i < C; ++i) d[i] = see >> i & 1 ? d[i] * a.scale_log2 : -INFINITY;
+                    const float mx = warp_columns(d, lane, [](float x, float y) { return fmaxf(x, y); });
                     if (lane % (32 / C) == 0) sm_part[q][c0 + lane / (32 / C)] = mx;
                     soft_sync<kSync>();
                     if (tid < N) {
@@ -724,73 +705,66 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0)
-                    for (int x = 0; x < np; ++x) arrive(&sfree[(g + x) & 1]);
+                if (lane == 0) arrive(&sfree[g & 1]);
+                if (g >= kPB) wait(&pfree[g % kPB], g / kPB - 1);
+                uint8_t *ph = sm + S::kOffP + (g % kPB) * 2 * S::kPB + key * 16 + c0 / 8 * (kRowsT * 16);
 #pragma unroll
-                for (int x = 0; x < kPair; ++x) {
-                    if (x >= np) break;
-                    const int gx = g + x, j = (t0 + t + x) * kRowsT + key;
-                    if (gx >= kPB) wait(&pfree[gx % kPB], gx / kPB - 1);
-                    uint8_t *ph = sm + S::kOffP + (gx % kPB) * 2 * S::kPB + key * 16 + c0 / 8 * (kRowsT * 16);
+                for (int i = 0; i < C; i += 8) {
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < C; i += 8) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 p =
-                                make_float2(tree::exp2_approx(d[x][i + 2 * k]), tree::exp2_approx(d[x][i + 2 * k + 1]));
-                            if constexpr (!S::kOnes) l[i / 2 + k] = add2(l[i / 2 + k], p);
-                            split_pair<BF>(p, hi[k], lo[k]);
-                        }
-                        *reinterpret_cast<uint4 *>(ph + i / 8 * (kRowsT * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(ph + S::kPB + i / 8 * (kRowsT * 16)) =
-                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 p =
+                            make_float2(tree::exp2_approx(d[i + 2 * k]), tree::exp2_approx(d[i + 2 * k + 1]));
+                        if constexpr (!S::kOnes) l[i / 2 + k] = add2(l[i / 2 + k], p);
+                        split_pair<BF>(p, hi[k], lo[k]);
                     }
-                    // rows past the end hold anything, and a value that is not finite must
-                    // not meet the weight zero of a row that does not see it: taken out
-                    // here (by the first warps), the latter added at the end
-                    if (tail && warp < 4 && (partial || (t0 + t + x + 1) * kRowsT > sq.total)) {
-                        const int st = kKR + gx % kVR;
-                        wait(&full[st], gx / kVR);
-                        if (j >= sq.total || (partial && j >= sq.pre)) {
-                            bool bad = false;
-                            for (int y = 0; y < S::kBoxes; ++y) {
-                                uint4 *v = reinterpret_cast<uint4 *>(sm + st * S::kTileB + y * kBoxB + key * 128);
-                                for (int k = 0; k < 8; ++k) {
-                                    uint32_t w4[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, gone = 0;
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const uint32_t x16 =
-                                            j >= sq.total ? ~0u : tree::not_finite<BF ? tree::kBf16 : tree::kF16>(w4[e]);
-                                        gone |= x16;
-                                        w4[e] &= ~x16;
-                                    }
-                                    if (gone) v[k] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                                    bad = bad || (gone && j < sq.total);
-                                }
-                            }
-                            if (bad) sm_bad = 1;
-                        }
-                    }
-                    fence_async();
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(&pfull[gx % kPB]);
+                    *reinterpret_cast<uint4 *>(ph + i / 8 * (kRowsT * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(ph + S::kPB + i / 8 * (kRowsT * 16)) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                g += np;
+                // rows past the end hold anything, and a value that is not finite must
+                // not meet the weight zero of a row that does not see it: taken out
+                // here (by the first warps), the latter added at the end
+                if (tail && warp < 4 && (partial || (t0 + t + 1) * kRowsT > sq.total)) {
+                    const int st = kKR + g % kVR;
+                    wait(&full[st], g / kVR);
+                    if (j >= sq.total || (partial && j >= sq.pre)) {
+                        bool bad = false;
+                        for (int y = 0; y < S::kBoxes; ++y) {
+                            uint4 *v = reinterpret_cast<uint4 *>(sm + st * S::kTileB + y * kBoxB + key * 128);
+                            for (int k = 0; k < 8; ++k) {
+                                uint32_t w4[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, gone = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t x16 =
+                                        j >= sq.total ? ~0u : tree::not_finite<BF ? tree::kBf16 : tree::kF16>(w4[e]);
+                                    gone |= x16;
+                                    w4[e] &= ~x16;
+                                }
+                                if (gone) v[k] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                                bad = bad || (gone && j < sq.total);
+                            }
+                        }
+                        if (bad) sm_bad = 1;
+                    }
+                }
+                fence_async();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&pfull[g % kPB]);
                 // the next unit's query rows are fetched during this one, and its
                 // scores begin as soon as this one's have been computed
                 if (S::kQBufs == 2 && t == 0) {
                     more = w.next(a, N);
                     if (more) fetch_q(w, buf ^ 1);
-                } else if (S::kQBufs == 2 && t == kPair && more) {
+                } else if (S::kQBufs == 2 && t == 1 && more) {
                     have_q();
                 }
             }
             if (S::kQBufs == 1) {                // (every product that reads this unit's is complete)
                 more = w.next(a, N);
                 if (more) fetch_q(w, 0);
-            } else if (n <= kPair && more) {
+            } else if (n == 1 && more) {
                 have_q();
             }
 
