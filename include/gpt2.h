@@ -535,7 +535,7 @@ int gpt2_op_kv_load(const gpt2_kv *kv, const int32_t *slot, const int32_t *pos, 
  *   Types: q_dtype GPT2_F32 with any cache; GPT2_F16 and GPT2_BF16 with a cache
  *   of the same type, GPT2_INT8 or GPT2_E4M3.  Scores, softmax and sums are
  *   fp32.  q and out 16-byte aligned, strides multiples of 8 elements and >=
- *   n_head * head_dim; max_nodes in [1, GPT2_MAX_NODES] (of a sequence with
+ *   n_head * head_dim; out overlaps neither q nor the cache; max_nodes in [1, GPT2_MAX_NODES] (of a sequence with
  *   more, the rows from max_nodes on are left as they were).  workspace: 16-byte
  *   aligned DEVICE memory of gpt2_op_tree_attention_workspace bytes (which depends
  *   on the current device; 0, and NULL will do, for the shapes that need none). */
@@ -610,8 +610,8 @@ int gpt2_op_kv_commit(const gpt2_kv *kv, int32_t n_layer, const int32_t *slot, c
  * child), TOKEN_RANGE, POSITION_RANGE, OUT_OF_MEMORY, CUDA.
  *
  * gpt2_accept_tree_batch: verifies the nodes of the last such step against its
- * logits (gpt2_op_verify_tree with these arguments; DEVICE pointers, NULL where
- * that allows it; u_draw [n][vocab_size]), keeps the accepted path of each
+ * logits (gpt2_op_verify_tree with these arguments; DEVICE pointers, ready on the
+ * model's stream, NULL where that allows it; u_draw [n][vocab_size]), keeps the accepted path of each
  * sequence in every layer's cache (gpt2_op_kv_commit), and advances its cached
  * length over it.  host_tokens [n][GPT2_MAX_NODES] receives the tokens that each
  * sequence gained (the accepted drafts, then the next token, which the caller

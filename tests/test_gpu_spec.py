@@ -1,5 +1,6 @@
 """GPU parity of the speculative-decoding operations (quantised cache, tree
 attention, verification, commit) against plain implementations in 64 bits."""
+import ctypes
 import math
 
 import numpy as np
@@ -552,6 +553,101 @@ def test_strided_rows_streams_and_graphs():
     check_attention(held, want2, tol2)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_rows_ragged_batches(dtype, D):
+    """The tensor cores' kernel on a batch with slots outside the cache, two
+    sequences of one slot, sequences without nodes or cached rows, lengths past
+    the cache's end and negative ones, nodes behind max_nodes (left as they
+    were) and rows behind the last sequence."""
+    import torch
+    rng = np.random.default_rng(17)
+    K, P, S, mx = 5, 1700, 40, 24
+    cached = [int(x) for x in rng.integers(0, 900, 30)]
+    cached[:6] = [P - 5, P, P + 9, -3, 0, 1]
+    counts = [int(x) for x in rng.integers(1, mx + 1, 30)]
+    counts[:9] = [24, 24, 24, 24, 24, 0, 24, 24, 40]     # (one of more than max_nodes)
+    slot = [int(x) for x in rng.permutation(S)[:30]]
+    slot[6], slot[7], slot[9] = -1, S, slot[10]
+    first = np.concatenate([[0], np.cumsum(counts)])
+    masks = np.concatenate([binding.tree_masks(random_tree(rng, c)) if c else np.zeros(0, np.int64) for c in counts])
+    n = int(first[-1]) + 3
+    masks = np.concatenate([masks, np.full(3, -1, np.int64)])
+    masks[first[12]] = 0                                 # a node that sees the prefix only
+    masks[first[4] + 1] = 0                              # ... and one that sees nothing
+    kc, vc = (make_cache(rng, dtype, S, K, P, D)[0] for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((n, K, D)).astype(np.float32)).to(dt(dtype)).cuda()
+    out = torch.full_like(q, 77.0)
+    binding.op_tree_attention(q, kc, vc, i32(slot), i32(cached), i32(first), torch.from_numpy(masks).cuda(), mx, out=out)
+    seen = masks.copy()                                  # (no cache rows beyond max_nodes nodes)
+    seen[first[8]:first[9]] &= (1 << mx) - 1
+    want, tol = attend64(q, kc, vc, None, None, slot, cached, first, seen, 1 / math.sqrt(D))
+    kept = np.ones(n, bool)
+    kept[first[8] + mx:first[9]] = False
+    kept[first[-1]:] = False
+    k = torch.from_numpy(kept).cuda()
+    assert (out[~k] == 77).all()
+    check_attention(out[k], want[kept], tol[kept])
+    assert (out[first[4] + 1] == 0).all() and (out[first[6]:first[8]] == 0).all()
+
+
+def test_many_rows_more_sequences_than_threads():
+    """700 sequences over three slots: the list of tiles is searched in steps."""
+    rng = np.random.default_rng(18)
+    B = 700
+    counts = [int(x) for x in rng.integers(0, 4, B)]
+    counts[0], counts[699] = 17, 9
+    run_attention(rng, "bf16", "bf16", 64, 1, 1, 1536, [int(x) for x in rng.integers(0, 200, B)], counts,
+                  slots=[int(x) for x in rng.integers(0, 3, B)], S=3)
+
+
+@pytest.mark.parametrize("counts,D", [([24, 40, 3], 64), ([64, 2], 128)])
+def test_many_rows_strided_streams_and_graphs(counts, D):
+    """The tensor cores' kernel: q inside fused rows, out inside wider ones; the
+    same bits on another stream, with two calls in flight, with a workspace of
+    the caller's, and from two captured graphs that share it."""
+    import torch
+    rng = np.random.default_rng(19)
+    B, K, P = len(counts), 4, 8000
+    cached = [int(x) for x in rng.integers(0, 1500, B)]
+    kc, vc = (make_cache(rng, "bf16", B, K, P, D)[0] for _ in range(2))
+    masks = np.concatenate([binding.tree_masks(random_tree(rng, c)) for c in counts])
+    first = np.concatenate([[0], np.cumsum(counts)])
+    n, E = int(first[-1]), K * D
+    qkv = torch.from_numpy(rng.standard_normal((n, 3 * E)).astype(np.float32)).bfloat16().cuda()
+    q = qkv[:, E:2 * E].unflatten(1, (K, D))
+    args = (i32(np.arange(B)), i32(cached), i32(first), torch.from_numpy(masks).cuda(), max(counts))
+    base = binding.op_tree_attention(q, kc, vc, *args)
+    want, tol = attend64(q, kc, vc, None, None, list(range(B)), cached, first, masks, 1 / math.sqrt(D))
+    check_attention(base, want, tol)
+    wide = torch.full((n, 2 * E), 4.0, device="cuda", dtype=torch.bfloat16)
+    out = binding.op_tree_attention(q, kc, vc, *args, out=wide[:, E:].unflatten(1, (K, D)))
+    assert torch.equal(out, base) and (wide[:, :E] == 4).all()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [binding.op_tree_attention(q, kc, vc, *args, stream=s) for s in (s1, s2, s1, s2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, base) for o in outs)
+    kv = binding.KV(kc.data_ptr(), vc.data_ptr(), None, None, binding.GPT2_BF16, B, K, P, D)
+    need = binding.lib().gpt2_op_tree_attention_workspace(ctypes.byref(kv), binding.GPT2_BF16, K, max(counts))
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for bad in (ws[:need - 16], ws[16:], torch.empty(need + 16, dtype=torch.uint8, device="cuda")[8:]):
+        with pytest.raises(binding.GPT2Error):
+            binding.op_tree_attention(q, kc, vc, *args, workspace=bad)
+    graphs, held, q2 = [], [], (-0.5 * q).contiguous()
+    for x in (q, q2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(binding.op_tree_attention(x, kc, vc, *args, workspace=ws))
+        graphs.append(g)
+    for k in (0, 1, 0, 1, 1):
+        held[k].zero_()
+        graphs[k].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(held[0], base) and torch.equal(held[1], binding.op_tree_attention(q2, kc, vc, *args))
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 elements: store, attention, load and commit
     in its last slot."""
@@ -757,6 +853,50 @@ def test_verify_edges():
                 want, near = verify64(logits, tokens, parents, first, mx, temperature, d, ua, ud)
                 assert near > 1e-5
                 assert run_verify(logits, tokens, parents, first, mx, temperature, d, ua, ud) == want
+
+
+@pytest.mark.parametrize("dense", [True, False])
+@pytest.mark.parametrize("low", [-np.inf, -3.3e38])
+def test_verify_masked_children_among_siblings(low, dense):
+    """Drafted tokens of probability zero (a logit of -infinity, or so far below
+    the largest that the difference passes fp32's range) are rejected without
+    touching what is left for their siblings."""
+    rng = np.random.default_rng(30)
+    V, B = 300, 24
+    logits, draft, tokens, parents, first = verify_inputs(rng, [6] * B, V, 5)
+    logits[:, ::2] = low
+    logits[:, 1] += 3
+    logits[:, 3] = logits[:, 1] - 0.25
+    if low > -np.inf:
+        logits[:, 1:4:2] += np.float32(3.3e38)
+    parents = np.tile([-1, 0, 0, 0, 0, 0], B)
+    tokens = np.tile([0, 1, 8, 3, 10, 3], B)
+    for again in range(20):
+        ua, ud = uniform(rng, 6 * B), uniform(rng, B, V)
+        ua[1::6] = 1 - 2.0 ** -24
+        d = draft if dense else None
+        want, near = verify64(logits, tokens, parents, first, 6, 1.0, d, ua, ud)
+        if near > 1e-5:
+            break
+    else:
+        raise AssertionError("no draw of the random numbers is clear of the borders")
+    assert run_verify(logits, tokens, parents, first, 6, 1.0, d, ua, ud) == want
+
+
+@pytest.mark.parametrize("temperature", [3e38, 1.3e37, 2.0 ** 121, 5e-38])
+def test_verify_extreme_temperatures(temperature):
+    """With masked ids: the distribution over the others is flat, or on the
+    highest."""
+    rng = np.random.default_rng(31)
+    logits, draft, tokens, parents, first = verify_inputs(rng, [5] * 6, 64, 2)
+    logits[:, 5::7] = -np.inf
+    if temperature < 1:                          # (the highest clear of the others)
+        logits = np.round(logits * 4)
+        logits[:, 3] = 90
+    ua, ud = uniform(rng, 30), uniform(rng, 6, 64)
+    want, near = verify64(logits, tokens, parents, first, 5, temperature, draft, ua, ud)
+    assert near > 1e-5
+    assert run_verify(logits, tokens, parents, first, 5, temperature, draft, ua, ud) == want
 
 
 def test_verify_ties_take_the_lowest_id():

@@ -16,6 +16,7 @@
 // falls within about 1e-6 of its border.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -279,9 +280,10 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
     if (parent >= 0 && parent < tid) {
         w.u[tid] = ux;
         w.q[tid] = qx;
-        // lx - m in two parts, so that its rounding does not show
+        // lx - m in two parts, so that its rounding does not show (no second part
+        // where the first is -infinity: a logit of -infinity, or a difference past fp32's range)
         const float m = w.m[parent], d = lx - m, t = d + m, rest = (lx - t) + (m - (t - d));
-        w.prob[tid] = weight(a, d, rest) * w.inv_z[parent];
+        w.prob[tid] = d >= -FLT_MAX ? weight(a, d, rest) * w.inv_z[parent] : 0.f;
     }
     if (tid == 0) {
         w.cur = 0;
@@ -465,7 +467,7 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
         a.u_accept = u_accept;
         a.u_draw = u_draw;
         a.c_hi = std::nextafterf(float(c), 0.f);    // below c, so that the rest is positive
-        a.c_lo = float(c - double(a.c_hi));
+        a.c_lo = std::max(float(c - double(a.c_hi)), FLT_TRUE_MIN);   // (and not zero, for the largest temperatures)
         // the final draw reads a row with the CTAs of a cluster: as many as
         // keep 2048 ids or more each, while all sequences' fit the GPU together (two per SM)
         while (a.cluster < kMaxCluster && vocab >= 4096 * a.cluster && n_seqs * a.cluster * 2ll <= 2ll * sms)
