@@ -371,6 +371,19 @@ def test_single_tokens_long_and_short(qt, ct):
     run_attention(rng, qt, ct, 128, 1, 4, 3001, [2900], [1])
 
 
+@pytest.mark.parametrize("qt,ct", COMBOS)
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("P,K", [(700, 2), (2600, 3), (300, 30)])
+def test_few_rows(qt, ct, D, P, K):
+    """One to eight query rows per cache head, nodes and heads of a group, with
+    little and much beside them: tiles of one, two, four and sixteen rows, odd
+    rests, several CTAs per cache."""
+    rng = np.random.default_rng(P + D)
+    for G, counts in ((1, [1, 1]), (2, [1]), (1, [2, 1, 0]), (1, [3]), (4, [1, 1]), (1, [5, 2]), (7, [1]), (2, [4, 3])):
+        cached = [int(x) for x in rng.integers(0, P, len(counts))]
+        run_attention(rng, qt, ct, D, K, G, P, cached, counts, extra=1)
+
+
 @pytest.mark.parametrize("P", [1, 2, 31, 77, 128])
 @pytest.mark.parametrize("ct", ["f32", "int8"])
 def test_small_caches(P, ct):

@@ -194,6 +194,36 @@ def test_tree_steps_refuse():
         m.close()
 
 
+@pytest.mark.gpu
+def test_logits_without_a_choice():
+    """A token whose embedding is NaN ruins its own sequence's logits only: the
+    error carries what every sequence gained."""
+    cfg = synth.TINY
+    w = dict(synth.make_weights(cfg, 0))
+    clean = binding.BatchModel(cfg, binding.upload_weights(w), 8)
+    w["wpe"] = np.array(w["wpe"])
+    w["wpe"][9] = np.nan
+    m = binding.BatchModel(cfg, binding.upload_weights(w), 8)
+    try:
+        prompts = [[1, 2, 3], [4, 5, 6, 7, 8, 9, 10, 11, 12]]     # the second's next position is 9
+        for x in (clean, m):
+            x.prefill(prompts)
+        first = clean.argmax(2)
+        trees = [([first[0], 5], [-1, 0]), ([first[1], 6], [-1, 0])]
+        clean.decode_tree(trees)
+        want = clean.accept_tree()
+        m.decode_tree(trees)
+        with pytest.raises(binding.GPT2Error) as e:
+            m.accept_tree()
+        assert e.value.name == "DEVICE_STATE" and e.value.tokens == [want[0], []]
+        m.decode_tree([([want[0][-1]], [-1])])                    # the first goes on
+        clean.decode_tree([([want[0][-1]], [-1])])
+        assert m.accept_tree() == clean.accept_tree()
+    finally:
+        m.close()
+        clean.close()
+
+
 # ---- the int8 cache -----------------------------------------------------------------
 
 def quantise(x):

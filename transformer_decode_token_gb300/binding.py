@@ -451,7 +451,8 @@ class BatchModel:
         path and returns the tokens it gained (its accepted drafts, then its
         next token); see gpt2_accept_tree_batch.  CUDA fp32 tensors:
         draft_probs [nodes][vocab], u_accept [nodes], u_draw
-        [sequences][vocab]."""
+        [sequences][vocab].  Where some sequence's logits leave no choice, the
+        GPT2Error (DEVICE_STATE) has the gained tokens as `tokens`."""
         import torch
         counts = getattr(self, "_tree_counts", [0])
         n, rows, V = len(counts), sum(counts), self.cfg.vocab_size
@@ -462,9 +463,15 @@ class BatchModel:
                 raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape {shape}")
         out, op = _i32(np.zeros((n, MAX_NODES)))
         got, gp = _i32(np.zeros(n))
-        check(lib().gpt2_accept_tree_batch(self._h, float(temperature), _ptr(draft_probs), _ptr(u_accept),
-                                           _ptr(u_draw), op, gp), "gpt2_accept_tree_batch")
-        return [out[b, :got[b]].tolist() for b in range(n)]
+        status = lib().gpt2_accept_tree_batch(self._h, float(temperature), _ptr(draft_probs), _ptr(u_accept),
+                                              _ptr(u_draw), op, gp)
+        tokens = [out[b, :got[b]].tolist() for b in range(n)]
+        if STATUS.get(status) == "DEVICE_STATE":
+            e = GPT2Error(status, "gpt2_accept_tree_batch")
+            e.tokens = tokens
+            raise e
+        check(status, "gpt2_accept_tree_batch")
+        return tokens
 
     def argmax(self, n: int) -> list:
         out = np.zeros(n, np.int32)

@@ -30,6 +30,40 @@ bool tensor_pays(const gpt2_kv &kv, int n_seqs)
     return (long long)n_seqs * kv.n_head * kv.n_positions * kv.head_dim >= 4000000;
 }
 
+// Query rows per tile on the CUDA cores (tree_attn_few.cu; 0: the matrix
+// instructions): all rows of a single token or a pair, up to four over an fp32
+// cache (whose matrix products take three instructions each), and tiles of two
+// where there are few rows and sequences, and all that counts is how soon one
+// pass is over.  Measured in us against the matrix instructions (sequences x 12
+// heads of 64, up to so many positions, cache type):
+//   1 row: 64 x 575 bf16 14.5 / 23.7, int8 14.3 / 22.7, fp32 22.7 / 37.5;
+//     1 x 1,000 bf16 4.9 / 6.5, fp32 4.8 / 7.3
+//   2 rows: 64 x 575 bf16 17.3 / 24.4, int8 18.6 / 22.9
+//   4 rows in one tile: 64 x 575 fp32 28.7 / 38.4, but bf16 26.0 / 24.9, int8 29.3 / 23.1
+//   8 rows in tiles of two: 1 x 1,000 fp32 6.7 / 7.9, bf16 6.6 / 7.2, int8 7.0 / 7.2;
+//     2 x 1,000 fp32 7.7 / 9.5, bf16 7.3 / 7.8; but 1 x 16,000 bf16 25.4 / 21.5,
+//     4 x 1,000 bf16 9.4 / 8.9
+int few_rows(const gpt2_kv &kv, int n_seqs, int rows)
+{
+    if (rows <= 2) return rows;
+    if (rows <= 8 && kv.n_positions <= 2048 && (long long)n_seqs * kv.n_head * ((rows + 1) / 2) <= 108) return 2;
+    return rows <= 4 && kv.dtype == GPT2_F32 ? 4 : 0;
+}
+
+// CTAs (of a cluster) that share a unit's cache: twice as many while all clusters
+// still find a place at once, and each CTA has 128 positions or more.  Clusters of 2,
+// 4, 8 and 16 CTAs that run at once, per resident CTA of an SM (as the runtime
+// reports for 152 SMs): a cluster stays within a group of 16 to 20 SMs.  One
+// cluster more than that costs a second round: 24 units of 8 fp32 rows over
+// 1,024 positions took 9.4 us with 8 CTAs each, 15.3 with 16.
+int splits_for(long long units, int positions, int resident)
+{
+    constexpr int kFit[] = {76, 36, 17, 7};
+    int n = 1;
+    for (int i = 0; i < 4 && units <= kFit[i] * resident && positions >= 256 * n; ++i) n *= 2;
+    return n;
+}
+
 bool shape_ok(const gpt2_kv *kv, int q_dtype, int n_head, int max_nodes)
 {
     if (!kv_ok(kv) || !is_row_type(q_dtype)) return false;
@@ -82,7 +116,8 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     a.scale_log2 = scale * 1.4426950408889634f;
     const int rows = max_nodes * a.group, can = tensor_tile(*kv, q_dtype, rows);
     const int tc = can && tensor_pays(*kv, n_seqs) ? can : 0;
-    const int tile = tc ? tc : rows <= 16 ? 16 : 32;   // (else 16 query rows per warp, or 32)
+    const int few = few_rows(*kv, n_seqs, rows);
+    const int tile = tc ? tc : few ? few : rows <= 16 ? 16 : 32;   // (the matrix instructions: 16 query rows per warp, or 32)
     a.row_tiles = (rows + tile - 1) / tile;
     const long long units = (long long)n_seqs * kv->n_head * a.row_tiles;
     if (units * 16 >= (1ll << 31)) return GPT2_ERR_INVALID_ARG;
@@ -95,10 +130,8 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
                 workspace_bytes < tree_attn_tc_workspace(kv->head_dim, can, sms)))
         return GPT2_ERR_INVALID_ARG;
     if (tc) return spec_rc(tree_attn_tc(a, tile, sms, workspace, s));
-    // split the cache between up to 16 CTAs (a cluster) until there are about
-    // four per SM, as long as each has 128 positions or more
-    a.splits = 1;
-    while (a.splits < tree::kMaxSplits && units * a.splits < 2ll * sms && kv->n_positions >= 256 * a.splits) a.splits *= 2;
+    a.splits = splits_for(units, kv->n_positions, few ? (few == 1 ? 4 : few == 2 ? 3 : 2) : tile == 16 && kv->head_dim <= 64 ? 3 : 2);
+    if (few) return spec_rc(tree_attn_few(a, few, s));
     const int mt = tile / 16;
     if (kv->dtype == GPT2_F32) return spec_rc(tree_attn_f32(a, mt, s));
     if (is_scaled(kv->dtype)) return spec_rc(tree_attn_8(a, mt, s));

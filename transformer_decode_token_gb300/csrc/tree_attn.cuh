@@ -55,6 +55,8 @@ struct TreeArgs {
 cudaError_t tree_attn_f32(const TreeArgs &a, int mt, cudaStream_t s);
 cudaError_t tree_attn_16(const TreeArgs &a, int mt, cudaStream_t s);
 cudaError_t tree_attn_8(const TreeArgs &a, int mt, cudaStream_t s);
+// r: query rows of a tile, 1, 2, or 4 over an fp32 cache
+cudaError_t tree_attn_few(const TreeArgs &a, int r, cudaStream_t s);
 // n: query rows of a tile, 32 or 64
 cudaError_t tree_attn_tc(const TreeArgs &a, int n, int sms, void *workspace, cudaStream_t s);
 size_t tree_attn_tc_workspace(int head_dim, int n, int sms);
@@ -131,6 +133,23 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+// Two fp32 values at once (IEEE operations).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
 // B bytes at p (zeros where !there) into B / 4 registers.
 template <int B>
 __device__ __forceinline__ void load_piece(uint32_t *r, const uint8_t *p, bool there)
@@ -280,6 +299,112 @@ struct Smem {
     static constexpr size_t kO = size_t(kNW) * kRows * D * 4;
     static constexpr size_t kBytes = kQ > kO ? kQ : kO;   // q's operands, then the warps' sums
 };
+
+// The warps' sums so [kNW][R][D] (in units of 2^(the CTA's maximum)), with their
+// maxima and sums of weights, to results: over the warps, then over the CTAs of
+// the cluster.  bad_sum(e): what is to be added to element e where some CTA is
+// `bad`.
+template <int D, int R, typename Bad>
+__device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)[R], float (*sm_l)[R],
+                                     float (*sm_f)[R], int *sm_bad, bool cta_bad, int rank, int f0, int row0, int kvh,
+                                     int rows, Bad bad_sum)
+{
+    const int tid = threadIdx.x;
+    float cta_m = 0.f, cta_l = 0.f;
+    if (tid < R) {
+        float top = sm_m[0][tid];
+        for (int w = 1; w < kNW; ++w) top = fmaxf(top, sm_m[w][tid]);
+        for (int w = 0; w < kNW; ++w)
+            cta_l += top == -INFINITY ? 0.f : sm_l[w][tid] * exp2_approx(sm_m[w][tid] - top);
+        cta_m = top;
+    }
+    for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
+        float4 v = *reinterpret_cast<const float4 *>(so + e);
+#pragma unroll
+        for (int w = 1; w < kNW; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(so + w * R * D + e);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        *reinterpret_cast<float4 *>(so + e) = v;
+    }
+    __syncthreads();
+    if (tid < R) {
+        sm_m[0][tid] = cta_m;
+        sm_l[0][tid] = cta_l;
+    }
+    // four elements of a row, from element e = row * D + dim on
+    auto store4 = [&](int e, const float (&v)[4]) {
+        const int r = e / D, d = e % D;
+        const size_t at = size_t(f0 + (row0 + r) / a.group) * a.out_stride + size_t(kvh * a.group + (row0 + r) % a.group) * D + d;
+        if (a.q_dtype == GPT2_F32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = a.q_dtype == GPT2_F16 ? *reinterpret_cast<const uint32_t *>(&h)
+                                             : *reinterpret_cast<const uint32_t *>(&x);
+            }
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(w[0], w[1]);
+        }
+    };
+    if (a.splits == 1) {
+        __syncthreads();
+        for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
+            const float sum = sm_l[0][e / D], inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float4 o4 = *reinterpret_cast<const float4 *>(so + e);
+            float v[4] = {o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv};
+            if (cta_bad)
+                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
+            store4(e, v);
+        }
+    } else {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        // every CTA finishes its share of the elements from all CTAs' sums: first
+        // each CTA's factor for each row (2^(its m - the largest) / the sum)
+        for (int r = tid; r < rows; r += kNW * 32) {
+            float mk[kMaxSplits], lk[kMaxSplits], top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                mk[k] = k < a.splits ? *cl.map_shared_rank(&sm_m[0][r], k) : -INFINITY;
+                lk[k] = k < a.splits ? *cl.map_shared_rank(&sm_l[0][r], k) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) top = fmaxf(top, mk[k]);
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                mk[k] = mk[k] == -INFINITY ? 0.f : exp2_approx(mk[k] - top);
+                sum += lk[k] * mk[k];
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) sm_f[k][r] = mk[k] * inv;
+        }
+        const bool any_bad = __syncthreads_or(tid < a.splits ? *cl.map_shared_rank(sm_bad, tid) : 0);
+        for (int e = (rank * kNW * 32 + tid) * 4; e < rows * D; e += a.splits * kNW * 32 * 4) {
+            float4 x[kMaxSplits];
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k)
+                x[k] = k < a.splits ? *reinterpret_cast<const float4 *>(cl.map_shared_rank(so + e, k))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                const float f = sm_f[k][e / D];
+                v[0] = fmaf(x[k].x, f, v[0]), v[1] = fmaf(x[k].y, f, v[1]);
+                v[2] = fmaf(x[k].z, f, v[2]), v[3] = fmaf(x[k].w, f, v[3]);
+            }
+            if (any_bad)
+                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
+            store4(e, v);
+        }
+        cl.sync();          // nobody leaves while its sums are read
+    }
+}
 
 template <class Tr, int D, int MT>
 __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_attn(const TreeArgs a)
@@ -714,48 +839,8 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
             }
         }
     __syncthreads();
-    float cta_m = 0.f, cta_l = 0.f;
-    if (tid < R) {
-        float top = sm_m[0][tid];
-        for (int w = 1; w < kNW; ++w) top = fmaxf(top, sm_m[w][tid]);
-        for (int w = 0; w < kNW; ++w)
-            cta_l += top == -INFINITY ? 0.f : sm_l[w][tid] * exp2_approx(sm_m[w][tid] - top);
-        cta_m = top;
-    }
-    for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
-        float4 v = *reinterpret_cast<const float4 *>(so + e);
-#pragma unroll
-        for (int w = 1; w < kNW; ++w) {
-            const float4 x = *reinterpret_cast<const float4 *>(so + w * R * D + e);
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        }
-        *reinterpret_cast<float4 *>(so + e) = v;
-    }
-    __syncthreads();
-    if (tid < R) {
-        sm_m[0][tid] = cta_m;
-        sm_l[0][tid] = cta_l;
-    }
-    // four elements of a row, from element e = row * D + dim on
-    auto store4 = [&](int e, const float (&v)[4]) {
-        const int r = e / D, d = e % D;
-        const size_t at = size_t(f0 + (row0 + r) / G) * a.out_stride + size_t(kvh * G + (row0 + r) % G) * D + d;
-        if (a.q_dtype == GPT2_F32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-            uint32_t w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-                const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                w[i] = a.q_dtype == GPT2_F16 ? *reinterpret_cast<const uint32_t *>(&h)
-                                             : *reinterpret_cast<const uint32_t *>(&x);
-            }
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(w[0], w[1]);
-        }
-    };
-    // the infinities and NaNs that were taken out, for the rows that see them
-    auto bad_sum = [&](int e) {
+    join<D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, cta_bad, rank, f0, row0, kvh, rows, [&](int e) {
+        // the infinities and NaNs that were taken out, for the rows that see them
         const int r = e / D, d = e % D;
         const uint64_t sees = a.mask[f0 + (row0 + r) / G];
         float x = 0.f;
@@ -765,68 +850,12 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
             if (!(fabsf(v) <= 3.0e38f)) x += v;
         }
         return x;
-    };
-    if (a.splits == 1) {
-        __syncthreads();
-        for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
-            const float sum = sm_l[0][e / D], inv = sum == 0.f ? 0.f : 1.f / sum;
-            const float4 o4 = *reinterpret_cast<const float4 *>(so + e);
-            float v[4] = {o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv};
-            if (cta_bad)
-                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
-            store4(e, v);
-        }
-    } else {
-        namespace cg = cooperative_groups;
-        cg::cluster_group cl = cg::this_cluster();
-        cl.sync();
-        // every CTA finishes its share of the elements from all CTAs' sums: first
-        // each CTA's factor for each row (2^(its m - the largest) / the sum)
-        for (int r = tid; r < rows; r += kNW * 32) {
-            float mk[kMaxSplits], lk[kMaxSplits], top = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) {
-                mk[k] = k < a.splits ? *cl.map_shared_rank(&sm_m[0][r], k) : -INFINITY;
-                lk[k] = k < a.splits ? *cl.map_shared_rank(&sm_l[0][r], k) : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) top = fmaxf(top, mk[k]);
-#pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) {
-                mk[k] = mk[k] == -INFINITY ? 0.f : exp2_approx(mk[k] - top);
-                sum += lk[k] * mk[k];
-            }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) sm_f[k][r] = mk[k] * inv;
-        }
-        const bool any_bad = __syncthreads_or(tid < a.splits ? *cl.map_shared_rank(&sm_bad, tid) : 0);
-        for (int e = (rank * kNW * 32 + tid) * 4; e < rows * D; e += a.splits * kNW * 32 * 4) {
-            float4 x[kMaxSplits];
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k)
-                x[k] = k < a.splits ? *reinterpret_cast<const float4 *>(cl.map_shared_rank(so + e, k))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) {
-                const float f = sm_f[k][e / D];
-                v[0] = fmaf(x[k].x, f, v[0]), v[1] = fmaf(x[k].y, f, v[1]);
-                v[2] = fmaf(x[k].z, f, v[2]), v[3] = fmaf(x[k].w, f, v[3]);
-            }
-            if (any_bad)
-                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
-            store4(e, v);
-        }
-        cl.sync();          // nobody leaves while its sums are read
-    }
+    });
 }
 
-template <class Tr, int D, int MT>
-cudaError_t launch(const TreeArgs &a, cudaStream_t s)
+template <typename K>
+cudaError_t launch_tree(K fn, const TreeArgs &a, size_t smem, cudaStream_t s)
 {
-    auto fn = k_tree_attn<Tr, D, MT>;
-    constexpr size_t smem = Smem<Tr, D, MT>::kBytes;
     cudaError_t e = cudaSuccess;
     if (smem > 40 * 1024)
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -844,6 +873,12 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t s)
     cfg.attrs = at;
     cfg.numAttrs = a.splits > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+template <class Tr, int D, int MT>
+cudaError_t launch(const TreeArgs &a, cudaStream_t s)
+{
+    return launch_tree(k_tree_attn<Tr, D, MT>, a, Smem<Tr, D, MT>::kBytes, s);
 }
 
 template <class Tr>

@@ -41,6 +41,9 @@
 namespace gpt2 {
 namespace {
 
+using tree::add2;
+using tree::fma2;
+
 constexpr int kRowsT = 128;                      // cache rows of a tile
 constexpr uint32_t kBoxB = kRowsT * 128;         // one TMA box: 128 rows of 64 16-bit dimensions
 constexpr float kRaise = 8.f;                    // log2 of the weight that raises a maximum
@@ -185,23 +188,6 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Two fp32 values at once (IEEE operations).
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
 // p as two parts of the 16-bit type, the second the rounding of what the first
 // leaves.
 template <bool BF>
