@@ -661,6 +661,75 @@ def test_many_rows_strided_streams_and_graphs(counts, D):
     assert torch.equal(held[0], base) and torch.equal(held[1], binding.op_tree_attention(q2, kc, vc, *args))
 
 
+def test_chained_calls_and_joined_streams():
+    """Calls that feed one another, back to back (each may be placed before the
+    last one has ended), and in a captured graph whose branches fork and join
+    between them; many times, with inputs that an ordinary operation writes just
+    before."""
+    import torch
+    rng = np.random.default_rng(20)
+    B, K, P, D, n = 6, 4, 2100, 64, 8
+    kc, vc = (torch.zeros((2, B, K, P, D), dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((2, B, K, P), device="cuda") for _ in range(2))
+    cached = i32(rng.integers(0, 1500, B))
+    first, slot = i32(np.arange(B + 1) * n), i32(rng.permutation(B))
+    mask = torch.from_numpy(np.tile(binding.tree_masks(random_tree(rng, n)), B)).cuda()
+    rs, rp = slot.repeat_interleave(n), (cached.repeat_interleave(n) + torch.arange(n, device="cuda").repeat(B)).int()
+    src = torch.from_numpy(rng.standard_normal((3, B * n, K, D)).astype(np.float32)).cuda()
+    x = torch.empty_like(src)
+    path = i32([[0, 2, 3, -1, -1, -1, -1, -1]] * B)
+    n_path = i32([3] * B)
+    side = torch.cuda.Stream()
+
+    def chain(fork):
+        outs = []
+        torch.mul(src, 1.0, out=x)
+        for layer in range(2):
+            c = (kc[layer], vc[layer])
+            binding.op_kv_store(x[1], x[2], *c, rs, rp, ks[layer], vs[layer])
+            if fork:
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    outs.append(binding.op_kv_load(*c, rs, rp, ks[layer], vs[layer])[0])
+            outs.append(binding.op_tree_attention(x[0], *c, slot, cached, first, mask, n, ks[layer], vs[layer]))
+            if fork:
+                torch.cuda.current_stream().wait_stream(side)
+            x[0].copy_(outs[-1])
+            outs.append(binding.op_tree_attention(x[0][:B], *c, slot, cached, i32_one, mask[:B], 1, ks[layer], vs[layer]))
+        binding.op_kv_commit(kc, vc, slot, cached, path, n_path, ks, vs)
+        outs.append(binding.op_kv_load(kc[1], vc[1], rs, rp, ks[1], vs[1])[1])
+        return outs
+
+    def reset():
+        for t in (kc, vc, ks, vs):
+            t.zero_()
+
+    i32_one = i32(np.arange(B + 1))
+    want = None
+    for _ in range(30):
+        reset()
+        got = chain(False)
+        torch.cuda.synchronize()
+        want = want or [g.clone() for g in got]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    m = mask.cpu().numpy()
+    reset()
+    binding.op_kv_store(src[1], src[2], kc[0], vc[0], rs, rp, ks[0], vs[0])
+    ref, tol = attend64(src[0], kc[0], vc[0], ks[0], vs[0], slot.tolist(), cached.tolist(), first.tolist(), m, 1 / 8)
+    check_attention(want[0], ref, tol)
+    for fork in (False, True):
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            held = chain(fork)
+        for _ in range(5):
+            reset()
+            g.replay()
+            torch.cuda.synchronize()
+            attended = [h for i, h in enumerate(held) if not fork or i not in (0, 3)]
+            assert all(torch.equal(a, b) for a, b in zip(attended, want))
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 elements: store, attention, load and commit
     in its last slot."""

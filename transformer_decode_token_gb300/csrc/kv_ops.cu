@@ -232,6 +232,8 @@ template <typename ST, typename CT, bool VEC, int U>
 __global__ void __launch_bounds__(256) k_kv_store(const RowArgs a)
 {
     constexpr bool kA = kApart<ST, CT>;
+    pdl_wait();
+    pdl_launch_dependents();
     const uint32_t D = a.kv.head_dim, H = a.kv.n_head, lanes = D / kVals, step = piece_step<kA>(D);
     const uint32_t per = 256 / lanes, l = threadIdx.x % lanes;
     const uint32_t unit0 = blockIdx.x * (U * per) + threadIdx.x / lanes;
@@ -297,6 +299,8 @@ template <typename CT, typename DT, bool VEC, int U>
 __global__ void __launch_bounds__(256) k_kv_load(const RowArgs a)
 {
     constexpr bool kA = kApart<DT, CT>;
+    pdl_wait();
+    pdl_launch_dependents();
     const uint32_t D = a.kv.head_dim, H = a.kv.n_head, lanes = D / kVals, step = piece_step<kA>(D);
     const uint32_t per = 256 / lanes, l = threadIdx.x % lanes;
     const uint32_t unit0 = blockIdx.x * (U * per) + threadIdx.x / lanes;
@@ -378,6 +382,8 @@ __global__ void __launch_bounds__(256) k_kv_commit(const CommitArgs a)
     __shared__ int path[GPT2_MAX_NODES];
     __shared__ int n_ok;
     const int b = blockIdx.x % a.n_seqs, layer = blockIdx.x / a.n_seqs;
+    pdl_wait();
+    pdl_launch_dependents();
     const int H = a.kv.n_head, P = a.kv.n_positions;
     const int slot = a.slot[b], cached = a.cached[b];
     const bool there = slot >= 0 && slot < a.kv.n_slots && cached >= 0;
@@ -467,10 +473,9 @@ int gpt2_op_kv_store(const gpt2_kv *kv, const void *k, const void *v, int32_t sr
         using ST = decltype(st);
         auto go = [&](auto ct) {
             using CT = decltype(ct);
-            if (!vec) k_kv_store<ST, CT, false, 1><<<row_blocks(kv, n_rows, 1), 256, 0, s>>>(a);
-            else if (many) k_kv_store<ST, CT, true, 2><<<row_blocks(kv, n_rows, 2), 256, 0, s>>>(a);
-            else k_kv_store<ST, CT, true, 1><<<row_blocks(kv, n_rows, 1), 256, 0, s>>>(a);
-            return spec_rc(cudaGetLastError());
+            if (!vec) return spec_rc(spec_launch(k_kv_store<ST, CT, false, 1>, dim3(row_blocks(kv, n_rows, 1)), 256, 0, 1, s, a));
+            if (many) return spec_rc(spec_launch(k_kv_store<ST, CT, true, 2>, dim3(row_blocks(kv, n_rows, 2)), 256, 0, 1, s, a));
+            return spec_rc(spec_launch(k_kv_store<ST, CT, true, 1>, dim3(row_blocks(kv, n_rows, 1)), 256, 0, 1, s, a));
         };
         if (kv->dtype == GPT2_INT8) return go(int8_t());
         if (kv->dtype == GPT2_E4M3) return go(__nv_fp8_e4m3());
@@ -493,13 +498,12 @@ int gpt2_op_kv_load(const gpt2_kv *kv, const int32_t *slot, const int32_t *pos, 
         using DT = decltype(dt);
         auto go = [&](auto ct) {
             using CT = decltype(ct);
-            if (!vec) k_kv_load<CT, DT, false, 1><<<row_blocks(kv, n_rows, 1), 256, 0, s>>>(a);
-            else if (many) {
+            if (!vec) return spec_rc(spec_launch(k_kv_load<CT, DT, false, 1>, dim3(row_blocks(kv, n_rows, 1)), 256, 0, 1, s, a));
+            if (many) {
                 constexpr int U = 4 / int(sizeof(CT));
-                k_kv_load<CT, DT, true, U><<<row_blocks(kv, n_rows, U), 256, 0, s>>>(a);
+                return spec_rc(spec_launch(k_kv_load<CT, DT, true, U>, dim3(row_blocks(kv, n_rows, U)), 256, 0, 1, s, a));
             }
-            else k_kv_load<CT, DT, true, 1><<<row_blocks(kv, n_rows, 1), 256, 0, s>>>(a);
-            return spec_rc(cudaGetLastError());
+            return spec_rc(spec_launch(k_kv_load<CT, DT, true, 1>, dim3(row_blocks(kv, n_rows, 1)), 256, 0, 1, s, a));
         };
         if (kv->dtype == GPT2_INT8) return go(int8_t());
         if (kv->dtype == GPT2_E4M3) return go(__nv_fp8_e4m3());
@@ -521,8 +525,7 @@ int gpt2_op_kv_commit(const gpt2_kv *kv, int32_t n_layer, const int32_t *slot, c
                        kv->head_dim * elem_size(kv->dtype) / 16};
     const int cols = 2 * kv->n_head * (a.row16 + 1);
     const dim3 grid(unsigned(n_layer) * n_seqs, (cols + 255) / 256);
-    k_kv_commit<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return spec_rc(cudaGetLastError());
+    return spec_rc(spec_launch(k_kv_commit, grid, 256, 0, 1, static_cast<cudaStream_t>(stream), a));
 }
 
 }  // extern "C"

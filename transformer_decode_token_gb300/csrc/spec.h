@@ -16,6 +16,31 @@ inline int spec_rc(cudaError_t e)
     return e == cudaErrorMemoryAllocation ? GPT2_ERR_OUT_OF_MEMORY : GPT2_ERR_CUDA;
 }
 
+// Launches a kernel as a programmatic dependent of the stream's last one: its
+// CTAs may be placed before that one has ended (right away where it was one of
+// these, which let the next one go as soon as they all run), and every thread
+// calls pdl_wait(), and then pdl_launch_dependents(), before it touches memory.
+// cluster: CTAs of a cluster along x, 1: none.
+template <typename... P, typename... A>
+inline cudaError_t spec_launch(void (*fn)(P...), dim3 grid, unsigned threads, size_t smem, int cluster, cudaStream_t s,
+                               A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = unsigned(cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
 inline bool is_row_type(int t) { return t == GPT2_F32 || t == GPT2_F16 || t == GPT2_BF16; }
 inline bool is_scaled(int t) { return t == GPT2_INT8 || t == GPT2_E4M3; }
 inline int elem_size(int t) { return t == GPT2_F32 ? 4 : is_scaled(t) ? 1 : 2; }

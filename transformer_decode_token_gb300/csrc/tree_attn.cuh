@@ -423,6 +423,8 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
     const int kvh = bh % a.kv.n_head, b = bh / a.kv.n_head;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int P = a.kv.n_positions, G = a.group;
+    pdl_wait();
+    pdl_launch_dependents();
 
     const int f0 = min(max(a.first[b], 0), a.n_rows), f1 = min(max(a.first[b + 1], f0), a.n_rows);
     const int nodes = min(f1 - f0, a.max_nodes);
@@ -861,18 +863,7 @@ cudaError_t launch_tree(K fn, const TreeArgs &a, size_t smem, cudaStream_t s)
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e == cudaSuccess && a.splits > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(a.n_seqs) * a.kv.n_head * a.row_tiles * a.splits);
-    cfg.blockDim = dim3(kNW * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = unsigned(a.splits);
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn, a);
+    return spec_launch(fn, dim3(unsigned(a.n_seqs) * a.kv.n_head * a.row_tiles * a.splits), kNW * 32, smem, a.splits, s, a);
 }
 
 template <class Tr, int D, int MT>

@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(kNW * 32, R == 1 ? 4 : R == 2 ? 3 : 2) k_tree_
     const int kvh = bh % a.kv.n_head, b = bh / a.kv.n_head;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane % LPR, grp = lane / LPR;
     const int P = a.kv.n_positions, G = a.group;
+    pdl_wait();
+    pdl_launch_dependents();
     const int f0 = min(max(a.first[b], 0), a.n_rows), f1 = min(max(a.first[b + 1], f0), a.n_rows);
     const int nodes = min(f1 - f0, a.max_nodes);
     const int row0 = rt * R, rows = min(nodes * G - row0, R);

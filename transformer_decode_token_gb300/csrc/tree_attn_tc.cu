@@ -388,7 +388,6 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
     __shared__ int start_b, start_u, start_t;
     __shared__ int sm_bad, sm_fail;
 
-    pdl_launch_dependents();                     // (k_tree_join waits for this kernel's end)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     uint8_t *sm = raw + (base - smem_addr(raw));
@@ -414,6 +413,8 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
             *reinterpret_cast<uint4 *>(sm + S::kOffOnes + i * 16) = make_uint4(one, one, one, one);
         fence_async();
     }
+    pdl_wait();
+    pdl_launch_dependents();                     // (k_tree_join waits for this kernel's end)
     // this CTA's run of the list
     const long long all = tiles_before(a, a.n_seqs, N, red);
     const long long begin = run_begin(all, blockIdx.x, gridDim.x), end = run_begin(all, blockIdx.x + 1, gridDim.x);
@@ -843,6 +844,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, co
     using T16 = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     const int runs = gridDim.x;
     pdl_wait();                                   // k_tree_tc's parts
+    pdl_launch_dependents();
     Head h;
     int first = -1;
 #pragma unroll
@@ -933,20 +935,9 @@ cudaError_t launch_tc(const TreeArgs &a, int sms, void *workspace, cudaStream_t 
     const int runs = sms * Shape<D, N>::kPerSM;
     Part<D, N> *parts = static_cast<Part<D, N> *>(workspace);
     Head *heads = reinterpret_cast<Head *>(parts + 2 * runs);
-    fn<<<runs, Shape<D, N>::kThreads, Shape<D, N>::kBytes, s>>>(km, vm, a, parts, heads);
-    e = cudaGetLastError();
+    e = spec_launch(fn, dim3(runs), Shape<D, N>::kThreads, Shape<D, N>::kBytes, 1, s, km, vm, a, parts, heads);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(runs, kJoinCut);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_tree_join<BF, D, N>, a, static_cast<const Part<D, N> *>(parts),
-                              static_cast<const Head *>(heads));
+    return spec_launch(k_tree_join<BF, D, N>, dim3(runs, kJoinCut), kJoinThreads, 0, 1, s, a, parts, heads);
 }
 
 template <int D, int N>

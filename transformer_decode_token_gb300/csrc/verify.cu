@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(kStatThreads) k_row_stats(const VerifyArgs a)
 {
     __shared__ float red[kStatThreads / 32];
     __shared__ unsigned long long keys[kStatThreads / 32];
-    pdl_launch_dependents();
+    pdl_wait();
+    pdl_launch_dependents();                       // (k_verify reads the call's inputs from then on)
     const int row = blockIdx.x, chunk = blockIdx.y, tid = threadIdx.x;
     if (row >= min(max(a.first[a.n_seqs], 0), a.n_rows)) return;
     // chunks of a row: equal shares, a multiple of 4
@@ -475,8 +476,7 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (n_rows > 0) {
-        k_row_stats<<<dim3(n_rows, a.chunks), kStatThreads, 0, s>>>(a);
-        rc = spec_rc(cudaGetLastError());
+        rc = spec_rc(spec_launch(k_row_stats, dim3(n_rows, a.chunks), kStatThreads, 0, 1, s, a));
         if (rc != GPT2_OK) return rc;
     }
     cudaLaunchConfig_t cfg = {};
