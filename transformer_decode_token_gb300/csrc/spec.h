@@ -58,6 +58,10 @@ inline bool kv_ok(const gpt2_kv *kv)
     return (long long)kv->n_head * kv->n_positions < (1ll << 31);
 }
 
+// Clusters of 2, 4, 8 and 16 CTAs that run at once, per resident CTA of an SM (as
+// the runtime reports them: a cluster stays within a group of 16 to 20 SMs).
+constexpr int kClustersFit[] = {76, 36, 17, 7};
+
 // Multiprocessors of the current device (0 and *rc on failure, also where it
 // is not of compute capability 10.3).  Looked up once per device.
 int spec_sms(int *rc);

@@ -51,16 +51,13 @@ int few_rows(const gpt2_kv &kv, int n_seqs, int rows)
 }
 
 // CTAs (of a cluster) that share a unit's cache: twice as many while all clusters
-// still find a place at once, and each CTA has 128 positions or more.  Clusters of 2,
-// 4, 8 and 16 CTAs that run at once, per resident CTA of an SM (as the runtime
-// reports for 152 SMs): a cluster stays within a group of 16 to 20 SMs.  One
-// cluster more than that costs a second round: 24 units of 8 fp32 rows over
-// 1,024 positions took 9.4 us with 8 CTAs each, 15.3 with 16.
+// still run at once (one too many costs a second round: 24 units of 8 fp32 rows
+// over 1,024 positions took 9.4 us with 8 CTAs each, 15.3 with 16), and each CTA has
+// 128 positions or more.
 int splits_for(long long units, int positions, int resident)
 {
-    constexpr int kFit[] = {76, 36, 17, 7};
     int n = 1;
-    for (int i = 0; i < 4 && units <= kFit[i] * resident && positions >= 256 * n; ++i) n *= 2;
+    for (int i = 0; i < 4 && units <= kClustersFit[i] * resident && positions >= 256 * n; ++i) n *= 2;
     return n;
 }
 

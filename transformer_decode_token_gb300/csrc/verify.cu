@@ -30,7 +30,7 @@ constexpr int kChunk = 8192;       // logits per CTA of k_row_stats
 constexpr int kStatThreads = 256;
 constexpr int kVec = kChunk / 4 / kStatThreads;   // 16-byte loads in flight per thread
 constexpr int kVThreads = 512;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kBatch = 8;          // ids whose loads a thread has in flight together
 
 struct Stat {
@@ -151,6 +151,9 @@ struct Walk {
     int choice[GPT2_MAX_NODES];        // temperature 0
     int token[GPT2_MAX_NODES];
     bool valid[GPT2_MAX_NODES];
+    // nodes that can be tried (token and parent's logits are sound), and those
+    // of them that are accepted if no sibling was rejected before
+    unsigned long long usable, first_ok;
     // children of `cur` rejected so far: their tokens (draft on one token), or
     // 1 / the sums that bring what is left back to a distribution
     int rejected[GPT2_MAX_NODES];
@@ -166,21 +169,21 @@ struct Walk {
 __device__ void walk_on(const VerifyArgs &a, Walk &w)
 {
     w.need_mass = false;
-    while (w.left) {
-        const int i = __ffsll((long long)w.left) - 1;
-        w.left &= w.left - 1;
-        const int x = w.token[i];
-        if (x < 0 || x >= a.V || !w.valid[w.cur]) continue;
+    const unsigned long long usable = w.usable, first_ok = w.first_ok;
+    unsigned long long left = w.left;
+    while (left &= usable) {
+        const int i = __ffsll((long long)left) - 1;
+        left &= left - 1;
         bool yes;
         float r = 0.f;
-        if (a.c_hi == 0.f) {
-            yes = w.choice[w.cur] == x;
+        if (w.n_rejected == 0) {
+            yes = first_ok >> i & 1;
+            r = w.prob[i];
         } else {
+            const int x = w.token[i];
             r = w.prob[i];
             if (a.draft) {
-                for (int k = 0; k < w.n_rejected; ++k) {
-                    r = fmaxf(r - w.q[i], 0.f) * w.inv_mass[k];
-                }
+                for (int k = 0; k < w.n_rejected; ++k) r = fmaxf(r - w.q[i], 0.f) * w.inv_mass[k];
             } else {
                 r = w.dead ? 0.f : r * w.scale;
                 for (int k = 0; k < w.n_rejected; ++k)
@@ -191,23 +194,24 @@ __device__ void walk_on(const VerifyArgs &a, Walk &w)
         if (yes) {
             w.path[w.length++] = i;
             w.cur = i;
-            w.left = w.children[i];
+            left = w.children[i];
             w.n_rejected = 0;
             w.scale = 1.f;
             w.dead = false;
         } else if (a.c_hi != 0.f) {
-            w.rejected[w.n_rejected] = x;
+            w.rejected[w.n_rejected] = w.token[i];
             w.inv_mass[w.n_rejected++] = 1.f;
             if (!a.draft) {
                 const float rest = 1.f - r;
                 if (rest > 0.f) w.scale *= __frcp_rn(rest);
                 else w.dead = true;
-            } else if (w.left) {
+            } else if (left & usable) {
                 w.need_mass = true;
-                return;
+                break;
             }
         }
     }
+    w.left = left;
 }
 
 __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
@@ -227,6 +231,7 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
         w.children[tid] = 0;
         if (tid > 0 && tid < nodes) parent = a.parents[f0 + tid];
         if (tid < nodes) w.token[tid] = a.tokens[f0 + tid];
+        if (tid == 0) w.usable = w.first_ok = 0;
     }
     __syncthreads();
     // (k_row_stats writes none of what is read before the wait)
@@ -240,6 +245,11 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
             ux = a.u_accept[f0 + tid];
             if (a.draft) qx = a.draft[at];
         }
+    }
+    if (a.c_hi != 0.f) {                           // the random numbers of the final draw, into L2
+        const int share = (a.V + a.cluster - 1) / a.cluster, to = min(a.V, (rank + 1) * share);
+        for (int v = rank * share + tid * 32; v < to; v += kVThreads * 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.u_draw + size_t(b) * a.V + v));
     }
     pdl_wait();                                    // k_row_stats' sums
     // eight threads per node join its chunks
@@ -278,13 +288,21 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
         }
     }
     __syncthreads();
-    if (parent >= 0 && parent < tid) {
+    if (parent >= 0 && parent < tid && w.valid[parent] && w.token[tid] >= 0 && w.token[tid] < a.V) {
         w.u[tid] = ux;
         w.q[tid] = qx;
-        // lx - m in two parts, so that its rounding does not show (no second part
-        // where the first is -infinity: a logit of -infinity, or a difference past fp32's range)
-        const float m = w.m[parent], d = lx - m, t = d + m, rest = (lx - t) + (m - (t - d));
-        w.prob[tid] = d >= -FLT_MAX ? weight(a, d, rest) * w.inv_z[parent] : 0.f;
+        bool ok;
+        if (a.c_hi == 0.f) {
+            ok = w.choice[parent] == w.token[tid];
+        } else {
+            // lx - m in two parts, so that its rounding does not show (no second part
+            // where the first is -infinity: a logit of -infinity, or a difference past fp32's range)
+            const float m = w.m[parent], d = lx - m, t = d + m, rest = (lx - t) + (m - (t - d));
+            w.prob[tid] = d >= -FLT_MAX ? weight(a, d, rest) * w.inv_z[parent] : 0.f;
+            ok = ux * qx < w.prob[tid];
+        }
+        atomicOr(&w.usable, 1ull << tid);
+        if (ok) atomicOr(&w.first_ok, 1ull << tid);
     }
     if (tid == 0) {
         w.cur = 0;
@@ -300,16 +318,18 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
     const cg::cluster_group cl = cg::this_cluster();
     const int per = (a.V + a.cluster - 1) / a.cluster, v0 = rank * per, v1 = min(a.V, v0 + per);
     int round = 0;
-    // what is left of p at id v after the rejected children (scaled by any factor)
-    auto residual = [&](float p, float q, int v, int n) {
-        if (a.draft) {
-            for (int k = 0; k < n; ++k) p = fmaxf(p - q, 0.f) * w.inv_mass[k];
-        } else {
-            if (w.dead) return 0.f;
-            for (int k = 0; k < n; ++k)
-                if (w.rejected[k] == v) p = 0.f;
+    // what is left of p at ids v, v + kVThreads, .. after n rejected children
+    // (scaled by any factor)
+    auto residual = [&](float (&p)[kBatch], const float (&q)[kBatch], int v, int n) {
+        for (int k = 0; k < n; ++k) {
+            const float inv = a.draft ? w.inv_mass[k] : w.dead ? 0.f : 1.f;
+            const int x = w.rejected[k];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (a.draft) p[i] = fmaxf(p[i] - q[i], 0.f) * inv;
+                else p[i] = x == v + i * kVThreads ? 0.f : p[i] * inv;
+            }
         }
-        return p;
     };
     for (;;) {
         if (tid == 0) walk_on(a, w);
@@ -328,7 +348,10 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
                 q[i] = v < v1 ? a.draft[row + v] : 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) s += residual(weight(a, x[i] - m) * iz, q[i], 0, n);
+            for (int i = 0; i < kBatch; ++i) x[i] = weight(a, x[i] - m) * iz;
+            residual(x, q, b0, n);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) s += x[i];
         }
         s = warp_sum(s);
         if ((tid & 31) == 0) red[tid >> 5] = double(s);
@@ -371,15 +394,15 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
                         q[i] = dense && v < v1 ? a.draft[row + v] : 0.f;
                     }
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int v = b0 + i * kVThreads;
-                        const float p = weight(a, x[i] - m) * iz;
-                        const float r = n > 0 ? residual(p, q[i], v, n) : p;
-                        if (r > 0.f) {
-                            const unsigned long long k = argmax_key(__fdividef(r, -logf(e[i])), uint32_t(v));
+                    for (int i = 0; i < kBatch; ++i) x[i] = weight(a, x[i] - m) * iz;
+                    residual(x, q, b0, n);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        if (x[i] > 0.f) {
+                            const unsigned long long k =
+                                argmax_key(__fdividef(x[i], -logf(e[i])), uint32_t(b0 + i * kVThreads));
                             best = k > best ? k : best;
                         }
-                    }
                 }
                 best = warp_max_u64(best);
                 if ((tid & 31) == 0) keys[tid >> 5] = best;
@@ -470,13 +493,16 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
         a.c_hi = std::nextafterf(float(c), 0.f);    // below c, so that the rest is positive
         a.c_lo = std::max(float(c - double(a.c_hi)), FLT_TRUE_MIN);   // (and not zero, for the largest temperatures)
         // the final draw reads a row with the CTAs of a cluster: as many as
-        // keep 2048 ids or more each, while all sequences' fit the GPU together (two per SM)
-        while (a.cluster < kMaxCluster && vocab >= 4096 * a.cluster && n_seqs * a.cluster * 2ll <= 2ll * sms)
-            a.cluster *= 2;
+        // keep 2048 ids or more each, while all sequences' clusters run at once
+        for (int i = 0; i < 4 && vocab >= 4096 * a.cluster && n_seqs <= kClustersFit[i] * 2; ++i) a.cluster *= 2;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (n_rows > 0) {
         rc = spec_rc(spec_launch(k_row_stats, dim3(n_rows, a.chunks), kStatThreads, 0, 1, s, a));
+        if (rc != GPT2_OK) return rc;
+    }
+    if (a.cluster > 8) {
+        rc = spec_rc(cudaFuncSetAttribute(k_verify, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
         if (rc != GPT2_OK) return rc;
     }
     cudaLaunchConfig_t cfg = {};
