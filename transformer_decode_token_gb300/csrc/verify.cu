@@ -27,7 +27,7 @@ namespace gpt2 {
 namespace {
 
 constexpr int kChunk = 8192;       // logits per CTA of k_row_stats
-constexpr int kStatThreads = 256;
+constexpr int kStatThreads = 128;
 constexpr int kVec = kChunk / 4 / kStatThreads;   // 16-byte loads in flight per thread
 constexpr int kVThreads = 512;
 constexpr int kMaxCluster = 16;
@@ -383,8 +383,12 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
             for (int pass = 0; pass < 2; ++pass) {
                 const int n = pass == 0 ? w.n_rejected : 0;
                 const bool dense = a.draft && n > 0;
-                unsigned long long best = 0;
-                for (int b0 = v0 + tid; b0 < v1; b0 += kBatch * kVThreads) {
+                // the best value and its id; what the warp's best rules out needs no
+                // logarithm (-log u >= 1 - u; the margin is far above its rounding)
+                float top = -1.f, bound = -1.f;
+                int id = -1;
+                for (int w0 = v0; w0 < v1; w0 += kBatch * kVThreads) {
+                    const int b0 = w0 + tid;
                     float x[kBatch], q[kBatch], e[kBatch];
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) {
@@ -398,12 +402,13 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
                     residual(x, q, b0, n);
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i)
-                        if (x[i] > 0.f) {
-                            const unsigned long long k =
-                                argmax_key(__fdividef(x[i], -logf(e[i])), uint32_t(b0 + i * kVThreads));
-                            best = k > best ? k : best;
+                        if (x[i] > 0.f && x[i] > bound * (1.f - e[i])) {
+                            const float y = __fdividef(x[i], -logf(e[i]));
+                            if (y > top) top = y, id = b0 + i * kVThreads;
                         }
+                    bound = warp_max(top) * 0.999f;
                 }
+                unsigned long long best = id >= 0 ? argmax_key(top, uint32_t(id)) : 0;
                 best = warp_max_u64(best);
                 if ((tid & 31) == 0) keys[tid >> 5] = best;
                 __syncthreads();
