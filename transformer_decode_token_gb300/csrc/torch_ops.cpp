@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -133,6 +134,21 @@ int64_t row_stride(const at::Tensor &t, const char *name, int64_t H, int64_t D, 
     return t.size(0) > 1 ? t.stride(0) : H * D;
 }
 
+// A tensor of this shape in `whole`'s memory, from element `from` on: results of
+// one call are made in one allocation (1.3 us each on the Arm host, as long as
+// the marshalling itself).
+at::Tensor part(const at::Tensor &whole, int64_t from, at::IntArrayRef shape)
+{
+    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+    t->set_sizes_contiguous(shape);
+    t->set_storage_offset(from);
+    return at::Tensor(std::move(t));
+}
+
+// Memory of a call in flight, returned to torch's allocator when the call has
+// been queued: what takes it next on this stream runs after it.
+c10::DataPtr scratch(size_t bytes) { return c10::cuda::CUDACachingAllocator::get()->allocate(bytes); }
+
 int32_t to_int(PyObject *o, const char *name)
 {
     const long v = PyLong_AsLong(o);
@@ -196,6 +212,27 @@ PyObject *guarded(const char *name, Py_ssize_t want, Py_ssize_t got, F f)
     return nullptr;
 }
 
+// The caller's workspace, or one of `need` bytes.
+struct Workspace {
+    void *p = nullptr;
+    size_t bytes = 0;
+    c10::DataPtr own;
+    Workspace(PyObject *o, size_t need, int dev)
+    {
+        if (o != Py_None) {
+            const at::Tensor &t = tensor(o, "workspace");
+            if (!t.is_contiguous() || !t.is_cuda() || t.get_device() != dev)
+                throw Bad{"workspace must be contiguous and on the current device"};
+            p = t.data_ptr();
+            bytes = t.nbytes();
+        } else if (need) {
+            own = scratch(need);
+            p = own.get();
+            bytes = need;
+        }
+    }
+};
+
 // k, v, k_cache, v_cache, slot, pos, k_scale, v_scale
 PyObject *kv_store(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -236,8 +273,9 @@ PyObject *kv_load(PyObject *, PyObject *const *a, Py_ssize_t n)
             const at::ScalarType t =
                 a[6] == Py_None ? at::kFloat : reinterpret_cast<THPDtype *>(a[6])->scalar_type;
             if (row_type(t) < 0) throw Bad{"rows are float32, float16 or bfloat16"};
-            k = at::empty({rows, H, D}, cache.options.dtype(t));
-            v = at::empty({rows, H, D}, cache.options.dtype(t));
+            const at::Tensor both = at::empty({2, rows, H, D}, cache.options.dtype(t));
+            k = part(both, 0, {rows, H, D});
+            v = part(both, rows * H * D, {rows, H, D});
         } else {
             k = tensor(a[7], "k");
             v = tensor(a[8], "v");
@@ -311,18 +349,10 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (rows > 0 && B > 0) {
             const int type = row_type(q.scalar_type());
             const size_t need = g_lib.tree_attention_workspace(&cache.kv, type, int32_t(H), nodes);
-            at::Tensor ws;
-            if (a[12] != Py_None) {
-                ws = tensor(a[12], "workspace");
-                if (!ws.is_contiguous() || !ws.is_cuda() || ws.get_device() != c.dev)
-                    throw Bad{"workspace must be contiguous and on the current device"};
-            } else if (need) {
-                ws = at::empty({int64_t(need)}, q.options().dtype(at::kByte));
-            }
+            const Workspace ws(a[12], need, c.dev);
             check(g_lib.tree_attention(&cache.kv, q.data_ptr(), type, stride, int32_t(H), slot, cached, first, mask,
                                        int32_t(B), int32_t(rows), nodes, scale, out.data_ptr(), out_stride,
-                                       ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? size_t(ws.nbytes()) : 0,
-                                       c.stream),
+                                       ws.p, ws.bytes, c.stream),
                   "gpt2_op_tree_attention");
         }
         if (a[11] != Py_None) return Py_NewRef(a[11]);
@@ -356,22 +386,16 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n)
             ud = whole<float>(a[8], "u_draw", at::kFloat, {B, V}, c.dev);
         }
         const at::TensorOptions ints = logits.options().dtype(at::kInt);
-        auto result = [&](PyObject *o, const char *name, at::IntArrayRef shape) {
-            at::Tensor t = o == Py_None ? at::empty(shape, ints) : tensor(o, name);
-            whole(t, name, at::kInt, shape, c.dev);
-            return t;
+        at::Tensor made;                           // the results that are not given, one after another
+        if (a[9] == Py_None || a[10] == Py_None || a[11] == Py_None) made = at::empty({B * (T + 2)}, ints);
+        auto result = [&](PyObject *o, const char *name, int64_t from, at::IntArrayRef shape) {
+            if (o == Py_None) return part(made, from, shape);
+            whole(tensor(o, name), name, at::kInt, shape, c.dev);
+            return tensor(o, name);
         };
-        at::Tensor path = result(a[9], "path", {B, T}), n_path = result(a[10], "n_path", {B}),
-                   next = result(a[11], "next_token", {B});
-        const int64_t need = int64_t(g_lib.verify_tree_workspace(int32_t(rows), int32_t(V)));
-        at::Tensor ws;
-        if (a[12] == Py_None) {
-            ws = at::empty({need}, logits.options().dtype(at::kByte));
-        } else {
-            ws = tensor(a[12], "workspace");
-            if (!ws.is_contiguous() || !ws.is_cuda() || ws.get_device() != c.dev)
-                throw Bad{"workspace must be contiguous and on the current device"};
-        }
+        at::Tensor path = result(a[9], "path", 0, {B, T}), n_path = result(a[10], "n_path", B * T, {B}),
+                   next = result(a[11], "next_token", B * (T + 1), {B});
+        const Workspace ws(a[12], g_lib.verify_tree_workspace(int32_t(rows), int32_t(V)), c.dev);
         if (B > 0 && rows == 0) {
             path.fill_(-1);
             n_path.zero_();
@@ -379,7 +403,7 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n)
         } else if (B > 0) {
             check(g_lib.verify_tree(lg, int32_t(V), tokens, parents, first, int32_t(B), int32_t(rows), T, temperature,
                                       draft, ua, ud, path.data_ptr<int32_t>(), n_path.data_ptr<int32_t>(),
-                                      next.data_ptr<int32_t>(), ws.data_ptr(), size_t(ws.nbytes()), c.stream),
+                                      next.data_ptr<int32_t>(), ws.p, ws.bytes, c.stream),
                   "gpt2_op_verify_tree");
         }
         return Py_BuildValue("(NNN)", THPVariable_Wrap(path), THPVariable_Wrap(n_path), THPVariable_Wrap(next));
