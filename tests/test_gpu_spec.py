@@ -347,6 +347,16 @@ def test_tree_attention_many_rows_long_caches(dtype, counts, G, D):
     run_attention(rng, dtype, dtype, D, 2, G, 36000 // len(counts), cached, counts)
 
 
+@pytest.mark.parametrize("counts,G", [([64, 33, 17], 1), ([20, 3], 3), ([40, 1], 1), ([9], 4), ([17], 1), ([21, 0, 32], 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_tree_attention_many_rows_longest_caches(dtype, counts, G):
+    """64 dimensions in caches so long that the tensor cores' kernel takes over
+    for few sequences too."""
+    rng = np.random.default_rng(sum(counts) + G)
+    cached = [int(x) for x in rng.integers(0, 3000, len(counts))]
+    run_attention(rng, dtype, dtype, 64, 2, G, 130000 // len(counts), cached, counts, S=len(counts))
+
+
 @pytest.mark.parametrize("counts,G,D", [(17, 1, 64), (33, 1, 128), (5, 4, 128), (40, 2, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_tree_attention_many_units(dtype, counts, G, D):
@@ -495,6 +505,12 @@ def test_what_is_not_seen_does_not_enter_many_rows(dtype, D, c, n, K, P):
             check_attention(got[sees][:, h:][..., rest], want[sees][..., rest], tol[sees][..., rest])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("c,n,K,P", [(1500, 24, 2, 130000), (1020, 40, 1, 180000)])
+def test_what_is_not_seen_does_not_enter_longest_caches(dtype, c, n, K, P):
+    test_what_is_not_seen_does_not_enter_many_rows(dtype, 64, c, n, K, P)
+
+
 def test_wide_value_scales():
     """int8 value scales that differ by 2^40 within a sequence, rising and
     falling over the tiles, zero among them."""
@@ -614,14 +630,14 @@ def test_many_rows_more_sequences_than_threads():
                   slots=[int(x) for x in rng.integers(0, 3, B)], S=3)
 
 
-@pytest.mark.parametrize("counts,D", [([24, 40, 3], 64), ([64, 2], 128)])
-def test_many_rows_strided_streams_and_graphs(counts, D):
+@pytest.mark.parametrize("counts,D,P", [([24, 40, 3], 64, 8000), ([24, 40, 3], 64, 16000), ([64, 2], 128, 8000)])
+def test_many_rows_strided_streams_and_graphs(counts, D, P):
     """The tensor cores' kernel: q inside fused rows, out inside wider ones; the
     same bits on another stream, with two calls in flight, with a workspace of
     the caller's, and from two captured graphs that share it."""
     import torch
     rng = np.random.default_rng(19)
-    B, K, P = len(counts), 4, 8000
+    B, K = len(counts), 4
     cached = [int(x) for x in rng.integers(0, 1500, B)]
     kc, vc = (make_cache(rng, "bf16", B, K, P, D)[0] for _ in range(2))
     masks = np.concatenate([binding.tree_masks(random_tree(rng, c)) for c in counts])

@@ -53,8 +53,8 @@ struct RowArgs {
 // A thread's kVals values of a row are two pieces of four.  Where the rows or
 // the cache are fp32 the pieces lie half a row apart, so that the 16-byte
 // accesses of neighbouring threads follow one another and fill whole sectors
-// (8 consecutive fp32 values per thread wrote half sectors: 40 us instead of 24
-// for 17,408 rows of 12 x 64 int8 read back as fp32); else they are
+// (8 consecutive fp32 values per thread wrote half sectors: 1.7 times as long for
+// 17,408 rows of 12 x 64 int8 read back as fp32); else they are
 // neighbours.
 template <typename T, typename CT>
 constexpr bool kApart = sizeof(T) == 4 || sizeof(CT) == 4;
@@ -214,8 +214,10 @@ __device__ __forceinline__ float e4m3_scale(float top)
 // kVals threads are neighbours in a warp and find the largest value by
 // shuffles.  A block's units follow one another, so its accesses do.  With U
 // units a thread has U units' loads in flight; measured for 17,408 rows of 12 x
-// 64 fp32 into int8 and back (two launches): U = 2 and 4 (store, load) 48.7 us,
-// 5.6 TB/s; 1 and 2 49.4; 4 and 8 54.4; 8 and 16 85 (registers).
+// 64 fp32 into int8 and back (two launches): U = 2 and 4 (store, load) 46 us, 5.9
+// TB/s, 0.87 of the measured copy's rate; 1 and 2 0.7 us more, 4 and 8 6 us, 8
+// and 16 36 us (registers).  64 rows, a decode step's: 3.1 us for both, the
+// launches.
 // CT: the cache's element type (int8_t and __nv_fp8_e4m3 with scales).
 struct Unit {
     int i, part, h;                // row, 0: k / 1: v, head

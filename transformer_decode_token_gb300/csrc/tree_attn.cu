@@ -20,14 +20,18 @@ int tensor_tile(const gpt2_kv &kv, int q_dtype, int rows)
 }
 
 // They pay for their second kernel and for the change from one unit to the next
-// where caches are long and there is much of them.  Measured in us against the
-// other kernel (query rows x cache heads x sequences, positions, dimensions):
-// 64 x 12 x 32, 4,000, 64: 86 / 155; 64 x 12 x 4, 2,000, 64: 27 / 31; 32 x 8 x 2,
-// 8,000, 128: 27 / 53; 32 x 8 x 2, 2,000, 128: 16 / 18; but 32 x 12, 4,000, 64:
-// 18 / 11; 24 x 12 x 64, 540, 64: 56 / 35.
-bool tensor_pays(const gpt2_kv &kv, int n_seqs)
+// where there is much of the cache, sooner with more rows per tile and with
+// longer rows of the cache.  Measured in us against the other kernel (query rows x
+// cache heads x sequences, positions, dimensions; in millions of elements of k):
+//   64 x 12 x 32, 4,096, 64 (101): 94 / 170;  64 x 12 x 16, 1,600 (20): 42 / 53;
+//   64 x 12 x 4, 4,096 (13): 31 / 36;  64 x 12 x 8, 1,600 (10): 32 / 30
+//   32 x 12 x 8, 4,096, 64 (25): 31 / 38;  32 x 12 x 8, 2,400 (15): 27 / 26
+//   32 x 8 x 2, 4,096, 128 (8): 20 / 28;  32 x 8 x 1, 4,096 (4): 18 / 20;
+//   32 x 8 x 2, 1,600 (3): 17 / 16
+bool tensor_pays(const gpt2_kv &kv, int n_seqs, int tile)
 {
-    return (long long)n_seqs * kv.n_head * kv.n_positions * kv.head_dim >= 4000000;
+    const long long least = kv.head_dim == 128 ? 4000000 : tile == 64 ? 11000000 : 16000000;
+    return (long long)n_seqs * kv.n_head * kv.n_positions * kv.head_dim >= least;
 }
 
 // Query rows per tile on the CUDA cores (tree_attn_few.cu; 0: the matrix
@@ -112,7 +116,7 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     a.group = n_head / kv->n_head;
     a.scale_log2 = scale * 1.4426950408889634f;
     const int rows = max_nodes * a.group, can = tensor_tile(*kv, q_dtype, rows);
-    const int tc = can && tensor_pays(*kv, n_seqs) ? can : 0;
+    const int tc = can && tensor_pays(*kv, n_seqs, can) ? can : 0;
     const int few = few_rows(*kv, n_seqs, rows);
     const int tile = tc ? tc : few ? few : rows <= 16 ? 16 : 32;   // (the matrix instructions: 16 query rows per warp, or 32)
     a.row_tiles = (rows + tile - 1) / tile;

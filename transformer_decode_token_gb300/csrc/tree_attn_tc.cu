@@ -9,9 +9,9 @@
 // dimension contiguous: an MN-major A operand).
 //   a warp     one lane: TMA loads of K and V tiles (128 rows, 64 dimensions
 //              per box, 128-byte swizzle) into two rings
-//   two warps  tcgen05.mma of the scores (ready a tile ahead) and of the weighted
-//              sums (the weights' two parts as 2 N columns of one MMA)
-//   the others a thread owns one cache row of the tile (its TMEM lane) and 16
+//   one or two tcgen05.mma of the scores (ready a tile ahead) and of the weighted
+//   warps      sums (the weights' two parts as 2 N columns of one MMA)
+//   the others a thread owns one cache row of the tile (its TMEM lane) and kC
 //              of the query rows: p = 2^(s - m), split in two 16-bit parts
 //              (hi + lo: 16 bits and more of every weight), written to shared
 //              memory as the B operand (MN-major, without swizzle: a thread's
@@ -24,16 +24,23 @@
 // Work split.  The tiles of all (sequence, cache head, query row tile) units form
 // one list; each CTA of a grid that fills the GPU once takes an equal run of it,
 // so ragged lengths and odd numbers of units leave no SM idle (with a CTA per
-// unit, 384 units on 304 places took two rounds: 111 us instead of 68 for 32
-// trees of 64 over 4,000 positions; splitting units over clusters left SMs
-// without a place for a whole cluster).  The producer runs ahead into the next
+// unit, 384 units on 304 places took two rounds, 1.6 times as long; splitting
+// units over clusters left SMs without a place for a whole cluster).  The producer runs ahead into the next
 // unit.  A unit that lies within one run is written at once; of one that several
 // runs share, each leaves (m, sum, O) in the workspace and k_tree_join adds them
 // up in the runs' order, so every call gives the same bits.
 //
-// What bounds it: HBM, by design: a tile of 128 rows is 32 KB (64 dimensions)
-// and takes an SM's share of the measured bandwidth 1,400 cycles; the MMAs of N
-// = 64 take about 800 and the softmax about 900, on different units.
+// What bounds it: 32 f16 trees of 64 nodes over 2,000 to 4,000 positions, 12 heads
+// of 64: 87 us, 3.5 TB/s, 214 TFLOP/s, where reading the cache takes 45.  An SM's
+// share of HBM brings a tile of 128 rows (32 KB) in 1,400 cycles and its MMAs take
+// 800, but the softmax of 64 query rows keeps the SM 1,700 (of 16 exponentials and
+// two conversions per thread and 16 columns, and the barriers between the
+// warps), and every change from one unit to the next costs a CTA some 15,000
+// cycles of empty pipeline.  With 32 query rows of 128 dimensions (8 sequences, 4,000
+// to 16,000 bf16 positions, 8 heads) the softmax is a quarter of that per byte:
+// 62 us, 5.3 TB/s.  Not kept: one part of the weights only (the error is 1.4
+// times the plain form's), a pair of tiles per step (registers spill: 170 us), 16
+// softmax warps in one CTA per SM (127 us).
 #include <cuda.h>
 
 #include "tree_attn.cuh"
@@ -48,7 +55,6 @@ constexpr int kRowsT = 128;                      // cache rows of a tile
 constexpr uint32_t kBoxB = kRowsT * 128;         // one TMA box: 128 rows of 64 16-bit dimensions
 constexpr float kRaise = 8.f;                    // log2 of the weight that raises a maximum
 constexpr float kNone = -1e30f;                  // the maximum of a row that has seen nothing
-
 
 // 64 dimensions: two CTAs per SM, which overlap one another's softmax, products
 // and changes of unit (one CTA of 16 softmax warps took 2,400 cycles a tile, two
