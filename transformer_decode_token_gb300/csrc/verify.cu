@@ -13,7 +13,7 @@
 // What bounds it, at a vocabulary of 50,257: 64 chains of 8 nodes 28.4 us (4.1
 // TB/s): about 18 for the rows (5.7 TB/s) and 10 for the draw, whose loads begin
 // where the walk ends and whose logarithms and keys cost half of it; one chain of 6
-// nodes 8.0 us, 8 trees of 8 11.4: two launches and the chain first, tokens,
+// nodes 8.5 us, 8 trees of 8 12: two launches and the chain first, tokens,
 // logits; sums; walk; row and random numbers; the cluster's join.
 //
 // Rounding: everything is fp32 (a few units in the last place; the sums over
