@@ -1009,6 +1009,28 @@ def test_verify_ties_take_the_lowest_id():
     assert got == [([0], 77)]
 
 
+@pytest.mark.parametrize("V", [1, 7, 130, 8192, 20000, 50257])
+def test_verify_greedy_takes_the_lowest_of_equals(V):
+    """Equal highest logits anywhere in the row, zeros of both signs among them,
+    next to NaN and -infinity."""
+    rng = np.random.default_rng(V)
+    n = 40
+    logits = -rng.random((n, V)).astype(np.float32) - 1
+    for i in range(n):
+        at = rng.integers(0, V, 4)
+        logits[i, at[3]] = (np.nan, -np.inf)[i % 2]
+        if i % 3:
+            logits[i, at[:3]] = 0.0
+            logits[i, at[:3].min()] = -0.0
+        else:
+            logits[i, at[:3]] = 5.0
+    got = run_verify(logits, np.zeros(n, int), -np.ones(n, int), np.arange(n + 1), 1, 0.0, None, None, None)
+    for i in range(n):
+        x = logits[i]
+        ok = (x > -np.inf).any()
+        assert got[i] == ([0], int(np.nanargmax(x)) if ok else -1)
+
+
 def test_verify_gives_the_targets_distribution():
     """The first token a sequence gains (an accepted child's, or the drawn one)
     is distributed as softmax(logits / T) whatever the draft: chi-square of

@@ -10,11 +10,12 @@
 // random numbers once).  A rejected child that has a sibling behind it costs
 // one more pass over the row, for the sum that makes the rest a distribution.
 //
-// What bounds it, at a vocabulary of 50,257: 64 chains of 8 nodes 28.4 us (4.1
-// TB/s): about 18 for the rows (5.7 TB/s) and 10 for the draw, whose loads begin
-// where the walk ends and whose logarithms and keys cost half of it; one chain of 6
-// nodes 8.5 us, 8 trees of 8 12: two launches and the chain first, tokens,
-// logits; sums; walk; row and random numbers; the cluster's join.
+// What bounds it, at a vocabulary of 50,257: 64 chains of 8 nodes 28.3 us (4.1
+// TB/s; greedy 18.9): about 18 for the rows (5.7 TB/s) and 10 for the draw, whose
+// loads begin where the walk ends and whose logarithms and keys cost half of it;
+// one chain of 6 nodes 7.9 us, 8 trees of 8 10.7 (greedy chains of 8: 4.9, 6.9): two
+// launches and a chain of dependent steps (first, tokens, logits; sums; walk; row
+// and random numbers; the cluster's join).
 //
 // Rounding: everything is fp32 (a few units in the last place; the sums over
 // the vocabulary are of a few dozen terms per thread, then pairwise or in 64
@@ -100,20 +101,20 @@ __global__ void __launch_bounds__(kStatThreads) k_row_stats(const VerifyArgs a)
     v[kVec][2] = v[kVec][3] = -INFINITY;
     Stat *out = a.stats + size_t(row) * a.chunks + chunk;
     if (a.c_hi == 0.f) {
-        // (a NaN or -infinity gets no key)
-        unsigned long long best = 0;
+        // in order of the ids, so that the lowest of equals stays (a NaN or
+        // -infinity is never above)
+        float top = -INFINITY;
+        int id = -1;
         auto take = [&](float x, int i) {
-            if (x > -INFINITY) {
-                const unsigned long long k = argmax_key(x, uint32_t(lo + i));
-                best = k > best ? k : best;
-            }
+            if (x > top) top = x, id = i;
         };
+        take(v[kVec][0], tid);
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) take(v[i][j], head + (tid + i * kStatThreads) * 4 + j);
-        take(v[kVec][0], tid);
         take(v[kVec][1], rest + tid);
+        unsigned long long best = id >= 0 ? argmax_key(top + 0.f, uint32_t(lo + id)) : 0;   // (-0 as 0: they tie)
         best = warp_max_u64(best);
         if ((tid & 31) == 0) keys[tid >> 5] = best;
         __syncthreads();
@@ -407,12 +408,21 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) x[i] = weight(a, x[i] - m) * iz;
                     residual(x, q, b0, n);
+                    if (bound < 0.f) {             // (the first ones: side by side)
+                        float y[kBatch];
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
-                        if (x[i] > 0.f && x[i] > bound * (1.f - e[i])) {
-                            const float y = __fdividef(x[i], -logf(e[i]));
-                            if (y > top) top = y, id = b0 + i * kVThreads;
-                        }
+                        for (int i = 0; i < kBatch; ++i) y[i] = __fdividef(x[i], -logf(e[i]));
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            if (x[i] > 0.f && y[i] > top) top = y[i], id = b0 + i * kVThreads;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            if (x[i] > 0.f && x[i] > bound * (1.f - e[i])) {
+                                const float y = __fdividef(x[i], -logf(e[i]));
+                                if (y > top) top = y, id = b0 + i * kVThreads;
+                            }
+                    }
                     bound = warp_max(top) * 0.999f;
                 }
                 unsigned long long best = id >= 0 ? argmax_key(top, uint32_t(id)) : 0;
@@ -505,8 +515,9 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
         a.c_hi = std::nextafterf(float(c), 0.f);    // below c, so that the rest is positive
         a.c_lo = std::max(float(c - double(a.c_hi)), FLT_TRUE_MIN);   // (and not zero, for the largest temperatures)
         // the final draw reads a row with the CTAs of a cluster: as many as
-        // keep 2048 ids or more each, while all sequences' clusters run at once
-        for (int i = 0; i < 4 && vocab >= 4096 * a.cluster && n_seqs <= kClustersFit[i] * 2; ++i) a.cluster *= 2;
+        // keep 2048 ids or more each, while all sequences' clusters run at once (of
+        // 16 CTAs one per SM: 8 sequences took 11.6 us with 16, 10.6 with 8)
+        for (int i = 0; i < 4 && vocab >= 4096 * a.cluster && n_seqs <= kClustersFit[i] * (i == 3 ? 1 : 2); ++i) a.cluster *= 2;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (n_rows > 0) {
