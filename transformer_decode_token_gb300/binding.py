@@ -581,7 +581,7 @@ def op_kv_store(k, v, k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, s
 def op_kv_load(k_cache, v_cache, slot, pos, k_scale=None, v_scale=None, dtype=None, k=None, v=None, stream=None):
     """Reads cache rows (slot[i], pos[i]) back as (k, v), each [rows][heads]
     [head_dim] of `dtype` (float32 unless given, or the given k's); rows
-    outside the cache are zeros."""
+    outside the cache are zeros.  k and v made here share one allocation."""
     if stream is not None:
         with _on(stream):
             return op_kv_load(k_cache, v_cache, slot, pos, k_scale, v_scale, dtype, k, v)

@@ -12,9 +12,12 @@
 // lanes are made for all query rows together, so that their latencies overlap
 // (four fp32 rows of one sequence: 6.1 us instead of 6.8).  No rounding but
 // fp32's: two products and additions per instruction.
-// What bounds it: for 64 sequences of 32 to 575 bf16 rows, 12 heads of 64, 14.5 us
-// (4.1 TB/s): one round of short sequences, each a chain of dependent loads; with
+// What bounds it: for 64 sequences of 32 to 575 bf16 rows, 12 heads of 64, 14.1 us
+// (4.3 TB/s): one round of short sequences, each a chain of dependent loads; with
 // long caches HBM: 64 x 2,000 to 4,000 rows 94.9 us, 6.3 TB/s; fp32 176.6 us, 6.7.
+// Four CTAs per SM: with five, registers spill (one sequence 5.2 us instead of 4.8;
+// 64 short ones 13.9 instead of 14.3); half the accesses per tile were no better (int8
+// 83 us instead of 72 for the long caches).
 #include "tree_attn.cuh"
 
 #include <type_traits>
