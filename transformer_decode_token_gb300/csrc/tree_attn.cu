@@ -10,7 +10,9 @@ namespace {
 
 // The 5th-generation tensor cores (tree_attn_tc.cu), in tiles of 32 or 64 query
 // rows (0: not): for more than 16 query rows on a cache head over a 16-bit cache
-// of the rows' own type.
+// of the rows' own type, of 1,536 positions or more (in shorter ones the units are
+// a few tiles each: 24 rows x 12 heads x 64 sequences, 540 positions, took 56 us
+// against 35).
 int tensor_tile(const gpt2_kv &kv, int q_dtype, int rows)
 {
     if (rows <= 16 || q_dtype != kv.dtype || q_dtype == GPT2_F32 || kv.head_dim < 64) return 0;
@@ -118,7 +120,7 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     const int rows = max_nodes * a.group, can = tensor_tile(*kv, q_dtype, rows);
     const int tc = can && tensor_pays(*kv, n_seqs, can) ? can : 0;
     const int few = few_rows(*kv, n_seqs, rows);
-    const int tile = tc ? tc : few ? few : rows <= 16 ? 16 : 32;   // (the matrix instructions: 16 query rows per warp, or 32)
+    const int tile = tc ? tc : few ? few : rows <= 16 ? 16 : 32;   // (matrix instructions: 16 or 32 query rows per warp)
     a.row_tiles = (rows + tile - 1) / tile;
     const long long units = (long long)n_seqs * kv->n_head * a.row_tiles;
     if (units * 16 >= (1ll << 31)) return GPT2_ERR_INVALID_ARG;
@@ -131,7 +133,9 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
                 workspace_bytes < tree_attn_tc_workspace(kv->head_dim, can, sms)))
         return GPT2_ERR_INVALID_ARG;
     if (tc) return spec_rc(tree_attn_tc(a, tile, sms, workspace, s));
-    a.splits = splits_for(units, kv->n_positions, few ? (few == 1 ? 4 : few == 2 ? 3 : 2) : tile == 16 && kv->head_dim <= 64 ? 3 : 2);
+    // (the CTAs per SM that each kernel is compiled for)
+    const int resident = tile == 1 ? 4 : tile == 2 || (tile == 16 && kv->head_dim <= 64) ? 3 : 2;
+    a.splits = splits_for(units, kv->n_positions, resident);
     if (few) return spec_rc(tree_attn_few(a, few, s));
     const int mt = tile / 16;
     if (kv->dtype == GPT2_F32) return spec_rc(tree_attn_f32(a, mt, s));

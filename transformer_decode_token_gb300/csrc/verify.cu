@@ -13,7 +13,7 @@
 // What bounds it, at a vocabulary of 50,257: 64 chains of 8 nodes 28.3 us (4.1
 // TB/s; greedy 18.9): about 18 for the rows (5.7 TB/s) and 10 for the draw, whose
 // loads begin where the walk ends and whose logarithms and keys cost half of it;
-// one chain of 6 nodes 7.9 us, 8 trees of 8 10.7 (greedy chains of 8: 4.9, 6.9): two
+// one chain of 6 nodes 7.9 to 8.3 us, 8 trees of 8 10.7 to 11.4 (greedy chains of 8: 4.9, 6.9): two
 // launches and a chain of dependent steps (first, tokens, logits; sums; walk; row
 // and random numbers; the cluster's join).
 //
