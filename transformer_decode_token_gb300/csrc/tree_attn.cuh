@@ -677,6 +677,9 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
                 }
 #pragma unroll
                 for (int i = 0; i < T::kVR; ++i) {
+                    // (prefix rows are seen by every row and stay as they are)
+                    const int row = i / (T::kVR / (2 * T::kT8));   // the register's of this thread's 2 kT8 rows
+                    if (t * KS + row / 2 * 8 + 2 * c + row % 2 < pre) continue;
                     const uint32_t x = vr[i];
                     uint32_t gone = 0;
                     if constexpr (Tr::kMma == kTf32) gone = (x & 0x7f800000u) == 0x7f800000u ? ~0u : 0u;
