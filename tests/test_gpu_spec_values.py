@@ -7,7 +7,7 @@ import pytest
 
 from transformer_decode_token_gb300 import binding
 
-from test_gpu_spec import COMBOS, check_attention, dt, i32, make_cache, random_tree
+from test_gpu_spec import COMBOS, attend64, check_attention, dt, i32, make_cache, random_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,18 @@ def test_bad_values_of_the_prefix_reach_every_node(qt, ct, D, kernel, n, c, P, K
             if t is vc:
                 rest = [d for d in range(D) if d != 17]
                 assert torch.isfinite(got[:, h][:, rest]).all() and torch.isfinite(got[:, :h]).all()
+
+
+@pytest.mark.parametrize("qt,ct", [c for c in COMBOS if c[1] in ("int8", "e4m3")])
+@pytest.mark.parametrize("n", [1, 9, 23])
+def test_scales_of_either_sign(qt, ct, n):
+    """A value is code * scale whatever the scale's sign: negative scales give
+    what the negated codes with positive ones give."""
+    import torch
+    c = 170
+    q, kc, vc, ks, vs, mask, args = poison_setup(qt, ct, 64, n, c, 200, 2)
+    sign = torch.where(torch.arange(200, device="cuda") % 3 == 0, -1.0, 1.0)
+    for flip in (torch.full_like(sign, -1.0), sign):
+        turn = lambda t: (t.float() * flip[:, None]).to(t.dtype)
+        want, tol = attend64(q, turn(kc), turn(vc), ks, vs, [0], [c], [0, n], mask, 1 / 8)
+        check_attention(binding.op_tree_attention(q, kc, vc, *args, ks * flip, vs * flip), want, tol)

@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
         if constexpr (Tr::kScaled) {
             float top = 0.f;
 #pragma unroll
-            for (int u = 0; u < T::kT8; ++u) top = fmaxf(top, fmaxf(vs[u][0], vs[u][1]));
+            for (int u = 0; u < T::kT8; ++u) top = fmaxf(top, fmaxf(fabsf(vs[u][0]), fabsf(vs[u][1])));   // (of either sign)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             if (top > gv) {      // (the same in every thread: rows 2c, 2c + 1 of all c)
