@@ -526,8 +526,10 @@ int gpt2_op_kv_load(const gpt2_kv *kv, const int32_t *slot, const int32_t *pos, 
  * GPT-2.  mask: DEVICE uint64 [n_rows]; bit j of a node's mask lets it see node
  * j of its own sequence (a tree: itself and its ancestors); it always sees rows
  * 0..cached[b]-1.  One node per sequence with mask 1 is a decode step.  What a
- * node does not see does not enter its result, infinities and NaN included; a
- * node that sees nothing gets zeros.  slot[b] outside the cache: zeros; nodes
+ * node does not see does not enter its result, infinities and NaN included; those
+ * that it sees give what the formula gives (an infinite value with a weight above
+ * zero an infinity, a key of score -infinity the weight zero), whatever the number
+ * of rows; a node that sees nothing, or only scores of -infinity, gets zeros.  slot[b] outside the cache: zeros; nodes
  * whose cache row would be n_positions or more are not seen.
  *   q: DEVICE, q_dtype, row i's n_head heads of head_dim at element i *
  *   q_stride; out: the same type, row i at i * out_stride.  n_head is a multiple

@@ -75,3 +75,96 @@ def test_scales_of_either_sign(qt, ct, n):
         turn = lambda t: (t.float() * flip[:, None]).to(t.dtype)
         want, tol = attend64(q, turn(kc), turn(vc), ks, vs, [0], [c], [0, n], mask, 1 / 8)
         check_attention(binding.op_tree_attention(q, kc, vc, *args, ks * flip, vs * flip), want, tol)
+
+
+def by_definition64(q, kc, vc, ks, vs, c, mask, scale):
+    """Results of one head's nodes q [n][D] over rows kc, vc [P][D] in float64,
+    infinities and NaN included, and the tolerance of what is finite: as
+    test_gpu_spec.attend64's, over the keys of finite scores."""
+    host = lambda t: t.float().cpu().numpy().astype(np.float64)
+    q, k, v = host(q), host(kc), host(vc)
+    n = len(mask)
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    coarse = kc.dtype.itemsize < 4 and "bfloat" not in str(kc.dtype)
+    with np.errstate(all="ignore"):
+        if ks is not None:
+            k, v = k * host(ks)[:, None], v * host(vs)[:, None]
+        for i in range(n):
+            see = list(range(c)) + [c + j for j in range(n) if int(mask[i]) >> j & 1]
+            kk, vv = k[see], v[see]
+            a = kk @ q[i] * scale
+            w = np.exp(a - a.max())
+            w /= w.sum()
+            out[i] = w @ vv
+            sane = np.isfinite(kk).all(1)
+            size = (np.abs(kk[sane]) @ np.abs(q[i])).max() * abs(scale)
+            flat = np.where(np.isfinite(vv), np.abs(vv), 0)
+            tol[i] = (2 * size * 2.0 ** -18 + 2.0 ** -16) * (w @ flat)
+            if coarse:
+                tol[i] += len(see) * 2.0 ** -38 * (1 if vs is None else 2) * flat.max()
+    return out, tol
+
+
+def check_with_bad(got, want, tol):
+    """NaN for NaN, infinities of the same sign, and what is finite within tol
+    and half a step of the result's type."""
+    import torch
+    g = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(g), np.isnan(want))
+    assert np.array_equal(np.isinf(g), np.isinf(want)) and np.array_equal(np.sign(g[np.isinf(g)]),
+                                                                         np.sign(want[np.isinf(want)]))
+    fine = np.isfinite(want)
+    lim = tol + np.abs(want) * torch.finfo(got.dtype).eps / 2 + 2.0 ** -25
+    assert np.all(np.abs(g[fine] - want[fine]) <= lim[fine])
+
+
+@pytest.mark.parametrize("qt,ct,D,kernel,n,c,P,K", list(attention_cases()))
+def test_seen_infinities_are_as_defined(qt, ct, D, kernel, n, c, P, K):
+    """Infinite and NaN values, keys and scales in rows that all nodes see and
+    in a node's row: infinity times a weight above zero is infinite, of both signs
+    NaN; a key of score -infinity has weight zero and one of +infinity leaves
+    NaN; whichever kernel runs."""
+    import torch
+    q, kc, vc, ks, vs, mask, args = poison_setup(qt, ct, D, n, c, P, K)
+    h, inf, nan = K - 1, math.inf, math.nan
+    spots = []                                       # {(tensor, row, dimension or None): value}
+    bad = [nan] if ct == "e4m3" else [nan, inf, -inf] if ct != "int8" else []
+    at = [0, c // 2, c - 1, c + n // 2]
+    spots += [{(vc, row, 17): x} for row in at for x in bad]
+    spots += [{(kc, row, 5): x} for row in at for x in bad]
+    if len(bad) == 3:
+        spots += [{(vc, 3, 9): inf, (vc, c - 2, 9): -inf}, {(vc, 3, 9): inf, (vc, c - 2, 9): inf, (vc, 4, 11): -inf},
+                  {(kc, 7, 5): -inf, (kc, c - 1, 5): -inf, (vc, 9, 1): inf}]
+    if ks is not None:
+        spots += [{(vs, row, None): x} for row in at for x in (nan, inf)] + [{(ks, c - 1, None): nan}]
+    for spot in spots:
+        old = {}
+        for (t, row, d), x in spot.items():
+            where = (0, h, row) if d is None else (0, h, row, d)
+            old[t, where] = t[where].clone()
+            t[where] = torch.tensor(x).to(t.dtype)
+        got = binding.op_tree_attention(q, kc, vc, *args, ks, vs)
+        s = lambda t: None if t is None else t[0, h]
+        want, tol = by_definition64(q[:, h], kc[0, h], vc[0, h], s(ks), s(vs), c, mask, 1 / math.sqrt(D))
+        check_with_bad(got[:, h], want, tol)
+        assert torch.isfinite(got[:, :h].float()).all()
+        for (t, where), x in old.items():
+            t[where] = x
+
+
+@pytest.mark.parametrize("n", [1, 3, 9, 30])
+def test_values_next_to_the_largest(n):
+    """fp32 values within a rounding of the largest number: the products' first
+    parts round to infinity, the results are finite."""
+    import torch
+    top = float(np.finfo(np.float32).max)
+    q, kc, vc, ks, vs, mask, args = poison_setup("f32", "f32", 64, n, 100, 150, 2)
+    vc[0, 1, :, 3] = top
+    vc[0, 1, 50, 7] = -top
+    vc[0, 0, 99, 63] = top
+    got = binding.op_tree_attention(q, kc, vc, *args)
+    for h in range(2):
+        want, tol = by_definition64(q[:, h], kc[0, h], vc[0, h], None, None, 100, mask, 1 / 8)
+        g = got[:, h].double().cpu().numpy()
+        # (a mean of the largest number may round past it by what tol allows)
+        assert np.all((np.abs(g - want) <= tol + np.abs(want) * 2.0 ** -22 + 1e-30) | (np.isinf(g) & (want + tol > top)))

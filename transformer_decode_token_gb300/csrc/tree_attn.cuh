@@ -308,14 +308,88 @@ struct Smem {
     static constexpr size_t kBytes = kQ > kO ? kQ : kO;   // q's operands, then the warps' sums
 };
 
+// Element i of a cache (a code without its scale) or of rows as fp32.
+__device__ __forceinline__ float row_value(const void *p, size_t i, int dtype)
+{
+    switch (dtype) {
+    case GPT2_F32: return static_cast<const float *>(p)[i];
+    case GPT2_F16: return __half2float(static_cast<const __half *>(p)[i]);
+    case GPT2_BF16: return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+    case GPT2_INT8: return float(static_cast<const int8_t *>(p)[i]);
+    default: {
+        const uint32_t h = codes_to_half2<true>(static_cast<const uint8_t *>(p)[i], 0x4140u);
+        return __half2float(__ushort_as_half(uint16_t(h)));
+    }
+    }
+}
+
+// A query row's inputs: the cache rows of its head, its place in q, its mask.
+struct RowOf {
+    gpt2_kv kv;
+    const void *q;
+    size_t q_at, row_base;
+    uint64_t mask;
+    int32_t q_dtype, pre, total;
+    float scale_log2;
+};
+
+// Dimensions dim .. dim + N - 1 (each lane its own) of one row's result, by a warp
+// in fp32 as the definition says, in three passes: the maximum, the sum of the
+// weights, the weighted values.  For results that came out not finite: the
+// kernels' products of several parts make a NaN of a seen infinity (infinity
+// times a second part of zero, infinity minus infinity), and so they do of an
+// infinite key whose weight is zero.  Slow (a cache row at a time); a row of
+// which some score is NaN or +infinity is NaN after the first pass.
+template <int D, int N>
+__device__ __noinline__ void row_by_definition(const RowOf r, int dim, float (&out)[N])
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const bool scaled = r.kv.dtype == GPT2_INT8 || r.kv.dtype == GPT2_E4M3;
+    float q[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) q[i] = row_value(r.q, r.q_at + lane * E + i, r.q_dtype) * r.scale_log2;
+    auto sees = [&](int j) { return j < r.pre || (r.mask >> (j - r.pre) & 1); };
+    auto score = [&](int j) {
+        const size_t row = r.row_base + j;
+        const float s = scaled ? r.kv.k_scale[row] : 1.f;
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) x = fmaf(q[i], row_value(r.kv.k, row * D + lane * E + i, r.kv.dtype) * s, x);
+        return warp_sum(x);
+    };
+    float m = -INFINITY, l = 0.f;
+    bool nan = false;
+    for (int j = 0; j < r.total; ++j) {
+        if (!sees(j)) continue;
+        const float s = score(j);
+        m = fmaxf(m, s);
+        nan = nan || s != s;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = nan || m == INFINITY ? __int_as_float(0x7fc00000) : 0.f;
+    if (nan || m == INFINITY || m == -INFINITY) return;
+    for (int j = 0; j < r.total; ++j)
+        if (sees(j)) l += exp2_approx(score(j) - m);
+    for (int j = 0; j < r.total; ++j) {
+        if (!sees(j)) continue;
+        const size_t row = r.row_base + j;
+        const float p = exp2_approx(score(j) - m) / l, s = scaled ? r.kv.v_scale[row] : 1.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = fmaf(p, row_value(r.kv.v, row * D + dim + i, r.kv.dtype) * s, out[i]);
+    }
+}
+
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
 // The warps' sums so [kNW][R][D] (in units of 2^(the CTA's maximum)), with their
 // maxima and sums of weights, to results: over the warps, then over the CTAs of
 // the cluster.  bad_sum(e): what is to be added to element e where some CTA is
-// `bad`.
+// `bad`.  What is not finite then is computed anew (row_by_definition).
 template <int D, int R, typename Bad>
 __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)[R], float (*sm_l)[R],
                                      float (*sm_f)[R], int *sm_bad, bool cta_bad, int rank, int f0, int row0, int kvh,
-                                     int rows, Bad bad_sum)
+                                     int rows, size_t row_base, int pre, int total, Bad bad_sum)
 {
     const int tid = threadIdx.x;
     float cta_m = 0.f, cta_l = 0.f;
@@ -340,10 +414,13 @@ __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)
         sm_m[0][tid] = cta_m;
         sm_l[0][tid] = cta_l;
     }
+    // element of q and out where row r begins
+    auto begins = [&](int r, int64_t stride) {
+        return size_t(f0 + (row0 + r) / a.group) * stride + size_t(kvh * a.group + (row0 + r) % a.group) * D;
+    };
     // four elements of a row, from element e = row * D + dim on
     auto store4 = [&](int e, const float (&v)[4]) {
-        const int r = e / D, d = e % D;
-        const size_t at = size_t(f0 + (row0 + r) / a.group) * a.out_stride + size_t(kvh * a.group + (row0 + r) % a.group) * D + d;
+        const size_t at = begins(e / D, a.out_stride) + e % D;
         if (a.q_dtype == GPT2_F32) {
             *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
@@ -358,16 +435,43 @@ __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)
             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(w[0], w[1]);
         }
     };
+    float sane = 0.f;                                // NaN once a result is not finite
+    auto finish4 = [&](int e, bool any_bad, float (&v)[4]) {
+        if (any_bad)
+            for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
+        store4(e, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sane = fmaf(v[i], 0.f, sane);
+    };
+    // results that are not finite, by whole warps, whose elements follow one
+    // another: first, the warp's first; step between its turns
+    auto anew = [&](int first, int step) {
+        if (!__any_sync(0xffffffffu, sane != 0.f)) return;
+        for (int e0 = first; e0 < rows * D; e0 += step) {
+            const int e = e0 + (tid & 31) * 4;
+            bool odd = false;
+            for (int i = 0; i < 4; ++i)
+                odd = odd || (e < rows * D && !is_finite(row_value(a.out, begins(e / D, a.out_stride) + e % D + i, a.q_dtype)));
+            for (uint32_t left = __ballot_sync(0xffffffffu, odd); left;) {   // a row at a time
+                const int r = __shfl_sync(0xffffffffu, e / D, __ffs(left) - 1), node = f0 + (row0 + r) / a.group;
+                const RowOf of{a.kv, a.q, begins(r, a.q_stride), row_base, a.mask[node], a.q_dtype, pre, total, a.scale_log2};
+                float x[4];
+                row_by_definition<D, 4>(of, e % D, x);
+                const bool mine = odd && e / D == r;
+                if (mine) store4(e, x);
+                left &= ~__ballot_sync(0xffffffffu, mine);
+            }
+        }
+    };
     if (a.splits == 1) {
         __syncthreads();
         for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
             const float sum = sm_l[0][e / D], inv = sum == 0.f ? 0.f : 1.f / sum;
             const float4 o4 = *reinterpret_cast<const float4 *>(so + e);
             float v[4] = {o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv};
-            if (cta_bad)
-                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
-            store4(e, v);
+            finish4(e, cta_bad, v);
         }
+        anew((tid & ~31) * 4, kNW * 32 * 4);
     } else {
         namespace cg = cooperative_groups;
         cg::cluster_group cl = cg::this_cluster();
@@ -397,19 +501,18 @@ __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)
             float4 x[kMaxSplits];
             float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k)
-                x[k] = k < a.splits ? *reinterpret_cast<const float4 *>(cl.map_shared_rank(so + e, k))
+            for (int i = 0; i < kMaxSplits; ++i)
+                x[i] = i < a.splits ? *reinterpret_cast<const float4 *>(cl.map_shared_rank(so + e, i))
                                     : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) {
-                const float f = sm_f[k][e / D];
-                v[0] = fmaf(x[k].x, f, v[0]), v[1] = fmaf(x[k].y, f, v[1]);
-                v[2] = fmaf(x[k].z, f, v[2]), v[3] = fmaf(x[k].w, f, v[3]);
+            for (int i = 0; i < kMaxSplits; ++i) {
+                const float f = sm_f[i][e / D];
+                v[0] = fmaf(x[i].x, f, v[0]), v[1] = fmaf(x[i].y, f, v[1]);
+                v[2] = fmaf(x[i].z, f, v[2]), v[3] = fmaf(x[i].w, f, v[3]);
             }
-            if (any_bad)
-                for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
-            store4(e, v);
+            finish4(e, any_bad, v);
         }
+        anew((rank * kNW * 32 + (tid & ~31)) * 4, a.splits * kNW * 32 * 4);
         cl.sync();          // nobody leaves while its sums are read
     }
 }
@@ -672,7 +775,7 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int j = t * KS + u * 8 + 2 * c + e;
-                            if (j >= pre && !(fabsf(vs[u][e]) <= 3.0e38f)) vs[u][e] = 0.f, bad = true;
+                            if (j >= pre && !is_finite(vs[u][e])) vs[u][e] = 0.f, bad = true;
                         }
                 }
 #pragma unroll
@@ -852,7 +955,7 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
             }
         }
     __syncthreads();
-    join<D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, cta_bad, rank, f0, row0, kvh, rows, [&](int e) {
+    join<D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, cta_bad, rank, f0, row0, kvh, rows, row_base, pre, total, [&](int e) {
         // the infinities and NaNs that were taken out, for the rows that see them
         const int r = e / D, d = e % D;
         const uint64_t sees = a.mask[f0 + (row0 + r) / G];
@@ -860,7 +963,7 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
         for (int j = pre; j < total; ++j) {
             if (!(sees >> (j - pre) & 1)) continue;
             const float v = element<Tr>(vbase + size_t(j) * T::kRowB, d) * (Tr::kScaled ? vscale[j] : 1.f);
-            if (!(fabsf(v) <= 3.0e38f)) x += v;
+            if (!is_finite(v)) x += v;
         }
         return x;
     });

@@ -363,15 +363,23 @@ __device__ __noinline__ float not_finite_seen(const void *v, int64_t row, uint64
     for (int j = pre; j < total; ++j)
         if (mask >> (j - pre) & 1) {
             const float x = float(vb[size_t(j) * D]);
-            if (!(fabsf(x) <= 3.0e38f)) sum += x;
+            if (!tree::is_finite(x)) sum += x;
         }
     return sum;
 }
 
-// Element of `out` where query row r (of a cache head's) begins.
-__device__ __forceinline__ int64_t out_row(const TreeArgs &a, const Sequence &s, int D, int kvh, int r)
+// Element of q or `out` where query row r (of a cache head's) begins.
+__device__ __forceinline__ int64_t row_at(const TreeArgs &a, const Sequence &s, int64_t stride, int D, int kvh, int r)
 {
-    return int64_t(s.f0 + r / a.group) * a.out_stride + int64_t(kvh * a.group + r % a.group) * D;
+    return int64_t(s.f0 + r / a.group) * stride + int64_t(kvh * a.group + r % a.group) * D;
+}
+
+// What row_by_definition needs of query row r.
+__device__ __forceinline__ tree::RowOf row_of(const TreeArgs &a, const Sequence &s, int D, int kvh, int r)
+{
+    return tree::RowOf{a.kv, a.q, size_t(row_at(a, s, a.q_stride, D, kvh, r)),
+                       size_t(s.row_base + int64_t(kvh) * a.kv.n_positions), a.mask[s.f0 + r / a.group], a.q_dtype, s.pre,
+                       s.total, a.scale_log2};
 }
 
 template <bool BF, int D, int N>
@@ -791,7 +799,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
                 if constexpr (!S::kOnes) sum += sm_part[1][tid] + sm_part[2][tid] + sm_part[3][tid];
                 // (what a wait that ran out leaves is NaN)
                 sm_inv[tid] = sm_fail ? nan : sum == 0.f ? 0.f : 1.f / sum;
-                if (tid < rows) sm_out[tid] = out_row(a, sq, D, kvh, row0 + tid);
+                if (tid < rows) sm_out[tid] = row_at(a, sq, a.out_stride, D, kvh, row0 + tid);
                 if (!whole) parts[place].m[tid] = sm_m[tid], parts[place].l[tid] = sm_fail ? nan : sum;
                 if (!whole && tid == 0) heads[place] = Head{w_b, unit, t0, n, sq.tiles, bad};
             }
@@ -803,6 +811,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
             if (q * 32 < D) {
                 const int dim = q * 32 + lane;
                 T16 *out = static_cast<T16 *>(a.out) + dim;
+                float sane = 0.f;                // NaN once a result is not finite
                 // (in a loop: what is run once per unit should be short, its
                 // instructions come from memory)
 #pragma unroll 1
@@ -812,20 +821,29 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
                     const int r0 = c0 + i0;
                     if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (r0 + i < rows) out[sm_out[r0 + i]] = T16(o[i] * sm_inv[r0 + i]);
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = o[i] * sm_inv[r0 + i];
+                            sane = fmaf(x, 0.f, sane);
+                            if (r0 + i < rows) out[sm_out[r0 + i]] = T16(x);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (r0 + i < rows) parts[place].o[r0 + i][dim] = o[i];
                     }
                 }
-                if (bad && whole)
-                    for (int r = c0; r < min(c0 + C, rows); ++r)
-                        out[sm_out[r]] = T16(float(out[sm_out[r]]) +
-                                             not_finite_seen<T16>(a.kv.v, sq.row_base + int64_t(kvh) * a.kv.n_positions,
-                                                                  a.mask[sq.f0 + (row0 + r) / a.group], sq.pre, sq.total,
-                                                                  D, dim));
+                // what is not finite, or should not be, is computed anew (what a wait that ran
+                // out left stays NaN)
+                if (__any_sync(0xffffffffu, sane != 0.f || (bad && whole)) && !sm_fail)
+                    for (int r = c0; r < min(c0 + C, rows); ++r) {
+                        const tree::RowOf of = row_of(a, sq, D, kvh, row0 + r);
+                        const bool odd = !tree::is_finite(float(out[sm_out[r]])) ||
+                                         (bad && not_finite_seen<T16>(a.kv.v, of.row_base, of.mask, of.pre, of.total, D, dim) != 0.f);
+                        if (!__any_sync(0xffffffffu, odd)) continue;
+                        float x[1];
+                        tree::row_by_definition<D, 1>(of, dim, x);
+                        if (odd) out[sm_out[r]] = T16(x[0]);
+                    }
                 fence_before();
             }
             if (S::kQBufs == 1 && more) have_q();
@@ -841,11 +859,31 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
 }
 
+constexpr int kJoinThreads = 256, kJoinCut = 8, kJoinAhead = 8;
+
+// Computes the results of a joined unit that are not finite anew (those of this
+// thread's turns; a warp's elements are 32 dimensions of one row).
+template <typename T16, int D, int N>
+__device__ __noinline__ void join_anew(const TreeArgs &a, const Head *head)
+{
+    const Head h = *head;
+    const Sequence s(a, h.b, N);
+    const int kvh = h.u % a.kv.n_head, row0 = h.u / a.kv.n_head * N, rows = min(s.rows - row0, N);
+    for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * D; e += kJoinCut * kJoinThreads) {
+        const int r = e / D, d = e % D;
+        T16 *out = static_cast<T16 *>(a.out) + row_at(a, s, a.out_stride, D, kvh, row0 + r) + d;
+        const bool odd = !tree::is_finite(float(*out));
+        if (!__any_sync(0xffffffffu, odd)) continue;
+        float x[1];
+        tree::row_by_definition<D, 1>(row_of(a, s, D, kvh, row0 + r), d, x);
+        if (odd) *out = T16(x[0]);
+    }
+}
+
 // Adds up the parts of a unit that several runs share, in the runs' order: a
 // row of CTAs for the run that holds the unit's first tile.
-constexpr int kJoinThreads = 256, kJoinCut = 8, kJoinAhead = 8;
 template <bool BF, int D, int N>
-__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, const Part<D, N> *parts, const Head *heads)
+__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const __grid_constant__ TreeArgs a, const Part<D, N> *parts, const Head *heads)
 {
     using T16 = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     const int runs = gridDim.x;
@@ -869,6 +907,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, co
     }
     const Sequence s(a, h.b, N);
     const int kvh = h.u % a.kv.n_head, row0 = h.u / a.kv.n_head * N, rows = min(s.rows - row0, N);
+    float sane = 0.f;                             // NaN once a result is not finite
     for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * D; e += kJoinCut * kJoinThreads) {
         const int r = e / D, d = e % D;
         float m = -parts[first].m[r], sum = parts[first].l[r], v = parts[first].o[r][d];
@@ -895,8 +934,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, co
         if (bad)
             v += not_finite_seen<T16>(a.kv.v, s.row_base + int64_t(kvh) * a.kv.n_positions,
                                       a.mask[s.f0 + (row0 + r) / a.group], s.pre, s.total, D, d);
-        static_cast<T16 *>(a.out)[out_row(a, s, D, kvh, row0 + r) + d] = T16(v);
+        static_cast<T16 *>(a.out)[row_at(a, s, a.out_stride, D, kvh, row0 + r) + d] = T16(v);
+        sane = fmaf(v, 0.f, sane);
     }
+    if (__any_sync(0xffffffffu, sane != 0.f)) join_anew<T16, D, N>(a, heads + first);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
