@@ -168,3 +168,39 @@ def test_values_next_to_the_largest(n):
         g = got[:, h].double().cpu().numpy()
         # (a mean of the largest number may round past it by what tol allows)
         assert np.all((np.abs(g - want) <= tol + np.abs(want) * 2.0 ** -22 + 1e-30) | (np.isinf(g) & (want + tol > top)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [24, 40])
+def test_many_small_weights_count(dtype, D, n):
+    """One key of weight 1 among 131,071 of weight 2^-26 each (a unit per CTA, so
+    that they are summed against its maximum): together they are 2^-9 of the
+    result, and all of it in the dimensions where the first value is zero.
+    Scores are exact in 16 bits but for the scale; the weights' own error is
+    that of an exponent of 26 in fp32, below 2^-17.  The tensor cores' fp32 sums
+    are cut off, not rounded: each of the c / 16 additions of 16 products to
+    either sum loses less than a unit in the last place, 2^-23 of the sum, per
+    product, so the numerator and the denominator (1 + 2^-9) are each off by
+    less than c 2^-23 = 2^-6 relatively.  (Dropping the small weights is off by
+    the whole result.)"""
+    import torch
+    P, c = 131072 + 64, 131072
+    K = 304 if D == 64 else 152
+    kc = torch.zeros((1, K, P, D), dtype=dt(dtype), device="cuda")
+    vc = torch.ones((1, K, P, D), dtype=dt(dtype), device="cuda")
+    kc[:, :, 1:, 0] = -8.0
+    vc[:, :, 0] = 0.0
+    q = torch.zeros((n, K, D), dtype=dt(dtype), device="cuda")
+    q[:, :, 0] = 1.0
+    kc[:, :, c:, 0] = -8.0
+    got = binding.op_tree_attention(q, kc, vc, i32([0]), i32([c]), i32([0, n]),
+                                    torch.from_numpy(binding.tree_masks([-1] + [0] * (n - 1))).cuda(), n,
+                                    scale=26 * math.log(2) / 8)
+    for i in (0, 1, n - 1):
+        tail = (c - 1 + (1 if i == 0 else 2)) * 2.0 ** -26
+        want = tail / (1 + tail)
+        worst = (got[i].double() - want).abs().max().item()
+        assert worst <= want * (2 * 2.0 ** -6 + 2.0 ** -16 + torch.finfo(dt(dtype)).eps / 2), (i, worst / want)
+    del kc, vc
+    torch.cuda.empty_cache()

@@ -17,9 +17,9 @@
 //              memory as the B operand (MN-major, without swizzle: a thread's
 //              8 query rows are one 16-byte store, a warp's stores are
 //              contiguous).
-// The maxima m are those of the tiles so far, and are only raised when a score
-// exceeds its row's by more than 2^8 in weight (a vote; the sums then rescaled
-// in TMEM): weights stay below 2^8, sums are exact multiples, and most tiles
+// The maxima m are those of the tiles so far (less a lift in fp16, kLift), and are
+// only raised when a score exceeds its row's by more than 2^8 in weight (a vote;
+// the sums then rescaled in TMEM): weights stay below 2^8 (2^15), and most tiles
 // need no reduction over their cache rows at all.
 // Work split.  The tiles of all (sequence, cache head, query row tile) units form
 // one list; each CTA of a grid that fills the GPU once takes an equal run of it,
@@ -53,7 +53,11 @@ using tree::fma2;
 
 constexpr int kRowsT = 128;                      // cache rows of a tile
 constexpr uint32_t kBoxB = kRowsT * 128;         // one TMA box: 128 rows of 64 16-bit dimensions
-constexpr float kRaise = 8.f;                    // log2 of the weight that raises a maximum
+constexpr float kRaise = 8.f;                    // log2 of the weight, over the maximum's, that raises a maximum
+// fp16 weights are 2^(s - m + 7): at most 2^15, and those down to 2^-32 of the
+// maximum's are not lost below fp16's smallest number
+template <bool BF>
+constexpr float kLift = BF ? 0.f : 7.f;
 constexpr float kNone = -1e30f;                  // the maximum of a row that has seen nothing
 
 // 64 dimensions: two CTAs per SM, which overlap one another's softmax, products
@@ -350,7 +354,7 @@ struct Head {
 };
 template <int D, int N>
 struct Part {
-    float o[N][D], m[N], l[N];                   // m: minus the maxima
+    float o[N][D], m[N], l[N];                   // m: minus the maxima (less the lift)
 };
 
 // What is not finite among the values of node rows that a query row sees (0:
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
                     for (int i = 0; i < C; ++i) most = fmaxf(most, d[i]);
                     return most;
                 };
-                if (soft_any<kSync>(distances() > kRaise)) {
+                if (soft_any<kSync>(distances() > kRaise + kLift<BF>)) {
                     // raise the maxima: this tile's per query row, over the warp's
                     // cache rows and then the warps
 #pragma unroll
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
                     if (tid < N) {
                         const float old = -sm_m[tid];
                         float m = old;
-                        for (int k = 0; k < 4; ++k) m = fmaxf(m, sm_part[k][tid]);
+                        for (int k = 0; k < 4; ++k) m = fmaxf(m, sm_part[k][tid] - kLift<BF>);
                         sm_m[tid] = -m;
                         sm_alpha[tid] = tree::exp2_approx(old - m);
                     }
