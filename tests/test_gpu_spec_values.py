@@ -204,3 +204,25 @@ def test_many_small_weights_count(dtype, D, n):
         assert worst <= want * (2 * 2.0 ** -6 + 2.0 ** -16 + torch.finfo(dt(dtype)).eps / 2), (i, worst / want)
     del kc, vc
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n", [1, 9, 24])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_far_below_zero(n, D):
+    """Every score is about -10^35, the same for all keys: the mean of the values,
+    from whichever kernel (bf16 q and k of 10^18)."""
+    import torch
+    K, P, c = 200, 1600, 1500
+    rng = np.random.default_rng(n)
+    vc, _ = make_cache(rng, "bf16", 1, K, P, D)
+    kc = torch.zeros_like(vc)
+    kc[..., 0] = -1e18
+    q = torch.zeros((n, K, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1e18
+    got = binding.op_tree_attention(q, kc, vc, i32([0]), i32([c]), i32([0, n]),
+                                    torch.from_numpy(binding.tree_masks(list(range(-1, n - 1)))).cuda(), n)
+    v = vc[0].double()
+    for i in (0, n - 1):
+        want = v[:, :c + i + 1].mean(1)
+        lim = 2.0 ** -16 * v[:, :c + i + 1].abs().mean(1) + want.abs() * 2.0 ** -8
+        assert ((got[i].double() - want).abs() <= lim).all()

@@ -58,7 +58,7 @@ constexpr float kRaise = 8.f;                    // log2 of the weight, over the
 // maximum's are not lost below fp16's smallest number
 template <bool BF>
 constexpr float kLift = BF ? 0.f : 7.f;
-constexpr float kNone = -1e30f;                  // the maximum of a row that has seen nothing
+constexpr float kNone = -3.402823466e38f;        // the maximum of a row that has seen nothing: no score is below it
 
 // 64 dimensions: two CTAs per SM, which overlap one another's softmax, products
 // and changes of unit (one CTA of 16 softmax warps took 2,400 cycles a tile, two
@@ -801,8 +801,10 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
             if (tid < N) {
                 float sum = sm_part[0][tid];
                 if constexpr (!S::kOnes) sum += sm_part[1][tid] + sm_part[2][tid] + sm_part[3][tid];
-                // (what a wait that ran out leaves is NaN)
-                sm_inv[tid] = sm_fail ? nan : sum == 0.f ? 0.f : 1.f / sum;
+                // (what a wait that ran out leaves is NaN; so is, for now, a row without a
+                // weight: it sees nothing, or scores of 2^30 and more, whose rounding
+                // alone passes the exponent's range)
+                sm_inv[tid] = sm_fail || sum == 0.f ? nan : 1.f / sum;
                 if (tid < rows) sm_out[tid] = row_at(a, sq, a.out_stride, D, kvh, row0 + tid);
                 if (!whole) parts[place].m[tid] = sm_m[tid], parts[place].l[tid] = sm_fail ? nan : sum;
                 if (!whole && tid == 0) heads[place] = Head{w_b, unit, t0, n, sq.tiles, bad};
@@ -934,7 +936,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const __grid_constan
                     m = top;
                 }
         }
-        v = sum == 0.f ? 0.f : v / sum;
+        v = sum == 0.f ? __int_as_float(0x7fc00000) : v / sum;   // (no weight: computed anew)
         if (bad)
             v += not_finite_seen<T16>(a.kv.v, s.row_base + int64_t(kvh) * a.kv.n_positions,
                                       a.mask[s.f0 + (row0 + r) / a.group], s.pre, s.total, D, d);
