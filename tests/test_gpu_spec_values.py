@@ -7,7 +7,8 @@ import pytest
 
 from transformer_decode_token_gb300 import binding
 
-from test_gpu_spec import COMBOS, attend64, check_attention, dt, i32, make_cache, random_tree
+from test_gpu_spec import (COMBOS, attend64, check_attention, dt, i32, make_cache, random_tree, run_verify, uniform,
+                           verify64, verify_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -226,3 +227,34 @@ def test_scores_far_below_zero(n, D):
         want = v[:, :c + i + 1].mean(1)
         lim = 2.0 ** -16 * v[:, :c + i + 1].abs().mean(1) + want.abs() * 2.0 ** -8
         assert ((got[i].double() - want).abs() <= lim).all()
+
+
+@pytest.mark.parametrize("temperature", [0.0, 0.8])
+@pytest.mark.parametrize("dense", [True, False])
+@pytest.mark.parametrize("V", [65537, 70000, 140001])
+def test_verify_large_vocabularies(V, dense, temperature):
+    """Vocabularies of more than 65,536 ids (more than eight chunks): ordinary
+    rows, rows of which only ids behind the first 65,536 are possible, and such
+    rows with one NaN among the others, which end the walk at temperature > 0."""
+    rng = np.random.default_rng(V)
+    logits, draft, tokens, parents, first = verify_inputs(rng, [4] * 9, V, 2)
+    for b in (1, 2, 4, 5, 7, 8):
+        logits[4 * b:4 * b + 4, :65536 if b < 6 else V // 2] = -np.inf
+        if b in (2, 5, 8):
+            logits[4 * b + (0 if b != 5 else 1), 100 if b < 8 else V // 2 - 1] = np.nan
+    # (drafts among the possible ids, the highest first)
+    for b in (1, 2, 4, 5, 7, 8):
+        for i in range(1, 4):
+            tokens[4 * b + i] = np.nanargmax(logits[4 * b + parents[4 * b + i]])
+    for again in range(20):
+        ua, ud = uniform(rng, 36), uniform(rng, 9, V)
+        ua[::2] *= 0.01
+        d = draft if dense else None
+        want, near = verify64(logits, tokens, parents, first, 4, temperature, d, ua, ud)
+        if near > 1e-5:
+            break
+    else:
+        raise AssertionError("no draw of the random numbers is clear of the borders")
+    if temperature > 0:
+        assert want[2] == ([0], -1) and want[8] == ([0], -1)
+    assert run_verify(logits, tokens, parents, first, 4, temperature, d, ua, ud) == want

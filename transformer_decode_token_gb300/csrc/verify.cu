@@ -276,6 +276,8 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
             if (mn > -INFINITY) {
                 if (m > -INFINITY) z *= weight(a, m - mn);
                 if (v.z != 0.f) z += v.z * weight(a, v.m - mn);
+            } else {
+                z += v.z;                          // (0, or the NaN of a chunk without a number)
             }
             m = mn;
         }
