@@ -415,11 +415,14 @@ int gpt2_prefill_batch(gpt2_batch *m, const int32_t *ids, const int32_t *lens, i
 
 /* n_steps device-resident greedy steps for every sequence with a cached
  * prefix: each continues at its own length with its last choice; the host is
- * not involved between steps.  Errors: NOT_READY, POSITION_RANGE (a sequence
- * would pass n_positions), INVALID_ARG. */
+ * not involved between steps.  Errors: NOT_READY (no choice yet, or a sequence
+ * whose last gpt2_accept_tree_batch left none: give it a token, or a prompt),
+ * POSITION_RANGE (a sequence would pass n_positions), INVALID_ARG. */
 int gpt2_decode_batch_greedy(gpt2_batch *m, int32_t n_steps);
 
-/* The greedy choice of the last step for sequences 0..n-1 (synchronises). */
+/* The greedy choice of the last step for sequences 0..n-1 (synchronises); after
+ * gpt2_accept_tree_batch its next tokens, -1 where it left none.  A tree step
+ * makes no choice.  NOT_READY before the first. */
 int gpt2_argmax_batch(gpt2_batch *m, int32_t *host_ids, int32_t n);
 
 /* The tokens chosen by the passes at positions first_pos .. first_pos +

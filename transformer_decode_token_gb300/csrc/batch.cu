@@ -492,11 +492,11 @@ __global__ void __launch_bounds__(kBT) k_b_tree_out(const float *x, const int32_
     for (int i = threadIdx.x; i < E; i += kBT) put_hi_lo(out, b, E, i, node ? x[size_t(b) * E + i] : 0.f);
 }
 
-// The next tokens of the sequences that took part in a tree step.
+// The next tokens of the sequences that took part in a tree step (-1: no choice).
 __global__ void k_b_set_next(int32_t *next_tok, const int32_t *next, const int32_t *n_path, int n)
 {
     const int b = threadIdx.x;
-    if (b < n && n_path[b] > 0 && next[b] >= 0) next_tok[b] = next[b];
+    if (b < n && n_path[b] > 0) next_tok[b] = next[b];
 }
 
 struct BArgmaxArgs {
@@ -676,7 +676,9 @@ struct gpt2_batch {
         std::vector<int32_t> h_first, h_tokens;                // the last step's nodes (empty: none pending)
     } tree;
     std::vector<int> cached;        // host view: cached length of each sequence
-    bool has_step = false;
+    std::vector<uint8_t> choice;    // host view: next_tok holds the sequence's choice at its cached length
+    bool has_step = false;          // there are logits
+    bool has_choice = false;        // next_tok has been written
     unsigned long long launches = 0;
     unsigned long long wait_ns = kWaitLimitNs;
 };
@@ -1125,6 +1127,7 @@ int engine_build(gpt2_batch *m, const gpt2_config &cfg, const EngineSrc &src, cu
     m->stream = stream;
     m->num_sms = sms;
     m->cached.assign(src.rows, 0);
+    m->choice.assign(src.rows, 0);
     const int mat_in[4] = {E, E, E, F}, mat_out[4] = {3 * E, E, F, E};
     const int pl = src.planes;
     // rows of one plane: a multiple of the tile height when there are two
@@ -1485,8 +1488,8 @@ int gpt2_decode_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *posit
     m->launches += m->kernels_per_step;
     m->tree.h_first.clear();                       // a tree step's nodes, if any, are gone
     for (int b = 0; b < n; ++b)
-        if (p[b] >= 0) m->cached[b] = p[b] + 1;
-    m->has_step = true;
+        if (p[b] >= 0) m->cached[b] = p[b] + 1, m->choice[b] = 1;
+    m->has_step = m->has_choice = true;
     if (dev_logits) *dev_logits = m->logits;
     return GPT2_OK;
 }
@@ -1502,6 +1505,7 @@ int gpt2_prefill_batch(gpt2_batch *m, const int32_t *ids, const int32_t *lens, i
     for (size_t i = 0; i < total; ++i)
         if (ids[i] < 0 || ids[i] >= m->cfg.vocab_size) return GPT2_ERR_TOKEN_RANGE;
     std::fill(m->cached.begin(), m->cached.end(), 0);
+    std::fill(m->choice.begin(), m->choice.end(), 0);
     m->tree.h_first.clear();
     std::vector<size_t> start(n, 0);
     for (int b = 1; b < n; ++b) start[b] = start[b - 1] + size_t(lens[b - 1]);
@@ -1576,9 +1580,11 @@ int gpt2_prefill_batch(gpt2_batch *m, const int32_t *ids, const int32_t *lens, i
 int gpt2_decode_batch_greedy(gpt2_batch *m, int32_t n_steps)
 {
     if (!m || n_steps < 0) return GPT2_ERR_INVALID_ARG;
-    if (!m->has_step) return GPT2_ERR_NOT_READY;
+    if (!m->has_choice) return GPT2_ERR_NOT_READY;
     for (int b = 0; b < m->max_batch; ++b)
         if (m->cached[b] > 0 && m->cached[b] + n_steps > m->cfg.n_positions) return GPT2_ERR_POSITION_RANGE;
+    for (int b = 0; b < m->max_batch; ++b)
+        if (m->cached[b] > 0 && !m->choice[b]) return GPT2_ERR_NOT_READY;
     if (n_steps == 0) return GPT2_OK;
     m->tree.h_first.clear();
     // every sequence with a cached prefix continues from its own length with
@@ -1667,8 +1673,11 @@ int gpt2_accept_tree_batch(gpt2_batch *m, float temperature, const float *draft_
     const gpt2_kv kv = layer_kv(m, 0);
     rc = gpt2_op_kv_commit(&kv, c.n_layer, tr.each, tr.cached, tr.path, tr.n_path, n, GPT2_MAX_NODES, m->stream);
     if (rc != GPT2_OK) return rc;
+    for (int b = 0; b < n; ++b)                    // (until the new ones are known)
+        if (tr.h_first[b + 1] > tr.h_first[b]) m->choice[b] = 0;
     k_b_set_next<<<1, kTcMaxRows, 0, m->stream>>>(m->next_tok, tr.next, tr.n_path, n);
     BTRY(cudaGetLastError());
+    m->has_choice = true;
     m->launches += 4;
     std::vector<int32_t> path(size_t(n) * GPT2_MAX_NODES), n_path(n), next(n);
     BTRY(cudaMemcpyAsync(path.data(), tr.path, path.size() * 4, cudaMemcpyDeviceToHost, m->stream));
@@ -1683,6 +1692,7 @@ int gpt2_accept_tree_batch(gpt2_batch *m, float temperature, const float *draft_
         for (int i = 1; i < n_path[b]; ++i)
             host_tokens[size_t(b) * GPT2_MAX_NODES + k++] = tr.h_tokens[first[b] + path[size_t(b) * GPT2_MAX_NODES + i]];
         if (n_path[b] > 0) {
+            m->choice[b] = next[b] >= 0;
             if (next[b] >= 0) host_tokens[size_t(b) * GPT2_MAX_NODES + k++] = next[b];
             else rc = GPT2_ERR_DEVICE_STATE;
         }
@@ -1695,7 +1705,7 @@ int gpt2_accept_tree_batch(gpt2_batch *m, float temperature, const float *draft_
 int gpt2_argmax_batch(gpt2_batch *m, int32_t *host_ids, int32_t n)
 {
     if (!m || !host_ids || n < 1 || n > m->max_batch) return GPT2_ERR_INVALID_ARG;
-    if (!m->has_step) return GPT2_ERR_NOT_READY;
+    if (!m->has_choice) return GPT2_ERR_NOT_READY;
     const int rc = read_batch_state(m);
     if (rc != GPT2_OK) return rc;
     BTRY(cudaMemcpy(host_ids, m->next_tok, size_t(n) * 4, cudaMemcpyDeviceToHost));
