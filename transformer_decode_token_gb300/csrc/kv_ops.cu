@@ -431,6 +431,7 @@ int rows_ok(const gpt2_kv *kv, const void *k, const void *v, int32_t dtype, int6
     const int E = kv->n_head * kv->head_dim, es = elem_size(dtype);
     if ((long long)kv->n_head * kv->head_dim > (1ll << 24) || stride < E) return GPT2_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(k) % es || reinterpret_cast<uintptr_t>(v) % es) return GPT2_ERR_INVALID_ARG;
+    if (!aligned4(slot, pos)) return GPT2_ERR_INVALID_ARG;
     // (row, part, head) units, and a block's last ones past the end, are counted in 32 bits
     if (((long long)n_rows + 1) * 2 * kv->n_head + 4096 >= (1ll << 31)) return GPT2_ERR_INVALID_ARG;
     return GPT2_OK;
@@ -520,6 +521,7 @@ int gpt2_op_kv_commit(const gpt2_kv *kv, int32_t n_layer, const int32_t *slot, c
     if (max_nodes < 1 || max_nodes > GPT2_MAX_NODES || (long long)n_layer * n_seqs >= (1ll << 31) - 1)
         return GPT2_ERR_INVALID_ARG;
     if ((long long)kv->n_head * kv->head_dim > (1ll << 24)) return GPT2_ERR_INVALID_ARG;
+    if (!aligned4(slot, cached, path, n_path)) return GPT2_ERR_INVALID_ARG;
     if (n_seqs == 0) return GPT2_OK;
     int rc;
     if (!spec_sms(&rc)) return rc;

@@ -45,12 +45,18 @@ inline bool is_row_type(int t) { return t == GPT2_F32 || t == GPT2_F16 || t == G
 inline bool is_scaled(int t) { return t == GPT2_INT8 || t == GPT2_E4M3; }
 inline int elem_size(int t) { return t == GPT2_F32 ? 4 : is_scaled(t) ? 1 : 2; }
 inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// int32 and fp32 arrays (a NULL one is aligned)
+template <typename... P>
+inline bool aligned4(const P *...p)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) == 0;
+}
 
 inline bool kv_ok(const gpt2_kv *kv)
 {
     if (!kv || !kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v)) return false;
     if (!is_row_type(kv->dtype) && !is_scaled(kv->dtype)) return false;
-    if (is_scaled(kv->dtype) && (!kv->k_scale || !kv->v_scale)) return false;
+    if (is_scaled(kv->dtype) && (!kv->k_scale || !kv->v_scale || !aligned4(kv->k_scale, kv->v_scale))) return false;
     if (kv->n_slots < 1 || kv->n_head < 1 || kv->n_positions < 1) return false;
     if (kv->head_dim != 32 && kv->head_dim != 64 && kv->head_dim != 128) return false;
     // (slot, head, position) rows are counted in 64 bits; heads x positions of

@@ -100,7 +100,7 @@ extern "C" int gpt2_op_tree_attention(const gpt2_kv *kv, const void *q, int32_t 
     const int64_t E = int64_t(n_head) * kv->head_dim;
     if (q_stride < E || out_stride < E || q_stride % 8 || out_stride % 8) return GPT2_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out)) return GPT2_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(mask) % 8) return GPT2_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(mask) % 8 || !aligned4(slot, cached, first)) return GPT2_ERR_INVALID_ARG;
     TreeArgs a{};
     a.kv = *kv;
     a.q = q;

@@ -488,7 +488,9 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
     const double c = temperature > 0.f ? 1.4426950408889634 / double(temperature) : 0.0;
     if (c > double(FLT_MAX)) return GPT2_ERR_INVALID_ARG;
     if (temperature > 0.f && (!u_accept || !u_draw)) return GPT2_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(logits) % 4 || !aligned16(workspace)) return GPT2_ERR_INVALID_ARG;
+    if (!aligned4(logits, tokens, parents, first, path, n_path, next_token) || !aligned16(workspace))
+        return GPT2_ERR_INVALID_ARG;
+    if (temperature > 0.f && !aligned4(draft_probs, u_accept, u_draw)) return GPT2_ERR_INVALID_ARG;
     if (workspace_bytes < gpt2_op_verify_tree_workspace(n_rows, vocab)) return GPT2_ERR_INVALID_ARG;
     if (chunks_of(vocab) > 65535 || (long long)n_seqs * kMaxCluster >= (1ll << 31)) return GPT2_ERR_INVALID_ARG;
     if (n_seqs == 0) return GPT2_OK;
