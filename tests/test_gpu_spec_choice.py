@@ -73,3 +73,44 @@ def test_no_choice_is_not_an_earlier_one():
     finally:
         m.close()
         ref.close()
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_acceptance_waits_for_its_tensors(own_stream):
+    """Probabilities and random numbers that another stream is still making when
+    accept_tree is called there: the tokens are those of the finished tensors.
+    Tensors elsewhere than on the model's device are refused."""
+    import torch
+    cfg = synth.TINY
+    V = cfg.vocab_size
+    rng = np.random.default_rng(4)
+    ours = torch.cuda.Stream() if own_stream else None
+    m = binding.BatchModel(cfg, binding.upload_weights(synth.make_weights(cfg, 0)), 16, stream=ours)
+    try:
+        torch.cuda.synchronize()
+        tree = [([5, 9, 11, 2], [-1, 0, 1, 0]), ([7, 3], [-1, 0])]
+        host = [torch.from_numpy(rng.random(s, np.float32).clip(1e-6, 0.999)) for s in ((6, V), (6,), (2, V))]
+        host[0] /= host[0].sum(1, keepdim=True)
+        host[1][1] = 1e-6                               # node 1 is taken
+        pinned = [h.pin_memory() for h in host]
+        m.decode_tree(tree)
+        lg = torch.from_numpy(m.logits(6)).cuda()
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        path, n_path, nxt = binding.op_verify_tree(lg, i32([5, 9, 11, 2, 7, 3]), i32([-1, 0, 1, 0, -1, 0]), i32([0, 4, 6]),
+                                                   64, 0.9, *[h.cuda() for h in host])
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            made = [torch.full_like(h, 0.5, device="cuda") for h in host]
+            torch.cuda._sleep(100_000_000)              # (some 50 ms)
+            for t, h in zip(made, pinned):
+                t.copy_(h, non_blocking=True)
+            got = m.accept_tree(0.9, *made)
+        toks = [[5, 9, 11, 2], [7, 3]]
+        assert got == [[toks[b][i] for i in path[b, 1:n_path[b]].tolist()] + [nxt[b].item()] for b in range(2)]
+        m.decode_tree([([got[0][-1]], [-1])])
+        with pytest.raises(ValueError):
+            m.accept_tree(0.9, None, host[1][:1], host[2][:1])
+        m.accept_tree()
+    finally:
+        m.close()

@@ -406,11 +406,12 @@ class BatchModel:
         w = Weights(dev_weights["wte"].data_ptr(), dev_weights["wpe"].data_ptr(),
                     dev_weights["ln_f_w"].data_ptr(), dev_weights["ln_f_b"].data_ptr(),
                     ctypes.cast(layers, ctypes.POINTER(LayerWeights)))
-        h = ctypes.c_void_p()
+        h, sh = ctypes.c_void_p(), _stream_handle(stream)
         check(L.gpt2_create_batch_ex(ctypes.byref(c), ctypes.byref(w), WDTYPES[wdtype], int(max_batch),
-                                     {"f32": 0, "bf16": BATCH_KV_BF16, "int8": BATCH_KV_INT8}[kv], _stream_handle(stream), ctypes.byref(h)),
+                                     {"f32": 0, "bf16": BATCH_KV_BF16, "int8": BATCH_KV_INT8}[kv], sh, ctypes.byref(h)),
               "gpt2_create_batch_ex")
         self.kv = kv
+        self._device, self._stream = dev_weights["wte"].device, sh.value or 0
         self._h = h
 
     def decode(self, tokens, positions) -> int:
@@ -449,9 +450,9 @@ class BatchModel:
     def accept_tree(self, temperature: float = 0.0, draft_probs=None, u_accept=None, u_draw=None) -> list:
         """Verifies the last tree step's nodes, keeps each sequence's accepted
         path and returns the tokens it gained (its accepted drafts, then its
-        next token); see gpt2_accept_tree_batch.  CUDA fp32 tensors:
-        draft_probs [nodes][vocab], u_accept [nodes], u_draw
-        [sequences][vocab].  Where some sequence's logits leave no choice, the
+        next token); see gpt2_accept_tree_batch.  fp32 tensors on the model's
+        device, made on the current stream or ready: draft_probs [nodes][vocab],
+        u_accept [nodes], u_draw [sequences][vocab].  Where some sequence's logits leave no choice, the
         GPT2Error (DEVICE_STATE) has the gained tokens as `tokens`."""
         import torch
         counts = getattr(self, "_tree_counts", [0])
@@ -459,8 +460,14 @@ class BatchModel:
         for name, t, shape in (("draft_probs", draft_probs, (rows, V)), ("u_accept", u_accept, (rows,)),
                                ("u_draw", u_draw, (n, V))):
             if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or
-                                  t.device.type != "cuda"):
-                raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape {shape}")
+                                  t.device != self._device):
+                raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on {self._device}")
+        if draft_probs is not None or u_accept is not None or u_draw is not None:
+            now = torch.cuda.current_stream(self._device)
+            if now.cuda_stream != self._stream:      # the model's stream waits for what makes them
+                own = torch.cuda.ExternalStream(self._stream, self._device) if self._stream else \
+                    torch.cuda.default_stream(self._device)
+                own.wait_stream(now)
         out, op = _i32(np.zeros((n, MAX_NODES)))
         got, gp = _i32(np.zeros(n))
         status = lib().gpt2_accept_tree_batch(self._h, float(temperature), _ptr(draft_probs), _ptr(u_accept),
