@@ -138,10 +138,12 @@ def test_seen_infinities_are_as_defined(qt, ct, D, kernel, n, c, P, K):
                   {(kc, 7, 5): -inf, (kc, c - 1, 5): -inf, (vc, 9, 1): inf}]
     if ks is not None:
         spots += [{(vs, row, None): x} for row in at for x in (nan, inf)] + [{(ks, c - 1, None): nan}]
+    # a NaN among the last node's queries: all of its scores, whatever the values
+    spots += [{(q, n - 1, 7): nan}, {(q, n - 1, 7): nan, (vs if ct == "int8" else vc, c - 1, None): inf if ct != "e4m3" else nan}]
     for spot in spots:
         old = {}
         for (t, row, d), x in spot.items():
-            where = (0, h, row) if d is None else (0, h, row, d)
+            where = (row, h, d) if t is q else (0, h, row) if d is None else (0, h, row, d)
             old[t, where] = t[where].clone()
             t[where] = torch.tensor(x).to(t.dtype)
         got = binding.op_tree_attention(q, kc, vc, *args, ks, vs)

@@ -84,6 +84,7 @@ struct Traits {
     static constexpr int kNQ = NQ, kNP = NP;
     static constexpr bool kE4M3 = E4M3;
     static constexpr bool kScaled = ES == 1;
+    static constexpr int kKind = ES == 4 ? GPT2_F32 : ES == 1 ? (E4M3 ? GPT2_E4M3 : GPT2_INT8) : M == kBf16 ? GPT2_BF16 : GPT2_F16;
     static constexpr bool kNorm = M == kF16 && (NQ > 1 || ES == 1);   // q brought into fp16's range by a power of two
 };
 
@@ -285,20 +286,6 @@ __device__ __forceinline__ float4 load_row4(const void *p, size_t i, int dtype)
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Element d of a cache row, as fp32 (a code without its scale).
-template <class Tr>
-__device__ __forceinline__ float element(const uint8_t *row, int d)
-{
-    if constexpr (Tr::kMma == kTf32) return reinterpret_cast<const float *>(row)[d];
-    else if constexpr (Tr::kES == 2 && Tr::kMma == kBf16)
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[d]);
-    else if constexpr (Tr::kES == 2) return __half2float(reinterpret_cast<const __half *>(row)[d]);
-    else if constexpr (Tr::kE4M3) {
-        const uint32_t h = codes_to_half2<true>(row[d], 0x4140u);
-        return __half2float(__ushort_as_half(uint16_t(h)));
-    } else return float(reinterpret_cast<const int8_t *>(row)[d]);
-}
-
 template <class Tr, int D, int MT>
 struct Smem {
     static constexpr int kRows = 16 * MT;
@@ -308,20 +295,25 @@ struct Smem {
     static constexpr size_t kBytes = kQ > kO ? kQ : kO;   // q's operands, then the warps' sums
 };
 
-// Element i of a cache (a code without its scale) or of rows as fp32.
-__device__ __forceinline__ float row_value(const void *p, size_t i, int dtype)
+// Element i of rows or of a cache (a code without its scale) as fp32.
+template <int KIND>
+__device__ __forceinline__ float value_at(const void *p, size_t i)
 {
-    switch (dtype) {
-    case GPT2_F32: return static_cast<const float *>(p)[i];
-    case GPT2_F16: return __half2float(static_cast<const __half *>(p)[i]);
-    case GPT2_BF16: return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    case GPT2_INT8: return float(static_cast<const int8_t *>(p)[i]);
-    default: {
+    if constexpr (KIND == GPT2_F32) return static_cast<const float *>(p)[i];
+    else if constexpr (KIND == GPT2_F16) return __half2float(static_cast<const __half *>(p)[i]);
+    else if constexpr (KIND == GPT2_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+    else if constexpr (KIND == GPT2_INT8) return float(static_cast<const int8_t *>(p)[i]);
+    else {
         const uint32_t h = codes_to_half2<true>(static_cast<const uint8_t *>(p)[i], 0x4140u);
         return __half2float(__ushort_as_half(uint16_t(h)));
     }
-    }
 }
+__device__ __forceinline__ float row_value(const void *p, size_t i, int dtype)
+{
+    return dtype == GPT2_F32 ? value_at<GPT2_F32>(p, i) : dtype == GPT2_F16 ? value_at<GPT2_F16>(p, i) : value_at<GPT2_BF16>(p, i);
+}
+
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // A query row's inputs: the cache rows of its head, its place in q, its mask.
 struct RowOf {
@@ -333,63 +325,92 @@ struct RowOf {
     float scale_log2;
 };
 
+// The sum of what is not finite among the values of dimension d that the row sees
+// in cache rows from .. to - 1: 0 where all of them are finite.
+template <int KIND, int D>
+__device__ __noinline__ float seen_not_finite(const RowOf r, int d, int from, int to)
+{
+    constexpr bool kScaled = KIND == GPT2_INT8 || KIND == GPT2_E4M3;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int j = from; j < to; ++j) {
+        const size_t row = r.row_base + j;
+        float v = value_at<KIND>(r.kv.v, row * D + d);
+        if constexpr (kScaled) v *= r.kv.v_scale[row];
+        if (!is_finite(v) && (j < r.pre || (r.mask >> (j - r.pre) & 1))) sum += v;
+    }
+    return sum;
+}
+
+// What becomes of results that are not finite.  The kernels' products of several
+// parts make a NaN of a seen infinity (infinity times a second part of zero,
+// infinity minus infinity), and so they do of an infinite key whose weight is
+// zero.  Where the sum of the weights is sound and there are values that are not
+// finite, the result is the sum of those; else the row is computed by its
+// definition, below.
+//
 // Dimensions dim .. dim + N - 1 (each lane its own) of one row's result, by a warp
-// in fp32 as the definition says, in three passes: the maximum, the sum of the
-// weights, the weighted values.  For results that came out not finite: the
-// kernels' products of several parts make a NaN of a seen infinity (infinity
-// times a second part of zero, infinity minus infinity), and so they do of an
-// infinite key whose weight is zero.  Slow (a cache row at a time); a row of
-// which some score is NaN or +infinity is NaN after the first pass.
-template <int D, int N>
+// in fp32: the maximum and the sum of the weights, a key per lane, then the
+// weighted values.  Slow beside the kernels, but a row with a score that is NaN or
+// +infinity is NaN as soon as that has been met.
+template <int KIND, int D, int N>
 __device__ __noinline__ void row_by_definition(const RowOf r, int dim, float (&out)[N])
 {
-    constexpr int E = D / 32;
+    constexpr bool kScaled = KIND == GPT2_INT8 || KIND == GPT2_E4M3;
     const int lane = threadIdx.x & 31;
-    const bool scaled = r.kv.dtype == GPT2_INT8 || r.kv.dtype == GPT2_E4M3;
-    float q[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) q[i] = row_value(r.q, r.q_at + lane * E + i, r.q_dtype) * r.scale_log2;
-    auto sees = [&](int j) { return j < r.pre || (r.mask >> (j - r.pre) & 1); };
-    auto score = [&](int j) {
+    auto sees = [&](int j) { return j < r.pre || (j < r.total && (r.mask >> (j - r.pre) & 1)); };
+    auto score = [&](int j) {                        // -infinity where it is not seen
+        if (!sees(j)) return -INFINITY;
         const size_t row = r.row_base + j;
-        const float s = scaled ? r.kv.k_scale[row] : 1.f;
+        const float s = kScaled ? r.kv.k_scale[row] : 1.f;
         float x = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            const float4 q = load_row4(r.q, r.q_at + d, r.q_dtype);
+            const float y[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < E; ++i) x = fmaf(q[i], row_value(r.kv.k, row * D + lane * E + i, r.kv.dtype) * s, x);
-        return warp_sum(x);
+            for (int i = 0; i < 4; ++i) x = fmaf(y[i] * r.scale_log2, value_at<KIND>(r.kv.k, row * D + d + i) * s, x);
+        }
+        return x;
     };
     float m = -INFINITY, l = 0.f;
     bool nan = false;
-    for (int j = 0; j < r.total; ++j) {
-        if (!sees(j)) continue;
-        const float s = score(j);
-        m = fmaxf(m, s);
-        nan = nan || s != s;
+    for (int j0 = 0; j0 < r.total && !nan; j0 += 32) {
+        const float s = score(j0 + lane), top = fmaxf(m, s), safe = top == -INFINITY ? 0.f : top;
+        nan = __any_sync(0xffffffffu, s != s || s == INFINITY);
+        l = l * exp2_approx(m - safe) + exp2_approx(s - safe);
+        m = top;
     }
+    const float top = warp_max(m);
 #pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = nan || m == INFINITY ? __int_as_float(0x7fc00000) : 0.f;
-    if (nan || m == INFINITY || m == -INFINITY) return;
-    for (int j = 0; j < r.total; ++j)
-        if (sees(j)) l += exp2_approx(score(j) - m);
-    for (int j = 0; j < r.total; ++j) {
-        if (!sees(j)) continue;
-        const size_t row = r.row_base + j;
-        const float p = exp2_approx(score(j) - m) / l, s = scaled ? r.kv.v_scale[row] : 1.f;
+    for (int i = 0; i < N; ++i) out[i] = nan ? __int_as_float(0x7fc00000) : 0.f;
+    if (nan || top == -INFINITY) return;
+    l = warp_sum(l * exp2_approx(m - top));
+    for (int j0 = 0; j0 < r.total; j0 += 32) {
+        const float p = exp2_approx(score(j0 + lane) - top) / l;
+        const uint32_t seen = __ballot_sync(0xffffffffu, sees(j0 + lane));
+#pragma unroll 8
+        for (int t = 0; t < 32; ++t) {
+            const size_t row = r.row_base + j0 + t;
+            const bool yes = seen >> t & 1;
+            const float w = __shfl_sync(0xffffffffu, p, t), s = !kScaled ? 1.f : yes ? r.kv.v_scale[row] : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) out[i] = fmaf(p, row_value(r.kv.v, row * D + dim + i, r.kv.dtype) * s, out[i]);
+            for (int i = 0; i < N; ++i) {
+                const float v = yes ? value_at<KIND>(r.kv.v, row * D + dim + i) : 0.f;
+                out[i] = fmaf(w, v * s, out[i]);
+            }
+        }
     }
 }
 
-__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
-
 // The warps' sums so [kNW][R][D] (in units of 2^(the CTA's maximum)), with their
 // maxima and sums of weights, to results: over the warps, then over the CTAs of
-// the cluster.  bad_sum(e): what is to be added to element e where some CTA is
-// `bad`.  What is not finite then is computed anew (row_by_definition).
-template <int D, int R, typename Bad>
+// the cluster.  cta_bad: values of nodes that are not finite were taken out.  What
+// is not finite in the end is computed anew (seen_not_finite, row_by_definition).
+template <int KIND, int D, int R>
 __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)[R], float (*sm_l)[R],
                                      float (*sm_f)[R], int *sm_bad, bool cta_bad, int rank, int f0, int row0, int kvh,
-                                     int rows, size_t row_base, int pre, int total, Bad bad_sum)
+                                     int rows, size_t row_base, int pre, int total)
 {
     const int tid = threadIdx.x;
     float cta_m = 0.f, cta_l = 0.f;
@@ -435,30 +456,53 @@ __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)
             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(w[0], w[1]);
         }
     };
+    auto row_of = [&](int r) {
+        return RowOf{a.kv,  a.q,   begins(r, a.q_stride), row_base, a.mask[f0 + (row0 + r) / a.group], a.q_dtype, pre,
+                     total, a.scale_log2};
+    };
     float sane = 0.f;                                // NaN once a result is not finite
     auto finish4 = [&](int e, bool any_bad, float (&v)[4]) {
         if (any_bad)
-            for (int i = 0; i < 4; ++i) v[i] += bad_sum(e + i);
+            for (int i = 0; i < 4; ++i) v[i] += seen_not_finite<KIND, D>(row_of(e / D), e % D + i, pre, total);
         store4(e, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sane = fmaf(v[i], 0.f, sane);
     };
     // results that are not finite, by whole warps, whose elements follow one
-    // another: first, the warp's first; step between its turns
+    // another: first, the warp's first; step between its turns (a multiple of D, so
+    // that a lane's dimensions stay)
     auto anew = [&](int first, int step) {
         if (!__any_sync(0xffffffffu, sane != 0.f)) return;
+        float prefix[4];                             // what is not finite in the prefix, in this lane's dimensions
+        bool have = false;
         for (int e0 = first; e0 < rows * D; e0 += step) {
-            const int e = e0 + (tid & 31) * 4;
-            bool odd = false;
-            for (int i = 0; i < 4; ++i)
-                odd = odd || (e < rows * D && !is_finite(row_value(a.out, begins(e / D, a.out_stride) + e % D + i, a.q_dtype)));
+            const int e = e0 + (tid & 31) * 4, d = e % D;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (e < rows * D)
+                for (int i = 0; i < 4; ++i) v[i] = row_value(a.out, begins(e / D, a.out_stride) + d + i, a.q_dtype);
+            const bool odd = !(is_finite(v[0]) && is_finite(v[1]) && is_finite(v[2]) && is_finite(v[3]));
             for (uint32_t left = __ballot_sync(0xffffffffu, odd); left;) {   // a row at a time
-                const int r = __shfl_sync(0xffffffffu, e / D, __ffs(left) - 1), node = f0 + (row0 + r) / a.group;
-                const RowOf of{a.kv, a.q, begins(r, a.q_stride), row_base, a.mask[node], a.q_dtype, pre, total, a.scale_log2};
-                float x[4];
-                row_by_definition<D, 4>(of, e % D, x);
+                const int r = __shfl_sync(0xffffffffu, e / D, __ffs(left) - 1);
                 const bool mine = odd && e / D == r;
-                if (mine) store4(e, x);
+                const RowOf of = row_of(r);
+                float sum = a.splits == 1 ? sm_l[0][r] : 0.f;   // (or the sum of the CTAs' factors)
+                for (int k = 0; a.splits > 1 && k < kMaxSplits; ++k) sum += sm_f[k][r];
+                bool search = !(sum > 0.f && is_finite(sum));
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (!search) {
+                    for (int i = 0; i < 4; ++i) {
+                        if (!have) prefix[i] = seen_not_finite<KIND, D>(of, d + i, 0, pre);
+                        x[i] = prefix[i] + seen_not_finite<KIND, D>(of, d + i, pre, total);
+                        search = search || (mine && !is_finite(v[i]) && x[i] == 0.f);
+                    }
+                    have = true;
+                }
+                if (__any_sync(0xffffffffu, search)) row_by_definition<KIND, D, 4>(of, d, x);
+                if (mine) {
+                    for (int i = 0; i < 4; ++i)
+                        if (!is_finite(v[i])) v[i] = x[i];
+                    store4(e, v);
+                }
                 left &= ~__ballot_sync(0xffffffffu, mine);
             }
         }
@@ -955,18 +999,7 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
             }
         }
     __syncthreads();
-    join<D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, cta_bad, rank, f0, row0, kvh, rows, row_base, pre, total, [&](int e) {
-        // the infinities and NaNs that were taken out, for the rows that see them
-        const int r = e / D, d = e % D;
-        const uint64_t sees = a.mask[f0 + (row0 + r) / G];
-        float x = 0.f;
-        for (int j = pre; j < total; ++j) {
-            if (!(sees >> (j - pre) & 1)) continue;
-            const float v = element<Tr>(vbase + size_t(j) * T::kRowB, d) * (Tr::kScaled ? vscale[j] : 1.f);
-            if (!is_finite(v)) x += v;
-        }
-        return x;
-    });
+    join<Tr::kKind, D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, cta_bad, rank, f0, row0, kvh, rows, row_base, pre, total);
 }
 
 template <typename K>

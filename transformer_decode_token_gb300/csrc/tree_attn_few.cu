@@ -276,8 +276,7 @@ __global__ void __launch_bounds__(kNW * 32, R == 1 ? 4 : R == 2 ? 3 : 2) k_tree_
         }
     }
     __syncthreads();
-    join<D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, false, rank, f0, row0, kvh, rows, row_base, pre, total,
-               [](int) { return 0.f; });
+    join<KIND, D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, false, rank, f0, row0, kvh, rows, row_base, pre, total);
 }
 
 template <int KIND, int D>

@@ -357,21 +357,6 @@ struct Part {
     float o[N][D], m[N], l[N];                   // m: minus the maxima (less the lift)
 };
 
-// What is not finite among the values of node rows that a query row sees (0:
-// nothing), added to its result.
-template <typename T16>
-__device__ __noinline__ float not_finite_seen(const void *v, int64_t row, uint64_t mask, int pre, int total, int D, int d)
-{
-    const T16 *vb = static_cast<const T16 *>(v) + row * D + d;
-    float sum = 0.f;
-    for (int j = pre; j < total; ++j)
-        if (mask >> (j - pre) & 1) {
-            const float x = float(vb[size_t(j) * D]);
-            if (!tree::is_finite(x)) sum += x;
-        }
-    return sum;
-}
-
 // Element of q or `out` where query row r (of a cache head's) begins.
 __device__ __forceinline__ int64_t row_at(const TreeArgs &a, const Sequence &s, int64_t stride, int D, int kvh, int r)
 {
@@ -386,6 +371,23 @@ __device__ __forceinline__ tree::RowOf row_of(const TreeArgs &a, const Sequence 
                        s.total, a.scale_log2};
 }
 
+// This lane's result of a row that has come out not finite in some of the warp's
+// dimensions (odd: in this one); sound: the sum of its weights is a number above
+// zero.  have, prefix: what is not finite in the prefix, once looked up.
+template <int KIND, int D>
+__device__ __noinline__ float anew(const tree::RowOf of, int dim, bool odd, bool sound, bool &have, float &prefix)
+{
+    if (sound) {
+        if (!have) prefix = tree::seen_not_finite<KIND, D>(of, dim, 0, of.pre);
+        have = true;
+        const float x = prefix + tree::seen_not_finite<KIND, D>(of, dim, of.pre, of.total);
+        if (!__any_sync(0xffffffffu, odd && x == 0.f)) return x;
+    }
+    float x[1];
+    tree::row_by_definition<KIND, D, 1>(of, dim, x);
+    return x[0];
+}
+
 template <bool BF, int D, int N>
 __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
     k_tree_tc(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -393,6 +395,7 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
 {
     using S = Shape<D, N>;
     using T16 = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr int kKind = BF ? GPT2_BF16 : GPT2_F16;
     constexpr int kSt = S::kStages, kKR = S::kKRing, kVR = S::kVRing, kPB = S::kPBufs, kSoft = S::kSoft, kSync = kSoft * 32, C = S::kC;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full[kSt], empty[kSt], sfull[2], sfree[2], pfull[kPB], pfree[kPB], qfull, odone;
@@ -840,16 +843,18 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
                 }
                 // what is not finite, or should not be, is computed anew (what a wait that ran
                 // out left stays NaN)
-                if (__any_sync(0xffffffffu, sane != 0.f || (bad && whole)) && !sm_fail)
+                if (__any_sync(0xffffffffu, sane != 0.f || (bad && whole)) && !sm_fail) {
+                    float prefix = 0.f;
+                    bool have = false;
                     for (int r = c0; r < min(c0 + C, rows); ++r) {
                         const tree::RowOf of = row_of(a, sq, D, kvh, row0 + r);
-                        const bool odd = !tree::is_finite(float(out[sm_out[r]])) ||
-                                         (bad && not_finite_seen<T16>(a.kv.v, of.row_base, of.mask, of.pre, of.total, D, dim) != 0.f);
+                        const float nodes = bad ? tree::seen_not_finite<kKind, D>(of, dim, of.pre, of.total) : 0.f;
+                        const bool odd = !tree::is_finite(float(out[sm_out[r]])) || nodes != 0.f;
                         if (!__any_sync(0xffffffffu, odd)) continue;
-                        float x[1];
-                        tree::row_by_definition<D, 1>(of, dim, x);
-                        if (odd) out[sm_out[r]] = T16(x[0]);
+                        const float x = anew<kKind, D>(of, dim, odd, tree::is_finite(sm_inv[r]), have, prefix);
+                        if (odd) out[sm_out[r]] = T16(x);
                     }
+                }
                 fence_before();
             }
             if (S::kQBufs == 1 && more) have_q();
@@ -868,21 +873,28 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, Shape<D, N>::kPerSM)
 constexpr int kJoinThreads = 256, kJoinCut = 8, kJoinAhead = 8;
 
 // Computes the results of a joined unit that are not finite anew (those of this
-// thread's turns; a warp's elements are 32 dimensions of one row).
-template <typename T16, int D, int N>
-__device__ __noinline__ void join_anew(const TreeArgs &a, const Head *head)
+// thread's turns; a warp's elements are 32 dimensions of one row, the same in
+// every turn).
+template <bool BF, int D, int N>
+__device__ __noinline__ void join_anew(const TreeArgs &a, const Part<D, N> *parts, const Head *heads, int first, int last)
 {
-    const Head h = *head;
+    using T16 = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr int kKind = BF ? GPT2_BF16 : GPT2_F16;
+    const Head h = heads[first];
     const Sequence s(a, h.b, N);
     const int kvh = h.u % a.kv.n_head, row0 = h.u / a.kv.n_head * N, rows = min(s.rows - row0, N);
+    float prefix = 0.f;
+    bool have = false;
+    static_assert(kJoinCut * kJoinThreads % D == 0, "a lane's dimension stays");
     for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * D; e += kJoinCut * kJoinThreads) {
         const int r = e / D, d = e % D;
         T16 *out = static_cast<T16 *>(a.out) + row_at(a, s, a.out_stride, D, kvh, row0 + r) + d;
         const bool odd = !tree::is_finite(float(*out));
         if (!__any_sync(0xffffffffu, odd)) continue;
-        float x[1];
-        tree::row_by_definition<D, 1>(row_of(a, s, D, kvh, row0 + r), d, x);
-        if (odd) *out = T16(x[0]);
+        float sum = parts[first].l[r];               // (only whether it is a number, and not zero)
+        for (int i = blockIdx.x + 1; i <= last; ++i) sum += parts[2 * i].l[r];
+        const float x = anew<kKind, D>(row_of(a, s, D, kvh, row0 + r), d, odd, tree::is_finite(sum) && sum != 0.f, have, prefix);
+        if (odd) *out = T16(x);
     }
 }
 
@@ -937,13 +949,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const __grid_constan
                 }
         }
         v = sum == 0.f ? __int_as_float(0x7fc00000) : v / sum;   // (no weight: computed anew)
-        if (bad)
-            v += not_finite_seen<T16>(a.kv.v, s.row_base + int64_t(kvh) * a.kv.n_positions,
-                                      a.mask[s.f0 + (row0 + r) / a.group], s.pre, s.total, D, d);
+        if (bad) v += tree::seen_not_finite<(BF ? GPT2_BF16 : GPT2_F16), D>(row_of(a, s, D, kvh, row0 + r), d, s.pre, s.total);
         static_cast<T16 *>(a.out)[row_at(a, s, a.out_stride, D, kvh, row0 + r) + d] = T16(v);
         sane = fmaf(v, 0.f, sane);
     }
-    if (__any_sync(0xffffffffu, sane != 0.f)) join_anew<T16, D, N>(a, heads + first);
+    if (__any_sync(0xffffffffu, sane != 0.f)) join_anew<BF, D, N>(a, parts, heads, first, last);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
