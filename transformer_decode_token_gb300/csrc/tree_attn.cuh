@@ -403,16 +403,110 @@ __device__ __noinline__ void row_by_definition(const RowOf r, int dim, float (&o
     }
 }
 
+// The query rows and the cache rows of a CTA.
+struct Unit {
+    size_t row_base;                 // its head's first cache row
+    int f0, row0, kvh, rows, pre, total;
+    int cut;                         // values from this cache row on were taken out where they are not finite
+};
+
+// Element of q and out (of row stride `stride`) where row r begins.
+template <int D>
+__device__ __forceinline__ size_t begins(const TreeArgs &a, const Unit &u, int r, int64_t stride)
+{
+    return size_t(u.f0 + (u.row0 + r) / a.group) * stride + size_t(u.kvh * a.group + (u.row0 + r) % a.group) * D;
+}
+
+// Four elements of a result row, from element e = row * D + dim on.
+template <int D>
+__device__ __forceinline__ void store4(const TreeArgs &a, const Unit &u, int e, const float (&v)[4])
+{
+    const size_t at = begins<D>(a, u, e / D, a.out_stride) + e % D;
+    if (a.q_dtype == GPT2_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = a.q_dtype == GPT2_F16 ? *reinterpret_cast<const uint32_t *>(&h)
+                                         : *reinterpret_cast<const uint32_t *>(&x);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(w[0], w[1]);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ RowOf row_of(const TreeArgs &a, const Unit &u, int r)
+{
+    return RowOf{a.kv,      a.q,   begins<D>(a, u, r, a.q_stride), u.row_base, a.mask[u.f0 + (u.row0 + r) / a.group],
+                 a.q_dtype, u.pre, u.total, a.scale_log2};
+}
+
+// Adds what was taken out, and they see, to the four elements from e on.
+template <int KIND, int D>
+__device__ __noinline__ float4 with_taken_out(const TreeArgs &a, const Unit u, int e, float4 v)
+{
+    const RowOf of = row_of<D>(a, u, e / D);
+    v.x += seen_not_finite<KIND, D>(of, e % D, u.cut, u.total);
+    v.y += seen_not_finite<KIND, D>(of, e % D + 1, u.cut, u.total);
+    v.z += seen_not_finite<KIND, D>(of, e % D + 2, u.cut, u.total);
+    v.w += seen_not_finite<KIND, D>(of, e % D + 3, u.cut, u.total);
+    return v;
+}
+
+// Results that are not finite, by whole warps, whose elements follow one another:
+// first, the warp's first; step between its turns (a multiple of D, so that a
+// lane's dimensions stay).  sums [n][R]: the rows' sums of weights, or shares of
+// them that add up to a number above zero where the sum is one.
+template <int KIND, int D, int R>
+__device__ __noinline__ void unit_anew(const TreeArgs &a, const Unit u, const float (*sums)[R], int n, int first, int step)
+{
+    float prefix[4];                                 // what is not finite in the prefix, in this lane's dimensions
+    bool have = false;
+    for (int e0 = first; e0 < u.rows * D; e0 += step) {
+        const int e = e0 + (threadIdx.x & 31) * 4, d = e % D;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (e < u.rows * D)
+            for (int i = 0; i < 4; ++i) v[i] = row_value(a.out, begins<D>(a, u, e / D, a.out_stride) + d + i, a.q_dtype);
+        const bool odd = !(is_finite(v[0]) && is_finite(v[1]) && is_finite(v[2]) && is_finite(v[3]));
+        for (uint32_t left = __ballot_sync(0xffffffffu, odd); left;) {   // a row at a time
+            const int r = __shfl_sync(0xffffffffu, e / D, __ffs(left) - 1);
+            const bool mine = odd && e / D == r;
+            const RowOf of = row_of<D>(a, u, r);
+            float sum = 0.f;
+            for (int k = 0; k < n; ++k) sum += sums[k][r];
+            bool search = !(sum > 0.f && is_finite(sum));
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            if (!search) {
+                for (int i = 0; i < 4; ++i) {
+                    if (!have) prefix[i] = seen_not_finite<KIND, D>(of, d + i, 0, u.pre);
+                    x[i] = prefix[i] + seen_not_finite<KIND, D>(of, d + i, u.pre, u.total);
+                    search = search || (mine && !is_finite(v[i]) && x[i] == 0.f);
+                }
+                have = true;
+            }
+            if (__any_sync(0xffffffffu, search)) row_by_definition<KIND, D, 4>(of, d, x);
+            if (mine) {
+                for (int i = 0; i < 4; ++i)
+                    if (!is_finite(v[i])) v[i] = x[i];
+                store4<D>(a, u, e, v);
+            }
+            left &= ~__ballot_sync(0xffffffffu, mine);
+        }
+    }
+}
+
 // The warps' sums so [kNW][R][D] (in units of 2^(the CTA's maximum)), with their
 // maxima and sums of weights, to results: over the warps, then over the CTAs of
-// the cluster.  cta_bad: values of nodes that are not finite were taken out.  What
+// the cluster.  cta_bad: values that are not finite were taken out.  What
 // is not finite in the end is computed anew (seen_not_finite, row_by_definition).
 template <int KIND, int D, int R>
 __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)[R], float (*sm_l)[R],
-                                     float (*sm_f)[R], int *sm_bad, bool cta_bad, int rank, int f0, int row0, int kvh,
-                                     int rows, size_t row_base, int pre, int total)
+                                     float (*sm_f)[R], int *sm_bad, bool cta_bad, int rank, const Unit u)
 {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, rows = u.rows;
     float cta_m = 0.f, cta_l = 0.f;
     if (tid < R) {
         float top = sm_m[0][tid];
@@ -435,87 +529,22 @@ __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)
         sm_m[0][tid] = cta_m;
         sm_l[0][tid] = cta_l;
     }
-    // element of q and out where row r begins
-    auto begins = [&](int r, int64_t stride) {
-        return size_t(f0 + (row0 + r) / a.group) * stride + size_t(kvh * a.group + (row0 + r) % a.group) * D;
-    };
-    // four elements of a row, from element e = row * D + dim on
-    auto store4 = [&](int e, const float (&v)[4]) {
-        const size_t at = begins(e / D, a.out_stride) + e % D;
-        if (a.q_dtype == GPT2_F32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-            uint32_t w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-                const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                w[i] = a.q_dtype == GPT2_F16 ? *reinterpret_cast<const uint32_t *>(&h)
-                                             : *reinterpret_cast<const uint32_t *>(&x);
-            }
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(w[0], w[1]);
-        }
-    };
-    auto row_of = [&](int r) {
-        return RowOf{a.kv,  a.q,   begins(r, a.q_stride), row_base, a.mask[f0 + (row0 + r) / a.group], a.q_dtype, pre,
-                     total, a.scale_log2};
-    };
     float sane = 0.f;                                // NaN once a result is not finite
-    auto finish4 = [&](int e, bool any_bad, float (&v)[4]) {
-        if (any_bad)
-            for (int i = 0; i < 4; ++i) v[i] += seen_not_finite<KIND, D>(row_of(e / D), e % D + i, pre, total);
-        store4(e, v);
+    auto finish4 = [&](int e, bool any_bad, float4 v) {
+        if (any_bad) v = with_taken_out<KIND, D>(a, u, e, v);
+        const float w[4] = {v.x, v.y, v.z, v.w};
+        store4<D>(a, u, e, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sane = fmaf(v[i], 0.f, sane);
-    };
-    // results that are not finite, by whole warps, whose elements follow one
-    // another: first, the warp's first; step between its turns (a multiple of D, so
-    // that a lane's dimensions stay)
-    auto anew = [&](int first, int step) {
-        if (!__any_sync(0xffffffffu, sane != 0.f)) return;
-        float prefix[4];                             // what is not finite in the prefix, in this lane's dimensions
-        bool have = false;
-        for (int e0 = first; e0 < rows * D; e0 += step) {
-            const int e = e0 + (tid & 31) * 4, d = e % D;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (e < rows * D)
-                for (int i = 0; i < 4; ++i) v[i] = row_value(a.out, begins(e / D, a.out_stride) + d + i, a.q_dtype);
-            const bool odd = !(is_finite(v[0]) && is_finite(v[1]) && is_finite(v[2]) && is_finite(v[3]));
-            for (uint32_t left = __ballot_sync(0xffffffffu, odd); left;) {   // a row at a time
-                const int r = __shfl_sync(0xffffffffu, e / D, __ffs(left) - 1);
-                const bool mine = odd && e / D == r;
-                const RowOf of = row_of(r);
-                float sum = a.splits == 1 ? sm_l[0][r] : 0.f;   // (or the sum of the CTAs' factors)
-                for (int k = 0; a.splits > 1 && k < kMaxSplits; ++k) sum += sm_f[k][r];
-                bool search = !(sum > 0.f && is_finite(sum));
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
-                if (!search) {
-                    for (int i = 0; i < 4; ++i) {
-                        if (!have) prefix[i] = seen_not_finite<KIND, D>(of, d + i, 0, pre);
-                        x[i] = prefix[i] + seen_not_finite<KIND, D>(of, d + i, pre, total);
-                        search = search || (mine && !is_finite(v[i]) && x[i] == 0.f);
-                    }
-                    have = true;
-                }
-                if (__any_sync(0xffffffffu, search)) row_by_definition<KIND, D, 4>(of, d, x);
-                if (mine) {
-                    for (int i = 0; i < 4; ++i)
-                        if (!is_finite(v[i])) v[i] = x[i];
-                    store4(e, v);
-                }
-                left &= ~__ballot_sync(0xffffffffu, mine);
-            }
-        }
+        for (int i = 0; i < 4; ++i) sane = fmaf(w[i], 0.f, sane);
     };
     if (a.splits == 1) {
         __syncthreads();
         for (int e = tid * 4; e < rows * D; e += kNW * 32 * 4) {
             const float sum = sm_l[0][e / D], inv = sum == 0.f ? 0.f : 1.f / sum;
             const float4 o4 = *reinterpret_cast<const float4 *>(so + e);
-            float v[4] = {o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv};
-            finish4(e, cta_bad, v);
+            finish4(e, cta_bad, make_float4(o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv));
         }
-        anew((tid & ~31) * 4, kNW * 32 * 4);
+        if (__any_sync(0xffffffffu, sane != 0.f)) unit_anew<KIND, D, R>(a, u, sm_l, 1, (tid & ~31) * 4, kNW * 32 * 4);
     } else {
         namespace cg = cooperative_groups;
         cg::cluster_group cl = cg::this_cluster();
@@ -554,15 +583,16 @@ __device__ __forceinline__ void join(const TreeArgs &a, float *so, float (*sm_m)
                 v[0] = fmaf(x[i].x, f, v[0]), v[1] = fmaf(x[i].y, f, v[1]);
                 v[2] = fmaf(x[i].z, f, v[2]), v[3] = fmaf(x[i].w, f, v[3]);
             }
-            finish4(e, any_bad, v);
+            finish4(e, any_bad, make_float4(v[0], v[1], v[2], v[3]));
         }
-        anew((rank * kNW * 32 + (tid & ~31)) * 4, a.splits * kNW * 32 * 4);
+        if (__any_sync(0xffffffffu, sane != 0.f))
+            unit_anew<KIND, D, R>(a, u, sm_f, kMaxSplits, (rank * kNW * 32 + (tid & ~31)) * 4, a.splits * kNW * 32 * 4);
         cl.sync();          // nobody leaves while its sums are read
     }
 }
 
 template <class Tr, int D, int MT>
-__global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_attn(const TreeArgs a)
+__global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_attn(const __grid_constant__ TreeArgs a)
 {
     using T = Tile<Tr, D, MT>;
     using S = Smem<Tr, D, MT>;
@@ -813,6 +843,8 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
             if (partial) {
                 // a value that is not finite must not meet the weight zero of a
                 // row that does not see it: it is taken out here and added at the end
+                // (with those of the prefix's last rows, if they are in this tile: to tell
+                // them apart here cost 4 % of 8 trees of 16 nodes)
                 if constexpr (Tr::kScaled) {
 #pragma unroll
                     for (int u = 0; u < T::kT8; ++u)
@@ -824,9 +856,6 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
                 }
 #pragma unroll
                 for (int i = 0; i < T::kVR; ++i) {
-                    // (prefix rows are seen by every row and stay as they are)
-                    const int row = i / (T::kVR / (2 * T::kT8));   // the register's of this thread's 2 kT8 rows
-                    if (t * KS + row / 2 * 8 + 2 * c + row % 2 < pre) continue;
                     const uint32_t x = vr[i];
                     uint32_t gone = 0;
                     if constexpr (Tr::kMma == kTf32) gone = (x & 0x7f800000u) == 0x7f800000u ? ~0u : 0u;
@@ -999,7 +1028,7 @@ __global__ void __launch_bounds__(kNW * 32, MT == 1 && D <= 64 ? 3 : 2) k_tree_a
             }
         }
     __syncthreads();
-    join<Tr::kKind, D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, cta_bad, rank, f0, row0, kvh, rows, row_base, pre, total);
+    join<Tr::kKind, D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, cta_bad, rank, Unit{row_base, f0, row0, kvh, rows, pre, total, pre - pre % KS});
 }
 
 template <typename K>

@@ -67,7 +67,7 @@ __device__ __forceinline__ void widen(const uint32_t *r, float2 (&x)[E / 2])
 }
 
 template <int KIND, int D, int R>
-__global__ void __launch_bounds__(kNW * 32, R == 1 ? 4 : R == 2 ? 3 : 2) k_tree_few(const TreeArgs a)
+__global__ void __launch_bounds__(kNW * 32, R == 1 ? 4 : R == 2 ? 3 : 2) k_tree_few(const __grid_constant__ TreeArgs a)
 {
     using F = Few<KIND, D, R>;
     constexpr int E = F::kE, I = F::kLoads, NV = F::kNV, KS = F::KS, LPR = F::kLPR;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kNW * 32, R == 1 ? 4 : R == 2 ? 3 : 2) k_tree_
         }
     }
     __syncthreads();
-    join<KIND, D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, false, rank, f0, row0, kvh, rows, row_base, pre, total);
+    join<KIND, D, R>(a, so, sm_m, sm_l, sm_f, &sm_bad, false, rank, Unit{row_base, f0, row0, kvh, rows, pre, total, total});
 }
 
 template <int KIND, int D>
