@@ -478,7 +478,8 @@ int gpt2_op_linear_bf16(const void *W, const float *X, int32_t M, int32_t n, int
  *   - slot, pos, cached, first, path and the like are DEVICE int32 arrays: their
  *     values are not known to the host, so an entry outside its range is not
  *     reported; what it names is skipped, as each operation says, and no access
- *     leaves the buffers.
+ *     leaves the buffers.  The arrays, and scales and probabilities, are aligned to
+ *     their elements.
  *   - Every call is asynchronous on `stream`, allocates nothing, may be captured
  *     into a graph, and keeps nothing between calls.  Two calls may be in
  *     flight together if neither writes what the other uses (a workspace
@@ -532,14 +533,19 @@ int gpt2_op_kv_load(const gpt2_kv *kv, const int32_t *slot, const int32_t *pos, 
  * node does not see does not enter its result, infinities and NaN included; those
  * that it sees give what the formula gives (an infinite value with a weight above
  * zero an infinity, a key of score -infinity the weight zero), whatever the number
- * of rows; a node that sees nothing, or only scores of -infinity, gets zeros.  slot[b] outside the cache: zeros; nodes
- * whose cache row would be n_positions or more are not seen.
+ * of rows; a node that sees nothing, or only scores of -infinity, gets zeros.
+ * slot[b] outside the cache: zeros; nodes whose cache row would be n_positions or
+ * more are not seen; cached[b] below 0 counts as 0, above n_positions as
+ * n_positions.
  *   q: DEVICE, q_dtype, row i's n_head heads of head_dim at element i *
  *   q_stride; out: the same type, row i at i * out_stride.  n_head is a multiple
  *   of kv->n_head: query head h reads cache head h / (n_head / kv->n_head).
  *   Types: q_dtype GPT2_F32 with any cache; GPT2_F16 and GPT2_BF16 with a cache
  *   of the same type, GPT2_INT8 or GPT2_E4M3.  Scores, softmax and sums are
- *   fp32.  q and out 16-byte aligned, strides multiples of 8 elements and >=
+ *   fp32; by the number of rows the weights meet the values as fp32, or in parts:
+ *   two of tf32 (an fp32 cache), three of bf16 (fp32 rows over a bf16 cache), two of
+ *   bf16 (16 bits of every weight) or two of fp16 (weights below 2^-32 of the largest
+ *   may vanish).  q and out 16-byte aligned, strides multiples of 8 elements and >=
  *   n_head * head_dim; out overlaps neither q nor the cache; max_nodes in [1, GPT2_MAX_NODES] (of a sequence with
  *   more, the rows from max_nodes on are left as they were).  workspace: 16-byte
  *   aligned DEVICE memory of gpt2_op_tree_attention_workspace bytes (which depends
@@ -589,9 +595,10 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
  * cached[b] + path[b][i] moves to row cached[b] + i, i < n_path[b] (codes and
  * scales as they are).  kv describes layer 0; the n_layer layers' k, v (and
  * scales) follow one another without gaps.  path [n_seqs][max_nodes] and n_path
- * are gpt2_op_verify_tree's: strictly increasing nodes; a path is kept only up
- * to its first entry that breaks this, is max_nodes or more, or whose row is
- * outside the cache.  A slot outside the cache, or the same slot twice (then
+ * are gpt2_op_verify_tree's: strictly increasing nodes, the first of them node 0
+ * (of a path that begins otherwise nothing moves); a path is kept only up to its
+ * first entry that breaks this, is max_nodes or more, or whose row is outside the
+ * cache.  A slot outside the cache, or the same slot twice (then
  * undefined for that slot), see above. */
 int gpt2_op_kv_commit(const gpt2_kv *kv, int32_t n_layer, const int32_t *slot, const int32_t *cached,
                       const int32_t *path, const int32_t *n_path, int32_t n_seqs, int32_t max_nodes, void *stream);

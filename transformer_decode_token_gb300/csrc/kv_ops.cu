@@ -216,8 +216,11 @@ __device__ __forceinline__ float e4m3_scale(float top)
 // units a thread has U units' loads in flight; measured for 17,408 rows of 12 x
 // 64 fp32 into int8 and back (two launches): U = 2 and 4 (store, load) 46 us, 5.9
 // TB/s, 0.87 of the measured copy's rate; 1 and 2 0.7 us more, 4 and 8 6 us, 8
-// and 16 36 us (registers).  64 rows, a decode step's: 3.1 us for both, the
-// launches.
+// and 16 36 us (registers).  U is the same for 16-bit rows, of which a thread then
+// has half the bytes in flight: 8,191 rows of 8 x 128 bf16 into e4m3 and back 25.2
+// us, 4.0 TB/s, eight times as many 184 us, 4.4 TB/s; into bf16 24.5, 5.5 TB/s (fp32
+// into fp32, 17,408 rows of 12 x 64: 67.0, 6.4 TB/s).  64 rows, a decode step's: 3.0
+// us for both, the launches.
 // CT: the cache's element type (int8_t and __nv_fp8_e4m3 with scales).
 struct Unit {
     int i, part, h;                // row, 0: k / 1: v, head

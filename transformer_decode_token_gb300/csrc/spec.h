@@ -19,7 +19,8 @@ inline int spec_rc(cudaError_t e)
 // Launches a kernel as a programmatic dependent of the stream's last one: its
 // CTAs may be placed before that one has ended (right away where it was one of
 // these, which let the next one go as soon as they all run), and every thread
-// calls pdl_wait(), and then pdl_launch_dependents(), before it touches memory.
+// calls pdl_wait(), and then pdl_launch_dependents(), before it touches memory
+// (but for k_verify, see there).
 // cluster: CTAs of a cluster along x, 1: none.
 template <typename... P, typename... A>
 inline cudaError_t spec_launch(void (*fn)(P...), dim3 grid, unsigned threads, size_t smem, int cluster, cudaStream_t s,
@@ -64,8 +65,11 @@ inline bool kv_ok(const gpt2_kv *kv)
     return (long long)kv->n_head * kv->n_positions < (1ll << 31);
 }
 
-// Clusters of 2, 4, 8 and 16 CTAs that run at once, per resident CTA of an SM (as
-// the runtime reports them: a cluster stays within a group of 16 to 20 SMs).
+// Clusters of 2, 4, 8 and 16 CTAs that run at once, per resident CTA of an SM: what
+// the runtime reports for a GB300 of 152 SMs, where a cluster stays within a group
+// of 16 to 20 of them.  On other groups of SMs the shares of work are not the best
+// ones; clusters of 16 are taken only where few units leave room for them, and
+// would be refused by a device that has no group of 16 SMs.
 constexpr int kClustersFit[] = {76, 36, 17, 7};
 
 // Multiprocessors of the current device (0 and *rc on failure, also where it

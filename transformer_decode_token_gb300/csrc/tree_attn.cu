@@ -8,6 +8,10 @@ using namespace gpt2;
 
 namespace {
 
+// The lengths are on the device, so the rules below go by the cache's positions, and
+// were measured with caches that are nearly full: short sequences in a long cache
+// get the kernel and the clusters of long ones.
+
 // The 5th-generation tensor cores (tree_attn_tc.cu), in tiles of 32 or 64 query
 // rows (0: not): for more than 16 query rows on a cache head over a 16-bit cache
 // of the rows' own type, of 1,536 positions or more (in shorter ones the units are

@@ -33,11 +33,15 @@
 // final rounding to the row type is visible.
 //
 // What bounds it: 16 trees of 16 bf16 nodes over 100 to 1,000 int8 positions, 12
-// heads of 64: 12.8 us (1.2 TB/s) where the bytes take 2.3: one round of CTAs, a
-// chain of dependent steps (lengths, keys, scores, maxima, weights, sums, the
-// joins of warps and cluster) with one to three tiles per warp; with more
-// sequences the matrix instructions and what is done per weight (64 trees of 24
-// over 50 to 500 bf16 positions 35 us).  Tiles of 4 KB, 4 warps and 3 CTAs per SM
+// heads of 64: 12.9 us (1.2 TB/s) where the bytes take 2.3: a chain of dependent
+// steps (lengths, keys, scores, maxima, weights, sums, the joins of warps and
+// cluster) with one to three tiles per warp, of which only the next one's keys are
+// on their way (over bf16 13.9 us, 2.0 TB/s); with more sequences or rows the matrix
+// instructions and what is done per weight (64 trees of 24 over 50 to 500 bf16
+// positions 35.7 us; 8 trees of 64 fp32 rows over 100 to 1,000 positions: bf16 27.5,
+// fp32 44.8), and every tile of 32 rows reads the cache again (4 trees of 64 nodes,
+// 32 / 8 heads of 128 over 2,000 to 4,000 int8 positions: 118 us where the bytes take
+// 4.4).  Tiles of 4 KB, 4 warps and 3 CTAs per SM
 // were the best of 2 to 8 KB, 2 to 8 warps and 2 to 4 CTAs.
 #pragma once
 
@@ -127,8 +131,9 @@ __device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// x as a tf32 number (rounded to nearest) and what that leaves, which tf32
-// holds exactly.
+// x as a tf32 number (rounded to nearest) and what that leaves, up to 12 bits, of
+// which the product takes the first 11.  (An infinity leaves a NaN, and so do
+// numbers that round to one: unit_anew.)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo)
 {
     hi = (x + 0x1000u) & 0xffffe000u;

@@ -12,9 +12,11 @@
 // lanes are made for all query rows together, so that their latencies overlap
 // (four fp32 rows of one sequence: 6.1 us instead of 6.8).  No rounding but
 // fp32's: two products and additions per instruction.
-// What bounds it: for 64 sequences of 32 to 575 bf16 rows, 12 heads of 64, 14.1 us
-// (4.3 TB/s): one round of short sequences, each a chain of dependent loads; with
-// long caches HBM: 64 x 2,000 to 4,000 rows 94.9 us, 6.3 TB/s; fp32 176.6 us, 6.7.
+// What bounds it: for 64 sequences of 32 to 575 bf16 rows, 12 heads of 64, 14.2 us
+// (4.2 TB/s): 768 CTAs for 608 places, so that the last ones, whatever their
+// lengths, start when the first have ended, and each is a chain of dependent loads
+// (int8, half the bytes: 13.4 us; fp32, twice: 22.2, 5.4 TB/s); with
+// long caches HBM: 64 x 2,000 to 4,000 rows 93.7 us, 6.3 TB/s; fp32 176.6 us, 6.7.
 // Four CTAs per SM: with five, registers spill (one sequence 5.2 us instead of 4.8;
 // 64 short ones 13.9 instead of 14.3); half the accesses per tile were no better (int8
 // 83 us instead of 72 for the long caches).

@@ -31,14 +31,14 @@
 // up in the runs' order, so every call gives the same bits.
 //
 // What bounds it: 32 f16 trees of 64 nodes over 2,000 to 4,000 positions, 12 heads
-// of 64: 87 us, 3.5 TB/s, 214 TFLOP/s, where reading the cache takes 45.  An SM's
+// of 64: 87.5 us, 3.5 TB/s, 214 TFLOP/s, where reading the cache takes 45.  An SM's
 // share of HBM brings a tile of 128 rows (32 KB) in 1,400 cycles and its MMAs take
 // 800, but the softmax of 64 query rows keeps the SM 1,700 (of 16 exponentials and
 // two conversions per thread and 16 columns, and the barriers between the
 // warps), and every change from one unit to the next costs a CTA some 15,000
 // cycles of empty pipeline.  With 32 query rows of 128 dimensions (8 sequences, 4,000
 // to 16,000 bf16 positions, 8 heads) the softmax is a quarter of that per byte:
-// 62 us, 5.3 TB/s.  Not kept: one part of the weights only (the error is 1.4
+// 62.9 us, 5.2 TB/s.  Not kept: one part of the weights only (the error is 1.4
 // times the plain form's), a pair of tiles per step (registers spill: 170 us), 16
 // softmax warps in one CTA per SM (127 us).
 #include <cuda.h>

@@ -10,17 +10,22 @@
 // random numbers once).  A rejected child that has a sibling behind it costs
 // one more pass over the row, for the sum that makes the rest a distribution.
 //
-// What bounds it, at a vocabulary of 50,257: 64 chains of 8 nodes 28.3 us (4.1
-// TB/s; greedy 18.9): about 18 for the rows (5.7 TB/s) and 10 for the draw, whose
-// loads begin where the walk ends and whose logarithms and keys cost half of it;
-// one chain of 6 nodes 7.9 to 8.3 us, 8 trees of 8 10.7 to 11.4 (greedy chains of 8: 4.9, 6.9): two
-// launches and a chain of dependent steps (first, tokens, logits; sums; walk; row
-// and random numbers; the cluster's join).
+// What bounds it, at a vocabulary of 50,257: 64 chains of 8 nodes 28.7 us (4.0
+// TB/s; greedy 18.1): 18 for the rows (90 MB at 5.0 TB/s) and the walks, 10 for the
+// draws, whose loads begin where a walk ends and whose logarithms and keys cost half
+// of it, and none of which begins before every sequence's rows have been read;
+// one chain of 6 nodes 7.8 to 8.4 us, 8 trees of 8 10.5 to 11.5 (greedy chains of 8:
+// 4.9, 5.6): two launches and a chain of dependent steps (first, tokens, logits;
+// sums; walk; row and random numbers; the cluster's join).
 //
 // Rounding: everything is fp32 (a few units in the last place; the sums over
 // the vocabulary are of a few dozen terms per thread, then pairwise or in 64
 // bits), so a decision can differ from the exact one where a random number
-// falls within about 1e-6 of its border.
+// falls within about 1e-6 of its border.  After a rejected child of probability
+// r, what is left, 1 - r or the sum of max(p - q, 0), has cancelled: it is off by some
+// 3e-7 / (1 - r) relatively, and so are its siblings' borders (3e-5 for r = 0.99);
+// the distribution of the tokens, in which that child's r weighs as much, moves by
+// 1e-6 at most.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -242,7 +247,10 @@ __global__ void __launch_bounds__(kVThreads) k_verify(const VerifyArgs a)
         if (tid == 0) w.usable = w.first_ok = 0;
     }
     __syncthreads();
-    // (k_row_stats writes none of what is read before the wait)
+    // What is read before the wait are the call's inputs, which k_row_stats does not
+    // write.  They are complete: this kernel is launched right behind k_row_stats, and
+    // can start only when all of that one's CTAs have passed their own wait for
+    // whatever was before.
     float lx = 0.f, qx = 1.f, ux = 0.f;            // of this thread's node: target's logit at its parent, draft's, random number
     if (parent >= 0 && parent < tid) {
         atomicOr(&w.children[parent], 1ull << tid);
@@ -520,7 +528,7 @@ int gpt2_op_verify_tree(const float *logits, int32_t vocab, const int32_t *token
         a.c_lo = std::max(float(c - double(a.c_hi)), FLT_TRUE_MIN);   // (and not zero, for the largest temperatures)
         // the final draw reads a row with the CTAs of a cluster: as many as
         // keep 2048 ids or more each, while all sequences' clusters run at once (of
-        // 16 CTAs one per SM: 8 sequences took 11.6 us with 16, 10.6 with 8)
+        // 16 CTAs one per SM: 8 trees of 8 took 11.5 us with 16, 10.5 with 8, on one GPU in turn)
         for (int i = 0; i < 4 && vocab >= 4096 * a.cluster && n_seqs <= kClustersFit[i] * (i == 3 ? 1 : 2); ++i) a.cluster *= 2;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
