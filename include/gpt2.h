@@ -637,6 +637,101 @@ int gpt2_decode_tree_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *
 int gpt2_accept_tree_batch(gpt2_batch *m, float temperature, const float *draft_probs, const float *u_accept,
                            const float *u_draw, int32_t *host_tokens, int32_t *host_counts);
 
+/* ---- serving over a paged cache, on caller buffers ------------------------- */
+
+/* A server keeps its sequences' keys and values ("Let's make GPT-2 in assembly",
+ * Step 6) in blocks of a few rows that any sequence may hold, instead of a slot of
+ * n_positions rows for each.  Such a cache is a gpt2_kv whose slots are the blocks:
+ * n_slots of them, n_positions rows each (the block size).  Row p of a sequence lies
+ * in the block that entry p / block size of its line of the block table names, at
+ * offset p % block size.  A step is gpt2_op_page_map, then for each layer
+ * gpt2_op_kv_store with the slots and offsets that this gives, and
+ * gpt2_op_paged_attention, and gpt2_op_sample on the logits.  The conventions are
+ * those of the operations above: DEVICE arrays aligned to their elements, entries
+ * outside their range are skipped and no access leaves the buffers, every call is
+ * asynchronous on `stream`, allocates nothing and may be captured. */
+#define GPT2_MAX_PAGED_SEQS 8192
+
+/* Blocks and places for a step's tokens.  Sequence b (of n_seqs, at most
+ * GPT2_MAX_PAGED_SEQS) has cached[b] rows (int32, below 0: 0) in the blocks of its
+ * line of table (int32 [n_seqs][max_blocks]); it is to gain grow[b] (int32) rows, or,
+ * with grow[b] below 0, leaves: its blocks become free.  The free blocks are a ring:
+ * free_blocks (int32 [n_blocks]), of which free_state[1] count, from entry
+ * free_state[0] on.  Blocks are taken at its front, for sequence after sequence;
+ * those of leaving sequences go to its end, and are there for the next call.
+ * A sequence is served if its rows lie within the first n_rows, its table line has room,
+ * and the blocks needed by it and by those before it (that meet these two) are free;
+ * one that needs no block is not kept by blocks.  The others gain nothing.
+ * Outputs: cached_out [n_seqs] the new lengths; free_state_out [2]; table, the new
+ * blocks' entries (others stay as they are, those of leaving sequences too);
+ * free_blocks; first [n_seqs + 1], where each sequence's rows begin among the step's
+ * rows, grow[b] rows (0 for a leaving one) one after another, served or not, at most
+ * n_rows; and for each of the n_rows rows: seq, its sequence, -1 behind the last;
+ * slot and offset, its place in the cache as gpt2_op_kv_store takes it, and position,
+ * its row in the sequence as gpt2_op_paged_attention takes it, all three -1 where
+ * the sequence is not served and behind the last.  cached_out may be cached, and
+ * free_state_out free_state; other arrays do not overlap.  block_size * max_blocks <
+ * 2^30.  No two sequences' tables and the ring may hold the same block twice (it
+ * would be given out twice).  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
+int gpt2_op_page_map(const int32_t *cached, const int32_t *grow, int32_t n_seqs, int32_t block_size, int32_t *table,
+                     int32_t max_blocks, int32_t *free_blocks, int32_t n_blocks, const int32_t *free_state,
+                     int32_t *cached_out, int32_t *free_state_out, int32_t *first, int32_t *seq, int32_t *slot,
+                     int32_t *offset, int32_t *position, int32_t n_rows, void *stream);
+
+/* Attention of single tokens over a paged cache (Step 6: score q.k * scale, softmax,
+ * weighted sum).  Row i (of n_rows) belongs to sequence seq[i] (int32; NULL: to
+ * sequence i, n_rows <= n_seqs) and sees its rows 0..position[i] (int32; those past
+ * the table's line are not there).  So one row per sequence is a decode step, and
+ * the rows of a prompt or of a drafted chain are its positions.  A row with a position
+ * below 0, with a sequence outside [0, n_seqs), or none of whose blocks is in the cache,
+ * gets zeros; rows in a block outside the cache are not seen.  What a row does not
+ * see does not enter its result, infinities and NaN included; what it sees gives what
+ * the formula gives in fp32; a row that sees only scores of -infinity gets zeros.
+ * q, q_dtype, q_stride, n_head, scale, out and the types are as for
+ * gpt2_op_tree_attention; scores, softmax and sums are fp32 (for three or more 16-bit
+ * query heads on a cache head the weights meet the values in two parts of 16 bits: in
+ * fp16 those below 2^-37 of the largest may vanish).  n_slots * n_head * n_positions of
+ * the cache < 2^32 - 1, max_blocks * n_positions < 2^31.
+ * workspace: 16-byte aligned DEVICE memory of gpt2_op_paged_attention_workspace
+ * bytes (which depends on the current device, not on the number of rows), not used by another call in
+ * flight.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
+size_t gpt2_op_paged_attention_workspace(const gpt2_kv *kv, int32_t q_dtype, int32_t n_head);
+int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, int64_t q_stride, int32_t n_head,
+                            const int32_t *table, int32_t n_seqs, int32_t max_blocks, const int32_t *seq,
+                            const int32_t *position, int32_t n_rows, float scale, void *out, int64_t out_stride,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* The next token of each row of logits (Step 7: divide the scores by a
+ * temperature, softmax, draw at random), with the usual cuts.  logits: DEVICE, dtype
+ * GPT2_F32, GPT2_F16 or GPT2_BF16, row i's vocab values at element i * row_stride
+ * (>= vocab).  Each row has its own settings (DEVICE, one per row; a NULL array:
+ * off in every row):
+ *   temperature fp32: not above 0 (or NULL): greedy, the highest logit (exact ties to the lowest
+ *     id).  Above 0: r = softmax(logits / temperature), cut as follows, with the ids
+ *     ordered by their logits (highest first, exact ties to the lowest id).
+ *   top_k int32: only the first top_k ids are kept (below 1, or vocab and more: all).
+ *   top_p fp32: of these, the fewest first ones whose r makes up top_p of theirs, at
+ *     least one (1 and more, or NaN: all).
+ *   min_p fp32: of these, the ones with r at least min_p times the highest (not above 0,
+ *     or NaN: all; above 1: as 1).
+ * The token is drawn from what is kept in the Gumbel-max form of gpt2_set_sampling:
+ * the id v with the highest r(v) / -log(u[row][v]) (ties to the lowest id); u: DEVICE
+ * fp32 [n_rows][vocab], uniform in (0, 1), of which the kept ids' numbers are read (u
+ * may be NULL with temperature).  Logits of -infinity have probability zero; at temperature 0 a NaN is
+ * never chosen; a row without a logit above -infinity, or with a NaN or +infinity at a
+ * temperature above 0, gives token -1.  Ids of probability below 2^-124 of the highest
+ * count as of probability zero.
+ * Outputs (DEVICE): token int32 [n_rows]; prob fp32 [n_rows], the probability that the
+ * drawn token had among the kept ones (greedy 1; token -1: 0), may be NULL; dist fp32
+ * [n_rows][vocab], the whole distribution drawn from (greedy: 1 at the token; token -1:
+ * zeros), as gpt2_op_verify_tree takes it for draft_probs, may be NULL.  Sums are
+ * exact, weights fp32: a cut or a draw can differ from the exact one within 1e-6 of its border.
+ * vocab <= GPT2_SAMPLE_MAX_VOCAB.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
+#define GPT2_SAMPLE_MAX_VOCAB 524288
+int gpt2_op_sample(const void *logits, int32_t dtype, int64_t row_stride, int32_t n_rows, int32_t vocab,
+                   const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                   const float *u, int32_t *token, float *prob, float *dist, void *stream);
+
 /* ---- errors ------------------------------------------------------------- */
 const char *gpt2_strerror(int status);
 

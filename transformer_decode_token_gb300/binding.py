@@ -34,7 +34,8 @@ EXPORTED = ("gpt2_create", "gpt2_create_ex", "gpt2_path", "gpt2_launch_count", "
             "gpt2_export_kv_batch", "gpt2_batch_info", "gpt2_sync_batch", "gpt2_op_linear_bf16_workspace",
             "gpt2_op_linear_bf16", "gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit",
             "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree", "gpt2_decode_tree_batch",
-            "gpt2_accept_tree_batch", "gpt2_strerror")
+            "gpt2_accept_tree_batch", "gpt2_op_page_map", "gpt2_op_paged_attention_workspace", "gpt2_op_paged_attention",
+            "gpt2_op_sample", "gpt2_strerror")
 
 
 class GPT2Error(RuntimeError):
@@ -161,12 +162,18 @@ def lib(build_if_stale: bool = True, path: str = None):
                                               vp]
             L.gpt2_decode_tree_batch.argtypes = [vp, pi32, pi32, pi32, i32, ctypes.POINTER(vp)]
             L.gpt2_accept_tree_batch.argtypes = [vp, f32, vp, vp, vp, pi32, pi32]
+            L.gpt2_op_page_map.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp]
+            L.gpt2_op_paged_attention_workspace.argtypes = [kv, i32, i32]
+            L.gpt2_op_paged_attention_workspace.restype = sz
+            L.gpt2_op_paged_attention.argtypes = [kv, vp, i32, i64, i32, vp, i32, i32, vp, vp, i32, f32, vp, i64, vp, sz,
+                                                  vp]
+            L.gpt2_op_sample.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
             L.gpt2_strerror.argtypes = [ctypes.c_int]
             L.gpt2_strerror.restype = ctypes.c_char_p
             for n in EXPORTED:
                 if n not in ("gpt2_destroy", "gpt2_destroy_batch", "gpt2_op_head_argmax_workspace",
                              "gpt2_op_linear_bf16_workspace", "gpt2_op_tree_attention_workspace",
-                             "gpt2_op_verify_tree_workspace", "gpt2_strerror"):
+                             "gpt2_op_verify_tree_workspace", "gpt2_op_paged_attention_workspace", "gpt2_strerror"):
                     getattr(L, n).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -565,7 +572,9 @@ def _native():
         loader.exec_module(m)
         m.bind(GPT2Error, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
                             ("gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit",
-                             "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree")))
+                             "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace",
+                             "gpt2_op_verify_tree", "gpt2_op_page_map", "gpt2_op_paged_attention_workspace",
+                             "gpt2_op_paged_attention", "gpt2_op_sample")))
         _torch_ops = m
     return _torch_ops
 
@@ -646,3 +655,56 @@ def op_verify_tree(logits, tokens, parents, first, max_nodes, temperature=0.0, d
                                   u_draw, path, n_path, next_token, workspace)
     return (_torch_ops or _native()).verify_tree(logits, tokens, parents, first, max_nodes, temperature, draft_probs,
                                                  u_accept, u_draw, path, n_path, next_token, workspace)
+
+
+# ---- serving over a paged cache, on caller tensors -----------------------------------
+#
+# A paged cache is a cache as above whose slots are the blocks: [blocks][heads]
+# [block size][head_dim].  table [sequences][blocks] (int32) names each sequence's
+# blocks; the free ones are a ring, free_blocks [blocks] with free_state (next,
+# count).  op_kv_store and op_kv_load take op_page_map's slot and offset.
+
+MAX_PAGED_SEQS = 8192          # GPT2_MAX_PAGED_SEQS
+SAMPLE_MAX_VOCAB = 524288      # GPT2_SAMPLE_MAX_VOCAB
+
+
+def op_page_map(cached, grow, table, free_blocks, free_state, block_size, n_rows, cached_out=None,
+                free_state_out=None, stream=None):
+    """Blocks and places for a step's tokens: sequence b has cached[b] rows and
+    is to gain grow[b] of them (below 0: it leaves, its blocks become free).
+    Updates table and free_blocks, and returns (cached_out, free_state_out,
+    first, seq, slot, offset, position), the last four for each of the n_rows
+    packed rows; see gpt2_op_page_map.  cached_out and free_state_out may be
+    cached and free_state."""
+    if stream is not None:
+        with _on(stream):
+            return op_page_map(cached, grow, table, free_blocks, free_state, block_size, n_rows, cached_out,
+                               free_state_out)
+    return (_torch_ops or _native()).page_map(cached, grow, table, free_blocks, free_state, block_size, n_rows,
+                                              cached_out, free_state_out)
+
+
+def op_paged_attention(q, k_cache, v_cache, table, position, seq=None, k_scale=None, v_scale=None, scale=None, out=None,
+                       workspace=None, stream=None):
+    """Attention of rows q [rows][query heads][head_dim] over a paged cache: row
+    i sees rows 0..position[i] of sequence seq[i] (of sequence i unless given);
+    scale 1/sqrt(head_dim) unless given.  Returns out, like q."""
+    if stream is not None:
+        with _on(stream):
+            return op_paged_attention(q, k_cache, v_cache, table, position, seq, k_scale, v_scale, scale, out,
+                                      workspace)
+    return (_torch_ops or _native()).paged_attention(q, k_cache, v_cache, table, position, seq, k_scale, v_scale, scale,
+                                                     out, workspace)
+
+
+def op_sample(logits, temperature=None, u=None, top_k=None, top_p=None, min_p=None, token=None, prob=None, dist=None,
+              stream=None):
+    """The next token of each row of logits [rows][vocab] (fp32, fp16 or bf16)
+    by its own temperature, top_k (int32), top_p and min_p, [rows] each, None:
+    off (no temperature: greedy), from uniform numbers u [rows][vocab] in (0, 1).
+    Returns (token, prob): int32 ids and the probability that each had among the
+    ids left; dist [rows][vocab] (fp32), if given, receives the distribution."""
+    if stream is not None:
+        with _on(stream):
+            return op_sample(logits, temperature, u, top_k, top_p, min_p, token, prob, dist)
+    return (_torch_ops or _native()).sample(logits, temperature, u, top_k, top_p, min_p, token, prob, dist)

@@ -1,0 +1,272 @@
+// Attention over a paged cache: what its kernels share.
+//
+// A unit is one (query row, cache head, tile of up to R of the query heads that
+// share the head).  Its cache rows come in tiles of KS; the tiles of all units,
+// one unit after another, are one list, and every warp takes an equal share of
+// it, whatever the lengths: no warp waits for a longer row, none meets a barrier.
+// A unit that lies in one warp's share is written by that warp.  Of a unit that is
+// cut, each warp writes its part (maximum, sum of the weights, weighted sum, in
+// fp32) to the workspace, and a second kernel joins the parts in the order of the
+// list, so every call gives the same bits.
+#pragma once
+
+#include "tree_attn.cuh"
+
+namespace gpt2 {
+
+struct PagedArgs {
+    gpt2_kv kv;
+    const void *q;
+    void *out;
+    int64_t q_stride, out_stride;
+    const int32_t *table, *seq, *position;
+    int4 *heads;                    // workspace: [warps] the unit whose parts begin with this warp's
+    float2 *ml;                     // [warps][2][R]
+    float *sums;                    // [warps][2][R][D]
+    int32_t n_seqs, n_rows, max_blocks, group, row_tiles, q_dtype, warps;
+    float scale_log2;               // scale * log2(e)
+};
+
+// R: 1, 2 or 4 query heads of a tile, on the CUDA cores
+cudaError_t paged_few_f32(const PagedArgs &a, int r, int ctas, cudaStream_t s);
+cudaError_t paged_few_16(const PagedArgs &a, int r, int ctas, cudaStream_t s);
+cudaError_t paged_few_8(const PagedArgs &a, int r, int ctas, cudaStream_t s);
+// 8 query heads of a tile, on the matrix instructions (16-bit rows)
+cudaError_t paged_mma(const PagedArgs &a, int ctas, cudaStream_t s);
+cudaError_t paged_join(const PagedArgs &a, int r, cudaStream_t s);
+
+namespace paged {
+
+using namespace tree;
+
+constexpr int kThreads = kNW * 32;
+constexpr uint32_t kNone = 0xffffffffu;      // no cache row
+
+// Cache rows that query row i sees.
+__device__ __forceinline__ int seen(const PagedArgs &a, int i)
+{
+    const long long cap = (long long)a.max_blocks * a.kv.n_positions;
+    const long long n = (long long)a.position[i] + 1;
+    if (n <= 0) return 0;
+    if (a.seq) {
+        const int b = a.seq[i];
+        if (b < 0 || b >= a.n_seqs) return 0;
+    }
+    return int(n < cap ? n : cap);
+}
+__device__ __forceinline__ const int32_t *table_of(const PagedArgs &a, int i)
+{
+    return a.table + size_t(a.seq ? a.seq[i] : i) * a.max_blocks;
+}
+
+// The cache row of a sequence's row j for head h (kNone where its block is none).
+__device__ __forceinline__ uint32_t cache_row(const PagedArgs &a, const int32_t *table, uint32_t j, int h)
+{
+    const uint32_t bs = uint32_t(a.kv.n_positions), k = j / bs;
+    const int32_t block = table[k];
+    if (block < 0 || block >= a.kv.n_slots) return kNone;
+    return (uint32_t(block) * uint32_t(a.kv.n_head) + uint32_t(h)) * bs + (j - k * bs);
+}
+
+// Equal shares of n tiles: share w begins at w * q + min(w, rest).
+struct Shares {
+    uint32_t q, rest;
+    __device__ __forceinline__ Shares(uint32_t n, uint32_t parts) : q(n / parts), rest(n % parts) {}
+    __device__ __forceinline__ uint32_t begin(uint32_t w) const { return w * q + min(w, rest); }
+    __device__ __forceinline__ uint32_t of(uint32_t x) const      // the share of tile x
+    {
+        const uint32_t big = rest * (q + 1);
+        return x < big ? x / (q + 1) : rest + (x - big) / q;
+    }
+};
+
+// A place in the list: a tile of a unit.
+template <int KS>
+struct Place {
+    const int32_t *table;
+    int row, unit;                  // unit of the row: cache head * row_tiles + tile of query heads
+    uint32_t tile, tiles, len;
+
+    __device__ __forceinline__ void enter(const PagedArgs &a, int i)
+    {
+        row = i;
+        len = uint32_t(seen(a, i));
+        tiles = (len + KS - 1) / KS;
+        table = len ? table_of(a, i) : nullptr;
+    }
+    __device__ __forceinline__ void next(const PagedArgs &a)
+    {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++unit < a.kv.n_head * a.row_tiles) return;
+        unit = 0;
+        do enter(a, row + 1);
+        while (len == 0);           // (there is a next tile)
+    }
+    // the cache row of the tile's row `lane`
+    __device__ __forceinline__ uint32_t at(const PagedArgs &a, int lane) const
+    {
+        const uint32_t j = tile * KS + lane;
+        return lane < KS && j < len ? cache_row(a, table, j, unit / a.row_tiles) : kNone;
+    }
+};
+
+// This warp's share of the list, and the place where it begins.  Called by all
+// threads of the CTA; also writes the zeros of rows that see nothing.
+template <int KS, int D>
+__device__ __forceinline__ bool find_share(const PagedArgs &a, uint32_t w, Shares &sh, uint32_t &x0, uint32_t &x1,
+                                           Place<KS> &at)
+{
+    __shared__ uint32_t sums[kNW], base[kNW];
+    __shared__ int rows[kNW];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (a.n_rows + kThreads - 1) / kThreads, r0 = min(tid * per, a.n_rows), r1 = min(r0 + per, a.n_rows);
+    uint32_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += (seen(a, r) + KS - 1) / KS;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    uint32_t total = 0;
+#pragma unroll
+    for (int i = 0; i < kNW; ++i) {
+        if (i < warp) incl += sums[i];
+        total += sums[i];
+    }
+    const uint32_t units = uint32_t(a.kv.n_head) * a.row_tiles, n = total * units;
+    const uint32_t parts = max(1u, min(uint32_t(a.warps), n));
+    sh = Shares(n, parts);
+#pragma unroll
+    for (int i = 0; i < kNW; ++i) {              // the rows where this CTA's warps begin
+        const uint32_t wi = i * gridDim.x + blockIdx.x;
+        if (wi >= parts || n == 0) continue;
+        const uint32_t y = sh.begin(wi) / units;
+        if (y >= incl - mine && y < incl) {
+            uint32_t t = incl - mine;
+            int r = r0;
+            for (;; ++r) {
+                const uint32_t k = (seen(a, r) + KS - 1) / KS;
+                if (y < t + k) break;
+                t += k;
+            }
+            rows[i] = r;
+            base[i] = t;
+        }
+    }
+    for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
+        if (seen(a, r) != 0) continue;
+        const int cols = a.kv.n_head * a.group * D;
+        for (int e = tid * 4; e < cols; e += kThreads * 4) {
+            const size_t o = size_t(r) * a.out_stride + e;
+            if (a.q_dtype == GPT2_F32) *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = make_float4(0.f, 0.f, 0.f, 0.f);
+            else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + o) = make_uint2(0u, 0u);
+        }
+    }
+    __syncthreads();
+    if (w >= parts || n == 0) return false;
+    x0 = sh.begin(w);
+    x1 = sh.begin(w + 1);
+    at.enter(a, rows[warp]);
+    const uint32_t off = x0 - base[warp] * units;
+    at.unit = int(off / at.tiles);
+    at.tile = off % at.tiles;
+    return true;
+}
+
+// Query heads of a unit, and where its first one's row of q (or out) begins.
+template <int R>
+__device__ __forceinline__ int heads_of(const PagedArgs &a, int unit)
+{
+    return min(R, a.group - unit % a.row_tiles * R);
+}
+template <int D, int R>
+__device__ __forceinline__ size_t row_at(const PagedArgs &a, int row, int unit, int64_t stride)
+{
+    return size_t(row) * stride + size_t(unit / a.row_tiles * a.group + unit % a.row_tiles * R) * D;
+}
+
+// Four elements of a result.
+__device__ __forceinline__ void put4(const PagedArgs &a, size_t at, float x, float y, float z, float w)
+{
+    if (a.q_dtype == GPT2_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(x, y, z, w);
+    } else {
+        uint2 v;
+        if (a.q_dtype == GPT2_F16) {
+            const __half2 p = __floats2half2_rn(x, y), r = __floats2half2_rn(z, w);
+            v = make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&r));
+        } else {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x, y), r = __floats2bfloat162_rn(z, w);
+            v = make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&r));
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = v;
+    }
+}
+
+// One result row (query head h of the unit's tile) by its definition, by a warp in
+// fp32: the maximum and the sum of the weights, a key per lane, then the weighted
+// values, D / 32 dimensions per lane.  For results that are not finite where the
+// kernel's products in parts make a NaN of an infinity.
+template <int KIND, int D, int R>
+__device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int h)
+{
+    constexpr bool kScaled = KIND == GPT2_INT8 || KIND == GPT2_E4M3;
+    constexpr int N = D / 32;
+    const int lane = threadIdx.x & 31, len = seen(a, row), head = unit / a.row_tiles;
+    const int32_t *table = table_of(a, row);
+    const size_t q_at = row_at<D, R>(a, row, unit, a.q_stride) + size_t(h) * D;
+    auto score = [&](uint32_t j, uint32_t r) {       // -infinity where it is not seen
+        if (r == kNone) return -INFINITY;
+        const float s = kScaled ? a.kv.k_scale[r] : 1.f;
+        float x = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            const float4 q = load_row4(a.q, q_at + d, a.q_dtype);
+            const float y[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x = fmaf(y[i] * a.scale_log2, value_at<KIND>(a.kv.k, size_t(r) * D + d + i) * s, x);
+        }
+        return x;
+    };
+    auto at = [&](int j) { return j < len ? cache_row(a, table, uint32_t(j), head) : kNone; };
+    float m = -INFINITY, l = 0.f, out[N];
+    bool nan = false;
+    for (int j0 = 0; j0 < len && !nan; j0 += 32) {
+        const float s = score(j0 + lane, at(j0 + lane)), top = fmaxf(m, s), safe = top == -INFINITY ? 0.f : top;
+        nan = __any_sync(0xffffffffu, s != s || s == INFINITY);
+        l = l * exp2_approx(m - safe) + exp2_approx(s - safe);
+        m = top;
+    }
+    const float top = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = nan ? __int_as_float(0x7fc00000) : 0.f;
+    if (!nan && top != -INFINITY) {
+        l = warp_sum(l * exp2_approx(m - top));
+        for (int j0 = 0; j0 < len; j0 += 32) {
+            const uint32_t r = at(j0 + lane);
+            const float p = exp2_approx(score(j0 + lane, r) - top) / l;
+            for (int t = 0; t < 32; ++t) {
+                const uint32_t rt = __shfl_sync(0xffffffffu, r, t);
+                const float w = __shfl_sync(0xffffffffu, p, t);
+                if (rt == kNone) continue;
+                const float s = kScaled ? a.kv.v_scale[rt] : 1.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) out[i] = fmaf(w, value_at<KIND>(a.kv.v, size_t(rt) * D + lane * N + i) * s, out[i]);
+            }
+        }
+    }
+    const size_t o = row_at<D, R>(a, row, unit, a.out_stride) + size_t(h) * D + lane * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (a.q_dtype == GPT2_F32) static_cast<float *>(a.out)[o + i] = out[i];
+        else if (a.q_dtype == GPT2_F16) static_cast<__half *>(a.out)[o + i] = __float2half_rn(out[i]);
+        else static_cast<__nv_bfloat16 *>(a.out)[o + i] = __float2bfloat16_rn(out[i]);
+    }
+}
+
+}  // namespace paged
+}  // namespace gpt2

@@ -1,0 +1,299 @@
+// Attention over a paged cache on the matrix instructions, for 16-bit rows and
+// three or more query heads on a cache head, over the list of paged.cuh.
+//
+// The 16 rows of an instruction's A side are the 8 query heads of a tile twice: the
+// upper half takes the second part of what the lower half is the first part of
+// (the weights p = hi + lo, and fp16 queries over 8-bit caches, whose codes are
+// exact in bf16), so that both parts cost one instruction and meet in one thread,
+// which adds the two halves of the accumulators.  Cache rows go from global memory
+// to the operand registers as in tree_attn.cuh: keys by 16-byte pieces c, c + 4, ..,
+// values by pieces g, g + 8, .. of the rows whose weights the thread holds.
+#include "paged.cuh"
+
+namespace gpt2 {
+namespace paged {
+namespace {
+
+// Two 8-bit codes (bytes 0, 1 of x for HIGH = 0, else 2, 3) as a bf16 pair.
+// int8: 0x43uu with the code's low seven bits is 128 + those, and 128 or, for a
+// negative code, 256 is taken off.
+template <int KIND, int HIGH>
+__device__ __forceinline__ uint32_t codes_to_bf162(uint32_t x)
+{
+    if constexpr (KIND == GPT2_INT8) {
+        const uint32_t y = __byte_perm(x, 0x43434343u, HIGH ? 0x4342u : 0x4140u);
+        const uint32_t u = y & 0xff7fff7fu, v = y & 0xff80ff80u;
+        const __nv_bfloat162 d =
+            __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), *reinterpret_cast<const __nv_bfloat162 *>(&v));
+        return *reinterpret_cast<const uint32_t *>(&d);
+    } else {
+        const uint32_t h = codes_to_half2<true>(x, HIGH ? 0x4342u : 0x4140u);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        const __nv_bfloat162 d = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&d);
+    }
+}
+
+template <int KIND, int D>
+struct Shape {
+    static constexpr int kES = KIND == GPT2_INT8 || KIND == GPT2_E4M3 ? 1 : 2;
+    static constexpr bool kScaled = kES == 1, kHalf = KIND == GPT2_F16;
+    static constexpr int kRowB = D * kES;
+    static constexpr int kKLd = kRowB / 4 < 16 ? kRowB / 4 : 16, kNK = kRowB / (4 * kKLd);
+    static constexpr int kVLd = kRowB / 8 < 16 ? kRowB / 8 : 16, kNV = kRowB / (8 * kVLd);
+    static constexpr int kEK = kKLd / kES, kEV = kVLd / kES;   // elements of an access
+    static constexpr int KS = 4096 / kRowB > 32 ? 32 : 4096 / kRowB;
+    static constexpr int kT8 = KS / 8, kSteps = D / 16, kNT = D / 8;
+};
+
+template <int KIND, int D, bool QF16>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const __grid_constant__ PagedArgs a)
+{
+    using S = Shape<KIND, D>;
+    constexpr int R = 8, KS = S::KS, T8 = S::kT8;
+    constexpr bool kBf = !S::kHalf, kTwo = S::kScaled && QF16;   // (queries in two parts)
+    constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t w = warp * gridDim.x + blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    Shares sh(1, 1);
+    uint32_t x0 = 0, x1 = 0;
+    Place<KS> at;
+    if (!find_share<KS, D>(a, w, sh, x0, x1, at)) {
+        if (lane == 0) a.heads[w] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const uint8_t *kbase = static_cast<const uint8_t *>(a.kv.k) + c * S::kKLd;
+    const uint8_t *vbase = static_cast<const uint8_t *>(a.kv.v) + g * S::kVLd;
+    uint32_t kr[T8][S::kRowB / 16], vr[T8][2][S::kRowB / 32];
+    auto load_keys = [&](uint32_t rows) {
+#pragma unroll
+        for (int t = 0; t < T8; ++t) {
+            const uint32_t r = __shfl_sync(0xffffffffu, rows, t * 8 + g);
+#pragma unroll
+            for (int p = 0; p < S::kNK; ++p)
+                load_piece<S::kKLd>(kr[t] + p * S::kKLd / 4, kbase + size_t(r) * S::kRowB + p * 4 * S::kKLd, r != kNone);
+        }
+    };
+    auto load_values = [&](uint32_t rows) {
+#pragma unroll
+        for (int t = 0; t < T8; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t r = __shfl_sync(0xffffffffu, rows, t * 8 + 2 * c + i);
+#pragma unroll
+                for (int p = 0; p < S::kNV; ++p)
+                    load_piece<S::kVLd>(vr[t][i] + p * S::kVLd / 4, vbase + size_t(r) * S::kRowB + p * 8 * S::kVLd,
+                                        r != kNone);
+            }
+    };
+    uint32_t qa[S::kSteps][kTwo ? 4 : 2];
+    float o[S::kNT][4], m = 0.f, l = 0.f;                // m, l: of query head g
+    int heads = 0;
+    uint32_t from = 0;
+    auto begin_unit = [&]() {
+        heads = heads_of<R>(a, at.unit);
+        from = at.tile;
+        const uint16_t *q = static_cast<const uint16_t *>(a.q) + row_at<D, R>(a, at.row, at.unit, a.q_stride) +
+                            size_t(g < heads ? g : 0) * D;
+#pragma unroll
+        for (int s = 0; s < S::kSteps; ++s) {
+            constexpr int kPer = S::kEK / 4;             // steps of an access
+            const uint2 v = *reinterpret_cast<const uint2 *>(q + (s / kPer * 4 + c) * S::kEK + s % kPer * 4);
+            if constexpr (kTwo) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+                uint32_t p[2];
+                split16<kBf16, 2>(x.x, x.y, p);
+                qa[s][0] = p[0], qa[s][1] = p[1];
+                split16<kBf16, 2>(y.x, y.y, p);
+                qa[s][2] = p[0], qa[s][3] = p[1];
+            } else {
+                qa[s][0] = v.x, qa[s][1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < S::kNT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+        m = -INFINITY;
+        l = 0.f;
+    };
+    uint32_t rows = at.at(a, lane);
+    load_keys(rows);
+    begin_unit();
+    int4 head = make_int4(0, 0, 0, 0);
+
+    for (uint32_t x = x0; x < x1; ++x) {
+        load_values(rows);
+        float ks = 0.f, vs = 0.f;                        // of the tile's row `lane`
+        if constexpr (S::kScaled) {
+            ks = load_scale(a.kv.k_scale + rows, rows != kNone);
+            vs = load_scale(a.kv.v_scale + rows, rows != kNone);
+        }
+        const bool more = x + 1 < x1;
+        Place<KS> then = at;
+        uint32_t rows_then = kNone;
+        if (more) {
+            then.next(a);
+            rows_then = then.at(a, lane);
+        }
+        float s[T8][4];
+#pragma unroll
+        for (int t = 0; t < T8; ++t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < S::kSteps; ++k) {
+                uint32_t b0, b1;
+                if constexpr (S::kScaled) {
+                    b0 = codes_to_bf162<KIND, 0>(kr[t][k]);
+                    b1 = codes_to_bf162<KIND, 1>(kr[t][k]);
+                } else {
+                    b0 = kr[t][2 * k];
+                    b1 = kr[t][2 * k + 1];
+                }
+                const uint32_t A[4] = {qa[k][0], kTwo ? qa[k][1] : 0u, kTwo ? qa[k][2] : qa[k][1], kTwo ? qa[k][3] : 0u};
+                mma16816(s[t], A, b0, b1, kBf);
+            }
+        }
+        if (more) load_keys(rows_then);
+        const uint32_t there = __ballot_sync(0xffffffffu, rows != kNone) & kAll;
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < T8; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int key = t * 8 + 2 * c + i;
+                float y = (kTwo ? s[t][i] + s[t][i + 2] : s[t][i]) * a.scale_log2;
+                if constexpr (S::kScaled) y *= __shfl_sync(0xffffffffu, ks, key);
+                if (there != kAll && !(there >> key & 1)) y = -INFINITY;
+                s[t][i] = y;
+                top = fmaxf(top, y);
+            }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float mn = fmaxf(m, top), safe = mn == -INFINITY ? 0.f : mn;
+        // (a warp none of whose maxima has moved keeps its sums as they are)
+        if (__any_sync(0xffffffffu, mn != m)) {
+            const float keep = exp2_approx(m - safe);
+            l *= keep;
+#pragma unroll
+            for (int j = 0; j < S::kNT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[j][i] *= keep;
+        }
+        m = mn;
+        uint32_t hi[T8], lo[T8];                         // weights of keys 2c, 2c + 1 of each eight, in two parts
+#pragma unroll
+        for (int t = 0; t < T8; ++t) {
+            float p[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                p[i] = exp2_approx(s[t][i] - safe + (S::kHalf ? kShift : 0.f));
+                l += p[i];
+                if constexpr (S::kScaled) p[i] *= __shfl_sync(0xffffffffu, vs, t * 8 + 2 * c + i);
+            }
+            uint32_t part[2];
+            split16<S::kHalf ? kF16 : kBf16, 2>(p[0], p[1], part);
+            hi[t] = part[0], lo[t] = part[1];
+        }
+#pragma unroll
+        for (int t = 0; t < T8; t += 2) {
+            const uint32_t A[4] = {hi[t], lo[t], hi[t + 1], lo[t + 1]};
+#pragma unroll
+            for (int j = 0; j < S::kNT; ++j) {
+                constexpr int EV = S::kEV;
+                const int at4 = j / EV * (S::kVLd / 4), e = j % EV;
+                uint32_t b[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t *r0 = vr[t + h][0] + at4, *r1 = vr[t + h][1] + at4;
+                    if constexpr (S::kScaled) {
+                        const uint32_t z = __byte_perm(r0[e / 4], r1[e / 4], e % 4 < 2 ? 0x5140u : 0x7362u);   // a0 b0 a1 b1
+                        b[h] = e % 2 == 0 ? codes_to_bf162<KIND, 0>(z) : codes_to_bf162<KIND, 1>(z);
+                    } else {
+                        b[h] = __byte_perm(r0[e / 2], r1[e / 2], e % 2 == 0 ? 0x5410u : 0x7632u);
+                    }
+                }
+                mma16816(o[j], A, b[0], b[1], kBf);
+            }
+        }
+
+        const bool ends = at.tile + 1 == at.tiles;
+        if (ends || !more) {                             // the unit's result, or this warp's part of it
+            const bool whole = ends && from == 0;
+            const uint32_t part = w * 2 + (from == 0);
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            float sane = 0.f;                            // NaN once a result is not finite
+            if (g < heads) {
+                const size_t to = row_at<D, R>(a, at.row, at.unit, a.out_stride) + size_t(g) * D;
+                float *sum = a.sums + (size_t(part) * R + g) * D;
+#pragma unroll
+                for (int p = 0; p < S::kNV; ++p)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)          // dimensions of columns 2c and 2c + 1
+#pragma unroll
+                        for (int e = 0; e < S::kEV; e += 4) {
+                            float v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float *y = o[p * S::kEV + e + k];
+                                v[k] = (y[i] + y[i + 2]) * inv;
+                                sane = fmaf(v[k], 0.f, sane);
+                            }
+                            const int d = (8 * p + 2 * c + i) * S::kEV + e;
+                            if (whole) put4(a, to + d, v[0], v[1], v[2], v[3]);
+                            else *reinterpret_cast<float4 *>(sum + d) = make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                if (!whole && c == 0) a.ml[size_t(part) * R + g] = make_float2(m, l);
+            }
+            if (whole) {
+                uint32_t odd = __ballot_sync(0xffffffffu, sane != 0.f);
+                while (odd) {
+                    const int h = (__ffs(odd) - 1) >> 2;
+                    row_anew<KIND, D, R>(a, at.row, at.unit, h);
+                    odd &= ~(0xfu << (h * 4));
+                }
+            } else if (from == 0) {
+                head = make_int4(at.row, at.unit, int(sh.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
+            }
+            if (more) {
+                at = then;
+                begin_unit();
+            }
+        }
+        at = then;
+        rows = rows_then;
+    }
+    if (lane == 0) a.heads[w] = head;
+}
+
+template <int KIND, bool QF16>
+cudaError_t mma_dims(const PagedArgs &a, int ctas, cudaStream_t s)
+{
+    switch (a.kv.head_dim) {
+    case 32: return spec_launch(k_paged_mma<KIND, 32, QF16>, dim3(ctas), kThreads, 0, 1, s, a);
+    case 64: return spec_launch(k_paged_mma<KIND, 64, QF16>, dim3(ctas), kThreads, 0, 1, s, a);
+    default: return spec_launch(k_paged_mma<KIND, 128, QF16>, dim3(ctas), kThreads, 0, 1, s, a);
+    }
+}
+
+}  // namespace
+}  // namespace paged
+
+cudaError_t paged_mma(const PagedArgs &a, int ctas, cudaStream_t s)
+{
+    const bool f16 = a.q_dtype == GPT2_F16;
+    switch (a.kv.dtype) {
+    case GPT2_F16: return paged::mma_dims<GPT2_F16, true>(a, ctas, s);
+    case GPT2_BF16: return paged::mma_dims<GPT2_BF16, false>(a, ctas, s);
+    case GPT2_INT8: return f16 ? paged::mma_dims<GPT2_INT8, true>(a, ctas, s) : paged::mma_dims<GPT2_INT8, false>(a, ctas, s);
+    default: return f16 ? paged::mma_dims<GPT2_E4M3, true>(a, ctas, s) : paged::mma_dims<GPT2_E4M3, false>(a, ctas, s);
+    }
+}
+
+}  // namespace gpt2

@@ -1,4 +1,4 @@
-// The speculative-decoding calls of binding.py on torch tensors: checks of
+// The speculative-decoding and paged-cache calls of binding.py on torch tensors: checks of
 // types, shapes and devices, allocation of results, and the call into
 // libgpt2.so on the current stream.  Argument marshalling only, compiled
 // because it is most of a small call's time: for the attention of one
@@ -30,6 +30,10 @@ struct {
     decltype(&gpt2_op_tree_attention) tree_attention;
     decltype(&gpt2_op_verify_tree_workspace) verify_tree_workspace;
     decltype(&gpt2_op_verify_tree) verify_tree;
+    decltype(&gpt2_op_page_map) page_map;
+    decltype(&gpt2_op_paged_attention_workspace) paged_attention_workspace;
+    decltype(&gpt2_op_paged_attention) paged_attention;
+    decltype(&gpt2_op_sample) sample;
 } g_lib;
 
 struct Bad {                   // a ValueError
@@ -134,15 +138,19 @@ int64_t row_stride(const at::Tensor &t, const char *name, int64_t H, int64_t D, 
     return t.size(0) > 1 ? t.stride(0) : H * D;
 }
 
-// A tensor of this shape in `whole`'s memory, from element `from` on: results of
+// A tensor of this shape (and type, of the same size) in `whole`'s memory, from element `from` on: results of
 // one call are made in one allocation (1.3 us each on the Arm host, as long as
 // the marshalling itself).
-at::Tensor part(const at::Tensor &whole, int64_t from, at::IntArrayRef shape)
+at::Tensor part(const at::Tensor &whole, int64_t from, at::IntArrayRef shape, caffe2::TypeMeta type)
 {
-    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), type);
     t->set_sizes_contiguous(shape);
     t->set_storage_offset(from);
     return at::Tensor(std::move(t));
+}
+at::Tensor part(const at::Tensor &whole, int64_t from, at::IntArrayRef shape)
+{
+    return part(whole, from, shape, whole.dtype());
 }
 
 // Memory of a call in flight, returned to torch's allocator when the call has
@@ -410,12 +418,139 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// cached, grow, table, free_blocks, free_state, block_size, n_rows, cached_out, free_state_out (the last two may be
+// None)
+PyObject *page_map(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("page_map", 9, n, [&]() -> PyObject * {
+        const Call c;
+        const at::Tensor &cached = tensor(a[0], "cached"), &table = tensor(a[2], "table");
+        const int64_t B = one_dim(cached), W = table.dim() == 2 ? table.size(1) : -1, N = one_dim(tensor(a[3], "free_blocks"));
+        const int32_t bs = to_int(a[5], "block_size"), rows = to_int(a[6], "n_rows");
+        if (B < 0 || W < 1 || W >= (int64_t(1) << 31) || N < 1 || N >= (int64_t(1) << 31))
+            throw Bad{"cached must be [sequences], table [sequences][blocks] and free_blocks [blocks]"};
+        if (B > GPT2_MAX_PAGED_SEQS) throw Bad{"at most 8192 sequences"};
+        if (rows < 0) throw Bad{"n_rows must not be negative"};
+        const int32_t *len = whole<int32_t>(a[0], "cached", at::kInt, {B}, c.dev);
+        const int32_t *grow = whole<int32_t>(a[1], "grow", at::kInt, {B}, c.dev);
+        int32_t *tab = whole<int32_t>(a[2], "table", at::kInt, {B, W}, c.dev);
+        int32_t *ring = whole<int32_t>(a[3], "free_blocks", at::kInt, {N}, c.dev);
+        const int32_t *state = whole<int32_t>(a[4], "free_state", at::kInt, {2}, c.dev);
+        const int64_t R = rows;
+        const at::Tensor made = at::empty({2 * B + 3 + 4 * R}, cached.options());
+        auto result = [&](PyObject *o, const char *name, int64_t from, at::IntArrayRef shape) {
+            if (o == Py_None) return part(made, from, shape);
+            whole(tensor(o, name), name, at::kInt, shape, c.dev);
+            return tensor(o, name);
+        };
+        const at::Tensor out = result(a[7], "cached_out", 0, {B}), state_out = result(a[8], "free_state_out", B, {2}),
+                         first = part(made, B + 2, {B + 1}), seq = part(made, 2 * B + 3, {R}),
+                         slot = part(made, 2 * B + 3 + R, {R}), offset = part(made, 2 * B + 3 + 2 * R, {R}),
+                         position = part(made, 2 * B + 3 + 3 * R, {R});
+        // (an empty tensor has no address; the call wants none of its elements)
+        const int32_t *some = made.data_ptr<int32_t>();
+        check(g_lib.page_map(B ? len : some, B ? grow : some, int32_t(B), bs, B ? tab : const_cast<int32_t *>(some),
+                             int32_t(W), ring, int32_t(N), state, B ? out.data_ptr<int32_t>() : const_cast<int32_t *>(some),
+                             state_out.data_ptr<int32_t>(), first.data_ptr<int32_t>(), seq.data_ptr<int32_t>(),
+                             slot.data_ptr<int32_t>(), offset.data_ptr<int32_t>(), position.data_ptr<int32_t>(), rows,
+                             c.stream),
+              "gpt2_op_page_map");
+        return Py_BuildValue("(NNNNNNN)", THPVariable_Wrap(out), THPVariable_Wrap(state_out), THPVariable_Wrap(first),
+                             THPVariable_Wrap(seq), THPVariable_Wrap(slot), THPVariable_Wrap(offset),
+                             THPVariable_Wrap(position));
+    });
+}
+
+// q, k_cache, v_cache, table, position, seq, k_scale, v_scale, scale, out, workspace (seq and the last five may be None)
+PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("paged_attention", 11, n, [&]() -> PyObject * {
+        const Call c;
+        const Cache cache(a[1], a[2], a[6], a[7], c.dev);
+        const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[3], "table");
+        const int64_t D = cache.kv.head_dim;
+        if (q.dim() != 3) throw Bad{"q must be [rows][heads][head_dim]"};
+        if (table.dim() != 2 || table.size(0) >= (int64_t(1) << 31) || table.size(1) >= (int64_t(1) << 31))
+            throw Bad{"table must be [sequences][blocks]"};
+        const int64_t rows = q.size(0), H = q.size(1), stride = row_stride(q, "q", H, D, c.dev);
+        const int32_t *tab = whole<int32_t>(a[3], "table", at::kInt, table.sizes(), c.dev);
+        const int32_t *position = whole<int32_t>(a[4], "position", at::kInt, {rows}, c.dev);
+        const int32_t *seq = a[5] == Py_None ? nullptr : whole<int32_t>(a[5], "seq", at::kInt, {rows}, c.dev);
+        if (!seq && rows > table.size(0)) throw Bad{"without seq the table must have a line for each row of q"};
+        const float scale = a[8] == Py_None ? float(1.0 / std::sqrt(double(D))) : to_float(a[8], "scale");
+        if (H >= (1 << 30)) throw Bad{"too many heads"};
+        at::Tensor out;
+        int64_t out_stride = H * D;
+        if (a[9] == Py_None) {
+            out = at::empty({rows, H, D}, q.options());
+        } else {
+            out = tensor(a[9], "out");
+            if (out.scalar_type() != q.scalar_type() || out.sizes() != q.sizes())
+                throw Bad{"out must have q's type and shape"};
+            out_stride = row_stride(out, "out", H, D, c.dev);
+        }
+        if (rows > 0 && table.numel() == 0) {
+            out.zero_();                           // nothing to see
+        } else if (rows > 0) {
+            const int type = row_type(q.scalar_type());
+            const Workspace ws(a[10], g_lib.paged_attention_workspace(&cache.kv, type, int32_t(H)), c.dev);
+            check(g_lib.paged_attention(&cache.kv, q.data_ptr(), type, stride, int32_t(H), tab, int32_t(table.size(0)),
+                                        int32_t(table.size(1)), seq, position, int32_t(rows), scale, out.data_ptr(),
+                                        out_stride, ws.p, ws.bytes, c.stream),
+                  "gpt2_op_paged_attention");
+        }
+        if (a[9] != Py_None) return Py_NewRef(a[9]);
+        return THPVariable_Wrap(out);
+    });
+}
+
+// logits, temperature, u, top_k, top_p, min_p, token, prob, dist (all but the first may be None)
+PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("sample", 9, n, [&]() -> PyObject * {
+        const Call c;
+        const at::Tensor &logits = tensor(a[0], "logits");
+        if (logits.dim() != 2) throw Bad{"logits must be [rows][vocab]"};
+        const int64_t rows = logits.size(0), V = logits.size(1);
+        if (row_type(logits.scalar_type()) < 0 || !logits.is_cuda() || logits.get_device() != c.dev)
+            throw Bad{"logits must be float32, float16 or bfloat16 on the current device, not " + describe(logits)};
+        if (V < 1 || V > GPT2_SAMPLE_MAX_VOCAB || rows >= (int64_t(1) << 31)) throw Bad{"logits have a wrong shape"};
+        if (V > 1 && logits.stride(1) != 1) throw Bad{"a row of logits must be contiguous"};
+        const int64_t stride = rows > 1 ? logits.stride(0) : V;
+        if (stride < V) throw Bad{"rows of logits must not overlap"};
+        auto each = [&](int i, const char *name, at::ScalarType t) -> void * {
+            return a[i] == Py_None ? nullptr : whole(tensor(a[i], name), name, t, {rows}, c.dev);
+        };
+        const auto *temperature = static_cast<const float *>(each(1, "temperature", at::kFloat));
+        const auto *top_k = static_cast<const int32_t *>(each(3, "top_k", at::kInt));
+        const auto *top_p = static_cast<const float *>(each(4, "top_p", at::kFloat));
+        const auto *min_p = static_cast<const float *>(each(5, "min_p", at::kFloat));
+        const float *u = a[2] == Py_None ? nullptr : whole<float>(a[2], "u", at::kFloat, {rows, V}, c.dev);
+        if (temperature && !u) throw Bad{"temperature needs u"};
+        at::Tensor made, token, prob;
+        if (a[6] == Py_None || a[7] == Py_None) made = at::empty({2 * rows}, logits.options().dtype(at::kInt));
+        if (a[6] == Py_None) token = part(made, 0, {rows});
+        else each(6, "token", at::kInt), token = tensor(a[6], "token");
+        if (a[7] == Py_None) prob = part(made, rows, {rows}, caffe2::TypeMeta::fromScalarType(at::kFloat));
+        else each(7, "prob", at::kFloat), prob = tensor(a[7], "prob");
+        float *dist = a[8] == Py_None ? nullptr : whole<float>(a[8], "dist", at::kFloat, {rows, V}, c.dev);
+        if (rows > 0)
+            check(g_lib.sample(logits.data_ptr(), row_type(logits.scalar_type()), stride, int32_t(rows), int32_t(V),
+                               temperature, top_k, top_p, min_p, u, static_cast<int32_t *>(token.data_ptr()),
+                               static_cast<float *>(prob.data_ptr()), dist, c.stream),
+                  "gpt2_op_sample");
+        return Py_BuildValue("(NN)", THPVariable_Wrap(token), THPVariable_Wrap(prob));
+    });
+}
+
 // GPT2Error, then the addresses of the library's functions in g_lib's order.
 PyObject *bind(PyObject *, PyObject *args)
 {
     PyObject *cls;
-    unsigned long long f[7];
-    if (!PyArg_ParseTuple(args, "OKKKKKKK", &cls, f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6)) return nullptr;
+    unsigned long long f[11];
+    if (!PyArg_ParseTuple(args, "OKKKKKKKKKKK", &cls, f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7, f + 8, f + 9,
+                          f + 10))
+        return nullptr;
     g_lib.kv_store = reinterpret_cast<decltype(g_lib.kv_store)>(f[0]);
     g_lib.kv_load = reinterpret_cast<decltype(g_lib.kv_load)>(f[1]);
     g_lib.kv_commit = reinterpret_cast<decltype(g_lib.kv_commit)>(f[2]);
@@ -423,13 +558,18 @@ PyObject *bind(PyObject *, PyObject *args)
     g_lib.tree_attention = reinterpret_cast<decltype(g_lib.tree_attention)>(f[4]);
     g_lib.verify_tree_workspace = reinterpret_cast<decltype(g_lib.verify_tree_workspace)>(f[5]);
     g_lib.verify_tree = reinterpret_cast<decltype(g_lib.verify_tree)>(f[6]);
+    g_lib.page_map = reinterpret_cast<decltype(g_lib.page_map)>(f[7]);
+    g_lib.paged_attention_workspace = reinterpret_cast<decltype(g_lib.paged_attention_workspace)>(f[8]);
+    g_lib.paged_attention = reinterpret_cast<decltype(g_lib.paged_attention)>(f[9]);
+    g_lib.sample = reinterpret_cast<decltype(g_lib.sample)>(f[10]);
     Py_XSETREF(g_error, Py_NewRef(cls));
     Py_RETURN_NONE;
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(kv_store),       FAST(kv_load),     FAST(kv_commit),
-                           FAST(tree_attention), FAST(verify_tree), {"bind", bind, METH_VARARGS, nullptr},
+                           FAST(tree_attention), FAST(verify_tree), FAST(page_map),
+                           FAST(paged_attention), FAST(sample),     {"bind", bind, METH_VARARGS, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

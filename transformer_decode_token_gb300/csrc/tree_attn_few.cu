@@ -29,49 +29,9 @@ namespace tree {
 namespace {
 
 template <int KIND, int D, int R>
-struct Few {
-    static constexpr int kES = KIND == GPT2_F32 ? 4 : KIND == GPT2_INT8 || KIND == GPT2_E4M3 ? 1 : 2;
-    static constexpr bool kScaled = kES == 1;
-    static constexpr int kRowB = D * kES;
-    static constexpr int kLPR = kRowB / 16;              // lanes per cache row
-    static constexpr int kRPL = 32 / kLPR;               // cache rows per access of a warp
-    static constexpr int kE = 16 / kES;                  // elements of a lane
-    static constexpr int kLoads = kRPL >= 4 ? 32 / kRPL : 8;   // accesses per tile: 32 rows, or 4 KB
-    static constexpr int KS = kLoads * kRPL;
-    static constexpr int kSplit = kLPR < kLoads ? kLPR : kLoads;   // lanes that a row's scores are spread over
-    static constexpr int kNV = kLoads / kSplit;          // scores of a lane
-    static constexpr int kSame = kLPR / kSplit;          // lanes with the same scores
-};
-
-// The 16 bytes of a lane as fp32 (codes without their scale), in pairs.
-template <int KIND, int E>
-__device__ __forceinline__ void widen(const uint32_t *r, float2 (&x)[E / 2])
-{
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-        float2 &y = x[i / 2];
-        if constexpr (KIND == GPT2_F32) {
-            y = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-        } else if constexpr (KIND == GPT2_BF16) {
-            y = make_float2(__uint_as_float(r[i / 2] << 16), __uint_as_float(r[i / 2] & 0xffff0000u));
-        } else if constexpr (KIND == GPT2_INT8) {
-            // 2^23 + u in fp32, u = code + 128
-            const uint32_t u = r[i / 4] ^ 0x80808080u;
-            y = add2(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540u | (i % 4))),
-                                 __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540u | (i % 4 + 1)))),
-                     make_float2(-8388736.f, -8388736.f));
-        } else {
-            uint32_t h = r[i / 2];
-            if constexpr (KIND == GPT2_E4M3) h = codes_to_half2<true>(r[i / 4], i % 4 == 0 ? 0x4140u : 0x4342u);
-            y = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        }
-    }
-}
-
-template <int KIND, int D, int R>
 __global__ void __launch_bounds__(kNW * 32, R == 1 ? 4 : R == 2 ? 3 : 2) k_tree_few(const __grid_constant__ TreeArgs a)
 {
-    using F = Few<KIND, D, R>;
+    using F = Few<KIND, D>;
     constexpr int E = F::kE, I = F::kLoads, NV = F::kNV, KS = F::KS, LPR = F::kLPR;
     __shared__ __align__(16) float so[kNW * R * D];
     __shared__ float sm_m[kNW][R], sm_l[kNW][R];
