@@ -8,6 +8,11 @@
 // cut, each warp writes its part (maximum, sum of the weights, weighted sum, in
 // fp32) to the workspace, and a second kernel joins the parts in the order of the
 // list, so every call gives the same bits.
+//
+// What bounds such kernels is how much of the cache is on its way to an SM at a
+// time, so every warp has a ring of tiles in shared memory that asynchronous
+// copies fill: each thread copies the pieces that it will read itself, in the order
+// of its registers, so that no barrier is needed and no access has a bank conflict.
 #pragma once
 
 #include "tree_attn.cuh"
@@ -24,6 +29,7 @@ struct PagedArgs {
     float2 *ml;                     // [warps][2][R]
     float *sums;                    // [warps][2][R][D]
     int32_t n_seqs, n_rows, max_blocks, group, row_tiles, q_dtype, warps;
+    int32_t per_block;              // 65536 / block size, rounded up (blocks of fewer than 32 rows)
     float scale_log2;               // scale * log2(e)
 };
 
@@ -80,12 +86,21 @@ struct Shares {
     }
 };
 
+// x / block size for x < block size + 32: a comparison, or, for blocks of fewer than
+// 32 rows, a product (65536 / size rounded up is near enough for x < 64).
+__device__ __forceinline__ uint32_t blocks_in(const PagedArgs &a, uint32_t x)
+{
+    const uint32_t bs = uint32_t(a.kv.n_positions);
+    return bs >= 32 ? (x >= bs ? 1u : 0u) : x * uint32_t(a.per_block) >> 16;
+}
+
 // A place in the list: a tile of a unit.
 template <int KS>
 struct Place {
-    const int32_t *table;
+    const int32_t *table;           // of the row's sequence
     int row, unit;                  // unit of the row: cache head * row_tiles + tile of query heads
     uint32_t tile, tiles, len;
+    uint32_t block, offset;         // where the tile's first key lies: entry of the table, row of the block
 
     __device__ __forceinline__ void enter(const PagedArgs &a, int i)
     {
@@ -96,20 +111,94 @@ struct Place {
     }
     __device__ __forceinline__ void next(const PagedArgs &a)
     {
-        if (++tile < tiles) return;
-        tile = 0;
+        if (++tile < tiles) {
+            const uint32_t k = blocks_in(a, offset + KS);
+            block += k;
+            offset += KS - k * uint32_t(a.kv.n_positions);
+            return;
+        }
+        tile = block = offset = 0;
         if (++unit < a.kv.n_head * a.row_tiles) return;
         unit = 0;
         do enter(a, row + 1);
-        while (len == 0);           // (there is a next tile)
-    }
-    // the cache row of the tile's row `lane`
-    __device__ __forceinline__ uint32_t at(const PagedArgs &a, int lane) const
-    {
-        const uint32_t j = tile * KS + lane;
-        return lane < KS && j < len ? cache_row(a, table, j, unit / a.row_tiles) : kNone;
+        while (tiles == 0);         // (there is a next tile)
     }
 };
+
+// The cache rows of a tile, one per lane.  32 entries of the table, from the tile's
+// first block on, are held one per lane until a tile passes them (or another
+// row begins), so that most tiles need no load.
+struct Lookup {
+    int row = -1;
+    uint32_t from = 0;
+    int32_t entry = -1;
+    template <int KS>
+    __device__ __forceinline__ uint32_t rows(const PagedArgs &a, const Place<KS> &at, int lane)
+    {
+        const uint32_t bs = uint32_t(a.kv.n_positions), x = at.offset + lane, k = blocks_in(a, x);
+        const uint32_t most = blocks_in(a, at.offset + KS - 1);
+        if (row != at.row || at.block < from || at.block + most >= from + 32) {
+            row = at.row;
+            from = at.block;
+            // (the last block that the row sees: its length is above the tile's first key)
+            const uint32_t left = at.len - at.tile * KS + at.offset;   // rows from the block's first on
+            entry = uint32_t(lane) * bs < left ? at.table[from + lane] : -1;
+        }
+        const int32_t e = __shfl_sync(0xffffffffu, entry, (at.block - from + k) & 31);
+        const bool yes = lane < KS && at.tile * KS + lane < at.len && e >= 0 && e < a.kv.n_slots;
+        return yes ? (uint32_t(e) * uint32_t(a.kv.n_head) + uint32_t(at.unit / a.row_tiles)) * bs + (x - k * bs) : kNone;
+    }
+};
+
+// B bytes from global to shared memory, asynchronously (zeros where !there).  Through
+// L1: past it (.cg) the same kernel fetched every sector from L2 twice (64 requests of
+// 2,000 to 4,000 fp32 rows, 12 heads of 64: 215 us instead of 178).
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool there)
+{
+    const int n = there ? B : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()       // until at most the last N groups are on their way
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// B bytes of shared memory into registers.
+template <int B>
+__device__ __forceinline__ void fetch(uint32_t *r, const uint8_t *p)
+{
+    if constexpr (B == 16) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    } else if constexpr (B == 8) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r[0] = v.x, r[1] = v.y;
+    } else {
+        r[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+// Stages of a warp's ring of tiles of `bytes` (keys and values).
+constexpr int stages_for(int bytes, int ctas)
+{
+    const int n = (ctas == 2 ? 24 : 16) * 1024 / bytes;
+    return n < 2 ? 2 : n > 6 ? 6 : n;
+}
+
+// Lets a kernel use so much dynamic shared memory (once per device and kernel).
+template <auto FN>
+cudaError_t allow_smem(size_t bytes)
+{
+    static uint64_t done = 0;       // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (__atomic_load_n(&done, __ATOMIC_RELAXED) >> (dev & 63) & 1)) return e;
+    e = cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e == cudaSuccess) __atomic_fetch_or(&done, 1ull << (dev & 63), __ATOMIC_RELAXED);
+    return e;
+}
 
 // This warp's share of the list, and the place where it begins.  Called by all
 // threads of the CTA; also writes the zeros of rows that see nothing.
@@ -174,6 +263,8 @@ __device__ __forceinline__ bool find_share(const PagedArgs &a, uint32_t w, Share
     const uint32_t off = x0 - base[warp] * units;
     at.unit = int(off / at.tiles);
     at.tile = off % at.tiles;
+    at.block = at.tile * KS / uint32_t(a.kv.n_positions);
+    at.offset = at.tile * KS - at.block * uint32_t(a.kv.n_positions);
     return true;
 }
 
@@ -204,6 +295,24 @@ __device__ __forceinline__ void put4(const PagedArgs &a, size_t at, float x, flo
             v = make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&r));
         }
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = v;
+    }
+}
+
+// N elements of a result, v times f.
+template <int N>
+__device__ __forceinline__ void put(const PagedArgs &a, size_t at, const float *v, float f)
+{
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) put4(a, at + i, v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float x = v[i] * f;
+            if (a.q_dtype == GPT2_F32) static_cast<float *>(a.out)[at + i] = x;
+            else if (a.q_dtype == GPT2_F16) static_cast<__half *>(a.out)[at + i] = __float2half_rn(x);
+            else static_cast<__nv_bfloat16 *>(a.out)[at + i] = __float2bfloat16_rn(x);
+        }
     }
 }
 

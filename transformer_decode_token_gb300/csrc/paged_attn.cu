@@ -94,22 +94,22 @@ cudaError_t join_dims(const PagedArgs &a, cudaStream_t s)
 }
 
 // Query heads of a tile: 1, 2 or 4 on the CUDA cores, 8 on the matrix instructions.
-int tile_heads(const gpt2_kv &kv, int q_dtype, int group)
+int tile_heads(int q_dtype, int group)
 {
     if (group <= 2) return group;
     return q_dtype == GPT2_F32 ? 4 : 8;
 }
 
 // CTAs that an SM holds of the kernel for these tiles.
-int resident(const gpt2_kv &kv, int r)
+int resident(int r)
 {
-    return r == 1 ? 4 : r == 2 ? 3 : r == 4 ? 2 : kv.head_dim == 128 ? 2 : 3;
+    return r == 4 ? 2 : 3;
 }
 
 // Cache rows of a tile, as the kernels have them.
-int tile_rows(const gpt2_kv &kv, int r)
+int tile_rows(const gpt2_kv &kv)
 {
-    const int bytes = kv.head_dim * elem_size(kv.dtype), n = r < 8 && bytes >= 256 ? 8 * (512 / bytes) : 4096 / bytes;
+    const int n = 4096 / (kv.head_dim * elem_size(kv.dtype));
     return n > 32 ? 32 : n;
 }
 
@@ -118,7 +118,7 @@ struct Layout {
     size_t heads, ml, total;          // bytes: of the heads, of (m, l), of everything
     Layout(const gpt2_kv &kv, int r, int sms)
     {
-        warps = sms * resident(kv, r) * tree::kNW;
+        warps = sms * resident(r) * tree::kNW;
         heads = size_t(warps) * sizeof(int4);
         ml = (size_t(warps) * 2 * r * sizeof(float2) + 15) / 16 * 16;
         total = heads + ml + size_t(warps) * 2 * r * kv.head_dim * sizeof(float);
@@ -161,7 +161,7 @@ extern "C" size_t gpt2_op_paged_attention_workspace(const gpt2_kv *kv, int32_t q
     if (!paged::shape_ok(kv, q_dtype, n_head)) return 0;
     int rc;
     const int sms = spec_sms(&rc);
-    return sms ? paged::Layout(*kv, paged::tile_heads(*kv, q_dtype, n_head / kv->n_head), sms).total : 0;
+    return sms ? paged::Layout(*kv, paged::tile_heads(q_dtype, n_head / kv->n_head), sms).total : 0;
 }
 
 extern "C" int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, int64_t q_stride, int32_t n_head,
@@ -180,9 +180,9 @@ extern "C" int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t
     PagedArgs a{};
     a.kv = *kv;
     a.group = n_head / kv->n_head;
-    const int r = paged::tile_heads(*kv, q_dtype, a.group);
+    const int r = paged::tile_heads(q_dtype, a.group);
     a.row_tiles = (a.group + r - 1) / r;
-    const int ks = paged::tile_rows(*kv, r);
+    const int ks = paged::tile_rows(*kv);
     const double tiles = double(n_rows) * kv->n_head * a.row_tiles * double((longest + ks - 1) / ks);
     if (tiles >= 4.0e9) return GPT2_ERR_INVALID_ARG;
     if (n_rows == 0) return GPT2_OK;
@@ -207,6 +207,7 @@ extern "C" int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t
     a.n_rows = n_rows;
     a.max_blocks = max_blocks;
     a.q_dtype = q_dtype;
+    a.per_block = (65536 + kv->n_positions - 1) / kv->n_positions;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int ctas = at.warps / tree::kNW;

@@ -1,10 +1,16 @@
 // Attention over a paged cache on the CUDA cores in fp32, for one to four query
-// heads on a cache head: the layout of tree_attn_few.cu's kernel (a cache row in
-// neighbouring lanes, 16 bytes in each, scores summed over them by halving), over
-// the list of paged.cuh.  Lane l looks up the place of the tile's row l in the
-// block table, so that pages may have any size and end anywhere in a tile; the
-// next tile's places are looked up, and its keys are on their way, while this
-// tile's weights are formed.
+// heads on a cache head, over the list and the rings of paged.cuh.
+//
+// A row of the cache lies in a few neighbouring lanes (four for one query head):
+// the more of a row a lane holds, the fewer steps across lanes a tile takes, and
+// those steps, one waiting for the other, are what a warp's time goes to.  A lane
+// multiplies its pieces of T keys with its pieces of q; the products are summed over
+// the row's lanes by halving, after which every lane holds keys of its own, and the
+// weighted sum takes the weights from the lanes that hold them.  The weights are
+// taken relative to a maximum that is only raised when a score passes it by more
+// than kSlack (a vote instead of a reduction per tile; fp32 holds 2^kSlack as well as
+// 1).  Lane l looks up the place of the tile's row l in the block table, so that pages
+// may have any size and end anywhere in a tile.
 #pragma once
 
 #include "paged.cuh"
@@ -13,16 +19,42 @@ namespace gpt2 {
 namespace paged {
 namespace {
 
+constexpr float kSlack = 8.f;
+
+// CTAs of an SM.
+constexpr int few_ctas(int r) { return r <= 2 ? 3 : 2; }
+
 template <int KIND, int D, int R>
-__global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged_few(const __grid_constant__ PagedArgs a)
+struct Few {
+    static constexpr int kES = KIND == GPT2_F32 ? 4 : KIND == GPT2_INT8 || KIND == GPT2_E4M3 ? 1 : 2;
+    static constexpr bool kScaled = kES == 1;
+    static constexpr int kRowB = D * kES, kPieces = kRowB / 16;
+    static constexpr int kWant = R == 1 || D <= 64 ? 4 : 8;
+    static constexpr int LPR = kPieces < kWant ? kPieces : kWant;    // lanes of a cache row
+    static constexpr int P = kPieces / LPR;                          // 16-byte pieces of a lane: c, c + LPR, ..
+    static constexpr int EP = 16 / kES, E = P * EP;                  // elements of a piece, of a lane
+    static constexpr int RPL = 32 / LPR;                             // rows that a warp holds side by side
+    static constexpr int KS = 4096 / kRowB > 32 ? 32 : 4096 / kRowB; // rows of a tile: 32, or 4 KB
+    static constexpr int T = KS / RPL < 1 ? 1 : KS / RPL;            // of which a lane has this many
+    static constexpr int kSplit = LPR < T ? LPR : T;                 // lanes that a row's T scores are spread over
+    static constexpr int NV = T / kSplit, kSame = LPR / kSplit;      // scores of a lane; lanes with the same ones
+    static constexpr int kBytes = 2 * T * P * 512;                   // keys and values of a tile
+    static constexpr int kStage = kBytes + (kScaled ? 256 : 0);      // and their scales
+    static constexpr int S = stages_for(kBytes, few_ctas(R));
+    static constexpr size_t kSmem = size_t(kNW) * S * kStage;
+};
+
+template <int KIND, int D, int R>
+__global__ void __launch_bounds__(kThreads, few_ctas(R)) k_paged_few(const __grid_constant__ PagedArgs a)
 {
-    using F = Few<KIND, D>;
-    constexpr int E = F::kE, I = F::kLoads, NV = F::kNV, KS = F::KS, LPR = F::kLPR, RPL = F::kRPL;
+    using F = Few<KIND, D, R>;
+    constexpr int E = F::E, EP = F::EP, P = F::P, T = F::T, NV = F::NV, KS = F::KS, LPR = F::LPR, RPL = F::RPL, S = F::S;
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
+    static_assert(RPL * T == KS && E >= RPL, "every lane has rows, and dimensions of the result");
+    extern __shared__ __align__(16) uint8_t dyn[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane % LPR, grp = lane / LPR;
     const uint32_t w = warp * gridDim.x + blockIdx.x;    // (so that fewer shares than warps spread over the SMs)
-    pdl_wait();
-    pdl_launch_dependents();
+    pdl_wait();                                          // (the joining kernel is placed when this one's CTAs leave)
     Shares sh(1, 1);
     uint32_t x0 = 0, x1 = 0;
     Place<KS> at;
@@ -30,18 +62,43 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged
         if (lane == 0) a.heads[w] = make_int4(0, 0, 0, 0);
         return;
     }
+    uint8_t *ring = dyn + warp * (S * F::kStage) + lane * 16;
     const uint8_t *kbase = static_cast<const uint8_t *>(a.kv.k) + c * 16;
     const uint8_t *vbase = static_cast<const uint8_t *>(a.kv.v) + c * 16;
-    // access i of a tile holds cache rows i * RPL + grp; after the halving this
-    // lane holds the scores of accesses i0 .. i0 + NV - 1
-    const int i0 = c / F::kSame * NV;
-    uint32_t kr[I][4], vr[I][4];
-    auto load = [&](uint32_t (&x)[I][4], const uint8_t *base, uint32_t rows) {
+    // rows t * RPL + grp of a tile are this lane's; after the halving it holds the
+    // scores of t0 .. t0 + NV - 1
+    const int t0 = c / F::kSame * NV;
+    uint32_t there[S];                                   // which of their rows the ring's tiles have, oldest first
+    Place<KS> far = at;                                  // the tile whose copies begin next
+    Lookup look;
+    uint32_t to_come = x1 - x0;                          // tiles whose copies have not begun
+    auto copy = [&](uint32_t stage) {
+        uint32_t yes = 0;
+        if (to_come) {
+            const uint32_t rows = look.rows(a, far, lane), base = smem_addr(ring) + stage * F::kStage;
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            const uint32_t r = __shfl_sync(0xffffffffu, rows, i * RPL + grp);
-            load_piece<16>(x[i], base + size_t(r) * F::kRowB, r != kNone);
+            for (int t = 0; t < T; ++t) {
+                const uint32_t r = __shfl_sync(0xffffffffu, rows, t * RPL + grp);
+                const bool ok = r != kNone;
+                const size_t off = ok ? size_t(r) * F::kRowB : 0;
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    copy_async<16>(base + (t * P + p) * 512, kbase + off + p * LPR * 16, ok);
+                    copy_async<16>(base + ((T + t) * P + p) * 512, vbase + off + p * LPR * 16, ok);
+                }
+            }
+            if constexpr (F::kScaled) {
+                const bool ok = rows != kNone;
+                copy_async<4>(base - lane * 12 + F::kBytes, a.kv.k_scale + (ok ? rows : 0), ok);
+                copy_async<4>(base - lane * 12 + F::kBytes + 128, a.kv.v_scale + (ok ? rows : 0), ok);
+            }
+            yes = __ballot_sync(0xffffffffu, rows != kNone) & kAll;
+            if (--to_come) far.next(a);
         }
+        copies_commit();
+#pragma unroll
+        for (int i = 0; i + 1 < S; ++i) there[i] = there[i + 1];
+        there[S - 1] = yes;
     };
     float2 q[R][E / 2], o[R][E / 2];
     float m[R], l[R];
@@ -50,12 +107,12 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged
     auto begin_unit = [&]() {
         heads = heads_of<R>(a, at.unit);
         from = at.tile;
-        const size_t q0 = row_at<D, R>(a, at.row, at.unit, a.q_stride) + c * E;
+        const size_t q0 = row_at<D, R>(a, at.row, at.unit, a.q_stride) + c * EP;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
-                const float4 v = load_row4(a.q, q0 + size_t(r < heads ? r : 0) * D + e, a.q_dtype);
+                const float4 v = load_row4(a.q, q0 + size_t(r < heads ? r : 0) * D + e / EP * (LPR * EP) + e % EP, a.q_dtype);
                 q[r][e / 2] = make_float2(v.x * a.scale_log2, v.y * a.scale_log2);
                 q[r][e / 2 + 1] = make_float2(v.z * a.scale_log2, v.w * a.scale_log2);
             }
@@ -65,42 +122,44 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged
             l[r] = 0.f;
         }
     };
-    uint32_t rows = at.at(a, lane);
-    load(kr, kbase, rows);
+#pragma unroll
+    for (int i = 0; i < S; ++i) there[i] = 0;
+    for (int i = 0; i < S - 1; ++i) copy(i);
     begin_unit();
     int4 head = make_int4(0, 0, 0, 0);
 
+    uint32_t stage = 0;
     for (uint32_t x = x0; x < x1; ++x) {
-        load(vr, vbase, rows);
-        float ks = 0.f, vs = 0.f;                        // of the tile's row `lane`
-        if constexpr (F::kScaled) {
-            ks = load_scale(a.kv.k_scale + rows, rows != kNone);
-            vs = load_scale(a.kv.v_scale + rows, rows != kNone);
-        }
+        copies_wait<S - 2>();
+        copy(stage == 0 ? S - 1 : stage - 1);
+        const uint8_t *tile = ring + stage * F::kStage;
+        const uint32_t got = there[0];
+        stage = stage == S - 1 ? 0 : stage + 1;
         const bool more = x + 1 < x1;
-        Place<KS> then = at;
-        uint32_t rows_then = kNone;
-        if (more) {
-            then.next(a);
-            rows_then = then.at(a, lane);
-        }
-        float s[R][I];
+        float s[R][T];
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            float2 k[E / 2];
-            widen<KIND, E>(kr[i], k);
+        for (int t = 0; t < T; ++t) {
+            float2 y[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float2 y = make_float2(k[0].x * q[r][0].x, k[0].y * q[r][0].y);
+            for (int p = 0; p < P; ++p) {
+                const uint4 raw = *reinterpret_cast<const uint4 *>(tile + (t * P + p) * 512);
+                const uint32_t word[4] = {raw.x, raw.y, raw.z, raw.w};
+                float2 k[EP / 2];
+                widen<KIND, EP>(word, k);
 #pragma unroll
-                for (int e = 1; e < E / 2; ++e) y = fma2(k[e], q[r][e], y);
-                s[r][i] = y.x + y.y;
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < EP / 2; ++e) {
+                        const float2 qe = q[r][p * (EP / 2) + e];
+                        y[r] = p == 0 && e == 0 ? make_float2(k[e].x * qe.x, k[e].y * qe.y) : fma2(k[e], qe, y[r]);
+                    }
             }
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r][t] = y[r].x + y[r].y;
         }
-        if (more) load(kr, kbase, rows_then);
         // sums over a cache row's lanes (a step of every query row before the next
         // step: the shuffles' latencies overlap)
-        int n = I;
+        int n = T;
 #pragma unroll
         for (int d = LPR / 2; d > 0; d /= 2) {
             const bool halve = n > NV, up = c & d;
@@ -108,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int i = 0; i < I; ++i)
+                for (int i = 0; i < T; ++i)
                     if (i < n) {
                         if (halve) {
                             const float mine = up ? s[r][i + n] : s[r][i], other = up ? s[r][i] : s[r][i + n];
@@ -118,38 +177,42 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged
                         }
                     }
         }
-        const uint32_t there = __ballot_sync(0xffffffffu, rows != kNone) & kAll;
         float kf[NV], vf[NV];
         if constexpr (F::kScaled) {
+            const float ks = *reinterpret_cast<const float *>(tile - lane * 12 + F::kBytes);   // of the tile's row `lane`
+            const float vs = *reinterpret_cast<const float *>(tile - lane * 12 + F::kBytes + 128);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                kf[k] = __shfl_sync(0xffffffffu, ks, (i0 + k) * RPL + grp);
-                vf[k] = __shfl_sync(0xffffffffu, vs, (i0 + k) * RPL + grp);
+                kf[k] = __shfl_sync(0xffffffffu, ks, (t0 + k) * RPL + grp);
+                vf[k] = __shfl_sync(0xffffffffu, vs, (t0 + k) * RPL + grp);
             }
         }
-        float top[R];
+        bool above = false;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            top[r] = -INFINITY;
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 if constexpr (F::kScaled) s[r][k] *= kf[k];
-                if (there != kAll && !(there >> ((i0 + k) * RPL + grp) & 1)) s[r][k] = -INFINITY;
-                top[r] = fmaxf(top[r], s[r][k]);
+                if (got != kAll && !(got >> ((t0 + k) * RPL + grp) & 1)) s[r][k] = -INFINITY;
+                above = above || s[r][k] > m[r] + kSlack;
+            }
+        if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float top = m[r];
+#pragma unroll
+                for (int k = 0; k < NV; ++k) top = fmaxf(top, s[r][k]);
+                top = warp_max(top);
+                const float keep = exp2_approx(m[r] - (top == -INFINITY ? 0.f : top));
+                m[r] = top;
+                l[r] *= keep;
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) o[r][e] = make_float2(o[r][e].x * keep, o[r][e].y * keep);
             }
         }
 #pragma unroll
-        for (int d = 16; d >= F::kSame; d /= 2)
-#pragma unroll
-            for (int r = 0; r < R; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], d));
-#pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float mn = fmaxf(m[r], top[r]), safe = mn == -INFINITY ? 0.f : mn;
-            const float keep = exp2_approx(m[r] - safe);
-            m[r] = mn;
-            l[r] *= keep;
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) o[r][e] = make_float2(o[r][e].x * keep, o[r][e].y * keep);
+            const float safe = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 s[r][k] = exp2_approx(s[r][k] - safe);
@@ -159,15 +222,23 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged
         }
         // (a row that is not there is not read: its zeros meet weights of zero)
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            const int src = grp * LPR + i / NV * F::kSame;
-            float2 v[E / 2];
-            widen<KIND, E>(vr[i], v);
+        for (int t = 0; t < T; ++t) {
+            float w8[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float p = __shfl_sync(0xffffffffu, s[r][i % NV], src);
+            for (int r = 0; r < R; ++r) w8[r] = __shfl_sync(0xffffffffu, s[r][t % NV], grp * LPR + t / NV * F::kSame);
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e) o[r][e] = fma2(make_float2(p, p), v[e], o[r][e]);
+            for (int p = 0; p < P; ++p) {
+                const uint4 raw = *reinterpret_cast<const uint4 *>(tile + ((T + t) * P + p) * 512);
+                const uint32_t word[4] = {raw.x, raw.y, raw.z, raw.w};
+                float2 v[EP / 2];
+                widen<KIND, EP>(word, v);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < EP / 2; ++e) {
+                        float2 &y = o[r][p * (EP / 2) + e];
+                        y = fma2(make_float2(w8[r], w8[r]), v[e], y);
+                    }
             }
         }
 
@@ -179,49 +250,62 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 4 : R == 2 ? 3 : 2) k_paged
             for (int r = 0; r < R; ++r) {
 #pragma unroll
                 for (int d = 16; d >= F::kSame; d /= 2) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
+                // the rows side by side are added by halving: each lane ends with N of its E elements
+                constexpr int N = E / RPL;
+                float v[E];
 #pragma unroll
-                for (int d = 16; d >= LPR; d /= 2)
+                for (int e = 0; e < E / 2; ++e) v[2 * e] = o[r][e].x, v[2 * e + 1] = o[r][e].y;
+                int first = 0, k = E;
 #pragma unroll
-                    for (int e = 0; e < E / 2; ++e) {
-                        o[r][e].x += __shfl_xor_sync(0xffffffffu, o[r][e].x, d);
-                        o[r][e].y += __shfl_xor_sync(0xffffffffu, o[r][e].y, d);
+                for (int d = 16; d >= LPR; d /= 2) {
+                    k /= 2;
+                    const bool up = lane & d;
+                    if (up) first += k;
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i)
+                        if (i < k) {
+                            const float mine = up ? v[i + k] : v[i], other = up ? v[i] : v[i + k];
+                            v[i] = mine + __shfl_xor_sync(0xffffffffu, other, d);
+                        }
+                }
+                if (r < heads) {
+                    const int dim = (c + first / EP * LPR) * EP + first % EP;
+                    if (whole) {
+                        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+                        put<N>(a, row_at<D, R>(a, at.row, at.unit, a.out_stride) + size_t(r) * D + dim, v, inv);
+                    } else {
+                        float *to = a.sums + (size_t(part) * R + r) * D + dim;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) to[i] = v[i];
+                        if (lane == 0) a.ml[size_t(part) * R + r] = make_float2(m[r], l[r]);
                     }
-                if (r >= heads || lane >= LPR) continue;
-                if (whole) {
-                    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-                    const size_t to = row_at<D, R>(a, at.row, at.unit, a.out_stride) + size_t(r) * D + c * E;
-#pragma unroll
-                    for (int e = 0; e < E; e += 4)
-                        put4(a, to + e, o[r][e / 2].x * inv, o[r][e / 2].y * inv, o[r][e / 2 + 1].x * inv,
-                             o[r][e / 2 + 1].y * inv);
-                } else {
-                    float *to = a.sums + (size_t(part) * R + r) * D + c * E;
-#pragma unroll
-                    for (int e = 0; e < E; e += 4)
-                        *reinterpret_cast<float4 *>(to + e) =
-                            make_float4(o[r][e / 2].x, o[r][e / 2].y, o[r][e / 2 + 1].x, o[r][e / 2 + 1].y);
-                    if (lane == 0) a.ml[size_t(part) * R + r] = make_float2(m[r], l[r]);
                 }
             }
             if (!whole && from == 0)
                 head = make_int4(at.row, at.unit, int(sh.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
-            if (more) {
-                at = then;
-                begin_unit();
-            }
         }
-        at = then;
-        rows = rows_then;
+        if (more) {
+            at.next(a);
+            if (ends) begin_unit();
+        }
     }
     if (lane == 0) a.heads[w] = head;
+}
+
+template <int KIND, int D, int R>
+cudaError_t few_launch(const PagedArgs &a, int ctas, cudaStream_t s)
+{
+    const size_t smem = Few<KIND, D, R>::kSmem;
+    const cudaError_t e = allow_smem<k_paged_few<KIND, D, R>>(smem);
+    return e != cudaSuccess ? e : spec_launch(k_paged_few<KIND, D, R>, dim3(ctas), kThreads, smem, 1, s, a);
 }
 
 template <int KIND, int D>
 cudaError_t few_rows(const PagedArgs &a, int r, int ctas, cudaStream_t s)
 {
-    if (r == 1) return spec_launch(k_paged_few<KIND, D, 1>, dim3(ctas), kThreads, 0, 1, s, a);
-    if (r == 2) return spec_launch(k_paged_few<KIND, D, 2>, dim3(ctas), kThreads, 0, 1, s, a);
-    return spec_launch(k_paged_few<KIND, D, 4>, dim3(ctas), kThreads, 0, 1, s, a);
+    if (r == 1) return few_launch<KIND, D, 1>(a, ctas, s);
+    if (r == 2) return few_launch<KIND, D, 2>(a, ctas, s);
+    return few_launch<KIND, D, 4>(a, ctas, s);
 }
 
 template <int KIND>

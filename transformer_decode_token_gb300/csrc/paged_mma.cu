@@ -5,8 +5,8 @@
 // upper half takes the second part of what the lower half is the first part of
 // (the weights p = hi + lo, and fp16 queries over 8-bit caches, whose codes are
 // exact in bf16), so that both parts cost one instruction and meet in one thread,
-// which adds the two halves of the accumulators.  Cache rows go from global memory
-// to the operand registers as in tree_attn.cuh: keys by 16-byte pieces c, c + 4, ..,
+// which adds the two halves of the accumulators.  Cache rows reach the operand
+// registers in the order of tree_attn.cuh: keys by 16-byte pieces c, c + 4, ..,
 // values by pieces g, g + 8, .. of the rows whose weights the thread holds.
 #include "paged.cuh"
 
@@ -46,8 +46,19 @@ struct Shape {
     static constexpr int kT8 = KS / 8, kSteps = D / 16, kNT = D / 8;
 };
 
+constexpr int kMmaCtas = 3;                              // CTAs of an SM
+
+template <int KIND, int D>
+struct MmaRing {
+    using S = Shape<KIND, D>;
+    static constexpr int kKeys = S::KS * S::kRowB;
+    static constexpr int kStage = 2 * kKeys + (S::kScaled ? 256 : 0);
+    static constexpr int kStages = stages_for(2 * kKeys, kMmaCtas);
+    static constexpr size_t kSmem = size_t(kNW) * kStages * kStage;
+};
+
 template <int KIND, int D, bool QF16>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const __grid_constant__ PagedArgs a)
+__global__ void __launch_bounds__(kThreads, kMmaCtas) k_paged_mma(const __grid_constant__ PagedArgs a)
 {
     using S = Shape<KIND, D>;
     constexpr int R = 8, KS = S::KS, T8 = S::kT8;
@@ -55,8 +66,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const uint32_t w = warp * gridDim.x + blockIdx.x;
-    pdl_wait();
-    pdl_launch_dependents();
+    pdl_wait();                                          // (the joining kernel is placed when this one's CTAs leave)
     Shares sh(1, 1);
     uint32_t x0 = 0, x1 = 0;
     Place<KS> at;
@@ -64,29 +74,52 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
         if (lane == 0) a.heads[w] = make_int4(0, 0, 0, 0);
         return;
     }
+    using G = MmaRing<KIND, D>;
+    constexpr int N = G::kStages;                      // stages
+    extern __shared__ __align__(16) uint8_t dyn[];
+    uint8_t *ring = dyn + warp * (N * G::kStage);
     const uint8_t *kbase = static_cast<const uint8_t *>(a.kv.k) + c * S::kKLd;
     const uint8_t *vbase = static_cast<const uint8_t *>(a.kv.v) + g * S::kVLd;
-    uint32_t kr[T8][S::kRowB / 16], vr[T8][2][S::kRowB / 32];
-    auto load_keys = [&](uint32_t rows) {
+    uint32_t there[N];                                   // which of their rows the ring's tiles have, oldest first
+    Place<KS> far = at;                                  // the tile whose copies begin next
+    Lookup look;
+    uint32_t to_come = x1 - x0;                          // tiles whose copies have not begun
+    auto copy = [&](uint32_t stage) {
+        uint32_t yes = 0;
+        if (to_come) {
+            const uint32_t rows = look.rows(a, far, lane), base = smem_addr(ring) + stage * G::kStage;
 #pragma unroll
-        for (int t = 0; t < T8; ++t) {
-            const uint32_t r = __shfl_sync(0xffffffffu, rows, t * 8 + g);
+            for (int t = 0; t < T8; ++t) {
+                const uint32_t r = __shfl_sync(0xffffffffu, rows, t * 8 + g);
+                const size_t off = r != kNone ? size_t(r) * S::kRowB : 0;
 #pragma unroll
-            for (int p = 0; p < S::kNK; ++p)
-                load_piece<S::kKLd>(kr[t] + p * S::kKLd / 4, kbase + size_t(r) * S::kRowB + p * 4 * S::kKLd, r != kNone);
-        }
-    };
-    auto load_values = [&](uint32_t rows) {
-#pragma unroll
-        for (int t = 0; t < T8; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t r = __shfl_sync(0xffffffffu, rows, t * 8 + 2 * c + i);
-#pragma unroll
-                for (int p = 0; p < S::kNV; ++p)
-                    load_piece<S::kVLd>(vr[t][i] + p * S::kVLd / 4, vbase + size_t(r) * S::kRowB + p * 8 * S::kVLd,
+                for (int p = 0; p < S::kNK; ++p)
+                    copy_async<S::kKLd>(base + ((t * S::kNK + p) * 32 + lane) * S::kKLd, kbase + off + p * 4 * S::kKLd,
                                         r != kNone);
             }
+#pragma unroll
+            for (int t = 0; t < T8; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t r = __shfl_sync(0xffffffffu, rows, t * 8 + 2 * c + i);
+                    const size_t off = r != kNone ? size_t(r) * S::kRowB : 0;
+#pragma unroll
+                    for (int p = 0; p < S::kNV; ++p)
+                        copy_async<S::kVLd>(base + G::kKeys + (((t * 2 + i) * S::kNV + p) * 32 + lane) * S::kVLd,
+                                            vbase + off + p * 8 * S::kVLd, r != kNone);
+                }
+            if constexpr (S::kScaled) {
+                const bool ok = rows != kNone;
+                copy_async<4>(base + 2 * G::kKeys + lane * 4, a.kv.k_scale + (ok ? rows : 0), ok);
+                copy_async<4>(base + 2 * G::kKeys + 128 + lane * 4, a.kv.v_scale + (ok ? rows : 0), ok);
+            }
+            yes = __ballot_sync(0xffffffffu, rows != kNone) & kAll;
+            if (--to_come) far.next(a);
+        }
+        copies_commit();
+#pragma unroll
+        for (int i = 0; i + 1 < N; ++i) there[i] = there[i + 1];
+        there[N - 1] = yes;
     };
     uint32_t qa[S::kSteps][kTwo ? 4 : 2];
     float o[S::kNT][4], m = 0.f, l = 0.f;                // m, l: of query head g
@@ -120,46 +153,48 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
         m = -INFINITY;
         l = 0.f;
     };
-    uint32_t rows = at.at(a, lane);
-    load_keys(rows);
+#pragma unroll
+    for (int i = 0; i < N; ++i) there[i] = 0;
+    for (int i = 0; i < N - 1; ++i) copy(i);
     begin_unit();
     int4 head = make_int4(0, 0, 0, 0);
 
+    uint32_t stage = 0;
     for (uint32_t x = x0; x < x1; ++x) {
-        load_values(rows);
-        float ks = 0.f, vs = 0.f;                        // of the tile's row `lane`
-        if constexpr (S::kScaled) {
-            ks = load_scale(a.kv.k_scale + rows, rows != kNone);
-            vs = load_scale(a.kv.v_scale + rows, rows != kNone);
-        }
+        copies_wait<N - 2>();
+        copy(stage == 0 ? N - 1 : stage - 1);
+        const uint8_t *tile = ring + stage * G::kStage;
+        const uint32_t got = there[0];
+        stage = stage == N - 1 ? 0 : stage + 1;
         const bool more = x + 1 < x1;
-        Place<KS> then = at;
-        uint32_t rows_then = kNone;
-        if (more) {
-            then.next(a);
-            rows_then = then.at(a, lane);
+        uint32_t ks = 0, vs = 0;                         // scales of the tile's row `lane`
+        if constexpr (S::kScaled) {
+            fetch<4>(&ks, tile + 2 * G::kKeys + lane * 4);
+            fetch<4>(&vs, tile + 2 * G::kKeys + 128 + lane * 4);
         }
         float s[T8][4];
 #pragma unroll
         for (int t = 0; t < T8; ++t) {
+            uint32_t kr[S::kRowB / 16];
+#pragma unroll
+            for (int p = 0; p < S::kNK; ++p)
+                fetch<S::kKLd>(kr + p * S::kKLd / 4, tile + ((t * S::kNK + p) * 32 + lane) * S::kKLd);
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
 #pragma unroll
             for (int k = 0; k < S::kSteps; ++k) {
                 uint32_t b0, b1;
                 if constexpr (S::kScaled) {
-                    b0 = codes_to_bf162<KIND, 0>(kr[t][k]);
-                    b1 = codes_to_bf162<KIND, 1>(kr[t][k]);
+                    b0 = codes_to_bf162<KIND, 0>(kr[k]);
+                    b1 = codes_to_bf162<KIND, 1>(kr[k]);
                 } else {
-                    b0 = kr[t][2 * k];
-                    b1 = kr[t][2 * k + 1];
+                    b0 = kr[2 * k];
+                    b1 = kr[2 * k + 1];
                 }
                 const uint32_t A[4] = {qa[k][0], kTwo ? qa[k][1] : 0u, kTwo ? qa[k][2] : qa[k][1], kTwo ? qa[k][3] : 0u};
                 mma16816(s[t], A, b0, b1, kBf);
             }
         }
-        if (more) load_keys(rows_then);
-        const uint32_t there = __ballot_sync(0xffffffffu, rows != kNone) & kAll;
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < T8; ++t)
@@ -167,24 +202,26 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
             for (int i = 0; i < 2; ++i) {
                 const int key = t * 8 + 2 * c + i;
                 float y = (kTwo ? s[t][i] + s[t][i + 2] : s[t][i]) * a.scale_log2;
-                if constexpr (S::kScaled) y *= __shfl_sync(0xffffffffu, ks, key);
-                if (there != kAll && !(there >> key & 1)) y = -INFINITY;
+                if constexpr (S::kScaled) y *= __uint_as_float(__shfl_sync(0xffffffffu, ks, key));
+                if (got != kAll && !(got >> key & 1)) y = -INFINITY;
                 s[t][i] = y;
                 top = fmaxf(top, y);
             }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m, top), safe = mn == -INFINITY ? 0.f : mn;
-        // (a warp none of whose maxima has moved keeps its sums as they are)
-        if (__any_sync(0xffffffffu, mn != m)) {
-            const float keep = exp2_approx(m - safe);
+        // (the maximum is raised only when a score passes it by more than fp16's weights,
+        // 2^13 of the largest, or fp32's sums have room for)
+        if (__any_sync(0xffffffffu, top > m + (S::kHalf ? 2.f : 8.f))) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            top = fmaxf(top, m);
+            const float keep = exp2_approx(m - (top == -INFINITY ? 0.f : top));
+            m = top;
             l *= keep;
 #pragma unroll
             for (int j = 0; j < S::kNT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[j][i] *= keep;
         }
-        m = mn;
+        const float safe = m == -INFINITY ? 0.f : m;
         uint32_t hi[T8], lo[T8];                         // weights of keys 2c, 2c + 1 of each eight, in two parts
 #pragma unroll
         for (int t = 0; t < T8; ++t) {
@@ -193,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
             for (int i = 0; i < 2; ++i) {
                 p[i] = exp2_approx(s[t][i] - safe + (S::kHalf ? kShift : 0.f));
                 l += p[i];
-                if constexpr (S::kScaled) p[i] *= __shfl_sync(0xffffffffu, vs, t * 8 + 2 * c + i);
+                if constexpr (S::kScaled) p[i] *= __uint_as_float(__shfl_sync(0xffffffffu, vs, t * 8 + 2 * c + i));
             }
             uint32_t part[2];
             split16<S::kHalf ? kF16 : kBf16, 2>(p[0], p[1], part);
@@ -202,6 +239,13 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
 #pragma unroll
         for (int t = 0; t < T8; t += 2) {
             const uint32_t A[4] = {hi[t], lo[t], hi[t + 1], lo[t + 1]};
+            uint32_t vr[4][S::kRowB / 32];               // rows 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int p = 0; p < S::kNV; ++p)
+                    fetch<S::kVLd>(vr[i] + p * S::kVLd / 4,
+                                   tile + G::kKeys + (((t * 2 + i) * S::kNV + p) * 32 + lane) * S::kVLd);
 #pragma unroll
             for (int j = 0; j < S::kNT; ++j) {
                 constexpr int EV = S::kEV;
@@ -209,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
                 uint32_t b[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t *r0 = vr[t + h][0] + at4, *r1 = vr[t + h][1] + at4;
+                    const uint32_t *r0 = vr[2 * h] + at4, *r1 = vr[2 * h + 1] + at4;
                     if constexpr (S::kScaled) {
                         const uint32_t z = __byte_perm(r0[e / 4], r1[e / 4], e % 4 < 2 ? 0x5140u : 0x7362u);   // a0 b0 a1 b1
                         b[h] = e % 2 == 0 ? codes_to_bf162<KIND, 0>(z) : codes_to_bf162<KIND, 1>(z);
@@ -261,24 +305,30 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) k_paged_mma(const 
             } else if (from == 0) {
                 head = make_int4(at.row, at.unit, int(sh.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
             }
-            if (more) {
-                at = then;
-                begin_unit();
-            }
         }
-        at = then;
-        rows = rows_then;
+        if (more) {
+            at.next(a);
+            if (ends) begin_unit();
+        }
     }
     if (lane == 0) a.heads[w] = head;
+}
+
+template <int KIND, int D, bool QF16>
+cudaError_t mma_launch(const PagedArgs &a, int ctas, cudaStream_t s)
+{
+    const size_t smem = MmaRing<KIND, D>::kSmem;
+    const cudaError_t e = allow_smem<k_paged_mma<KIND, D, QF16>>(smem);
+    return e != cudaSuccess ? e : spec_launch(k_paged_mma<KIND, D, QF16>, dim3(ctas), kThreads, smem, 1, s, a);
 }
 
 template <int KIND, bool QF16>
 cudaError_t mma_dims(const PagedArgs &a, int ctas, cudaStream_t s)
 {
     switch (a.kv.head_dim) {
-    case 32: return spec_launch(k_paged_mma<KIND, 32, QF16>, dim3(ctas), kThreads, 0, 1, s, a);
-    case 64: return spec_launch(k_paged_mma<KIND, 64, QF16>, dim3(ctas), kThreads, 0, 1, s, a);
-    default: return spec_launch(k_paged_mma<KIND, 128, QF16>, dim3(ctas), kThreads, 0, 1, s, a);
+    case 32: return mma_launch<KIND, 32, QF16>(a, ctas, s);
+    case 64: return mma_launch<KIND, 64, QF16>(a, ctas, s);
+    default: return mma_launch<KIND, 128, QF16>(a, ctas, s);
     }
 }
 

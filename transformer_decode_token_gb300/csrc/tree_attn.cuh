@@ -318,22 +318,6 @@ __device__ __forceinline__ float row_value(const void *p, size_t i, int dtype)
     return dtype == GPT2_F32 ? value_at<GPT2_F32>(p, i) : dtype == GPT2_F16 ? value_at<GPT2_F16>(p, i) : value_at<GPT2_BF16>(p, i);
 }
 
-// Shape of a warp's tile on the CUDA cores (tree_attn_few.cu, paged_few.cuh).
-template <int KIND, int D>
-struct Few {
-    static constexpr int kES = KIND == GPT2_F32 ? 4 : KIND == GPT2_INT8 || KIND == GPT2_E4M3 ? 1 : 2;
-    static constexpr bool kScaled = kES == 1;
-    static constexpr int kRowB = D * kES;
-    static constexpr int kLPR = kRowB / 16;              // lanes per cache row
-    static constexpr int kRPL = 32 / kLPR;               // cache rows per access of a warp
-    static constexpr int kE = 16 / kES;                  // elements of a lane
-    static constexpr int kLoads = kRPL >= 4 ? 32 / kRPL : 8;   // accesses per tile: 32 rows, or 4 KB
-    static constexpr int KS = kLoads * kRPL;
-    static constexpr int kSplit = kLPR < kLoads ? kLPR : kLoads;   // lanes that a row's scores are spread over
-    static constexpr int kNV = kLoads / kSplit;          // scores of a lane
-    static constexpr int kSame = kLPR / kSplit;          // lanes with the same scores
-};
-
 // The 16 bytes of a lane as fp32 (codes without their scale), in pairs.
 template <int KIND, int E>
 __device__ __forceinline__ void widen(const uint32_t *r, float2 (&x)[E / 2])

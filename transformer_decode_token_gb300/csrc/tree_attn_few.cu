@@ -29,9 +29,24 @@ namespace tree {
 namespace {
 
 template <int KIND, int D, int R>
+struct Few {
+    static constexpr int kES = KIND == GPT2_F32 ? 4 : KIND == GPT2_INT8 || KIND == GPT2_E4M3 ? 1 : 2;
+    static constexpr bool kScaled = kES == 1;
+    static constexpr int kRowB = D * kES;
+    static constexpr int kLPR = kRowB / 16;              // lanes per cache row
+    static constexpr int kRPL = 32 / kLPR;               // cache rows per access of a warp
+    static constexpr int kE = 16 / kES;                  // elements of a lane
+    static constexpr int kLoads = kRPL >= 4 ? 32 / kRPL : 8;   // accesses per tile: 32 rows, or 4 KB
+    static constexpr int KS = kLoads * kRPL;
+    static constexpr int kSplit = kLPR < kLoads ? kLPR : kLoads;   // lanes that a row's scores are spread over
+    static constexpr int kNV = kLoads / kSplit;          // scores of a lane
+    static constexpr int kSame = kLPR / kSplit;          // lanes with the same scores
+};
+
+template <int KIND, int D, int R>
 __global__ void __launch_bounds__(kNW * 32, R == 1 ? 4 : R == 2 ? 3 : 2) k_tree_few(const __grid_constant__ TreeArgs a)
 {
-    using F = Few<KIND, D>;
+    using F = Few<KIND, D, R>;
     constexpr int E = F::kE, I = F::kLoads, NV = F::kNV, KS = F::KS, LPR = F::kLPR;
     __shared__ __align__(16) float so[kNW * R * D];
     __shared__ float sm_m[kNW][R], sm_l[kNW][R];
