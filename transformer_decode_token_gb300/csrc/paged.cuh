@@ -7,7 +7,10 @@
 // A unit that lies in one warp's share is written by that warp.  Of a unit that is
 // cut, each warp writes its part (maximum, sum of the weights, weighted sum, in
 // fp32) to the workspace, and a second kernel joins the parts in the order of the
-// list, so every call gives the same bits.
+// list, so every call gives the same bits.  (It costs 2 to 3 us.  Joins by the warp
+// that comes last, through tickets, took 10 us more for one request's 63 parts, and
+// clusters of 16 CTAs that share out whole units and join behind their barrier 1.4
+// us more.)
 //
 // What bounds such kernels is how much of the cache is on its way to an SM at a
 // time, so every warp has a ring of tiles in shared memory that asynchronous
@@ -39,6 +42,7 @@ cudaError_t paged_few_16(const PagedArgs &a, int r, int ctas, cudaStream_t s);
 cudaError_t paged_few_8(const PagedArgs &a, int r, int ctas, cudaStream_t s);
 // 8 query heads of a tile, on the matrix instructions (16-bit rows)
 cudaError_t paged_mma(const PagedArgs &a, int ctas, cudaStream_t s);
+// the second kernel
 cudaError_t paged_join(const PagedArgs &a, int r, cudaStream_t s);
 
 namespace paged {
@@ -189,7 +193,7 @@ constexpr int stages_for(int bytes, int ctas)
 
 // Lets a kernel use so much dynamic shared memory (once per device and kernel).
 template <auto FN>
-cudaError_t allow_smem(size_t bytes)
+cudaError_t allow(size_t bytes)
 {
     static uint64_t done = 0;       // a bit per device
     int dev = 0;
@@ -200,11 +204,19 @@ cudaError_t allow_smem(size_t bytes)
     return e;
 }
 
-// This warp's share of the list, and the place where it begins.  Called by all
-// threads of the CTA; also writes the zeros of rows that see nothing.
+// A warp's tiles x0 .. x1 - 1 of the list, and the place where they begin.
+template <int KS>
+struct Share {
+    Shares all;
+    uint32_t w, x0, x1;
+    Place<KS> at;
+    __device__ __forceinline__ Share() : all(1, 1), w(0), x0(0), x1(0) {}
+};
+
+// This warp's share.  Called by all threads of the CTA; also writes the zeros of
+// rows that see nothing.
 template <int KS, int D>
-__device__ __forceinline__ bool find_share(const PagedArgs &a, uint32_t w, Shares &sh, uint32_t &x0, uint32_t &x1,
-                                           Place<KS> &at)
+__device__ __forceinline__ void find_share(const PagedArgs &a, Share<KS> &sh)
 {
     __shared__ uint32_t sums[kNW], base[kNW];
     __shared__ int rows[kNW];
@@ -226,25 +238,25 @@ __device__ __forceinline__ bool find_share(const PagedArgs &a, uint32_t w, Share
         if (i < warp) incl += sums[i];
         total += sums[i];
     }
-    const uint32_t units = uint32_t(a.kv.n_head) * a.row_tiles, n = total * units;
-    const uint32_t parts = max(1u, min(uint32_t(a.warps), n));
-    sh = Shares(n, parts);
+    const uint32_t units = uint32_t(a.kv.n_head) * a.row_tiles;
+    const uint32_t n = total * units, parts = max(1u, min(uint32_t(a.warps), n));
+    sh.all = Shares(n, parts);
+    sh.w = warp * gridDim.x + blockIdx.x;        // (so that fewer shares than warps spread over the SMs)
 #pragma unroll
-    for (int i = 0; i < kNW; ++i) {              // the rows where this CTA's warps begin
+    for (int i = 0; i < kNW; ++i) {              // the rows where this CTA's warps begin, and the tiles before them
         const uint32_t wi = i * gridDim.x + blockIdx.x;
         if (wi >= parts || n == 0) continue;
-        const uint32_t y = sh.begin(wi) / units;
-        if (y >= incl - mine && y < incl) {
-            uint32_t t = incl - mine;
-            int r = r0;
-            for (;; ++r) {
-                const uint32_t k = (seen(a, r) + KS - 1) / KS;
-                if (y < t + k) break;
-                t += k;
-            }
-            rows[i] = r;
-            base[i] = t;
+        const uint32_t y = sh.all.begin(wi) / units;
+        if (y < incl - mine || y >= incl) continue;
+        uint32_t t = incl - mine;
+        int r = r0;
+        for (;; ++r) {
+            const uint32_t k = (seen(a, r) + KS - 1) / KS;
+            if (y < t + k) break;
+            t += k;
         }
+        rows[i] = r;
+        base[i] = t * units;
     }
     for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
         if (seen(a, r) != 0) continue;
@@ -256,16 +268,16 @@ __device__ __forceinline__ bool find_share(const PagedArgs &a, uint32_t w, Share
         }
     }
     __syncthreads();
-    if (w >= parts || n == 0) return false;
-    x0 = sh.begin(w);
-    x1 = sh.begin(w + 1);
+    if (sh.w >= parts || n == 0) return;         // (x0 == x1)
+    sh.x0 = sh.all.begin(sh.w);
+    sh.x1 = sh.all.begin(sh.w + 1);
+    Place<KS> &at = sh.at;
     at.enter(a, rows[warp]);
-    const uint32_t off = x0 - base[warp] * units;
+    const uint32_t off = sh.x0 - base[warp];
     at.unit = int(off / at.tiles);
     at.tile = off % at.tiles;
     at.block = at.tile * KS / uint32_t(a.kv.n_positions);
     at.offset = at.tile * KS - at.block * uint32_t(a.kv.n_positions);
-    return true;
 }
 
 // Query heads of a unit, and where its first one's row of q (or out) begins.
@@ -375,6 +387,66 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
         else if (a.q_dtype == GPT2_F16) static_cast<__half *>(a.out)[o + i] = __float2half_rn(out[i]);
         else static_cast<__nv_bfloat16 *>(a.out)[o + i] = __float2bfloat16_rn(out[i]);
     }
+}
+
+// Part i of a unit whose parts begin with warp w: the end of that one's share, then
+// the beginnings of the others'.
+__device__ __forceinline__ size_t part_of(uint32_t w, uint32_t i) { return i == 0 ? size_t(w) * 2 + 1 : size_t(w + i) * 2; }
+
+// Joins the n parts (from warp w on) of query head r of a unit, by a warp.  KIND: the
+// cache's type where the parts come from the matrix instructions, whose results
+// that are not finite are computed anew; -1 otherwise.
+template <int KIND, int D, int R>
+__device__ __forceinline__ void join_row(const PagedArgs &a, int row, int unit, uint32_t w, uint32_t n, int r)
+{
+    constexpr int kLanes = D / 4, kSide = 32 / kLanes, kBatch = 16;   // lanes of a part, parts side by side
+    const int lane = threadIdx.x & 31, e = lane % kLanes * 4, side = lane / kLanes;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = -INFINITY, l = 0.f;
+    for (uint32_t i0 = 0; i0 < n; i0 += 32) {        // 32 parts' (m, l), one per lane, and their sums
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (i0 + lane < n) ml = __ldcg(a.ml + part_of(w, i0 + lane) * R + r);
+        const uint32_t here = min(32u, n - i0);
+        float4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t i = k * kSide + side;
+            x[k] = i < here ? __ldcg(reinterpret_cast<const float4 *>(a.sums + (part_of(w, i0 + i) * R + r) * D + e))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float mn = fmaxf(top, warp_max(ml.x)), safe = mn == -INFINITY ? 0.f : mn;
+        const float keep = exp2_approx(top - safe), f = exp2_approx(ml.x - safe);
+        top = mn;
+        l = l * keep + ml.y * f;
+        v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+        for (uint32_t j = 0; j < here; j += kBatch * kSide) {
+            if (j)
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const uint32_t i = j + k * kSide + side;
+                    x[k] = i < here ? __ldcg(reinterpret_cast<const float4 *>(a.sums + (part_of(w, i0 + i) * R + r) * D + e))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t i = j + k * kSide + side;
+                const float g = __shfl_sync(0xffffffffu, f, i & 31);
+                if (i >= here) continue;
+                v.x = fmaf(x[k].x, g, v.x), v.y = fmaf(x[k].y, g, v.y), v.z = fmaf(x[k].z, g, v.z), v.w = fmaf(x[k].w, g, v.w);
+            }
+        }
+    }
+    l = warp_sum(l);
+#pragma unroll
+    for (int d = kLanes; d < 32; d *= 2) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, d), v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, d), v.w += __shfl_xor_sync(0xffffffffu, v.w, d);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+    if (side == 0) put4(a, row_at<D, R>(a, row, unit, a.out_stride) + size_t(r) * D + e, v.x, v.y, v.z, v.w);
+    if constexpr (KIND >= 0)
+        if (__any_sync(0xffffffffu, !is_finite(v.x + v.y + v.z + v.w))) row_anew<KIND, D, R>(a, row, unit, r);
 }
 
 }  // namespace paged

@@ -8,88 +8,29 @@ namespace gpt2 {
 namespace paged {
 namespace {
 
-// One CTA per warp of the attention's kernel: where a cut unit's parts begin with
-// that warp, joins them (the first part is its second place, the others are the
-// first places of the warps that follow).  KIND: the cache's type where the parts
-// come from the matrix instructions, whose results that are not finite are
-// computed anew; -1 otherwise.
+// Joins the parts of the units that were cut: a warp per unit whose parts begin with
+// that warp of the attention's kernel, or, for four or eight query heads, a CTA.
 template <int KIND, int D, int R>
 __global__ void __launch_bounds__(kThreads) k_paged_join(const __grid_constant__ PagedArgs a)
 {
-    constexpr int kLanes = R * D / 4, kGroups = kLanes < kThreads ? kThreads / kLanes : 1;
-    constexpr int kTurns = kLanes > kThreads ? kLanes / kThreads : 1;
-    __shared__ float s_top[R], s_inv[R];
-    __shared__ float4 s_sum[kGroups > 1 ? kThreads : 1];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     pdl_launch_dependents();
-    const int4 head = a.heads[blockIdx.x];
-    const int n = head.z;
-    if (n == 0) return;
-    const uint32_t w = blockIdx.x;
-    auto place = [&](int i) { return size_t(i == 0 ? w * 2 + 1 : (w + i) * 2); };
-    const int heads = heads_of<R>(a, head.y);
-    for (int r = warp; r < heads; r += kNW) {
-        float top = -INFINITY, l = 0.f;
-        for (int i = lane; i < n; i += 32) {
-            const float2 v = a.ml[place(i) * R + r];
-            const float mn = fmaxf(top, v.x), safe = mn == -INFINITY ? 0.f : mn;
-            l = l * exp2_approx(top - safe) + v.y * exp2_approx(v.x - safe);
-            top = mn;
-        }
-        const float all = warp_max(top), safe = all == -INFINITY ? 0.f : all;
-        l = warp_sum(l * exp2_approx(top - safe));
-        if (lane == 0) {
-            s_top[r] = safe;
-            s_inv[r] = l == 0.f ? 0.f : 1.f / l;
-        }
-    }
-    __syncthreads();
-    bool odd = false;
-    const int grp = tid / kLanes;
-#pragma unroll
-    for (int turn = 0; turn < kTurns; ++turn) {
-        const int e = (kLanes < kThreads ? tid % kLanes : tid + turn * kThreads) * 4, r = e / D;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < heads) {
-            const float top = s_top[r];
-#pragma unroll 4
-            for (int i = grp; i < n; i += kGroups) {
-                const float4 y = *reinterpret_cast<const float4 *>(a.sums + place(i) * (R * D) + e);
-                const float f = exp2_approx(a.ml[place(i) * R + r].x - top);
-                v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
-            }
-        }
-        if constexpr (kGroups > 1) {
-            s_sum[tid] = v;
-            __syncthreads();
-            if (grp == 0)
-#pragma unroll
-                for (int k = 1; k < kGroups; ++k) {
-                    const float4 y = s_sum[k * kLanes + tid];
-                    v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-                }
-        }
-        if (grp == 0 && r < heads) {
-            const float inv = s_inv[r];
-            put4(a, row_at<D, R>(a, head.x, head.y, a.out_stride) + e, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            const float sum = (v.x + v.y + v.z + v.w) * inv;
-            odd = odd || !is_finite(sum);
-        }
-    }
-    if constexpr (KIND >= 0) {
-        if (!__syncthreads_or(odd)) return;
-        for (int r = warp; r < heads; r += kNW) row_anew<KIND, D, R>(a, head.x, head.y, r);
-    }
+    const int warp = threadIdx.x >> 5;
+    const uint32_t w = R >= kNW ? blockIdx.x : blockIdx.x * kNW + warp;
+    const int4 h = a.heads[w];
+    if (h.z == 0) return;
+    const int heads = heads_of<R>(a, h.y);
+    for (int r = R >= kNW ? warp : 0; r < heads; r += R >= kNW ? kNW : 1)
+        join_row<KIND, D, R>(a, h.x, h.y, w, uint32_t(h.z), r);
 }
 
 template <int KIND, int R>
 cudaError_t join_dims(const PagedArgs &a, cudaStream_t s)
 {
     switch (a.kv.head_dim) {
-    case 32: return spec_launch(k_paged_join<KIND, 32, R>, dim3(a.warps), kThreads, 0, 1, s, a);
-    case 64: return spec_launch(k_paged_join<KIND, 64, R>, dim3(a.warps), kThreads, 0, 1, s, a);
-    default: return spec_launch(k_paged_join<KIND, 128, R>, dim3(a.warps), kThreads, 0, 1, s, a);
+    case 32: return spec_launch(k_paged_join<KIND, 32, R>, dim3(R >= kNW ? a.warps : a.warps / kNW), kThreads, 0, 1, s, a);
+    case 64: return spec_launch(k_paged_join<KIND, 64, R>, dim3(R >= kNW ? a.warps : a.warps / kNW), kThreads, 0, 1, s, a);
+    default: return spec_launch(k_paged_join<KIND, 128, R>, dim3(R >= kNW ? a.warps : a.warps / kNW), kThreads, 0, 1, s, a);
     }
 }
 
@@ -101,9 +42,9 @@ int tile_heads(int q_dtype, int group)
 }
 
 // CTAs that an SM holds of the kernel for these tiles.
-int resident(int r)
+int resident(const gpt2_kv &kv, int r)
 {
-    return r == 4 ? 2 : 3;
+    return r == 4 || (r == 8 && kv.head_dim == 128) ? 2 : 3;
 }
 
 // Cache rows of a tile, as the kernels have them.
@@ -118,7 +59,7 @@ struct Layout {
     size_t heads, ml, total;          // bytes: of the heads, of (m, l), of everything
     Layout(const gpt2_kv &kv, int r, int sms)
     {
-        warps = sms * resident(r) * tree::kNW;
+        warps = sms * resident(kv, r) * tree::kNW;
         heads = size_t(warps) * sizeof(int4);
         ml = (size_t(warps) * 2 * r * sizeof(float2) + 15) / 16 * 16;
         total = heads + ml + size_t(warps) * 2 * r * kv.head_dim * sizeof(float);

@@ -29,7 +29,7 @@ struct Few {
     static constexpr int kES = KIND == GPT2_F32 ? 4 : KIND == GPT2_INT8 || KIND == GPT2_E4M3 ? 1 : 2;
     static constexpr bool kScaled = kES == 1;
     static constexpr int kRowB = D * kES, kPieces = kRowB / 16;
-    static constexpr int kWant = R == 1 || D <= 64 ? 4 : 8;
+    static constexpr int kWant = kES == 1 && (R == 1 || D <= 64) ? 4 : 8;
     static constexpr int LPR = kPieces < kWant ? kPieces : kWant;    // lanes of a cache row
     static constexpr int P = kPieces / LPR;                          // 16-byte pieces of a lane: c, c + LPR, ..
     static constexpr int EP = 16 / kES, E = P * EP;                  // elements of a piece, of a lane
@@ -53,15 +53,12 @@ __global__ void __launch_bounds__(kThreads, few_ctas(R)) k_paged_few(const __gri
     static_assert(RPL * T == KS && E >= RPL, "every lane has rows, and dimensions of the result");
     extern __shared__ __align__(16) uint8_t dyn[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane % LPR, grp = lane / LPR;
-    const uint32_t w = warp * gridDim.x + blockIdx.x;    // (so that fewer shares than warps spread over the SMs)
     pdl_wait();                                          // (the joining kernel is placed when this one's CTAs leave)
-    Shares sh(1, 1);
-    uint32_t x0 = 0, x1 = 0;
-    Place<KS> at;
-    if (!find_share<KS, D>(a, w, sh, x0, x1, at)) {
-        if (lane == 0) a.heads[w] = make_int4(0, 0, 0, 0);
-        return;
-    }
+    Share<KS> sh;
+    find_share<KS, D>(a, sh);
+    Place<KS> at = sh.at;
+    const uint32_t w = sh.w, x0 = sh.x0, x1 = sh.x1;
+    int4 head = make_int4(0, 0, 0, 0);                   // the unit whose parts begin with this warp's: row, unit, parts
     uint8_t *ring = dyn + warp * (S * F::kStage) + lane * 16;
     const uint8_t *kbase = static_cast<const uint8_t *>(a.kv.k) + c * 16;
     const uint8_t *vbase = static_cast<const uint8_t *>(a.kv.v) + c * 16;
@@ -125,8 +122,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(R)) k_paged_few(const __gri
 #pragma unroll
     for (int i = 0; i < S; ++i) there[i] = 0;
     for (int i = 0; i < S - 1; ++i) copy(i);
-    begin_unit();
-    int4 head = make_int4(0, 0, 0, 0);
+    if (x0 < x1) begin_unit();
 
     uint32_t stage = 0;
     for (uint32_t x = x0; x < x1; ++x) {
@@ -282,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(R)) k_paged_few(const __gri
                 }
             }
             if (!whole && from == 0)
-                head = make_int4(at.row, at.unit, int(sh.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
+                head = make_int4(at.row, at.unit, int(sh.all.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
         }
         if (more) {
             at.next(a);
@@ -296,7 +292,7 @@ template <int KIND, int D, int R>
 cudaError_t few_launch(const PagedArgs &a, int ctas, cudaStream_t s)
 {
     const size_t smem = Few<KIND, D, R>::kSmem;
-    const cudaError_t e = allow_smem<k_paged_few<KIND, D, R>>(smem);
+    const cudaError_t e = allow<k_paged_few<KIND, D, R>>(smem);
     return e != cudaSuccess ? e : spec_launch(k_paged_few<KIND, D, R>, dim3(ctas), kThreads, smem, 1, s, a);
 }
 

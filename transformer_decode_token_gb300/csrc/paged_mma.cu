@@ -46,37 +46,34 @@ struct Shape {
     static constexpr int kT8 = KS / 8, kSteps = D / 16, kNT = D / 8;
 };
 
-constexpr int kMmaCtas = 3;                              // CTAs of an SM
+// CTAs of an SM.
+constexpr int mma_ctas(int D) { return D == 128 ? 2 : 3; }
 
 template <int KIND, int D>
 struct MmaRing {
     using S = Shape<KIND, D>;
     static constexpr int kKeys = S::KS * S::kRowB;
     static constexpr int kStage = 2 * kKeys + (S::kScaled ? 256 : 0);
-    static constexpr int kStages = stages_for(2 * kKeys, kMmaCtas);
+    static constexpr int kStages = stages_for(2 * kKeys, mma_ctas(D));
     static constexpr size_t kSmem = size_t(kNW) * kStages * kStage;
 };
 
 template <int KIND, int D, bool QF16>
-__global__ void __launch_bounds__(kThreads, kMmaCtas) k_paged_mma(const __grid_constant__ PagedArgs a)
+__global__ void __launch_bounds__(kThreads, mma_ctas(D)) k_paged_mma(const __grid_constant__ PagedArgs a)
 {
     using S = Shape<KIND, D>;
-    constexpr int R = 8, KS = S::KS, T8 = S::kT8;
+    using G = MmaRing<KIND, D>;
+    constexpr int R = 8, KS = S::KS, T8 = S::kT8, N = G::kStages;
     constexpr bool kBf = !S::kHalf, kTwo = S::kScaled && QF16;   // (queries in two parts)
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const uint32_t w = warp * gridDim.x + blockIdx.x;
-    pdl_wait();                                          // (the joining kernel is placed when this one's CTAs leave)
-    Shares sh(1, 1);
-    uint32_t x0 = 0, x1 = 0;
-    Place<KS> at;
-    if (!find_share<KS, D>(a, w, sh, x0, x1, at)) {
-        if (lane == 0) a.heads[w] = make_int4(0, 0, 0, 0);
-        return;
-    }
-    using G = MmaRing<KIND, D>;
-    constexpr int N = G::kStages;                      // stages
     extern __shared__ __align__(16) uint8_t dyn[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    pdl_wait();                                          // (the joining kernel is placed when this one's CTAs leave)
+    Share<KS> sh;
+    find_share<KS, D>(a, sh);
+    Place<KS> at = sh.at;
+    const uint32_t w = sh.w, x0 = sh.x0, x1 = sh.x1;
+    int4 head = make_int4(0, 0, 0, 0);                   // the unit whose parts begin with this warp's: row, unit, parts
     uint8_t *ring = dyn + warp * (N * G::kStage);
     const uint8_t *kbase = static_cast<const uint8_t *>(a.kv.k) + c * S::kKLd;
     const uint8_t *vbase = static_cast<const uint8_t *>(a.kv.v) + g * S::kVLd;
@@ -156,8 +153,7 @@ __global__ void __launch_bounds__(kThreads, kMmaCtas) k_paged_mma(const __grid_c
 #pragma unroll
     for (int i = 0; i < N; ++i) there[i] = 0;
     for (int i = 0; i < N - 1; ++i) copy(i);
-    begin_unit();
-    int4 head = make_int4(0, 0, 0, 0);
+    if (x0 < x1) begin_unit();
 
     uint32_t stage = 0;
     for (uint32_t x = x0; x < x1; ++x) {
@@ -303,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, kMmaCtas) k_paged_mma(const __grid_c
                     odd &= ~(0xfu << (h * 4));
                 }
             } else if (from == 0) {
-                head = make_int4(at.row, at.unit, int(sh.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
+                head = make_int4(at.row, at.unit, int(sh.all.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
             }
         }
         if (more) {
@@ -318,7 +314,7 @@ template <int KIND, int D, bool QF16>
 cudaError_t mma_launch(const PagedArgs &a, int ctas, cudaStream_t s)
 {
     const size_t smem = MmaRing<KIND, D>::kSmem;
-    const cudaError_t e = allow_smem<k_paged_mma<KIND, D, QF16>>(smem);
+    const cudaError_t e = allow<k_paged_mma<KIND, D, QF16>>(smem);
     return e != cudaSuccess ? e : spec_launch(k_paged_mma<KIND, D, QF16>, dim3(ctas), kThreads, smem, 1, s, a);
 }
 
