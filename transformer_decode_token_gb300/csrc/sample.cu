@@ -8,15 +8,15 @@
 // ids end.
 //   - Nothing cut: one pass, the race argmax w / -log u and the sum of w; one
 //     exchange in the cluster.
-//   - Else each CTA first bounds what can be kept: the top_k highest lie above
+//   - Else the cluster first bounds what can be kept: the top_k highest lie above
 //     the k-th highest of its threads' own maxima (to a bin), and with top-p alone
-//     every id whose weight is at most (1 - top_p) z / V lies behind the cut, z a
-//     part of the sum.  What is left, usually dozens to a few hundred ids, goes to a list.
-//   - A list of up to kList ids is settled by one CTA: an id's rank and the mass
-//     before it are counted over the list, and the race is run over what is kept.
+//     every id whose weight is at most (1 - top_p) z / V, z the sum of all, lies
+//     behind the cut.  What is left, usually dozens to a few hundred ids, goes to a list.
+//   - A list of up to kList ids is settled by one CTA: sorted, the masses before
+//     each id from a prefix sum, the race over what is kept.
 //   - A longer one is narrowed by histograms over the cluster, of counts and
 //     masses, by digits of (weight, logit, id), until the digit where the cut
-//     lies holds at most kList ids, which are then ranked as above.
+//     lies holds at most kList ids, which are then sorted as above.
 // Masses are summed as integers (a weight in units of 2^-40 of the largest), so that
 // neither order nor shape of a sum shows and every call gives the same bits.
 //
@@ -40,10 +40,11 @@ typedef unsigned long long u64;
 
 constexpr int kST = 512;                  // threads of a CTA, and bins of a histogram
 constexpr int kSW = kST / 32;
-constexpr int kList = 256;                // ids that one CTA ranks
+constexpr int kList = 512;                // ids that one CTA sorts: one per thread
 constexpr int kCand = 4096;               // ids of a CTA's share that it lists
 constexpr int kMaxSplit = 16;
-constexpr int kShareBytes = 160 * 1024;   // a CTA's share of a row
+constexpr int kShareBytes = 160 * 1024;   // a CTA's share of a row, at most
+constexpr int kShareIds = 65535;          // (mass sums: see find_cut)
 constexpr float kUnit = 1099511627776.f;  // 2^40: units of mass
 
 struct SampleArgs {
@@ -69,6 +70,14 @@ struct Scale {
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-f));
         return y * __int_as_float((127 - int(n)) << 23);
     }
+    // the same, the exponent rounded as a whole: off by 2^-24 t ln 2 more, for sums (where t is
+    // large enough to show, there are many of them or they weigh nothing)
+    static __device__ __forceinline__ float rough(float t)
+    {
+        float y;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-t));
+        return y;
+    }
 };
 
 // Place in the order: smaller is earlier (the logit, then the id).
@@ -79,6 +88,12 @@ __device__ __forceinline__ uint32_t order_bits(float l)
 }
 __device__ __forceinline__ u64 place(float l, uint32_t id) { return u64(order_bits(l)) << 32 | id; }
 
+__device__ __forceinline__ float logit_at(u64 place)
+{
+    const uint32_t b = ~uint32_t(place >> 32);
+    return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
+}
+
 // t as a 32-bit number in units of 2^-26 (the weights below 2^-64 are one)
 __device__ __forceinline__ uint32_t fixed(float t) { return t < 63.9f ? uint32_t(t * 67108864.f) : 0xffffffffu; }
 
@@ -88,9 +103,9 @@ struct Range {                            // ids whose leading digits are these
     uint32_t t, t_mask, bits, bits_mask, id, id_mask;
 };
 
-struct Border {                           // where a cut lies: in a digit, or at an id
-    u64 before_mass;
-    uint32_t before, inside, digit;
+struct Border {                           // the digit where a cut lies, and what lies before it
+    u64 before;
+    uint32_t digit, inside;
     int found;
 };
 
@@ -107,15 +122,14 @@ struct Shared {
     float fred[kSW];
     uint32_t count[2][kST], lo[2][kST], hi[2][kST];
     uint32_t scan[kSW];
-    u64 mscan[kSW], total;
+    u64 mscan[kSW];
     Border border;
-    // the row's list, in the first CTA of the cluster
-    float list_l[kList];
-    uint32_t list_id[kList];
-    u64 list_mass[kList];
+    u64 list[kList];                      // places of the row's ids that are left, in the first CTA of the cluster
+    u64 sort[kList], mass_before[kList];
     uint32_t list_n;
     u64 cut, cut_mass;
     uint32_t n_cand;
+    float bound;
     uint32_t cand[kCand];
 };
 
@@ -150,6 +164,49 @@ __device__ __forceinline__ u64 block_max(Shared &s, u64 v)
     return r;
 }
 
+// What CTA `lane` of the cluster has to tell, in lane `lane` of every warp (lanes
+// behind the last CTA: nothing), so that the reads from all of them overlap.
+__device__ __forceinline__ Exchange told(Exchange &x, int split)
+{
+    const int lane = threadIdx.x & 31;
+    Exchange y{0, 0, -INFINITY, 0.f, 0};
+    if (lane < split) y = *cg::this_cluster().map_shared_rank(&x, lane);
+    return y;
+}
+
+// The sum of every CTA's *p.
+__device__ __forceinline__ uint32_t cluster_sum(uint32_t *p, int split)
+{
+    uint32_t v[kMaxSplit], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i) v[i] = i < split ? *cg::this_cluster().map_shared_rank(p, i) : 0;
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i) sum += v[i];
+    return sum;
+}
+__device__ __forceinline__ u64 cluster_sum_wide(uint32_t *p, int split)
+{
+    uint32_t v[kMaxSplit];
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i) v[i] = i < split ? *cg::this_cluster().map_shared_rank(p, i) : 0;
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i) sum += v[i];
+    return sum;
+}
+
+__device__ __forceinline__ float block_max(Shared &s, float v)
+{
+    v = warp_max(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s.fred[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = s.fred[0];
+#pragma unroll
+    for (int i = 1; i < kSW; ++i) r = fmaxf(r, s.fred[i]);
+    return r;
+}
+
 // Inclusive sums over the threads of the CTA.
 __device__ __forceinline__ void block_scan(Shared &s, uint32_t &n, u64 &mass)
 {
@@ -175,159 +232,247 @@ struct Row {
     const T *share;                       // this CTA's ids lo .. lo + n - 1
     int lo, n, rank;
     Scale c;
-    float t_max;                          // ids with t above it are not kept
-    bool listed;                          // they are in s.cand, else the whole share is looked at
+    float t_max, l_min;                   // ids with t above, or logits below, are not kept
+    bool listed;                          // the others are in s.cand, else the whole share is looked at
     int round = 0;                        // histograms so far
 
     // f(logit, id) for each id that can be kept
     template <typename F>
     __device__ __forceinline__ void each(F f) const
     {
-        if (listed) {
-            const int k = int(s.n_cand);
-            for (int i = threadIdx.x; i < k; i += kST) {
-                const uint32_t j = s.cand[i];
-                f(float(share[j]), uint32_t(lo) + j);
+        const int count = listed ? int(s.n_cand) : n;
+        for (int i0 = threadIdx.x; i0 < count; i0 += 4 * kST) {
+            float l[4];
+            uint32_t j[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * kST;
+                j[k] = i < count ? (listed ? s.cand[i] : uint32_t(i)) : 0;
+                l[k] = i < count ? float(share[j[k]]) : -INFINITY;
             }
-        } else {
-            for (int j = threadIdx.x; j < n; j += kST) {
-                const float l = float(share[j]);
-                if (c.t(l) <= t_max) f(l, uint32_t(lo + j));
-            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (l[k] >= l_min) f(l[k], uint32_t(lo) + j[k]);
         }
     }
 };
 
-// The digit of level 0..11 of an id: of the weight (9, 8, 8 and 7 bits), of the
-// logit (8 each), of the id (8 each).
-__device__ __forceinline__ uint32_t digit_of(int level, uint32_t t, uint32_t bits, uint32_t id)
-{
-    switch (level) {
-    case 0: return t >> 23;
-    case 1: return t >> 15 & 255;
-    case 2: return t >> 7 & 255;
-    case 3: return t & 127;
-    default: break;
+// A digit of an id: `width` bits from `shift` on of its weight (word 0), its logit
+// (1) or itself (2).
+struct Digit {
+    int word, shift, width;
+    __device__ __forceinline__ uint32_t of(uint32_t t, uint32_t bits, uint32_t id) const
+    {
+        return (word == 0 ? t : word == 1 ? bits : id) >> shift & ((1u << width) - 1);
     }
-    const uint32_t v = level < 8 ? bits : id;
-    return v >> (8 * (3 - (level & 3))) & 255;
-}
-__device__ __forceinline__ void narrow(Range &r, int level, uint32_t digit)
-{
-    switch (level) {
-    case 0: r.t = digit << 23, r.t_mask = 0xff800000u; return;
-    case 1: r.t |= digit << 15, r.t_mask |= 0x007f8000u; return;
-    case 2: r.t |= digit << 7, r.t_mask |= 0x00007f80u; return;
-    case 3: r.t |= digit, r.t_mask |= 0x7fu; return;
-    default: break;
+    __device__ __forceinline__ bool last() const { return word == 2 && shift == 0; }
+    __device__ __forceinline__ void next()
+    {
+        if (shift == 0) ++word, shift = 32;
+        width = min(8, shift);
+        shift -= width;
     }
-    const int shift = 8 * (3 - (level & 3));
-    if (level < 8) r.bits |= digit << shift, r.bits_mask |= 255u << shift;
-    else r.id |= digit << shift, r.id_mask |= 255u << shift;
-}
+    __device__ __forceinline__ void narrow(Range &r, uint32_t digit) const
+    {
+        const uint32_t v = digit << shift, mask = ((1u << width) - 1) << shift;
+        if (word == 0) r.t |= v, r.t_mask |= mask;
+        else if (word == 1) r.bits |= v, r.bits_mask |= mask;
+        else r.id |= v, r.id_mask |= mask;
+    }
+};
 __device__ __forceinline__ bool within(const Range &r, uint32_t t, uint32_t bits, uint32_t id)
 {
     return (((t ^ r.t) & r.t_mask) | ((bits ^ r.bits) & r.bits_mask) | ((id ^ r.id) & r.id_mask)) == 0;
 }
 
+// The first CTA's list of n places in order, one per thread (~0 behind them).
+__device__ u64 sorted(Shared &s, int n)
+{
+    const int tid = threadIdx.x;
+    u64 key = tid < n ? s.list[tid] : ~0ull;
+    int size = 32;
+    while (size < n) size *= 2;
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            u64 other;
+            if (j >= 32) {
+                __syncthreads();
+                s.sort[tid] = key;
+                __syncthreads();
+                other = s.sort[tid ^ j];
+            } else {
+                other = __shfl_xor_sync(0xffffffffu, key, j);
+            }
+            const bool low = ((tid & j) == 0) == ((tid & k) == 0);   // this thread takes the smaller one
+            key = (other < key) == low ? other : key;
+        }
+    return key;
+}
+
+// For the id `my` of mass `own` of this thread, one of n in the list: how many come
+// before it and with what mass; sum_k: the mass of the first top_k (where that is
+// not 0).  Short lists by comparing each with each (four threads per id: 128 ids
+// take 32 steps), longer ones by sorting.
+__device__ void settle(Shared &s, int n, u64 my, u64 own, int top_k, uint32_t &ahead, u64 &before, u64 &sum_k)
+{
+    const int tid = threadIdx.x;
+    if (n <= kST / 4) {
+        if (tid < n) s.sort[tid] = own;
+        __syncthreads();
+        const int i = tid >> 2;
+        const u64 key = i < n ? s.list[i] : 0;
+        uint32_t c = 0;
+        u64 b = 0;
+        for (int j = tid & 3; j < n; j += 4)
+            if (s.list[j] < key) ++c, b += s.sort[j];
+        c += __shfl_xor_sync(0xffffffffu, c, 1), b += __shfl_xor_sync(0xffffffffu, b, 1);
+        c += __shfl_xor_sync(0xffffffffu, c, 2), b += __shfl_xor_sync(0xffffffffu, b, 2);
+        if (i < n && (tid & 3) == 0) s.count[0][i] = c, s.mass_before[i] = b;
+        __syncthreads();
+        if (tid < n) ahead = s.count[0][tid], before = s.mass_before[tid];
+    } else {
+        const u64 at = sorted(s, n);
+        __syncthreads();
+        s.sort[tid] = at;
+        __syncthreads();
+        // every thread finds its own id in the order
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s.sort[mid] < my) lo = mid + 1;
+            else hi = mid;
+        }
+        ahead = uint32_t(lo);
+        // masses in order, and their sums
+        __syncthreads();
+        if (tid < n) s.sort[lo] = own;
+        __syncthreads();
+        u64 to = tid < n ? s.sort[tid] : 0;
+        const u64 mass = to;
+        uint32_t none = 0;
+        block_scan(s, none, to);
+        if (tid < n) s.mass_before[tid] = to - mass;
+        __syncthreads();
+        if (tid < n) before = s.mass_before[lo];
+    }
+    sum_k = top_k > 0 ? block_sum(s, tid < n && ahead < uint32_t(top_k) ? own : 0) : 0;
+}
+
 // The place of the last kept id: of the `want` first of the order (by_mass false),
 // or of the ids before which less than `want` mass lies; only ids up to `last`
-// count.  ~0 where all of them are kept.  mass: of the ids up to that place.
+// count.  ~0 where all of them are kept.
 template <typename T>
-__device__ u64 find_cut(Row<T> &r, bool by_mass, u64 want, u64 last, u64 &mass)
+__device__ u64 find_cut(Row<T> &r, bool by_mass, u64 want, u64 last)
 {
     Shared &s = r.s;
     const cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x;
     Range range{};
-    u64 before_mass = 0;
-    uint32_t before = 0;
-    for (int level = 0;; ++level) {
+    u64 before = 0;                       // ids, or mass, before the range
+    // the first digit: 256 to 512 bins up to the largest t that is left
+    const int top = 32 - __clz(fixed(r.t_max * 1.0001f) | 1);
+    for (Digit digit{0, max(top - 9, 0), min(top, 9)};; digit.next()) {
         const int k = r.round++ & 1;
         s.count[k][tid] = s.lo[k][tid] = s.hi[k][tid] = 0;
         __syncthreads();
         r.each([&](float l, uint32_t id) {
-            const uint32_t t = fixed(r.c.t(l)), bits = order_bits(l);
-            if ((u64(bits) << 32 | id) > last || !within(range, t, bits, id)) return;
-            const uint32_t d = digit_of(level, t, bits, id);
-            // in units of 2^-31 of the largest weight of an octave, so that every weight is whole
-            const uint32_t x = uint32_t(r.c.weight(l) * __int_as_float((158 + int(t >> 26)) << 23));
-            atomicAdd(&s.count[k][d], 1u);
-            const uint32_t old = atomicAdd(&s.lo[k][d], x);
-            if (old + x < old) atomicAdd(&s.hi[k][d], 1u);
+            const float tf = r.c.t(l);
+            const uint32_t t = fixed(tf);
+            uint32_t d = t >> digit.shift;
+            if (range.t_mask != 0 || last != ~0ull) {
+                const uint32_t bits = order_bits(l);
+                if ((u64(bits) << 32 | id) > last || !within(range, t, bits, id)) return;
+                d = digit.of(t, bits, id);
+            }
+            if (!by_mass) {
+                atomicAdd(&s.count[k][d], 1u);
+            } else {
+                // in units of 2^-31 of the largest weight of an octave, so that every weight
+                // is whole; 15 and 16 bits of it apart, so that a share's sums fit
+                const int octave = int(t >> 26);
+                const uint32_t x = uint32_t(fminf(Scale::rough(tf - float(octave + 31)), 2147483648.f));
+                atomicAdd(&s.lo[k][d], x & 0x7fffu);
+                atomicAdd(&s.hi[k][d], x >> 15);
+            }
         });
         cl.sync();
-        uint32_t n = 0;
-        u64 sum = 0;
-        for (int i = 0; i < r.a.split; ++i) {
-            n += *cl.map_shared_rank(&s.count[k][tid], i);
-            sum += (u64(*cl.map_shared_rank(&s.hi[k][tid], i)) << 32) + *cl.map_shared_rank(&s.lo[k][tid], i);
+        u64 own;
+        if (by_mass) {
+            own = (cluster_sum_wide(&s.hi[k][tid], r.a.split) << 15) + cluster_sum_wide(&s.lo[k][tid], r.a.split);
+            // to units of 2^-40 of the largest weight
+            const int octave = int((range.t_mask == 0 ? uint32_t(tid) << digit.shift : range.t) >> 26);
+            own = octave <= 9 ? own << (9 - octave) : own >> (octave - 9);
+        } else {
+            own = cluster_sum(&s.count[k][tid], r.a.split);
         }
-        // to units of 2^-40 of the largest weight
-        const int octave = int((level == 0 ? uint32_t(tid) << 23 : range.t) >> 26);
-        sum = octave <= 9 ? sum << (9 - octave) : sum >> (octave - 9);
-        uint32_t n_to = n;
-        u64 sum_to = sum;
         if (tid == 0) s.border.found = 0;
-        block_scan(s, n_to, sum_to);
-        const u64 at = by_mass ? before_mass + sum_to : before + n_to, was = at - (by_mass ? sum : u64(n));
-        if (n && was < want && at >= want) {
+        u64 at = own, none_wide = 0;
+        uint32_t none = 0;
+        block_scan(s, none, at);
+        at += before;
+        if (own && at - own < want && at >= want) {
             s.border.found = 1;
             s.border.digit = tid;
-            s.border.inside = n;
-            s.border.before = before + n_to - n;
-            s.border.before_mass = before_mass + sum_to - sum;
+            s.border.before = at - own;
+            s.border.inside = uint32_t(own);
         }
-        if (tid == kST - 1) s.total = before_mass + sum_to;
         __syncthreads();
-        if (!s.border.found) {
-            mass = s.total;
-            __syncthreads();
-            return ~0ull;
-        }
+        const bool found = s.border.found;
         before = s.border.before;
-        before_mass = s.border.before_mass;
-        const uint32_t inside = s.border.inside;
-        narrow(range, level, s.border.digit);
+        uint32_t inside = s.border.inside;         // (of counts)
+        if (found) digit.narrow(range, s.border.digit);
         __syncthreads();
-        if (inside > kList && level < 11) continue;
+        if (!found) return ~0ull;
 
-        // the first CTA ranks these
+        // the first CTA sorts these, if they are few enough
+        if (!by_mass && inside > kList && !digit.last()) continue;
         Shared *first = cl.map_shared_rank(&s, 0);
         if (r.rank == 0 && tid == 0) s.list_n = 0;
-        cl.sync();
-        r.each([&](float l, uint32_t id) {
+        auto in_range = [&](float l, uint32_t id, u64 &at) {
+            const uint32_t t = fixed(r.c.t(l));
+            if ((t ^ range.t) & range.t_mask) return false;
             const uint32_t bits = order_bits(l);
-            if ((u64(bits) << 32 | id) > last || !within(range, fixed(r.c.t(l)), bits, id)) return;
-            const uint32_t i = atomicAdd(&first->list_n, 1u);
-            if (i < kList) {
-                first->list_l[i] = l;
-                first->list_id[i] = id;
-                first->list_mass[i] = mass_of(r.c.weight(l));
-            }
+            at = u64(bits) << 32 | id;
+            return at <= last && within(range, t, bits, id);
+        };
+        uint32_t mine = 0;
+        r.each([&](float l, uint32_t id) {
+            u64 at;
+            mine += in_range(l, id, at);
         });
+        uint32_t to = mine;
+        block_scan(s, to, none_wide);
         cl.sync();
+        if (tid == kST - 1) {
+            s.scan[0] = atomicAdd(&first->list_n, to);
+            s.scan[1] = to;
+        }
+        __syncthreads();
+        if (s.scan[0] + s.scan[1] <= kList) {
+            uint32_t i = s.scan[0] + to - mine;
+            r.each([&](float l, uint32_t id) {
+                u64 at;
+                if (in_range(l, id, at)) first->list[i++] = at;
+            });
+        }
+        cl.sync();
+        inside = first->list_n;
+        if (inside > kList && !digit.last()) {
+            cl.sync();                    // (before the first CTA clears it)
+            continue;
+        }
         if (r.rank == 0) {
-            const int m = int(inside < kList ? inside : kList), i = tid >> 1;
-            uint32_t rank = 0;
-            u64 sums = 0, own = 0, my = ~0ull;
-            if (i < m) {
-                my = place(s.list_l[i], s.list_id[i]);
-                own = s.list_mass[i];
-                for (int j = tid & 1; j < m; j += 2)
-                    if (place(s.list_l[j], s.list_id[j]) < my) ++rank, sums += s.list_mass[j];
-            }
-            rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-            sums += __shfl_xor_sync(0xffffffffu, sums, 1);
-            // kept are those with a rank, or a mass before them, below what is wanted
-            const bool keep = i < m && (by_mass ? before_mass + sums < want : before + rank < want);
-            const u64 worst = block_max(s, keep ? my : 0);
-            const u64 total = block_sum(s, keep && !(tid & 1) ? own : 0);
-            if (tid == 0) s.cut = worst, s.cut_mass = before_mass + total;
+            const int m = int(min(inside, uint32_t(kList)));
+            const u64 key = sorted(s, m);
+            u64 own = tid < m ? (by_mass ? mass_of(r.c.weight(logit_at(key))) : 1) : 0, to = own;
+            uint32_t none = 0;
+            block_scan(s, none, to);
+            // kept are those with fewer ids, or less mass, before them than wanted
+            const int kept = __syncthreads_count(tid < m && before + to - own < want);
+            if (tid == kept - 1) s.cut = key;
         }
         cl.sync();
         const u64 cut = first->cut;
-        mass = first->cut_mass;
         cl.sync();                        // (before the first CTA writes another)
         return cut;
     }
@@ -340,7 +485,6 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
     __shared__ Shared s;
     const cg::cluster_group cl = cg::this_cluster();
     const int row = blockIdx.x / a.split, rank = blockIdx.x % a.split, tid = threadIdx.x;
-    T *share = reinterpret_cast<T *>(dyn);
     pdl_wait();
     pdl_launch_dependents();
     const int lo = min(rank * a.per, a.V), n = min(a.per, a.V - lo);
@@ -355,24 +499,25 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
     min_p = fminf(min_p, 1.f);
     const bool cut = top_k > 0 || top_p < 1.f || min_p > 0.f;
     const float *u = a.u + size_t(row) * a.V;
-    if (tid == 0) s.list_n = s.n_cand = 0;
+    if (tid == 0) s.list_n = s.n_cand = 0, s.bound = 0.f;
 
-    // ---- the share into shared memory, its highest logit ----
-    float top = -INFINITY;
-    int id = -1;
+    // ---- the share into shared memory (16-byte pieces as they lie in the row), its highest logit ----
+    constexpr int E = 16 / sizeof(T), U = 4;
+    const int front = min(n, int((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T)));
+    T *share = reinterpret_cast<T *>(dyn) + (E - front) % E;
+    float thread_top = -INFINITY;
     bool bad = false;
-    auto take = [&](T v, int j) {
-        share[j] = v;
+    auto take = [&](T v) {
         const float x = float(v);
-        if (x > top) top = x, id = j;     // (a NaN or -infinity is never above)
-        bad = bad || x != x || x == INFINITY;
+        thread_top = fmaxf(thread_top, x);        // (a NaN is never above)
+        bad = bad || !(x < INFINITY);
     };
     {
-        constexpr int E = 16 / sizeof(T), U = 4;
-        const int head = min(n, int((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T)));
-        const int nv = (n - head) / E, rest = head + nv * E;
-        const uint4 *pv = reinterpret_cast<const uint4 *>(p + head);
-        if (tid < head) take(p[tid], tid);
+        const int nv = (n - front) / E, rest = front + nv * E;
+        const uint4 *pv = reinterpret_cast<const uint4 *>(p + front);
+        uint4 *sv = reinterpret_cast<uint4 *>(share + front);
+        if (!greedy && !cut)                       // the random numbers follow the logits from memory
+            for (int j = tid * 32; j < n; j += kST * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(u + lo + j));
         for (int i0 = tid; i0 < nv; i0 += U * kST) {
             uint4 v[U];
 #pragma unroll
@@ -381,16 +526,30 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 if (i0 + k * kST < nv) {
+                    sv[i0 + k * kST] = v[k];
                     const T *e = reinterpret_cast<const T *>(&v[k]);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) take(e[j], head + (i0 + k * kST) * E + j);
+                    for (int j = 0; j < E; ++j) take(e[j]);
                 }
         }
-        if (tid < n - rest) take(p[rest + tid], rest + tid);
+        if (tid < front) take(share[tid] = p[tid]);
+        if (tid < n - rest) take(share[rest + tid] = p[rest + tid]);
     }
-    const float thread_top = top;
-    u64 best = block_max(s, id >= 0 ? argmax_key(top + 0.f, uint32_t(lo + id)) : 0);
+    constexpr int B = 8;
+    float e_first = 0.5f, e[B];           // the first random numbers, where nothing is cut, on their way before the maximum
+    auto load_u = [&](int j0) {
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int j = j0 + k * kST + tid;
+            e[k] = j < n ? __ldcs(u + lo + j) : 0.5f;
+        }
+    };
+    if (!greedy && !cut) {
+        if (tid < n) e_first = __ldcs(u + lo + tid);
+        load_u(kST);
+    }
     bad = __syncthreads_or(bad);
+    const float cta_top = block_max(s, thread_top);
     auto logit_of = [](u64 key) {         // of an argmax key
         const uint32_t b = uint32_t(key >> 32);
         return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
@@ -398,7 +557,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
     Row<T> r{a, s, share, lo, n, rank};
     {
         const float c = 1.4426950408889634f / temperature;
-        r.c.hi = fminf(c, FLT_MAX);
+        r.c.hi = fminf(fmaxf(c, FLT_TRUE_MIN), FLT_MAX);   // (above 0: a logit of -infinity has t = infinity)
         r.c.lo = 0.f;
         if (c > 0.f && c <= FLT_MAX)
             r.c.lo = (fmaf(-c, temperature, 1.4426950216293335f) + 1.9259629911e-8f) / temperature;
@@ -410,100 +569,108 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
 
     if (!greedy && !cut) {
         // ---- the race over all ids, by this CTA's own maximum ----
-        r.c.m = best ? logit_of(best) : 0.f;
-        float won = -1.f, won_w = 0.f, bound = 0.f;
+        r.c.m = cta_top;
+        float won = 0.f, won_w = 0.f;
         int who = -1;
         u64 mass = 0;
-        for (int j0 = 0; j0 < n; j0 += 4 * kST) {
-            float e[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = j0 + k * kST + tid;
-                e[k] = j < n ? u[lo + j] : 0.5f;
+        // an id's weight, and its part in the race unless `bound` rules it out, which
+        // needs no logarithm: -log u >= 1 - u
+        auto take_part = [&](float l, float e, int j, float bound, float &sum) {
+            const float t = r.c.t(l);
+            float w = Scale::rough(t);
+            sum += w;
+            if (w > bound * (1.f - e)) {
+                if (t < 125.f) w = r.c.weight(l);
+                const float y = __fdividef(w, -logf(e));
+                if (y > won) won = y, won_w = w, who = j;
             }
+        };
+        // the first id of every thread gives all of them a bound; the others raise it
+        float sum = 0.f;
+        if (tid < n) take_part(float(share[tid]), e_first, tid, 0.f, sum);
+        if (tid == 0) s.bound = 0.f;
+        const float first_best = block_max(s, won);
+        if (tid == 0) s.bound = first_best * 0.999f;
+        __syncthreads();
+        for (int j0 = kST; j0 < n; j0 += B * kST) {
+            if (j0 > kST) load_u(j0);
+            const float bound = fmaxf(*static_cast<volatile float *>(&s.bound), won * 0.999f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < B; ++k) {
                 const int j = j0 + k * kST + tid;
-                const float l = j < n ? float(share[j]) : -INFINITY;
-                if (!(r.c.t(l) < 125.f)) continue;
-                const float w = r.c.weight(l);
-                mass += mass_of(w);
-                // (what the warp's best rules out needs no logarithm: -log u >= 1 - u)
-                if (w > bound * (1.f - e[k])) {
-                    const float y = __fdividef(w, -logf(e[k]));
-                    if (y > won) won = y, won_w = w, who = j;
-                }
+                if (j < n) take_part(float(share[j]), e[k], j, bound, sum);
             }
-            bound = warp_max(won) * 0.999f;
+            if (won * 0.999f > bound) atomicMax(reinterpret_cast<int *>(&s.bound), __float_as_int(won * 0.999f));
+            mass += mass_of(sum);
+            sum = 0.f;
         }
+        mass += mass_of(sum);
         const u64 key = who >= 0 ? argmax_key(won, uint32_t(lo + who)) : 0, high = block_max(s, key);
         if (key && key == high) s.ex[0].w = won_w;
         mass = block_sum(s, mass);
         if (tid == 0) {
             s.ex[0].best = high;
             s.ex[0].z = mass;
-            s.ex[0].m = best ? r.c.m : -INFINITY;
+            s.ex[0].m = cta_top;
             s.ex[0].bad = bad;
         }
         cl.sync();
-        float m = -INFINITY, mw = 0.f;
-        int any_bad = 0;
-        for (int i = 0; i < a.split; ++i) {
-            const Exchange *x = cl.map_shared_rank(&s.ex[0], i);
-            m = fmaxf(m, x->m);
-            any_bad |= x->bad;
-        }
-        float score = -1.f, total = 0.f;
-        for (int i = 0; i < a.split && !any_bad; ++i) {
-            const Exchange *x = cl.map_shared_rank(&s.ex[0], i);
-            if (x->best == 0) continue;
-            const float t = (m - x->m) * r.c.hi, f = t < 125.f ? Scale{r.c.hi, r.c.lo, m}.weight(x->m) : 0.f;
-            total += f * (float(x->z) * (1.f / kUnit));
-            const float y = f * logit_of(x->best);
-            if (y > score) score = y, token = argmax_key_index(x->best), mw = f * x->w;
-        }
-        if (token >= 0) prob = mw / total;
+        const Exchange x = told(s.ex[0], a.split);
+        const bool any_bad = __any_sync(0xffffffffu, x.bad);
+        const float m = warp_max(x.m), t = (m - x.m) * r.c.hi;
+        const float f = x.best && t < 125.f ? Scale{r.c.hi, r.c.lo, m}.weight(x.m) : 0.f;
+        const float total = warp_sum(f * (float(x.z) * (1.f / kUnit)));
+        const u64 mine = f > 0.f ? argmax_key(f * logit_of(x.best), uint32_t(argmax_key_index(x.best))) : 0;
+        const u64 win = warp_max_u64(mine);
+        const float w = __shfl_sync(0xffffffffu, f * x.w, win ? __ffs(__ballot_sync(0xffffffffu, mine == win)) - 1 : 0);
+        if (win && !any_bad) token = argmax_key_index(win), prob = w / total;
         r.c.m = m;
         r.listed = false;
         r.t_max = 124.9f;
-        z = u64(double(total) * double(kUnit));
-        if (any_bad) token = -1;
+        z = token >= 0 ? u64(double(total) * double(kUnit)) : 0;
     } else {
         // ---- the row's highest logit ----
+        if (greedy && cta_top > -INFINITY) {       // the lowest id that has the CTA's
+            int id = n;
+            for (int j = tid; j < n; j += kST)
+                if (float(share[j]) == cta_top) {
+                    id = j;
+                    break;
+                }
+            const u64 key = block_max(s, id < n ? argmax_key(cta_top + 0.f, uint32_t(lo + id)) : 0);
+            if (tid == 0) s.ex[0].best = key;
+        }
         if (tid == 0) {
-            s.ex[0].best = best;
+            s.ex[0].m = cta_top;
             s.ex[0].bad = bad;
         }
         cl.sync();
-        int any_bad = 0;
-        best = 0;
-        for (int i = 0; i < a.split; ++i) {
-            const Exchange *x = cl.map_shared_rank(&s.ex[0], i);
-            best = x->best > best ? x->best : best;
-            any_bad |= x->bad;
-        }
+        const Exchange x = told(s.ex[0], a.split);
+        const bool any_bad = __any_sync(0xffffffffu, x.bad);
+        const float row_top = warp_max(x.m);
         if (greedy) {
+            const u64 best = warp_max_u64(x.m > -INFINITY ? x.best : 0);
             if (best) token = argmax_key_index(best), prob = 1.f;
-        } else if (best && !any_bad) {
-            r.c.m = logit_of(best);
+        } else if (row_top > -INFINITY && !any_bad) {
+            r.c.m = row_top;
             // ---- what can be kept ----
             r.t_max = 124.9f;
-            u64 all = 0;                  // this CTA's mass, then the row's
+            u64 all = 0;                  // the row's mass (top-p alone)
             // (top-p of the top_k needs all of these, those below min_p too)
             if (min_p > 0.f && !(top_k > 0 && top_p < 1.f)) r.t_max = fminf(r.t_max, -log2f(min_p) + 0.01f);
             if (top_k > 0) {
-                // the k-th highest of the threads' maxima, to a bin
+                // the k-th highest of the cluster's threads' maxima, to a bin
                 s.count[0][tid] = 0;
                 __syncthreads();
                 const float t = r.c.t(thread_top);
                 if (t < 63.f) atomicAdd(&s.count[0][fixed(t) >> 23], 1u);
-                __syncthreads();
-                uint32_t k = s.count[0][tid];
-                const uint32_t own = k;
+                cl.sync();
+                ++r.round;
+                const uint32_t own = cluster_sum(&s.count[0][tid], a.split);
+                uint32_t k = own;
                 u64 none = 0;
-                block_scan(s, k, none);
                 if (tid == 0) s.border.found = 0;
-                __syncthreads();
+                block_scan(s, k, none);
                 if (own && k >= uint32_t(top_k) && k - own < uint32_t(top_k)) {
                     s.border.found = 1;
                     s.border.digit = tid;
@@ -512,81 +679,80 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                 if (s.border.found) r.t_max = fminf(r.t_max, float(s.border.digit + 1) * 0.125f + 1e-5f);
             } else if (top_p < 1.f) {
                 u64 mass = 0;
-                for (int j = tid; j < n; j += kST) {
-                    const float l = float(share[j]);
-                    if (r.c.t(l) < 125.f) mass += mass_of(r.c.weight(l));
+                for (int j0 = 0; j0 < n; j0 += 8 * kST) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int j = j0 + k * kST + tid;
+                        if (j < n) sum += Scale::rough(r.c.t(float(share[j])));
+                    }
+                    mass += mass_of(sum);
                 }
-                all = block_sum(s, mass);
+                mass = block_sum(s, mass);
+                if (tid == 0) s.ex[1].z = mass;
+                cl.sync();
+                all = warp_sum64(told(s.ex[1], a.split).z);
                 const float least = (1.f - top_p) * (float(all) * (1.f / kUnit)) / float(a.V);
                 if (least > 0.f) r.t_max = fminf(r.t_max, -log2f(least) + 0.01f);
             }
-            // ---- their list ----
-            for (int j0 = 0; j0 < n; j0 += kST) {
-                const int j = j0 + tid;
-                const bool yes = j < n && r.c.t(float(share[j])) <= r.t_max;
-                const uint32_t who = __ballot_sync(0xffffffffu, yes);
-                if (!who) continue;
-                uint32_t at = 0;
-                if ((tid & 31) == 0) at = atomicAdd(&s.n_cand, uint32_t(__popc(who)));
-                at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << (tid & 31)) - 1));
-                if (yes && at < kCand) s.cand[at] = uint32_t(j);
+            // ---- their list: a thread's ids follow one another ----
+            // (by the logits, a little below the bound, and above those of no weight)
+            r.l_min = fmaxf(r.c.m - r.t_max / r.c.hi * 1.00001f, -FLT_MAX);
+            for (int j0 = 0; j0 < n; j0 += 32 * kST) {
+                uint32_t mask = 0;
+#pragma unroll 8
+                for (int k = 0; k < 32; ++k) {
+                    const int j = j0 + k * kST + tid;
+                    if (j < n && float(share[j]) >= r.l_min) mask |= 1u << k;
+                }
+                uint32_t at = __popc(mask);
+                u64 none = 0;
+                block_scan(s, at, none);
+                const uint32_t before = s.n_cand;
+                __syncthreads();
+                if (tid == kST - 1) s.n_cand = before + at;
+                at += before - __popc(mask);
+                for (; mask; mask &= mask - 1, ++at)
+                    if (at < kCand) s.cand[at] = uint32_t(j0 + (__ffs(mask) - 1) * kST + tid);
+                __syncthreads();
             }
-            __syncthreads();
             r.listed = s.n_cand <= kCand;
             // the lists to the first CTA, where they fit
             Shared *first = cl.map_shared_rank(&s, 0);
-            if (tid == 0) {
-                s.scan[0] = atomicAdd(&first->list_n, s.n_cand);
-                s.ex[1].z = all;
-            }
+            if (tid == 0) s.scan[0] = atomicAdd(&first->list_n, s.n_cand);
             __syncthreads();
             const uint32_t base = s.scan[0];
             if (base + s.n_cand <= kList)
                 for (int i = tid; i < int(s.n_cand); i += kST) {
                     const uint32_t j = s.cand[i];
-                    const float l = float(share[j]);
-                    first->list_l[base + i] = l;
-                    first->list_id[base + i] = uint32_t(lo) + j;
-                    first->list_mass[base + i] = mass_of(r.c.weight(l));
+                    first->list[base + i] = place(float(share[j]), uint32_t(lo) + j);
                 }
             cl.sync();
-            all = 0;
-            for (int i = 0; i < a.split; ++i) all += cl.map_shared_rank(&s.ex[1], i)->z;
             const uint32_t m = first->list_n;
             const u64 want = u64(double(top_p) * double(all));
             if (m <= kList) {
                 if (rank == 0) {
-                    // two threads per id: its rank, and the mass before it
-                    const int i = tid >> 1;
-                    const bool mine = i < int(m);
-                    const uint32_t my_id = mine ? s.list_id[i] : 0;
-                    const float e = mine ? u[my_id] : 0.5f, w = mine ? r.c.weight(s.list_l[i]) : 0.f;
-                    const u64 my = mine ? place(s.list_l[i], my_id) : ~0ull;
-                    uint32_t before = 0;
-                    u64 mass = 0;
-                    for (int j = tid & 1; j < int(m); j += 2)
-                        if (place(s.list_l[j], s.list_id[j]) < my) ++before, mass += s.list_mass[j];
-                    before += __shfl_xor_sync(0xffffffffu, before, 1);
-                    mass += __shfl_xor_sync(0xffffffffu, mass, 1);
-                    bool keep = mine && (top_k == 0 || before < uint32_t(top_k)) && w >= min_p;
-                    if (top_p < 1.f) {
-                        u64 bound = want;
-                        if (top_k > 0)
-                            bound = u64(double(top_p) *
-                                        double(block_sum(s, mine && !(tid & 1) && before < uint32_t(top_k) ? s.list_mass[i] : 0)));
-                        keep = keep && (mass < bound || before == 0);
-                    }
-                    const bool one = keep && !(tid & 1);
-                    z = block_sum(s, one ? s.list_mass[i] : 0);
-                    const u64 key = one ? argmax_key(__fdividef(w, -logf(e)), my_id) : 0, high = block_max(s, key);
-                    if (key && key == high) s.ex[0].w = w;
+                    // this thread's id in the race, and the number of ids and the mass before it
+                    const bool mine = tid < int(m);
+                    const u64 my = mine ? s.list[tid] : ~0ull;
+                    const float e = mine ? u[uint32_t(my)] : 0.5f, w = mine ? r.c.weight(logit_at(my)) : 0.f;
+                    const u64 own = mine ? mass_of(w) : 0;
+                    uint32_t ahead = 0;
+                    u64 before = 0, sum_k = 0;
+                    settle(s, int(m), my, own, top_k, ahead, before, sum_k);
+                    const u64 up_to = top_k > 0 ? u64(double(top_p) * double(sum_k)) : want;
+                    const bool keep = mine && (top_k == 0 || ahead < uint32_t(top_k)) && w >= min_p &&
+                                      (top_p >= 1.f || before < up_to || ahead == 0);
+                    z = block_sum(s, keep ? own : 0);
+                    const u64 key = keep ? argmax_key(__fdividef(w, -logf(e)), uint32_t(my)) : 0, high = block_max(s, key);
+                    if (key && key == high) s.ex[2].w = w;
                     if (a.dist) {
                         const u64 worst = block_max(s, keep ? my : 0);
                         if (tid == 0) s.cut = worst, s.cut_mass = z;
                     }
                     __syncthreads();
                     token = argmax_key_index(high);
-                    prob = s.ex[0].w / (float(z) * (1.f / kUnit));
+                    prob = s.ex[2].w / (float(z) * (1.f / kUnit));
                 }
                 if (a.dist) {
                     cl.sync();
@@ -594,38 +760,70 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                     z = first->cut_mass;
                 }
             } else {
-                u64 mass = all;
-                if (top_k > 0) last = find_cut(r, false, u64(top_k), ~0ull, mass);
+                u64 mass = 0;
+                if (top_k > 0) last = find_cut(r, false, u64(top_k), ~0ull);
                 if (top_p < 1.f) {
-                    const u64 up_to = top_k > 0 ? u64(double(top_p) * double(mass)) : want;
-                    u64 none;
-                    const u64 p_last = find_cut(r, true, up_to > 0 ? up_to : 1, last, none);
+                    u64 up_to = want;
+                    if (top_k > 0) {      // of the mass of these
+                        r.each([&](float l, uint32_t id) {
+                            if (place(l, id) <= last) mass += mass_of(Scale::rough(r.c.t(l)));
+                        });
+                        mass = block_sum(s, mass);
+                        if (tid == 0) s.ex[1].z = mass;
+                        cl.sync();
+                        up_to = u64(double(top_p) * double(warp_sum64(told(s.ex[1], a.split).z)));
+                    }
+                    const u64 p_last = find_cut(r, true, up_to > 0 ? up_to : 1, last);
                     last = p_last < last ? p_last : last;
                 }
                 // the race over the kept ids
-                float won = -1.f, won_w = 0.f;
+                float won = 0.f, won_w = 0.f;
                 int who = -1;
                 mass = 0;
-                r.each([&](float l, uint32_t v) {
-                    if (place(l, v) > last) return;
-                    const float w = r.c.weight(l);
-                    if (w < min_p) return;
-                    mass += mass_of(w);
-                    const float y = __fdividef(w, -logf(u[v]));
-                    if (y > won || (y == won && int(v) < who)) won = y, won_w = w, who = int(v);
-                });
+                const int count = r.listed ? int(s.n_cand) : n;
+                const float l_last = last == ~0ull ? r.l_min : logit_at(last);
+                const int id_last = last == ~0ull ? a.V : int(uint32_t(last));
+                for (int i0 = 0; i0 < count; i0 += B * kST) {
+                    float l[B], sum = 0.f;
+                    int id[B];
+                    const float bound = fmaxf(*static_cast<volatile float *>(&s.bound), won * 0.999f);
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {          // (the random numbers' loads overlap)
+                        const int i = i0 + k * kST + tid;
+                        id[k] = -1;
+                        e[k] = 0.5f;
+                        if (i >= count) continue;
+                        const int j = r.listed ? int(s.cand[i]) : i;
+                        l[k] = float(share[j]);
+                        if (l[k] > l_last || (l[k] == l_last && lo + j <= id_last)) {
+                            id[k] = lo + j;
+                            e[k] = __ldcs(u + lo + j);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {
+                        if (id[k] < 0) continue;
+                        const float t = r.c.t(l[k]);
+                        float w = Scale::rough(t);
+                        if (w < min_p) continue;
+                        sum += w;
+                        if (!(w > bound * (1.f - e[k]))) continue;
+                        w = r.c.weight(l[k]);
+                        const float y = __fdividef(w, -logf(e[k]));
+                        if (y > won || (y == won && id[k] < who)) won = y, won_w = w, who = id[k];
+                    }
+                    mass += mass_of(sum);
+                    if (won * 0.999f > bound) atomicMax(reinterpret_cast<int *>(&s.bound), __float_as_int(won * 0.999f));
+                }
                 const u64 key = who >= 0 ? argmax_key(won, uint32_t(who)) : 0, high = block_max(s, key);
                 if (key && key == high) s.ex[2].w = won_w;
                 mass = block_sum(s, mass);
                 if (tid == 0) s.ex[2].best = high, s.ex[2].z = mass;
                 cl.sync();
-                u64 win = 0;
-                float ww = 0.f;
-                for (int i = 0; i < a.split; ++i) {
-                    const Exchange *x = cl.map_shared_rank(&s.ex[2], i);
-                    z += x->z;
-                    if (x->best > win) win = x->best, ww = x->w;
-                }
+                const Exchange y = told(s.ex[2], a.split);
+                z = warp_sum64(y.z);
+                const u64 win = warp_max_u64(y.best);
+                const float ww = __shfl_sync(0xffffffffu, y.w, __ffs(__ballot_sync(0xffffffffu, y.best == win)) - 1);
                 token = argmax_key_index(win);
                 prob = ww / (float(z) * (1.f / kUnit));
             }
@@ -658,8 +856,8 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
 template <typename T>
 cudaError_t run(const SampleArgs &a, int rows, cudaStream_t s)
 {
-    const size_t smem = (size_t(a.per) * sizeof(T) + 15) / 16 * 16;
-    cudaError_t e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShareBytes);
+    const size_t smem = (size_t(a.per) * sizeof(T) + 15) / 16 * 16 + 16;
+    cudaError_t e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShareBytes + 32);
     if (e == cudaSuccess && a.split > 8)
         e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -687,13 +885,16 @@ extern "C" int gpt2_op_sample(const void *logits, int32_t dtype, int64_t row_str
     const int sms = spec_sms(&rc);
     if (!sms) return rc;
     SampleArgs a{logits, temperature, top_p, min_p, u, top_k, token, prob, dist, row_stride, vocab, 0, 1};
-    // as many CTAs as a share needs; more while every row's cluster runs at once and a
-    // share has 2048 ids or more
+    // As many CTAs as a share needs, and twice as many while every row's cluster still
+    // runs at once and a share has 2048 ids or more; for more rows than that, enough for
+    // two CTAs of an SM, so that one computes while the other loads.
     int split = 1;
     auto per = [&](int n) { return (vocab + n - 1) / n; };
-    while ((long long)per(split) * size > kShareBytes) split *= 2;
-    for (int i = 0; i < 4; ++i)
-        if (split == 1 << i && vocab >= 4096 * split && n_rows <= kClustersFit[i]) split *= 2;
+    auto held = [&](int n) { return (long long)per(n) * size + int(sizeof(Shared)) <= 112 * 1024 ? 2 : 1; };
+    while ((long long)per(split) * size > kShareBytes || per(split) > kShareIds) split *= 2;
+    for (int i = 0; i < 3; ++i)          // (16: one row 12.4 us instead of 10.6, eight rows 17.9 instead of 10.8)
+        if (split == 1 << i && vocab >= 4096 * split && (n_rows <= kClustersFit[i] * held(2 * split) || held(split) < 2))
+            split *= 2;
     a.split = split;
     a.per = per(split);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
