@@ -184,11 +184,30 @@ __device__ __forceinline__ void fetch(uint32_t *r, const uint8_t *p)
     }
 }
 
-// Stages of a warp's ring of tiles of `bytes` (keys and values).
-constexpr int stages_for(int bytes, int ctas)
+// The shape of the rings, for r query heads of a tile, cache elements of `size` bytes
+// and rows of `row` bytes.  The copies pass through L1, which takes what shared memory
+// leaves: a ring that is too large costs more than its depth gives.  Measured, us:
+//   8-bit codes, whose conversion takes the most instructions per byte: 4 CTAs of an SM
+//     with 2 stages of 4 KB 52.7, 4 stages with 3 CTAs 67.7, 3 with 4 66 (32 requests of
+//     3,000 to 8,000 int8 rows of 64); rows of 128: 64.7, stages of 8 KB with 3 CTAs 83
+//   16-bit and fp32 rows: 3 CTAs with 2 stages of 8 KB 92, with 4 of 4 KB 94.5, 2 CTAs 101
+//     (64 requests of 2,000 to 4,000 bf16 rows of 64); 4 CTAs with 3 of 4 KB 116
+//   the matrix instructions, 128 dimensions: 2 CTAs with 3 stages 54, with 2 55, 3 with 2
+//     58 (bf16); over int8 2 stages 35, 3 41
+constexpr int tile_rows(int r, int size, int row)        // cache rows of a tile, at most 32
 {
-    const int n = (ctas == 2 ? 24 : 16) * 1024 / bytes;
-    return n < 2 ? 2 : n > 6 ? 6 : n;
+    const int n = (r == 1 && size == 1 ? 2048 : 4096) / row;
+    return n > 32 ? 32 : n;
+}
+constexpr int ring_ctas(int r, int size, int row)        // CTAs of an SM
+{
+    return r == 8 ? (row / size == 128 ? 2 : 3) : r == 1 && size == 1 ? 4 : r <= 2 ? 3 : 2;
+}
+constexpr int ring_stages(int r, int size, int row)
+{
+    if (size == 1) return 2;
+    const int n = (ring_ctas(r, size, row) == 2 ? 24 : 16) * 1024 / (2 * tile_rows(r, size, row) * row);
+    return n > 6 ? 6 : n;
 }
 
 // Lets a kernel use so much dynamic shared memory (once per device and kernel).

@@ -41,25 +41,13 @@ int tile_heads(int q_dtype, int group)
     return q_dtype == GPT2_F32 ? 4 : 8;
 }
 
-// CTAs that an SM holds of the kernel for these tiles.
-int resident(const gpt2_kv &kv, int r)
-{
-    return r == 4 || (r == 8 && kv.head_dim == 128) ? 2 : 3;
-}
-
-// Cache rows of a tile, as the kernels have them.
-int tile_rows(const gpt2_kv &kv)
-{
-    const int n = 4096 / (kv.head_dim * elem_size(kv.dtype));
-    return n > 32 ? 32 : n;
-}
-
 struct Layout {
     int warps;
     size_t heads, ml, total;          // bytes: of the heads, of (m, l), of everything
     Layout(const gpt2_kv &kv, int r, int sms)
     {
-        warps = sms * resident(kv, r) * tree::kNW;
+        const int size = elem_size(kv.dtype);
+        warps = sms * ring_ctas(r, size, kv.head_dim * size) * tree::kNW;
         heads = size_t(warps) * sizeof(int4);
         ml = (size_t(warps) * 2 * r * sizeof(float2) + 15) / 16 * 16;
         total = heads + ml + size_t(warps) * 2 * r * kv.head_dim * sizeof(float);
@@ -123,7 +111,7 @@ extern "C" int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t
     a.group = n_head / kv->n_head;
     const int r = paged::tile_heads(q_dtype, a.group);
     a.row_tiles = (a.group + r - 1) / r;
-    const int ks = paged::tile_rows(*kv);
+    const int size = elem_size(kv->dtype), ks = paged::tile_rows(r, size, kv->head_dim * size);
     const double tiles = double(n_rows) * kv->n_head * a.row_tiles * double((longest + ks - 1) / ks);
     if (tiles >= 4.0e9) return GPT2_ERR_INVALID_ARG;
     if (n_rows == 0) return GPT2_OK;

@@ -21,9 +21,6 @@ namespace {
 
 constexpr float kSlack = 8.f;
 
-// CTAs of an SM.
-constexpr int few_ctas(int r) { return r <= 2 ? 3 : 2; }
-
 template <int KIND, int D, int R>
 struct Few {
     static constexpr int kES = KIND == GPT2_F32 ? 4 : KIND == GPT2_INT8 || KIND == GPT2_E4M3 ? 1 : 2;
@@ -34,18 +31,18 @@ struct Few {
     static constexpr int P = kPieces / LPR;                          // 16-byte pieces of a lane: c, c + LPR, ..
     static constexpr int EP = 16 / kES, E = P * EP;                  // elements of a piece, of a lane
     static constexpr int RPL = 32 / LPR;                             // rows that a warp holds side by side
-    static constexpr int KS = 4096 / kRowB > 32 ? 32 : 4096 / kRowB; // rows of a tile: 32, or 4 KB
+    static constexpr int KS = tile_rows(R, kES, kRowB);              // rows of a tile
     static constexpr int T = KS / RPL < 1 ? 1 : KS / RPL;            // of which a lane has this many
     static constexpr int kSplit = LPR < T ? LPR : T;                 // lanes that a row's T scores are spread over
     static constexpr int NV = T / kSplit, kSame = LPR / kSplit;      // scores of a lane; lanes with the same ones
     static constexpr int kBytes = 2 * T * P * 512;                   // keys and values of a tile
     static constexpr int kStage = kBytes + (kScaled ? 256 : 0);      // and their scales
-    static constexpr int S = stages_for(kBytes, few_ctas(R));
+    static constexpr int kCtas = ring_ctas(R, kES, kRowB), S = ring_stages(R, kES, kRowB);
     static constexpr size_t kSmem = size_t(kNW) * S * kStage;
 };
 
 template <int KIND, int D, int R>
-__global__ void __launch_bounds__(kThreads, few_ctas(R)) k_paged_few(const __grid_constant__ PagedArgs a)
+__global__ void __launch_bounds__(kThreads, Few<KIND, D, R>::kCtas) k_paged_few(const __grid_constant__ PagedArgs a)
 {
     using F = Few<KIND, D, R>;
     constexpr int E = F::E, EP = F::EP, P = F::P, T = F::T, NV = F::NV, KS = F::KS, LPR = F::LPR, RPL = F::RPL, S = F::S;

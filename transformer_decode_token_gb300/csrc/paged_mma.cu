@@ -42,24 +42,21 @@ struct Shape {
     static constexpr int kKLd = kRowB / 4 < 16 ? kRowB / 4 : 16, kNK = kRowB / (4 * kKLd);
     static constexpr int kVLd = kRowB / 8 < 16 ? kRowB / 8 : 16, kNV = kRowB / (8 * kVLd);
     static constexpr int kEK = kKLd / kES, kEV = kVLd / kES;   // elements of an access
-    static constexpr int KS = 4096 / kRowB > 32 ? 32 : 4096 / kRowB;
+    static constexpr int KS = tile_rows(8, kES, kRowB);
     static constexpr int kT8 = KS / 8, kSteps = D / 16, kNT = D / 8;
 };
-
-// CTAs of an SM.
-constexpr int mma_ctas(int D) { return D == 128 ? 2 : 3; }
 
 template <int KIND, int D>
 struct MmaRing {
     using S = Shape<KIND, D>;
     static constexpr int kKeys = S::KS * S::kRowB;
     static constexpr int kStage = 2 * kKeys + (S::kScaled ? 256 : 0);
-    static constexpr int kStages = stages_for(2 * kKeys, mma_ctas(D));
+    static constexpr int kCtas = ring_ctas(8, S::kES, S::kRowB), kStages = ring_stages(8, S::kES, S::kRowB);
     static constexpr size_t kSmem = size_t(kNW) * kStages * kStage;
 };
 
 template <int KIND, int D, bool QF16>
-__global__ void __launch_bounds__(kThreads, mma_ctas(D)) k_paged_mma(const __grid_constant__ PagedArgs a)
+__global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma(const __grid_constant__ PagedArgs a)
 {
     using S = Shape<KIND, D>;
     using G = MmaRing<KIND, D>;
