@@ -420,7 +420,19 @@ int gpt2_prefill_batch(gpt2_batch *m, const int32_t *ids, const int32_t *lens, i
  * POSITION_RANGE (a sequence would pass n_positions), INVALID_ARG. */
 int gpt2_decode_batch_greedy(gpt2_batch *m, int32_t n_steps);
 
-/* The greedy choice of the last step for sequences 0..n-1 (synchronises); after
+/* Draws the next tokens of sequences 0..n-1 from the logits of their last step (or
+ * prompt), with settings and random numbers of their own: gpt2_op_sample on the rows
+ * (DEVICE arrays [n], u [n][vocab_size], ready on the model's stream; NULL where that
+ * allows it).  host_ids [n] receives the tokens; they are then the sequences' choices,
+ * for gpt2_argmax_batch, gpt2_batch_ids and the next gpt2_decode_batch_greedy.  A sequence that
+ * took no part in the last step, or whose nodes the last tree step ran, keeps what it has
+ * and gets -1.  Synchronises.  Errors: NOT_READY (no such sequence among them), INVALID_ARG,
+ * DEVICE_STATE (logits without a choice: -1, and that sequence has none), CUDA. */
+int gpt2_sample_batch(gpt2_batch *m, int32_t n, const float *temperature, const int32_t *top_k, const float *top_p,
+                      const float *min_p, const float *u, int32_t *host_ids);
+
+/* The greedy choice of the last step for sequences 0..n-1 (synchronises), or the
+ * drawn one (gpt2_sample_batch); after
  * gpt2_accept_tree_batch its next tokens, -1 where it left none.  A tree step
  * makes no choice.  NOT_READY before the first. */
 int gpt2_argmax_batch(gpt2_batch *m, int32_t *host_ids, int32_t n);

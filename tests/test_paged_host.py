@@ -90,3 +90,9 @@ def test_constants_are_the_header_s():
     header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gpt2.h")).read()
     assert int(re.search(r"GPT2_MAX_PAGED_SEQS (\d+)", header).group(1)) == binding.MAX_PAGED_SEQS
     assert int(re.search(r"GPT2_SAMPLE_MAX_VOCAB (\d+)", header).group(1)) == binding.SAMPLE_MAX_VOCAB
+
+
+def test_sampling_of_a_model_is_refused_on_the_host():
+    L = binding.lib()
+    one = (ctypes.c_int32 * 1)(1)
+    assert L.gpt2_sample_batch(None, 1, None, None, None, None, None, one) == -1

@@ -35,7 +35,7 @@ EXPORTED = ("gpt2_create", "gpt2_create_ex", "gpt2_path", "gpt2_launch_count", "
             "gpt2_op_linear_bf16", "gpt2_op_kv_store", "gpt2_op_kv_load", "gpt2_op_kv_commit",
             "gpt2_op_tree_attention_workspace", "gpt2_op_tree_attention", "gpt2_op_verify_tree_workspace", "gpt2_op_verify_tree", "gpt2_decode_tree_batch",
             "gpt2_accept_tree_batch", "gpt2_op_page_map", "gpt2_op_paged_attention_workspace", "gpt2_op_paged_attention",
-            "gpt2_op_sample", "gpt2_strerror")
+            "gpt2_op_sample", "gpt2_sample_batch", "gpt2_strerror")
 
 
 class GPT2Error(RuntimeError):
@@ -168,6 +168,7 @@ def lib(build_if_stale: bool = True, path: str = None):
             L.gpt2_op_paged_attention.argtypes = [kv, vp, i32, i64, i32, vp, i32, i32, vp, vp, i32, f32, vp, i64, vp, sz,
                                                   vp]
             L.gpt2_op_sample.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.gpt2_sample_batch.argtypes = [vp, i32, vp, vp, vp, vp, vp, pi32]
             L.gpt2_strerror.argtypes = [ctypes.c_int]
             L.gpt2_strerror.restype = ctypes.c_char_p
             for n in EXPORTED:
@@ -470,11 +471,7 @@ class BatchModel:
                                   t.device != self._device):
                 raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on {self._device}")
         if draft_probs is not None or u_accept is not None or u_draw is not None:
-            now = torch.cuda.current_stream(self._device)
-            if now.cuda_stream != self._stream:      # the model's stream waits for what makes them
-                own = torch.cuda.ExternalStream(self._stream, self._device) if self._stream else \
-                    torch.cuda.default_stream(self._device)
-                own.wait_stream(now)
+            self._wait_for_tensors()
         out, op = _i32(np.zeros((n, MAX_NODES)))
         got, gp = _i32(np.zeros(n))
         status = lib().gpt2_accept_tree_batch(self._h, float(temperature), _ptr(draft_probs), _ptr(u_accept),
@@ -486,6 +483,44 @@ class BatchModel:
             raise e
         check(status, "gpt2_accept_tree_batch")
         return tokens
+
+    def _wait_for_tensors(self):
+        """The model's stream waits for what the current stream is making."""
+        import torch
+        now = torch.cuda.current_stream(self._device)
+        if now.cuda_stream != self._stream:
+            own = torch.cuda.ExternalStream(self._stream, self._device) if self._stream else \
+                torch.cuda.default_stream(self._device)
+            own.wait_stream(now)
+
+    def sample(self, n: int, temperature=None, u=None, top_k=None, top_p=None, min_p=None) -> list:
+        """Draws the next tokens of sequences 0..n-1 from their last step's
+        logits, by settings of their own ([n] tensors on the model's device,
+        made on the current stream or ready: top_k int32, the others fp32) and
+        uniform numbers u [n][vocab], as op_sample; see gpt2_sample_batch.
+        Returns the ids, -1 for a sequence that took no part in that step.  Where some
+        sequence's logits leave no choice, the GPT2Error (DEVICE_STATE) has
+        them as `tokens`."""
+        import torch
+        n, V = int(n), self.cfg.vocab_size
+        given = [(name, t, shape, dtype) for name, t, shape, dtype in
+                 (("temperature", temperature, (n,), torch.float32), ("u", u, (n, V), torch.float32),
+                  ("top_k", top_k, (n,), torch.int32), ("top_p", top_p, (n,), torch.float32),
+                  ("min_p", min_p, (n,), torch.float32)) if t is not None]
+        for name, t, shape, dtype in given:
+            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self._device:
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self._device}")
+        if given:
+            self._wait_for_tensors()
+        out, op = _i32(np.zeros(max(n, 0)))
+        status = lib().gpt2_sample_batch(self._h, n, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
+                                         op)
+        if STATUS.get(status) == "DEVICE_STATE":
+            e = GPT2Error(status, "gpt2_sample_batch")
+            e.tokens = out.tolist()
+            raise e
+        check(status, "gpt2_sample_batch")
+        return out.tolist()
 
     def argmax(self, n: int) -> list:
         out = np.zeros(n, np.int32)

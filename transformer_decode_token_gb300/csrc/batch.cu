@@ -499,6 +499,19 @@ __global__ void k_b_set_next(int32_t *next_tok, const int32_t *next, const int32
     if (b < n && n_path[b] > 0) next_tok[b] = next[b];
 }
 
+// The tokens drawn for sequences after the rows at[b] (-1: not this one): their next
+// tokens (-1: no choice), and the ids of those positions.
+struct DrawnAt {
+    int32_t at[kTcMaxRows];
+};
+__global__ void k_b_set_drawn(int32_t *next_tok, int32_t *out_ids, const int32_t *drawn, const DrawnAt d, int rows)
+{
+    const int b = threadIdx.x;
+    if (b >= rows || d.at[b] < 0) return;
+    next_tok[b] = drawn[b];
+    out_ids[size_t(d.at[b]) * rows + b] = drawn[b];
+}
+
 struct BArgmaxArgs {
     const float *logits;            // [rows][V]
     int32_t V, rows, P;
@@ -677,6 +690,7 @@ struct gpt2_batch {
     } tree;
     std::vector<int> cached;        // host view: cached length of each sequence
     std::vector<uint8_t> choice;    // host view: next_tok holds the sequence's choice at its cached length
+    std::vector<uint8_t> in_step;   // host view: the logits hold the sequence's last row's
     bool has_step = false;          // there are logits
     bool has_choice = false;        // next_tok has been written
     unsigned long long launches = 0;
@@ -1128,6 +1142,7 @@ int engine_build(gpt2_batch *m, const gpt2_config &cfg, const EngineSrc &src, cu
     m->num_sms = sms;
     m->cached.assign(src.rows, 0);
     m->choice.assign(src.rows, 0);
+    m->in_step.assign(src.rows, 0);
     const int mat_in[4] = {E, E, E, F}, mat_out[4] = {3 * E, E, F, E};
     const int pl = src.planes;
     // rows of one plane: a multiple of the tile height when there are two
@@ -1487,6 +1502,7 @@ int gpt2_decode_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *posit
     BTRY(cudaGraphLaunch(m->exec, m->stream));
     m->launches += m->kernels_per_step;
     m->tree.h_first.clear();                       // a tree step's nodes, if any, are gone
+    for (int b = 0; b < m->max_batch; ++b) m->in_step[b] = p[b] >= 0;
     for (int b = 0; b < n; ++b)
         if (p[b] >= 0) m->cached[b] = p[b] + 1, m->choice[b] = 1;
     m->has_step = m->has_choice = true;
@@ -1506,6 +1522,7 @@ int gpt2_prefill_batch(gpt2_batch *m, const int32_t *ids, const int32_t *lens, i
         if (ids[i] < 0 || ids[i] >= m->cfg.vocab_size) return GPT2_ERR_TOKEN_RANGE;
     std::fill(m->cached.begin(), m->cached.end(), 0);
     std::fill(m->choice.begin(), m->choice.end(), 0);
+    std::fill(m->in_step.begin(), m->in_step.end(), 0);
     m->tree.h_first.clear();
     std::vector<size_t> start(n, 0);
     for (int b = 1; b < n; ++b) start[b] = start[b - 1] + size_t(lens[b - 1]);
@@ -1597,9 +1614,44 @@ int gpt2_decode_batch_greedy(gpt2_batch *m, int32_t n_steps)
     BTRY(cudaMemcpyAsync(m->tok, m->next_tok, size_t(kTcMaxRows) * 4, cudaMemcpyDeviceToDevice, m->stream));
     for (int i = 0; i < n_steps; ++i) BTRY(cudaGraphLaunch(m->exec, m->stream));
     m->launches += (unsigned long long)n_steps * m->kernels_per_step;
-    for (int b = 0; b < m->max_batch; ++b)
+    for (int b = 0; b < m->max_batch; ++b) {
+        m->in_step[b] = m->cached[b] > 0;
         if (m->cached[b] > 0) m->cached[b] += n_steps;
+    }
     return GPT2_OK;
+}
+
+int gpt2_sample_batch(gpt2_batch *m, int32_t n, const float *temperature, const int32_t *top_k, const float *top_p,
+                      const float *min_p, const float *u, int32_t *host_ids)
+{
+    if (!m || !host_ids || n < 1 || n > m->max_batch) return GPT2_ERR_INVALID_ARG;
+    DrawnAt d;
+    bool any = false;
+    for (int b = 0; b < kTcMaxRows; ++b) {
+        d.at[b] = b < n && m->in_step[b] ? m->cached[b] - 1 : -1;
+        any = any || d.at[b] >= 0;
+    }
+    if (!any) return GPT2_ERR_NOT_READY;
+    // (the next step's tokens are written when it begins: their place is free)
+    int rc = gpt2_op_sample(m->logits, GPT2_F32, m->cfg.vocab_size, n, m->cfg.vocab_size, temperature, top_k, top_p,
+                            min_p, u, m->tok, nullptr, nullptr, m->stream);
+    if (rc != GPT2_OK) return rc;
+    for (int b = 0; b < n; ++b)                    // (until the new ones are known)
+        if (d.at[b] >= 0) m->choice[b] = 0;
+    k_b_set_drawn<<<1, kTcMaxRows, 0, m->stream>>>(m->next_tok, m->out_ids, m->tok, d, m->max_batch);
+    BTRY(cudaGetLastError());
+    m->launches += 2;
+    std::vector<int32_t> drawn(n);
+    BTRY(cudaMemcpyAsync(drawn.data(), m->tok, size_t(n) * 4, cudaMemcpyDeviceToHost, m->stream));
+    rc = read_batch_state(m);
+    if (rc != GPT2_OK) return rc;
+    for (int b = 0; b < n; ++b) {
+        host_ids[b] = d.at[b] >= 0 ? drawn[b] : -1;
+        if (d.at[b] < 0) continue;
+        m->choice[b] = drawn[b] >= 0;
+        if (drawn[b] < 0) rc = GPT2_ERR_DEVICE_STATE;
+    }
+    return rc;
 }
 
 int gpt2_decode_tree_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *parents, const int32_t *n_nodes,
@@ -1652,6 +1704,7 @@ int gpt2_decode_tree_batch(gpt2_batch *m, const int32_t *tokens, const int32_t *
     BTRY(cudaGraphLaunch(tr.exec[k], m->stream));
     m->launches += tr.kernels;
     m->has_step = true;
+    std::fill(m->in_step.begin(), m->in_step.end(), 0);
     tr.h_first.assign(first.begin(), first.begin() + n + 1);
     tr.h_tokens.assign(t.begin(), t.begin() + r);
     if (dev_logits) *dev_logits = m->logits;
