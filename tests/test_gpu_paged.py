@@ -231,7 +231,7 @@ def run_paged(rng, qt, ct, D, K, G, bs, position, seq=None, lens=None, scale=Non
 
 @pytest.mark.parametrize("D", DIMS)
 @pytest.mark.parametrize("qt,ct", COMBOS)
-@pytest.mark.parametrize("G", [1, 2, 3, 8])
+@pytest.mark.parametrize("G", [1, 2, 3, 8, 12])
 def test_paged_attention_types(qt, ct, D, G):
     """Every type, head size and kernel: lengths around the tiles and pages, a
     row that sees nothing."""
@@ -251,7 +251,7 @@ def test_groups_of_heads(qt, ct, G):
 
 
 @pytest.mark.parametrize("qt,ct,G", [("f32", "f32", 1), ("f32", "bf16", 1), ("f32", "int8", 2), ("bf16", "bf16", 8),
-                                     ("f16", "int8", 4)])
+                                     ("f16", "int8", 4), ("bf16", "bf16", 16), ("f16", "e4m3", 11)])
 @pytest.mark.parametrize("position", [[9000], [4500, -1, 3], [700] * 150, list(range(-1, 260, 3))])
 def test_splits(qt, ct, G, position):
     """One long row cut into many parts, rows shorter than a share, equal rows,
@@ -280,7 +280,7 @@ def test_scales(scale, G):
 
 
 @pytest.mark.parametrize("qt,ct", COMBOS)
-@pytest.mark.parametrize("G", [1, 4])
+@pytest.mark.parametrize("G", [1, 4, 12])
 def test_what_is_not_seen_does_not_enter(qt, ct, G):
     """NaN everywhere but in the rows that are seen (behind the last position in its
     page, in other pages): codes of 8-bit caches by their scales.  Blocks outside
@@ -310,7 +310,7 @@ def test_what_is_not_seen_does_not_enter(qt, ct, G):
 
 @pytest.mark.parametrize("qt,ct", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("f16", "f16"), ("bf16", "int8"),
                                    ("f16", "e4m3")])
-@pytest.mark.parametrize("G", [1, 4])
+@pytest.mark.parametrize("G", [1, 4, 12])
 @pytest.mark.parametrize("n", [20, 3000])
 def test_infinities_that_are_seen(qt, ct, G, n):
     """An infinite value gives an infinity in its dimension (in both: a NaN) and

@@ -40,8 +40,8 @@ struct PagedArgs {
 cudaError_t paged_few_f32(const PagedArgs &a, int r, int ctas, cudaStream_t s);
 cudaError_t paged_few_16(const PagedArgs &a, int r, int ctas, cudaStream_t s);
 cudaError_t paged_few_8(const PagedArgs &a, int r, int ctas, cudaStream_t s);
-// 8 query heads of a tile, on the matrix instructions (16-bit rows)
-cudaError_t paged_mma(const PagedArgs &a, int ctas, cudaStream_t s);
+// R: 8 or 16 query heads of a tile, on the matrix instructions (16-bit rows)
+cudaError_t paged_mma(const PagedArgs &a, int r, int ctas, cudaStream_t s);
 // the second kernel
 cudaError_t paged_join(const PagedArgs &a, int r, cudaStream_t s);
 
@@ -201,7 +201,7 @@ constexpr int tile_rows(int r, int size, int row)        // cache rows of a tile
 }
 constexpr int ring_ctas(int r, int size, int row)        // CTAs of an SM
 {
-    return r == 8 ? (row / size == 128 ? 2 : 3) : r == 1 && size == 1 ? 4 : r <= 2 ? 3 : 2;
+    return r >= 8 ? (row / size == 128 ? 2 : 3) : r == 1 && size == 1 ? 4 : r <= 2 ? 3 : 2;
 }
 constexpr int ring_stages(int r, int size, int row)
 {

@@ -34,11 +34,22 @@ cudaError_t join_dims(const PagedArgs &a, cudaStream_t s)
     }
 }
 
-// Query heads of a tile: 1, 2 or 4 on the CUDA cores, 8 on the matrix instructions.
+template <int R>
+cudaError_t join_kinds(const PagedArgs &a, cudaStream_t s)
+{
+    switch (a.kv.dtype) {
+    case GPT2_F16: return join_dims<GPT2_F16, R>(a, s);
+    case GPT2_BF16: return join_dims<GPT2_BF16, R>(a, s);
+    case GPT2_INT8: return join_dims<GPT2_INT8, R>(a, s);
+    default: return join_dims<GPT2_E4M3, R>(a, s);
+    }
+}
+
+// Query heads of a tile: 1, 2 or 4 on the CUDA cores, 8 or 16 on the matrix instructions.
 int tile_heads(int q_dtype, int group)
 {
     if (group <= 2) return group;
-    return q_dtype == GPT2_F32 ? 4 : 8;
+    return q_dtype == GPT2_F32 ? 4 : group <= 8 ? 8 : 16;
 }
 
 struct Layout {
@@ -71,13 +82,8 @@ cudaError_t paged_join(const PagedArgs &a, int r, cudaStream_t s)
     case 1: return paged::join_dims<-1, 1>(a, s);
     case 2: return paged::join_dims<-1, 2>(a, s);
     case 4: return paged::join_dims<-1, 4>(a, s);
-    default: break;
-    }
-    switch (a.kv.dtype) {
-    case GPT2_F16: return paged::join_dims<GPT2_F16, 8>(a, s);
-    case GPT2_BF16: return paged::join_dims<GPT2_BF16, 8>(a, s);
-    case GPT2_INT8: return paged::join_dims<GPT2_INT8, 8>(a, s);
-    default: return paged::join_dims<GPT2_E4M3, 8>(a, s);
+    case 8: return paged::join_kinds<8>(a, s);
+    default: return paged::join_kinds<16>(a, s);
     }
 }
 
@@ -140,7 +146,7 @@ extern "C" int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int ctas = at.warps / tree::kNW;
-    if (r == 8) rc = spec_rc(paged_mma(a, ctas, s));
+    if (r >= 8) rc = spec_rc(paged_mma(a, r, ctas, s));
     else if (kv->dtype == GPT2_F32) rc = spec_rc(paged_few_f32(a, r, ctas, s));
     else if (is_scaled(kv->dtype)) rc = spec_rc(paged_few_8(a, r, ctas, s));
     else rc = spec_rc(paged_few_16(a, r, ctas, s));

@@ -1,11 +1,12 @@
 // Attention over a paged cache on the matrix instructions, for 16-bit rows and
 // three or more query heads on a cache head, over the list of paged.cuh.
 //
-// The 16 rows of an instruction's A side are the 8 query heads of a tile twice: the
-// upper half takes the second part of what the lower half is the first part of
-// (the weights p = hi + lo, and fp16 queries over 8-bit caches, whose codes are
-// exact in bf16), so that both parts cost one instruction and meet in one thread,
-// which adds the two halves of the accumulators.  Cache rows reach the operand
+// The weights meet the values in two parts, p = hi + lo, and so do fp16 queries the
+// keys of 8-bit caches, whose codes are exact in bf16.  For up to 8 query heads the
+// 16 rows of an instruction's A side are the heads twice (HALVES = 1): the upper half
+// takes the second part of what the lower half is the first part of, so that both parts
+// cost one instruction and meet in one thread, which adds the two halves of the
+// accumulators.  For up to 16 heads (HALVES = 2) each part has its own instruction.  Cache rows reach the operand
 // registers in the order of tree_attn.cuh: keys by 16-byte pieces c, c + 4, ..,
 // values by pieces g, g + 8, .. of the rows whose weights the thread holds.
 #include "paged.cuh"
@@ -55,12 +56,13 @@ struct MmaRing {
     static constexpr size_t kSmem = size_t(kNW) * kStages * kStage;
 };
 
-template <int KIND, int D, bool QF16>
+template <int KIND, int D, bool QF16, int HALVES>
 __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma(const __grid_constant__ PagedArgs a)
 {
     using S = Shape<KIND, D>;
     using G = MmaRing<KIND, D>;
-    constexpr int R = 8, KS = S::KS, T8 = S::kT8, N = G::kStages;
+    constexpr int R = 8 * HALVES, KS = S::KS, T8 = S::kT8, N = G::kStages;
+    constexpr float kRaise = S::kHalf ? 2.f : 8.f;
     constexpr bool kBf = !S::kHalf, kTwo = S::kScaled && QF16;   // (queries in two parts)
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
     extern __shared__ __align__(16) uint8_t dyn[];
@@ -115,37 +117,41 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
         for (int i = 0; i + 1 < N; ++i) there[i] = there[i + 1];
         there[N - 1] = yes;
     };
-    uint32_t qa[S::kSteps][kTwo ? 4 : 2];
-    float o[S::kNT][4], m = 0.f, l = 0.f;                // m, l: of query head g
+    // the queries' operands: part 0, and 1 where there are two, of heads g and g + 8
+    uint32_t qa[S::kSteps][kTwo ? 2 : 1][HALVES][2];
+    float o[S::kNT][4], m[HALVES], l[HALVES];            // m, l: of query heads g and g + 8
     int heads = 0;
     uint32_t from = 0;
     auto begin_unit = [&]() {
         heads = heads_of<R>(a, at.unit);
         from = at.tile;
-        const uint16_t *q = static_cast<const uint16_t *>(a.q) + row_at<D, R>(a, at.row, at.unit, a.q_stride) +
-                            size_t(g < heads ? g : 0) * D;
 #pragma unroll
-        for (int s = 0; s < S::kSteps; ++s) {
-            constexpr int kPer = S::kEK / 4;             // steps of an access
-            const uint2 v = *reinterpret_cast<const uint2 *>(q + (s / kPer * 4 + c) * S::kEK + s % kPer * 4);
-            if constexpr (kTwo) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-                uint32_t p[2];
-                split16<kBf16, 2>(x.x, x.y, p);
-                qa[s][0] = p[0], qa[s][1] = p[1];
-                split16<kBf16, 2>(y.x, y.y, p);
-                qa[s][2] = p[0], qa[s][3] = p[1];
-            } else {
-                qa[s][0] = v.x, qa[s][1] = v.y;
+        for (int h = 0; h < HALVES; ++h) {
+            const uint16_t *q = static_cast<const uint16_t *>(a.q) + row_at<D, R>(a, at.row, at.unit, a.q_stride) +
+                                size_t(g + 8 * h < heads ? g + 8 * h : 0) * D;
+#pragma unroll
+            for (int s = 0; s < S::kSteps; ++s) {
+                constexpr int kPer = S::kEK / 4;         // steps of an access
+                const uint2 v = *reinterpret_cast<const uint2 *>(q + (s / kPer * 4 + c) * S::kEK + s % kPer * 4);
+                if constexpr (kTwo) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+                    uint32_t p[2];
+                    split16<kBf16, 2>(x.x, x.y, p);
+                    qa[s][0][h][0] = p[0], qa[s][1][h][0] = p[1];
+                    split16<kBf16, 2>(y.x, y.y, p);
+                    qa[s][0][h][1] = p[0], qa[s][1][h][1] = p[1];
+                } else {
+                    qa[s][0][h][0] = v.x, qa[s][0][h][1] = v.y;
+                }
             }
+            m[h] = -INFINITY;
+            l[h] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < S::kNT; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-        m = -INFINITY;
-        l = 0.f;
     };
 #pragma unroll
     for (int i = 0; i < N; ++i) there[i] = 0;
@@ -184,54 +190,79 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
                     b0 = kr[2 * k];
                     b1 = kr[2 * k + 1];
                 }
-                const uint32_t A[4] = {qa[k][0], kTwo ? qa[k][1] : 0u, kTwo ? qa[k][2] : qa[k][1], kTwo ? qa[k][3] : 0u};
-                mma16816(s[t], A, b0, b1, kBf);
+                if constexpr (HALVES == 1) {
+                    const uint32_t A[4] = {qa[k][0][0][0], kTwo ? qa[k][kTwo][0][0] : 0u, qa[k][0][0][1],
+                                           kTwo ? qa[k][kTwo][0][1] : 0u};
+                    mma16816(s[t], A, b0, b1, kBf);
+                } else {
+#pragma unroll
+                    for (int p = 0; p <= int(kTwo); ++p) {
+                        const uint32_t A[4] = {qa[k][p][0][0], qa[k][p][HALVES - 1][0], qa[k][p][0][1], qa[k][p][HALVES - 1][1]};
+                        mma16816(s[t], A, b0, b1, kBf);
+                    }
+                }
             }
         }
-        float top = -INFINITY;
+        bool above = false;
 #pragma unroll
         for (int t = 0; t < T8; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int key = t * 8 + 2 * c + i;
-                float y = (kTwo ? s[t][i] + s[t][i + 2] : s[t][i]) * a.scale_log2;
-                if constexpr (S::kScaled) y *= __uint_as_float(__shfl_sync(0xffffffffu, ks, key));
-                if (got != kAll && !(got >> key & 1)) y = -INFINITY;
-                s[t][i] = y;
-                top = fmaxf(top, y);
+                const float f = S::kScaled ? a.scale_log2 * __uint_as_float(__shfl_sync(0xffffffffu, ks, key)) : a.scale_log2;
+                const bool no = got != kAll && !(got >> key & 1);
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    float y = (HALVES == 1 && kTwo ? s[t][i] + s[t][i + 2] : s[t][i + 2 * h]) * f;
+                    if (no) y = -INFINITY;
+                    s[t][i + 2 * h] = y;
+                    above = above || y > m[h] + kRaise;
+                }
             }
         // (the maximum is raised only when a score passes it by more than fp16's weights,
         // 2^13 of the largest, or fp32's sums have room for)
-        if (__any_sync(0xffffffffu, top > m + (S::kHalf ? 2.f : 8.f))) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            top = fmaxf(top, m);
-            const float keep = exp2_approx(m - (top == -INFINITY ? 0.f : top));
-            m = top;
-            l *= keep;
+        if (__any_sync(0xffffffffu, above)) {
+            float keep[HALVES];
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                float top = m[h];
+#pragma unroll
+                for (int t = 0; t < T8; ++t) top = fmaxf(top, fmaxf(s[t][2 * h], s[t][2 * h + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                keep[h] = exp2_approx(m[h] - (top == -INFINITY ? 0.f : top));
+                m[h] = top;
+                l[h] *= keep[h];
+            }
 #pragma unroll
             for (int j = 0; j < S::kNT; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[j][i] *= keep;
+                for (int i = 0; i < 4; ++i) o[j][i] *= keep[i / 2 % HALVES];
         }
-        const float safe = m == -INFINITY ? 0.f : m;
-        uint32_t hi[T8], lo[T8];                         // weights of keys 2c, 2c + 1 of each eight, in two parts
+        uint32_t hi[T8][HALVES], lo[T8][HALVES];         // weights of keys 2c, 2c + 1 of each eight, in two parts
 #pragma unroll
         for (int t = 0; t < T8; ++t) {
-            float p[2];
+            float f[2] = {1.f, 1.f};
+            if constexpr (S::kScaled)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                p[i] = exp2_approx(s[t][i] - safe + (S::kHalf ? kShift : 0.f));
-                l += p[i];
-                if constexpr (S::kScaled) p[i] *= __uint_as_float(__shfl_sync(0xffffffffu, vs, t * 8 + 2 * c + i));
+                for (int i = 0; i < 2; ++i) f[i] = __uint_as_float(__shfl_sync(0xffffffffu, vs, t * 8 + 2 * c + i));
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                const float base = (m[h] == -INFINITY ? 0.f : m[h]) - (S::kHalf ? kShift : 0.f);
+                float p[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    p[i] = exp2_approx(s[t][i + 2 * h] - base);
+                    l[h] += p[i];
+                    p[i] *= f[i];
+                }
+                uint32_t part[2];
+                split16<S::kHalf ? kF16 : kBf16, 2>(p[0], p[1], part);
+                hi[t][h] = part[0], lo[t][h] = part[1];
             }
-            uint32_t part[2];
-            split16<S::kHalf ? kF16 : kBf16, 2>(p[0], p[1], part);
-            hi[t] = part[0], lo[t] = part[1];
         }
 #pragma unroll
         for (int t = 0; t < T8; t += 2) {
-            const uint32_t A[4] = {hi[t], lo[t], hi[t + 1], lo[t + 1]};
             uint32_t vr[4][S::kRowB / 32];               // rows 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -254,7 +285,15 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
                         b[h] = __byte_perm(r0[e / 2], r1[e / 2], e % 2 == 0 ? 0x5410u : 0x7632u);
                     }
                 }
-                mma16816(o[j], A, b[0], b[1], kBf);
+                if constexpr (HALVES == 1) {
+                    const uint32_t A[4] = {hi[t][0], lo[t][0], hi[t + 1][0], lo[t + 1][0]};
+                    mma16816(o[j], A, b[0], b[1], kBf);
+                } else {
+                    const uint32_t A[4] = {hi[t][0], hi[t][HALVES - 1], hi[t + 1][0], hi[t + 1][HALVES - 1]};
+                    const uint32_t B[4] = {lo[t][0], lo[t][HALVES - 1], lo[t + 1][0], lo[t + 1][HALVES - 1]};
+                    mma16816(o[j], A, b[0], b[1], kBf);
+                    mma16816(o[j], B, b[0], b[1], kBf);
+                }
             }
         }
 
@@ -262,40 +301,45 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
         if (ends || !more) {                             // the unit's result, or this warp's part of it
             const bool whole = ends && from == 0;
             const uint32_t part = w * 2 + (from == 0);
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            float sane = 0.f;                            // NaN once a result is not finite
-            if (g < heads) {
-                const size_t to = row_at<D, R>(a, at.row, at.unit, a.out_stride) + size_t(g) * D;
-                float *sum = a.sums + (size_t(part) * R + g) * D;
 #pragma unroll
-                for (int p = 0; p < S::kNV; ++p)
+            for (int h = 0; h < HALVES; ++h) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                const int r = g + 8 * h;
+                const float inv = !whole ? 1.f : l[h] == 0.f ? 0.f : 1.f / l[h];
+                float sane = 0.f;                        // NaN once a result is not finite
+                if (r < heads) {
+                    const size_t to = row_at<D, R>(a, at.row, at.unit, a.out_stride) + size_t(r) * D;
+                    float *sum = a.sums + (size_t(part) * R + r) * D;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)          // dimensions of columns 2c and 2c + 1
+                    for (int p = 0; p < S::kNV; ++p)
 #pragma unroll
-                        for (int e = 0; e < S::kEV; e += 4) {
-                            float v[4];
+                        for (int i = 0; i < 2; ++i)      // dimensions of columns 2c and 2c + 1
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float *y = o[p * S::kEV + e + k];
-                                v[k] = (y[i] + y[i + 2]) * inv;
-                                sane = fmaf(v[k], 0.f, sane);
+                            for (int e = 0; e < S::kEV; e += 4) {
+                                float v[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float *y = o[p * S::kEV + e + k];
+                                    v[k] = (HALVES == 1 ? y[i] + y[i + 2] : y[i + 2 * h]) * inv;
+                                    sane = fmaf(v[k], 0.f, sane);
+                                }
+                                const int d = (8 * p + 2 * c + i) * S::kEV + e;
+                                if (whole) put4(a, to + d, v[0], v[1], v[2], v[3]);
+                                else *reinterpret_cast<float4 *>(sum + d) = make_float4(v[0], v[1], v[2], v[3]);
                             }
-                            const int d = (8 * p + 2 * c + i) * S::kEV + e;
-                            if (whole) put4(a, to + d, v[0], v[1], v[2], v[3]);
-                            else *reinterpret_cast<float4 *>(sum + d) = make_float4(v[0], v[1], v[2], v[3]);
-                        }
-                if (!whole && c == 0) a.ml[size_t(part) * R + g] = make_float2(m, l);
-            }
-            if (whole) {
-                uint32_t odd = __ballot_sync(0xffffffffu, sane != 0.f);
-                while (odd) {
-                    const int h = (__ffs(odd) - 1) >> 2;
-                    row_anew<KIND, D, R>(a, at.row, at.unit, h);
-                    odd &= ~(0xfu << (h * 4));
+                    if (!whole && c == 0) a.ml[size_t(part) * R + r] = make_float2(m[h], l[h]);
                 }
-            } else if (from == 0) {
+                if (whole) {
+                    uint32_t odd = __ballot_sync(0xffffffffu, sane != 0.f);
+                    while (odd) {
+                        const int k = (__ffs(odd) - 1) >> 2;
+                        row_anew<KIND, D, R>(a, at.row, at.unit, k + 8 * h);
+                        odd &= ~(0xfu << (k * 4));
+                    }
+                }
+            }
+            if (!whole && from == 0) {
                 head = make_int4(at.row, at.unit, int(sh.all.of(x + at.tiles - 1 - at.tile) - w) + 1, 0);
             }
         }
@@ -308,34 +352,36 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
 }
 
 template <int KIND, int D, bool QF16>
-cudaError_t mma_launch(const PagedArgs &a, int ctas, cudaStream_t s)
+cudaError_t mma_launch(const PagedArgs &a, int r, int ctas, cudaStream_t s)
 {
     const size_t smem = MmaRing<KIND, D>::kSmem;
-    const cudaError_t e = allow<k_paged_mma<KIND, D, QF16>>(smem);
-    return e != cudaSuccess ? e : spec_launch(k_paged_mma<KIND, D, QF16>, dim3(ctas), kThreads, smem, 1, s, a);
+    const cudaError_t e = r == 8 ? allow<k_paged_mma<KIND, D, QF16, 1>>(smem) : allow<k_paged_mma<KIND, D, QF16, 2>>(smem);
+    if (e != cudaSuccess) return e;
+    if (r == 8) return spec_launch(k_paged_mma<KIND, D, QF16, 1>, dim3(ctas), kThreads, smem, 1, s, a);
+    return spec_launch(k_paged_mma<KIND, D, QF16, 2>, dim3(ctas), kThreads, smem, 1, s, a);
 }
 
 template <int KIND, bool QF16>
-cudaError_t mma_dims(const PagedArgs &a, int ctas, cudaStream_t s)
+cudaError_t mma_dims(const PagedArgs &a, int r, int ctas, cudaStream_t s)
 {
     switch (a.kv.head_dim) {
-    case 32: return mma_launch<KIND, 32, QF16>(a, ctas, s);
-    case 64: return mma_launch<KIND, 64, QF16>(a, ctas, s);
-    default: return mma_launch<KIND, 128, QF16>(a, ctas, s);
+    case 32: return mma_launch<KIND, 32, QF16>(a, r, ctas, s);
+    case 64: return mma_launch<KIND, 64, QF16>(a, r, ctas, s);
+    default: return mma_launch<KIND, 128, QF16>(a, r, ctas, s);
     }
 }
 
 }  // namespace
 }  // namespace paged
 
-cudaError_t paged_mma(const PagedArgs &a, int ctas, cudaStream_t s)
+cudaError_t paged_mma(const PagedArgs &a, int r, int ctas, cudaStream_t s)
 {
     const bool f16 = a.q_dtype == GPT2_F16;
     switch (a.kv.dtype) {
-    case GPT2_F16: return paged::mma_dims<GPT2_F16, true>(a, ctas, s);
-    case GPT2_BF16: return paged::mma_dims<GPT2_BF16, false>(a, ctas, s);
-    case GPT2_INT8: return f16 ? paged::mma_dims<GPT2_INT8, true>(a, ctas, s) : paged::mma_dims<GPT2_INT8, false>(a, ctas, s);
-    default: return f16 ? paged::mma_dims<GPT2_E4M3, true>(a, ctas, s) : paged::mma_dims<GPT2_E4M3, false>(a, ctas, s);
+    case GPT2_F16: return paged::mma_dims<GPT2_F16, true>(a, r, ctas, s);
+    case GPT2_BF16: return paged::mma_dims<GPT2_BF16, false>(a, r, ctas, s);
+    case GPT2_INT8: return f16 ? paged::mma_dims<GPT2_INT8, true>(a, r, ctas, s) : paged::mma_dims<GPT2_INT8, false>(a, r, ctas, s);
+    default: return f16 ? paged::mma_dims<GPT2_E4M3, true>(a, r, ctas, s) : paged::mma_dims<GPT2_E4M3, false>(a, r, ctas, s);
     }
 }
 
