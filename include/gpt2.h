@@ -703,7 +703,8 @@ int gpt2_op_page_map(const int32_t *cached, const int32_t *grow, int32_t n_seqs,
  * gpt2_op_tree_attention; scores, softmax and sums are fp32 (for three or more 16-bit
  * query heads on a cache head the weights meet the values in two parts of 16 bits: in
  * fp16 those below 2^-37 of the largest may vanish).  n_slots * n_head * n_positions of
- * the cache < 2^32 - 1, max_blocks * n_positions < 2^31.
+ * the cache < 2^32 - 1, max_blocks * n_positions < 2^31, n_rows < 2^30, and n_rows * n_head * max_blocks *
+ * n_positions / 8 < 4e9.
  * workspace: 16-byte aligned DEVICE memory of gpt2_op_paged_attention_workspace
  * bytes (which depends on the current device, not on the number of rows), not used by another call in
  * flight.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
@@ -736,8 +737,9 @@ int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, i
  * Outputs (DEVICE): token int32 [n_rows]; prob fp32 [n_rows], the probability that the
  * drawn token had among the kept ones (greedy 1; token -1: 0), may be NULL; dist fp32
  * [n_rows][vocab], the whole distribution drawn from (greedy: 1 at the token; token -1:
- * zeros), as gpt2_op_verify_tree takes it for draft_probs, may be NULL.  Sums are
- * exact, weights fp32: a cut or a draw can differ from the exact one within 1e-6 of its border.
+ * zeros), as gpt2_op_verify_tree takes it for draft_probs, may be NULL.  Weights
+ * and sums are fp32 or more: a cut or a draw can differ from the exact one within 1e-6 of its
+ * border.
  * vocab <= GPT2_SAMPLE_MAX_VOCAB.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
 #define GPT2_SAMPLE_MAX_VOCAB 524288
 int gpt2_op_sample(const void *logits, int32_t dtype, int64_t row_stride, int32_t n_rows, int32_t vocab,

@@ -429,6 +429,27 @@ def test_offsets_past_32_bits():
     check_close(got, want, tol)
 
 
+def test_blocks_of_very_many_rows():
+    """A table whose few blocks hold 2^28 rows each: what 32 of them would hold passes
+    32 bits, and the entries behind the table's end are not read."""
+    import torch
+    rng = np.random.default_rng(7)
+    bs, D = 1 << 28, 32
+    kc, vc = (torch.empty((1, 1, bs, D), dtype=torch.int8, device="cuda") for _ in "kv")
+    ks, vs = (torch.empty((1, 1, bs), device="cuda") for _ in "kv")
+    small = []
+    for c in (kc, vc):
+        c[0, 0, :200] = torch.from_numpy(rng.integers(-127, 128, (200, D)).astype(np.int8)).cuda()
+        small.append(c[:, :, :200].clone())
+    for s in (ks, vs):
+        s[0, 0, :200] = 0.02
+        small.append(s[:, :, :200].clone())
+    q = torch.from_numpy(rng.standard_normal((2, 1, D)).astype(np.float32)).cuda()
+    got = binding.op_paged_attention(q, kc, vc, i32([[0], [0]]), i32([150, 31]), None, ks, vs)
+    want, tol = paged64(q, *small, np.zeros((2, 1), np.int64), [150, 31], None, 1 / math.sqrt(D))
+    check_close(got, want, tol)
+
+
 def test_binding_refuses():
     import torch
     rng = np.random.default_rng(1)

@@ -60,6 +60,7 @@ def test_bad_paged_attentions_are_refused():
     # cache rows are counted in 32 bits, the tiles of all rows too
     assert attend(kv(n_slots=1 << 30, n_head=1, n_positions=16), heads=1) == -1
     assert attend(kv(n_head=1, n_positions=16), heads=1, rows=1 << 20, seqs=1 << 20, width=1 << 20) == -1
+    assert attend(kv(n_head=1, n_positions=16), heads=1, rows=1 << 30, seqs=1 << 30, width=1) == -1
 
 
 def test_bad_samplings_are_refused():

@@ -146,7 +146,7 @@ struct Lookup {
             from = at.block;
             // (the last block that the row sees: its length is above the tile's first key)
             const uint32_t left = at.len - at.tile * KS + at.offset;   // rows from the block's first on
-            entry = uint32_t(lane) * bs < left ? at.table[from + lane] : -1;
+            entry = uint64_t(lane) * bs < left ? at.table[from + lane] : -1;
         }
         const int32_t e = __shfl_sync(0xffffffffu, entry, (at.block - from + k) & 31);
         const bool yes = lane < KS && at.tile * KS + lane < at.len && e >= 0 && e < a.kv.n_slots;

@@ -106,7 +106,8 @@ extern "C" int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t
 {
     if (!paged::shape_ok(kv, q_dtype, n_head)) return GPT2_ERR_INVALID_ARG;
     if (!q || !table || !position || !out || !std::isfinite(scale)) return GPT2_ERR_INVALID_ARG;
-    if (n_seqs < 0 || n_rows < 0 || max_blocks < 1 || (!seq && n_rows > n_seqs)) return GPT2_ERR_INVALID_ARG;
+    if (n_seqs < 0 || n_rows < 0 || n_rows >= (1 << 30) || max_blocks < 1 || (!seq && n_rows > n_seqs))
+        return GPT2_ERR_INVALID_ARG;
     const int64_t E = int64_t(n_head) * kv->head_dim;
     if (q_stride < E || out_stride < E || q_stride % 8 || out_stride % 8) return GPT2_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned4(table, seq, position)) return GPT2_ERR_INVALID_ARG;
@@ -142,7 +143,7 @@ extern "C" int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t
     a.n_rows = n_rows;
     a.max_blocks = max_blocks;
     a.q_dtype = q_dtype;
-    a.per_block = (65536 + kv->n_positions - 1) / kv->n_positions;
+    a.per_block = 65535 / kv->n_positions + 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int ctas = at.warps / tree::kNW;

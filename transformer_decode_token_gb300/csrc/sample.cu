@@ -17,8 +17,9 @@
 //   - A longer one is narrowed by histograms over the cluster, of counts and
 //     masses, by digits of (weight, logit, id), until the digit where the cut
 //     lies holds at most kList ids, which are then sorted as above.
-// Masses are summed as integers (a weight in units of 2^-40 of the largest), so that
-// neither order nor shape of a sum shows and every call gives the same bits.
+// Masses are summed as integers (in units of 2^-40 of the largest weight; a few weights
+// of one thread at a time in fp32), so that the order in which CTAs and threads come does
+// not show and every call gives the same bits.
 //
 // Rounding: a weight is off by some 2^-22 of itself (the exponent's integer part
 // is taken off exactly before the exponential), so a cut by mass can differ from
@@ -119,7 +120,6 @@ struct Exchange {                         // what the CTAs of a row tell one ano
 struct Shared {
     Exchange ex[3];
     u64 red[kSW];
-    float fred[kSW];
     uint32_t count[2][kST], lo[2][kST], hi[2][kST];
     uint32_t scan[kSW];
     u64 mscan[kSW];
@@ -195,15 +195,15 @@ __device__ __forceinline__ u64 cluster_sum_wide(uint32_t *p, int split)
     return sum;
 }
 
-__device__ __forceinline__ float block_max(Shared &s, float v)
+__device__ __forceinline__ uint32_t block_max(Shared &s, uint32_t v)
 {
-    v = warp_max(v);
+    v = __reduce_max_sync(0xffffffffu, v);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.fred[threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) s.scan[threadIdx.x >> 5] = v;
     __syncthreads();
-    float r = s.fred[0];
+    uint32_t r = 0;
 #pragma unroll
-    for (int i = 1; i < kSW; ++i) r = fmaxf(r, s.fred[i]);
+    for (int i = 0; i < kSW; ++i) r = max(r, s.scan[i]);
     return r;
 }
 
@@ -512,10 +512,11 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
         thread_top = fmaxf(thread_top, x);        // (a NaN is never above)
         bad = bad || !(x < INFINITY);
     };
+    const int nv = (n - front) / E, rest = front + nv * E;
+    uint4 *sv = reinterpret_cast<uint4 *>(share + front);
+    const int edges = front + n - rest, edge = tid < front ? tid : rest + tid - front;   // the ids around the pieces
     {
-        const int nv = (n - front) / E, rest = front + nv * E;
         const uint4 *pv = reinterpret_cast<const uint4 *>(p + front);
-        uint4 *sv = reinterpret_cast<uint4 *>(share + front);
         if (!greedy && !cut)                       // the random numbers follow the logits from memory
             for (int j = tid * 32; j < n; j += kST * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(u + lo + j));
         for (int i0 = tid; i0 < nv; i0 += U * kST) {
@@ -532,8 +533,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                     for (int j = 0; j < E; ++j) take(e[j]);
                 }
         }
-        if (tid < front) take(share[tid] = p[tid]);
-        if (tid < n - rest) take(share[rest + tid] = p[rest + tid]);
+        if (tid < edges) take(share[edge] = p[edge]);
     }
     constexpr int B = 8;
     float e_first = 0.5f, e[B];           // the first random numbers, where nothing is cut, on their way before the maximum
@@ -548,8 +548,11 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
         if (tid < n) e_first = __ldcs(u + lo + tid);
         load_u(kST);
     }
-    bad = __syncthreads_or(bad);
-    const float cta_top = block_max(s, thread_top);
+    // (the order of the keys is the logits'; a logit that makes the row's choice none is above all)
+    constexpr uint32_t kBad = 0xffffffffu;
+    const uint32_t cta_key = block_max(s, bad && !greedy ? kBad : ~order_bits(thread_top));
+    bad = cta_key == kBad;
+    const float cta_top = logit_at(u64(~cta_key) << 32);
     auto logit_of = [](u64 key) {         // of an argmax key
         const uint32_t b = uint32_t(key >> 32);
         return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
         float sum = 0.f;
         if (tid < n) take_part(float(share[tid]), e_first, tid, 0.f, sum);
         if (tid == 0) s.bound = 0.f;
-        const float first_best = block_max(s, won);
+        const float first_best = __uint_as_float(block_max(s, __float_as_uint(won)));
         if (tid == 0) s.bound = first_best * 0.999f;
         __syncthreads();
         for (int j0 = kST; j0 < n; j0 += B * kST) {
@@ -679,15 +682,15 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                 if (s.border.found) r.t_max = fminf(r.t_max, float(s.border.digit + 1) * 0.125f + 1e-5f);
             } else if (top_p < 1.f) {
                 u64 mass = 0;
-                for (int j0 = 0; j0 < n; j0 += 8 * kST) {
+                for (int q = tid; q < nv; q += kST) {
+                    alignas(16) T e16[E];
+                    *reinterpret_cast<uint4 *>(e16) = sv[q];
                     float sum = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int j = j0 + k * kST + tid;
-                        if (j < n) sum += Scale::rough(r.c.t(float(share[j])));
-                    }
+                    for (int j = 0; j < E; ++j) sum += Scale::rough(r.c.t(float(e16[j])));
                     mass += mass_of(sum);
                 }
+                if (tid < edges) mass += mass_of(Scale::rough(r.c.t(float(share[edge]))));
                 mass = block_sum(s, mass);
                 if (tid == 0) s.ex[1].z = mass;
                 cl.sync();
@@ -698,12 +701,23 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
             // ---- their list: a thread's ids follow one another ----
             // (by the logits, a little below the bound, and above those of no weight)
             r.l_min = fmaxf(r.c.m - r.t_max / r.c.hi * 1.00001f, -FLT_MAX);
-            for (int j0 = 0; j0 < n; j0 += 32 * kST) {
+            if (tid < 32) {                                // the ids before and behind the whole pieces
+                const bool yes = tid < edges && float(share[edge]) >= r.l_min;
+                const uint32_t who = __ballot_sync(0xffffffffu, yes);
+                if (yes) s.cand[__popc(who & ((1u << tid) - 1))] = uint32_t(edge);
+                if (tid == 0) s.n_cand = __popc(who);
+            }
+            for (int q0 = 0; q0 < nv; q0 += 32 / E * kST) {
                 uint32_t mask = 0;
-#pragma unroll 8
-                for (int k = 0; k < 32; ++k) {
-                    const int j = j0 + k * kST + tid;
-                    if (j < n && float(share[j]) >= r.l_min) mask |= 1u << k;
+#pragma unroll
+                for (int k = 0; k < 32 / E; ++k) {
+                    const int q = q0 + k * kST + tid;
+                    if (q >= nv) continue;
+                    alignas(16) T e16[E];
+                    *reinterpret_cast<uint4 *>(e16) = sv[q];
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        if (float(e16[j]) >= r.l_min) mask |= 1u << (k * E + j);
                 }
                 uint32_t at = __popc(mask);
                 u64 none = 0;
@@ -712,10 +726,13 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                 __syncthreads();
                 if (tid == kST - 1) s.n_cand = before + at;
                 at += before - __popc(mask);
-                for (; mask; mask &= mask - 1, ++at)
-                    if (at < kCand) s.cand[at] = uint32_t(j0 + (__ffs(mask) - 1) * kST + tid);
+                for (; mask; mask &= mask - 1, ++at) {
+                    const int i = __ffs(mask) - 1;
+                    if (at < kCand) s.cand[at] = uint32_t(front + (q0 + i / E * kST + tid) * E + i % E);
+                }
                 __syncthreads();
             }
+            if (nv == 0) __syncthreads();
             r.listed = s.n_cand <= kCand;
             // the lists to the first CTA, where they fit
             Shared *first = cl.map_shared_rank(&s, 0);
