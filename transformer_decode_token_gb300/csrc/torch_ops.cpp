@@ -138,19 +138,31 @@ int64_t row_stride(const at::Tensor &t, const char *name, int64_t H, int64_t D, 
     return t.size(0) > 1 ? t.stride(0) : H * D;
 }
 
-// A tensor of this shape (and type, of the same size) in `whole`'s memory, from element `from` on: results of
+// A tensor of this shape in `whole`'s memory, from element `from` on: results of
 // one call are made in one allocation (1.3 us each on the Arm host, as long as
 // the marshalling itself).
-at::Tensor part(const at::Tensor &whole, int64_t from, at::IntArrayRef shape, caffe2::TypeMeta type)
+at::Tensor part(const at::Tensor &whole, int64_t from, at::IntArrayRef shape)
 {
-    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), type);
+    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
     t->set_sizes_contiguous(shape);
     t->set_storage_offset(from);
     return at::Tensor(std::move(t));
 }
-at::Tensor part(const at::Tensor &whole, int64_t from, at::IntArrayRef shape)
+
+// The same straight from the allocator, for results of the current device and of
+// several types of one size.
+c10::Storage fresh(size_t bytes)
 {
-    return part(whole, from, shape, whole.dtype());
+    c10::Allocator *from = c10::cuda::CUDACachingAllocator::get();
+    return c10::Storage(c10::Storage::use_byte_size_t(), int64_t(bytes), from->allocate(bytes), from, true);
+}
+at::Tensor part(const c10::Storage &whole, int64_t from, at::IntArrayRef shape, at::ScalarType type)
+{
+    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                  c10::scalarTypeToTypeMeta(type));
+    t->set_sizes_contiguous(shape);
+    t->set_storage_offset(from);
+    return at::Tensor(std::move(t));
 }
 
 // Memory of a call in flight, returned to torch's allocator when the call has
@@ -437,18 +449,18 @@ PyObject *page_map(PyObject *, PyObject *const *a, Py_ssize_t n)
         int32_t *ring = whole<int32_t>(a[3], "free_blocks", at::kInt, {N}, c.dev);
         const int32_t *state = whole<int32_t>(a[4], "free_state", at::kInt, {2}, c.dev);
         const int64_t R = rows;
-        const at::Tensor made = at::empty({2 * B + 3 + 4 * R}, cached.options());
+        const c10::Storage made = fresh((2 * B + 3 + 4 * R) * sizeof(int32_t));
+        auto ints = [&](int64_t from, at::IntArrayRef shape) { return part(made, from, shape, at::kInt); };
         auto result = [&](PyObject *o, const char *name, int64_t from, at::IntArrayRef shape) {
-            if (o == Py_None) return part(made, from, shape);
+            if (o == Py_None) return ints(from, shape);
             whole(tensor(o, name), name, at::kInt, shape, c.dev);
             return tensor(o, name);
         };
         const at::Tensor out = result(a[7], "cached_out", 0, {B}), state_out = result(a[8], "free_state_out", B, {2}),
-                         first = part(made, B + 2, {B + 1}), seq = part(made, 2 * B + 3, {R}),
-                         slot = part(made, 2 * B + 3 + R, {R}), offset = part(made, 2 * B + 3 + 2 * R, {R}),
-                         position = part(made, 2 * B + 3 + 3 * R, {R});
+                         first = ints(B + 2, {B + 1}), seq = ints(2 * B + 3, {R}), slot = ints(2 * B + 3 + R, {R}),
+                         offset = ints(2 * B + 3 + 2 * R, {R}), position = ints(2 * B + 3 + 3 * R, {R});
         // (an empty tensor has no address; the call wants none of its elements)
-        const int32_t *some = made.data_ptr<int32_t>();
+        const int32_t *some = static_cast<const int32_t *>(made.data());
         check(g_lib.page_map(B ? len : some, B ? grow : some, int32_t(B), bs, B ? tab : const_cast<int32_t *>(some),
                              int32_t(W), ring, int32_t(N), state, B ? out.data_ptr<int32_t>() : const_cast<int32_t *>(some),
                              state_out.data_ptr<int32_t>(), first.data_ptr<int32_t>(), seq.data_ptr<int32_t>(),
@@ -482,7 +494,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         at::Tensor out;
         int64_t out_stride = H * D;
         if (a[9] == Py_None) {
-            out = at::empty({rows, H, D}, q.options());
+            out = part(fresh(rows * H * D * q.element_size()), 0, {rows, H, D}, q.scalar_type());
         } else {
             out = tensor(a[9], "out");
             if (out.scalar_type() != q.scalar_type() || out.sizes() != q.sizes())
@@ -527,11 +539,12 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n)
         const auto *min_p = static_cast<const float *>(each(5, "min_p", at::kFloat));
         const float *u = a[2] == Py_None ? nullptr : whole<float>(a[2], "u", at::kFloat, {rows, V}, c.dev);
         if (temperature && !u) throw Bad{"temperature needs u"};
-        at::Tensor made, token, prob;
-        if (a[6] == Py_None || a[7] == Py_None) made = at::empty({2 * rows}, logits.options().dtype(at::kInt));
-        if (a[6] == Py_None) token = part(made, 0, {rows});
+        c10::Storage made;
+        at::Tensor token, prob;
+        if (a[6] == Py_None || a[7] == Py_None) made = fresh(2 * rows * sizeof(int32_t));
+        if (a[6] == Py_None) token = part(made, 0, {rows}, at::kInt);
         else each(6, "token", at::kInt), token = tensor(a[6], "token");
-        if (a[7] == Py_None) prob = part(made, rows, {rows}, caffe2::TypeMeta::fromScalarType(at::kFloat));
+        if (a[7] == Py_None) prob = part(made, rows, {rows}, at::kFloat);
         else each(7, "prob", at::kFloat), prob = tensor(a[7], "prob");
         float *dist = a[8] == Py_None ? nullptr : whole<float>(a[8], "dist", at::kFloat, {rows, V}, c.dev);
         if (rows > 0)
