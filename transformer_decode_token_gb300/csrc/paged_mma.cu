@@ -1,14 +1,21 @@
 // Attention over a paged cache on the matrix instructions, for 16-bit rows and
 // three or more query heads on a cache head, over the list of paged.cuh.
 //
-// The weights meet the values in two parts, p = hi + lo, and so do fp16 queries the
-// keys of 8-bit caches, whose codes are exact in bf16.  For up to 8 query heads the
-// 16 rows of an instruction's A side are the heads twice (HALVES = 1): the upper half
-// takes the second part of what the lower half is the first part of, so that both parts
-// cost one instruction and meet in one thread, which adds the two halves of the
-// accumulators.  For up to 16 heads (HALVES = 2) each part has its own instruction.  Cache rows reach the operand
-// registers in the order of tree_attn.cuh: keys by 16-byte pieces c, c + 4, ..,
-// values by pieces g, g + 8, .. of the rows whose weights the thread holds.
+// The weights meet the values in two parts, p = hi + lo.  For up to 8 query heads
+// the 16 rows of an instruction's A side are the heads twice (HALVES = 1): the upper
+// half takes the second part of what the lower half is the first part of, so that both
+// parts cost one instruction and meet in one thread, which adds the two halves of the
+// accumulators.  For up to 16 heads (HALVES = 2) each part has its own instruction.
+// Cache rows reach the operand registers in the order of tree_attn.cuh: keys by
+// 16-byte pieces c, c + 4, .., values by pieces g, g + 8, .. of the rows whose weights
+// the thread holds.
+//
+// What bounds the kernel over 8-bit caches is the conversion of their codes, two
+// thirds of its instructions.  As keys they become fp16, which takes five
+// instructions for four int8 codes where bf16 takes eight, and holds e4m3 as it is;
+// bf16 queries meet them as fp16 too, each head's times a power of two that brings its
+// largest to 2^14 .. 2^15, so that what fp16 cannot hold of the others is below 2^-39
+// of that.  The values' weights include the rows' scales, whose range only bf16 has.
 #include "paged.cuh"
 
 namespace gpt2 {
@@ -63,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
     using G = MmaRing<KIND, D>;
     constexpr int R = 8 * HALVES, KS = S::KS, T8 = S::kT8, N = G::kStages;
     constexpr float kRaise = S::kHalf ? 2.f : 8.f;
-    constexpr bool kBf = !S::kHalf, kTwo = S::kScaled && QF16;   // (queries in two parts)
+    constexpr bool kBf = !S::kHalf;
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
     extern __shared__ __align__(16) uint8_t dyn[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -117,8 +124,8 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
         for (int i = 0; i + 1 < N; ++i) there[i] = there[i + 1];
         there[N - 1] = yes;
     };
-    // the queries' operands: part 0, and 1 where there are two, of heads g and g + 8
-    uint32_t qa[S::kSteps][kTwo ? 2 : 1][HALVES][2];
+    uint32_t qa[S::kSteps][HALVES][2];                   // the queries' operands, of heads g and g + 8
+    float qs[HALVES];                                    // what their scores are times
     float o[S::kNT][4], m[HALVES], l[HALVES];            // m, l: of query heads g and g + 8
     int heads = 0;
     uint32_t from = 0;
@@ -133,17 +140,29 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
             for (int s = 0; s < S::kSteps; ++s) {
                 constexpr int kPer = S::kEK / 4;         // steps of an access
                 const uint2 v = *reinterpret_cast<const uint2 *>(q + (s / kPer * 4 + c) * S::kEK + s % kPer * 4);
-                if constexpr (kTwo) {
-                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-                    uint32_t p[2];
-                    split16<kBf16, 2>(x.x, x.y, p);
-                    qa[s][0][h][0] = p[0], qa[s][1][h][0] = p[1];
-                    split16<kBf16, 2>(y.x, y.y, p);
-                    qa[s][0][h][1] = p[0], qa[s][1][h][1] = p[1];
-                } else {
-                    qa[s][0][h][0] = v.x, qa[s][0][h][1] = v.y;
-                }
+                qa[s][h][0] = v.x, qa[s][h][1] = v.y;
+            }
+            qs[h] = a.scale_log2;
+            if constexpr (S::kScaled && !QF16) {
+                uint32_t top = 0;                        // the largest magnitude's bits
+#pragma unroll
+                for (int s = 0; s < S::kSteps; ++s)
+                    top = __vmaxu2(top, __vmaxu2(qa[s][h][0] & 0x7fff7fffu, qa[s][h][1] & 0x7fff7fffu));
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const uint32_t e = top >> 7, f = e == 255 ? 127 : min(268 - e, 253u);   // (infinities and NaN: as they are)
+                const float up = __uint_as_float(f << 23);
+#pragma unroll
+                for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t x = qa[s][h][i];
+                        const __half2 y = __floats2half2_rn(__uint_as_float(x << 16) * up,
+                                                            __uint_as_float(x & 0xffff0000u) * up);
+                        qa[s][h][i] = *reinterpret_cast<const uint32_t *>(&y);
+                    }
+                qs[h] *= __uint_as_float((254 - f) << 23);
             }
             m[h] = -INFINITY;
             l[h] = 0.f;
@@ -184,23 +203,16 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
             for (int k = 0; k < S::kSteps; ++k) {
                 uint32_t b0, b1;
                 if constexpr (S::kScaled) {
-                    b0 = codes_to_bf162<KIND, 0>(kr[k]);
-                    b1 = codes_to_bf162<KIND, 1>(kr[k]);
+                    const uint32_t z = KIND == GPT2_INT8 ? kr[k] ^ 0x80808080u : kr[k];
+                    b0 = codes_to_half2<KIND == GPT2_E4M3>(z, 0x4140u);
+                    b1 = codes_to_half2<KIND == GPT2_E4M3>(z, 0x4342u);
                 } else {
                     b0 = kr[2 * k];
                     b1 = kr[2 * k + 1];
                 }
-                if constexpr (HALVES == 1) {
-                    const uint32_t A[4] = {qa[k][0][0][0], kTwo ? qa[k][kTwo][0][0] : 0u, qa[k][0][0][1],
-                                           kTwo ? qa[k][kTwo][0][1] : 0u};
-                    mma16816(s[t], A, b0, b1, kBf);
-                } else {
-#pragma unroll
-                    for (int p = 0; p <= int(kTwo); ++p) {
-                        const uint32_t A[4] = {qa[k][p][0][0], qa[k][p][HALVES - 1][0], qa[k][p][0][1], qa[k][p][HALVES - 1][1]};
-                        mma16816(s[t], A, b0, b1, kBf);
-                    }
-                }
+                const uint32_t A[4] = {qa[k][0][0], HALVES == 1 ? 0u : qa[k][HALVES - 1][0], qa[k][0][1],
+                                       HALVES == 1 ? 0u : qa[k][HALVES - 1][1]};
+                mma16816(s[t], A, b0, b1, kBf && !S::kScaled);
             }
         }
         bool above = false;
@@ -209,11 +221,11 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int key = t * 8 + 2 * c + i;
-                const float f = S::kScaled ? a.scale_log2 * __uint_as_float(__shfl_sync(0xffffffffu, ks, key)) : a.scale_log2;
+                const float f = S::kScaled ? __uint_as_float(__shfl_sync(0xffffffffu, ks, key)) : 1.f;
                 const bool no = got != kAll && !(got >> key & 1);
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
-                    float y = (HALVES == 1 && kTwo ? s[t][i] + s[t][i + 2] : s[t][i + 2 * h]) * f;
+                    float y = s[t][i + 2 * h] * (S::kScaled ? qs[h] * f : qs[h]);
                     if (no) y = -INFINITY;
                     s[t][i + 2 * h] = y;
                     above = above || y > m[h] + kRaise;
