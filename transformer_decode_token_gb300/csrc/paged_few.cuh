@@ -11,6 +11,10 @@
 // than kSlack (a vote instead of a reduction per tile; fp32 holds 2^kSlack as well as
 // 1).  Lane l looks up the place of the tile's row l in the block table, so that pages
 // may have any size and end anywhere in a tile.
+//
+// Long caches run at the memory's rate (64 sequences of 2,000 to 4,000 rows, 12 heads
+// of 64: fp32 172 us, 1.0 of the copy rate, bf16 91, 0.95; int8 57.5, 0.8, where the
+// conversion of the codes takes as long as they take to arrive).
 #pragma once
 
 #include "paged.cuh"
