@@ -704,16 +704,13 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                 const float least = (1.f - top_p) * (float(all) * (1.f / kUnit)) / float(a.V);
                 if (least > 0.f) r.t_max = fminf(r.t_max, -log2f(least) + 0.01f);
             }
-            // ---- their list: a thread's ids follow one another ----
+            // ---- their list, and a common one in the first CTA, as far as it goes ----
             // (by the logits, a little below the bound, and above those of no weight)
             r.l_min = fmaxf(r.c.m - r.t_max / r.c.hi * 1.00001f, -FLT_MAX);
-            if (tid < 32) {                                // the ids before and behind the whole pieces
-                const bool yes = tid < edges && float(share[edge]) >= r.l_min;
-                const uint32_t who = __ballot_sync(0xffffffffu, yes);
-                if (yes) s.cand[__popc(who & ((1u << tid) - 1))] = uint32_t(edge);
-                if (tid == 0) s.n_cand = __popc(who);
-            }
-            for (int q0 = 0; q0 < nv; q0 += 32 / E * kST) {
+            Shared *first = cl.map_shared_rank(&s, 0);
+            const int lane = tid & 31;
+            bool at_edge = tid < edges && float(share[edge]) >= r.l_min;   // an id before or behind the whole pieces
+            for (int q0 = 0; q0 == 0 || q0 < nv; q0 += 32 / E * kST) {
                 uint32_t mask = 0;
 #pragma unroll
                 for (int k = 0; k < 32 / E; ++k) {
@@ -725,32 +722,31 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                     for (int j = 0; j < E; ++j)
                         if (float(e16[j]) >= r.l_min) mask |= 1u << (k * E + j);
                 }
-                uint32_t at = __popc(mask);
-                u64 none = 0;
-                block_scan(s, at, none);
-                const uint32_t before = s.n_cand;
-                __syncthreads();
-                if (tid == kST - 1) s.n_cand = before + at;
-                at += before - __popc(mask);
-                for (; mask; mask &= mask - 1, ++at) {
+                const uint32_t own = __popc(mask) + at_edge;
+                uint32_t to = own;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const uint32_t x = __shfl_up_sync(0xffffffffu, to, o);
+                    if (lane >= o) to += x;
+                }
+                uint32_t here = 0, there = 0;
+                if (lane == 31 && to) there = atomicAdd(&first->list_n, to), here = atomicAdd(&s.n_cand, to);
+                here = __shfl_sync(0xffffffffu, here, 31) + to - own;
+                there = __shfl_sync(0xffffffffu, there, 31) + to - own;
+                auto keep = [&](int j) {
+                    if (here < kCand) s.cand[here] = uint32_t(j);
+                    if (there < kList) first->list[there] = place(float(share[j]), uint32_t(lo + j));
+                    ++here, ++there;
+                };
+                if (at_edge) keep(edge);
+                at_edge = false;
+                for (; mask; mask &= mask - 1) {
                     const int i = __ffs(mask) - 1;
-                    if (at < kCand) s.cand[at] = uint32_t(front + (q0 + i / E * kST + tid) * E + i % E);
+                    keep(front + (q0 + i / E * kST + tid) * E + i % E);
                 }
-                __syncthreads();
             }
-            if (nv == 0) __syncthreads();
-            r.listed = s.n_cand <= kCand;
-            // the lists to the first CTA, where they fit
-            Shared *first = cl.map_shared_rank(&s, 0);
-            if (tid == 0) s.scan[0] = atomicAdd(&first->list_n, s.n_cand);
-            __syncthreads();
-            const uint32_t base = s.scan[0];
-            if (base + s.n_cand <= kList)
-                for (int i = tid; i < int(s.n_cand); i += kST) {
-                    const uint32_t j = s.cand[i];
-                    first->list[base + i] = place(float(share[j]), uint32_t(lo) + j);
-                }
             cl.sync();
+            r.listed = s.n_cand <= kCand;
             const uint32_t m = first->list_n;
             const u64 want = u64(double(top_p) * double(all));
             if (m <= kList) {
@@ -807,7 +803,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                 const float l_last = last == ~0ull ? r.l_min : logit_at(last);
                 const int id_last = last == ~0ull ? a.V : int(uint32_t(last));
                 for (int i0 = 0; i0 < count; i0 += B * kST) {
-                    float l[B], sum = 0.f;
+                    float l[B];
                     int id[B];
                     const float bound = fmaxf(*static_cast<volatile float *>(&s.bound), won * 0.999f);
 #pragma unroll
@@ -829,13 +825,12 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                         const float t = r.c.t(l[k]);
                         float w = Scale::rough(t);
                         if (w < min_p) continue;
-                        sum += w;
+                        mass += mass_of(w);
                         if (!(w > bound * (1.f - e[k]))) continue;
                         w = r.c.weight(l[k]);
                         const float y = __fdividef(w, -logf(e[k]));
                         if (y > won || (y == won && id[k] < who)) won = y, won_w = w, who = id[k];
                     }
-                    mass += mass_of(sum);
                     if (won * 0.999f > bound) atomicMax(reinterpret_cast<int *>(&s.bound), __float_as_int(won * 0.999f));
                 }
                 const u64 key = who >= 0 ? argmax_key(won, uint32_t(who)) : 0, high = block_max(s, key);
