@@ -23,9 +23,9 @@
 //
 // What bounds it is latency: the load of a share, two or three exchanges over the
 // cluster, and barriers around the list, its order and the race, most of them the same
-// for one row (9.0 us with top-p) as for 64 (13.3 with top-k and top-p, 11.5 uncut; the
+// for one row (8.7 us with top-p) as for 64 (12.8 with top-k and top-p, 11.5 uncut; the
 // logits alone would take 1.9, with the random numbers 3.8).  A flat row, whose cut lies
-// among thousands of ids, takes 57 us: two shared-memory atomics per id and digit.
+// among thousands of ids, takes 59 us: two shared-memory atomics per id and digit.
 //
 // Rounding: a weight is off by some 2^-22 of itself (the exponent's integer part
 // is taken off exactly before the exponential), so a cut by mass can differ from
