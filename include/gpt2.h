@@ -702,7 +702,8 @@ int gpt2_op_page_map(const int32_t *cached, const int32_t *grow, int32_t n_seqs,
  * q, q_dtype, q_stride, n_head, scale, out and the types are as for
  * gpt2_op_tree_attention; scores, softmax and sums are fp32 (for three or more 16-bit
  * query heads on a cache head the weights meet the values in two parts of 16 bits: in
- * fp16 those below 2^-37 of the largest may vanish).  n_slots * n_head * n_positions of
+ * fp16 those below 2^-37 of the largest may vanish; and bf16 queries meet 8-bit keys
+ * to within 2^-40 of a head's largest element).  n_slots * n_head * n_positions of
  * the cache < 2^32 - 1, max_blocks * n_positions < 2^31, n_rows < 2^30, and n_rows * n_head * max_blocks *
  * n_positions / 8 < 4e9.
  * workspace: 16-byte aligned DEVICE memory of gpt2_op_paged_attention_workspace

@@ -279,6 +279,38 @@ def test_scales(scale, G):
     run_paged(np.random.default_rng(1), "bf16", "bf16", 64, 2, G, 16, [100, 7], scale=scale)
 
 
+@pytest.mark.parametrize("ct,e", [(ct, e) for ct in ("int8", "e4m3", "bf16", "f32") for e in (-100, -60, 60, 110)] +
+                         [("int8", -113), ("e4m3", -113)])
+@pytest.mark.parametrize("G", [1, 4, 12])
+def test_sizes_of_queries(ct, G, e):
+    """bf16 queries far outside fp16's range, their elements 2^0 to 2^-24 apart, a
+    head of zeros: the scores are ordinary again by the call's scale."""
+    import torch
+    rng = np.random.default_rng(G)
+    D, K, position = 64, 2, [300, 40, 5]
+    kc, vc, ks, vs, table = pages(rng, ct, [p + 1 for p in position], 16, K, D)
+    q = 1.5 * rng.standard_normal((3, K * G, D)) * 2.0 ** (e - rng.integers(0, 25, (3, K * G, D)))
+    q[:, 1] = 0
+    q = torch.from_numpy(q).to(torch.bfloat16 if ct != "f32" else torch.float32).cuda()
+    got = binding.op_paged_attention(q, kc, vc, i32(table), i32(position), None, ks, vs, scale=2.0 ** -e / 4)
+    want, tol = paged64(q, kc, vc, ks, vs, table, position, None, 2.0 ** -e / 4)
+    check_close(got, want, tol)
+
+
+def test_nothing_to_do():
+    """No rows, no sequences: results of these shapes on the device."""
+    import torch
+    c = torch.zeros(2, 2, 4, 64, device="cuda")
+    got = binding.op_paged_attention(torch.zeros(0, 2, 64, device="cuda"), c, c, i32(np.zeros((3, 2))), i32([]))
+    assert got.shape == (0, 2, 64) and got.is_cuda and got.dtype == torch.float32 and got.clone().numel() == 0
+    token, prob = binding.op_sample(torch.zeros(0, 7, device="cuda"))
+    assert token.shape == prob.shape == (0,) and token.is_cuda and token.dtype == torch.int32 and prob.dtype == torch.float32
+    check_map(np.array([], np.int64), np.array([], np.int64), np.zeros((0, 1), np.int64), np.array([3]), [0, 1], 1, 0)
+    x = binding.op_page_map(i32([3]), i32([1]), i32([[0]]), i32([1]), i32([0, 1]), 4, 1)
+    assert all(t.is_contiguous() and t.device == c.device for t in x) and [len(t) for t in x] == [1, 2, 2, 1, 1, 1, 1]
+    assert (x[0] + 1).tolist() == [5] and torch.cat(x).tolist() == [4, 0, 1, 0, 1, 0, 0, 3, 3]
+
+
 @pytest.mark.parametrize("qt,ct", COMBOS)
 @pytest.mark.parametrize("G", [1, 4, 12])
 def test_what_is_not_seen_does_not_enter(qt, ct, G):

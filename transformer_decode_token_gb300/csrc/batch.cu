@@ -1641,8 +1641,8 @@ int gpt2_sample_batch(gpt2_batch *m, int32_t n, const float *temperature, const 
     k_b_set_drawn<<<1, kTcMaxRows, 0, m->stream>>>(m->next_tok, m->out_ids, m->tok, d, m->max_batch);
     BTRY(cudaGetLastError());
     m->launches += 2;
-    std::vector<int32_t> drawn(n);
-    BTRY(cudaMemcpyAsync(drawn.data(), m->tok, size_t(n) * 4, cudaMemcpyDeviceToHost, m->stream));
+    int32_t drawn[kTcMaxRows];
+    BTRY(cudaMemcpyAsync(drawn, m->tok, size_t(n) * 4, cudaMemcpyDeviceToHost, m->stream));
     rc = read_batch_state(m);
     if (rc != GPT2_OK) return rc;
     for (int b = 0; b < n; ++b) {
