@@ -25,7 +25,8 @@
 // cluster, and barriers around the list, its order and the race, most of them the same
 // for one row (8.7 us with top-p) as for 64 (12.8 with top-k and top-p, 11.5 uncut; the
 // logits alone would take 1.9, with the random numbers 3.8).  A flat row, whose cut lies
-// among thousands of ids, takes 59 us: two shared-memory atomics per id and digit.
+// among thousands of ids, takes 56 us: two passes of two shared-memory atomics per id,
+// two of lists, and the race.
 //
 // Rounding: a weight is off by some 2^-22 of itself (the exponent's integer part
 // is taken off exactly before the exponential), so a cut by mass can differ from
@@ -241,8 +242,9 @@ struct Row {
     float t_max, l_min;                   // ids with t above, or logits below, are not kept
     bool listed;                          // the others are in s.cand, else the whole share is looked at
     int round = 0;                        // histograms so far
+    float t_lo = 0.f, t_hi = INFINITY;    // only ids with t in this range are looked at
 
-    // f(logit, id) for each id that can be kept
+    // f(logit, id) for each id that can be kept and is in the range
     template <typename F>
     __device__ __forceinline__ void each(F f) const
     {
@@ -258,7 +260,7 @@ struct Row {
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (l[k] >= l_min) f(l[k], uint32_t(lo) + j[k]);
+                if (const float t = c.t(l[k]); l[k] >= l_min && t >= t_lo && t < t_hi) f(l[k], uint32_t(lo) + j[k]);
         }
     }
 };
@@ -375,6 +377,7 @@ __device__ u64 find_cut(Row<T> &r, bool by_mass, u64 want, u64 last)
     const int tid = threadIdx.x;
     Range range{};
     u64 before = 0;                       // ids, or mass, before the range
+    r.t_lo = 0.f, r.t_hi = INFINITY;
     // the first digit: 256 to 512 bins up to the largest t that is left
     const int top = 32 - __clz(fixed(r.t_max * 1.0001f) | 1);
     for (Digit digit{0, max(top - 9, 0), min(top, 9)};; digit.next()) {
@@ -416,7 +419,16 @@ __device__ u64 find_cut(Row<T> &r, bool by_mass, u64 want, u64 last)
         uint32_t none = 0;
         block_scan(s, none, at);
         at += before;
-        if (own && at - own < want && at >= want) {
+        u64 goal = want;
+        if (by_mass && range.t_mask != 0) {
+            // (within a digit that the cut is known to lie in, its bins' masses, rounded one by
+            // one, may end before it)
+            if (tid == kST - 1) s.border.before = at;
+            __syncthreads();
+            goal = min(want, s.border.before);
+            __syncthreads();
+        }
+        if (own && at - own < goal && at >= goal) {
             s.border.found = 1;
             s.border.digit = tid;
             s.border.before = at - own;
@@ -427,6 +439,11 @@ __device__ u64 find_cut(Row<T> &r, bool by_mass, u64 want, u64 last)
         before = s.border.before;
         uint32_t inside = s.border.inside;         // (of counts)
         if (found) digit.narrow(range, s.border.digit);
+        if (digit.word == 0 && digit.shift >= 8) {       // (fp32 holds the range's ends; see fixed)
+            const u64 end = u64(range.t) + (1ull << digit.shift);
+            r.t_lo = fminf(float(range.t) * (1.f / 67108864.f), 63.9f);
+            r.t_hi = end >> 32 ? INFINITY : float(end) * (1.f / 67108864.f);
+        }
         __syncthreads();
         if (!found) return ~0ull;
 
@@ -784,6 +801,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                 if (top_p < 1.f) {
                     u64 up_to = want;
                     if (top_k > 0) {      // of the mass of these
+                        r.t_lo = 0.f, r.t_hi = INFINITY;
                         r.each([&](float l, uint32_t id) {
                             if (place(l, id) <= last) mass += mass_of(Scale::rough(r.c.t(l)));
                         });
