@@ -1,0 +1,113 @@
+"""GPU parity of the sampling operation's cuts against a plain implementation in
+64 bits, on every row: where a cut lies next to its border, between the smallest
+and the largest set of ids that the border leaves open."""
+import math
+
+import numpy as np
+import pytest
+
+from transformer_decode_token_gb300 import binding
+
+from test_gpu_sample import NEAR, OFF, peaked
+from test_gpu_spec import dt, i32, uniform
+
+pytestmark = pytest.mark.gpu
+
+
+class Cut:
+    """A row by the definition in gpt2.h (temperature above 0, finite logits): its ids in
+    order, their weights, and how many of the first ones are kept: lo to hi."""
+
+    def __init__(self, row, t, k, p, m):
+        V = len(row)
+        w = np.exp((row - row.max()) / t)
+        self.ids = np.argsort(-row, kind="stable")
+        self.r = r = w[self.ids]
+        n = min(k, V) if k > 0 else V
+        lo = hi = n
+        if p < 1:
+            total = r[:n].sum()
+            before = (np.cumsum(r[:n]) - r[:n])[1:]
+            lo = min(lo, 1 + int((before < (max(p, 0) - NEAR) * total).sum()))
+            hi = min(hi, 1 + int((before < (max(p, 0) + NEAR) * total).sum()))
+        if m > 0:
+            m = min(m, 1.0)
+            lo = min(lo, max(1, int((r >= m + (NEAR if m < 1 else 0)).sum())))
+            hi = min(hi, max(1, int((r >= m - NEAR).sum())))
+        self.lo, self.hi = lo, hi
+        self.sums = np.cumsum(r)
+
+    def check(self, u, token, prob, dist):
+        lo, hi, ids, r = self.lo, self.hi, self.ids, self.r
+        most, least = r / self.sums[lo - 1], r / self.sums[hi - 1]
+        at = int(np.flatnonzero(ids == token)[0]) if token >= 0 else -1
+        assert 0 <= at < hi, (token, at, lo, hi)
+        # it wins among the first n for some n from lo to hi
+        n = max(lo, at + 1)
+        with np.errstate(divide="ignore"):
+            score = r[:n] / -np.log(u[ids[:n]].astype(np.float64))
+        assert score[at] >= score.max() * (1 - NEAR), (token, at, int(score.argmax()))
+        assert least[at] * (1 - OFF) <= prob <= most[at] * (1 + OFF) + 1e-30, (prob, least[at], most[at])
+        if dist is None:
+            return
+        d = dist[ids].astype(np.float64)
+        assert np.all(d[hi:] == 0)
+        assert np.all(d[:hi] <= most[:hi] * (1 + OFF) + 1e-34)
+        assert np.all(d[:lo] >= least[:lo] * (1 - OFF) - 1e-34)
+        open_ = d[lo:hi]
+        assert np.all((open_ == 0) | (open_ >= least[lo:hi] * (1 - OFF) - 1e-34))
+        # the draw and the distribution are of the same ids: the probability is the one
+        # that the distribution has (each off by OFF)
+        assert abs(d[at] - prob) <= 2 * OFF * prob + 1e-34, (d[at], prob)
+
+
+def check(logits, t, u, k=None, p=None, m=None, dtype="f32", dist=True):
+    """Every row; returns the tokens, and how many rows' borders left one set."""
+    import torch
+    n, V = logits.shape
+    f32 = lambda a, off: np.asarray(np.full(n, off) if a is None else np.broadcast_to(a, n), np.float32)
+    t, p, m = f32(t, 1.0), f32(p, 1.0), f32(m, 0.0)
+    k = np.zeros(n, np.int64) if k is None else np.broadcast_to(k, n)
+    x = torch.from_numpy(logits.astype(np.float32)).to(dt(dtype)).cuda()
+    held = x.float().cpu().numpy().astype(np.float64)
+    u = u.astype(np.float32)
+    whole = torch.full((n, V), 7.0, device="cuda") if dist else None
+    c = lambda a: torch.from_numpy(a.copy()).cuda()
+    token, prob = binding.op_sample(x, c(t), c(u), i32(k), c(p), c(m), dist=whole)
+    token, prob = token.tolist(), prob.cpu().numpy().astype(np.float64)
+    whole = whole.cpu().numpy() if dist else [None] * n
+    one = 0
+    for i in range(n):
+        cut = Cut(held[i], float(t[i]), int(k[i]), float(p[i]), float(m[i]))
+        try:
+            cut.check(u[i], token[i], prob[i], whole[i])
+        except AssertionError as e:
+            raise AssertionError(f"row {i}, kept {cut.lo} to {cut.hi}: {e}") from e
+        one += cut.lo == cut.hi
+    return token, one
+
+
+def far_rows(rng, n, V, top, step, levels):
+    """Rows of a few neighbouring fp32 values next to a large one."""
+    return np.float32(top) - np.float32(step) * rng.integers(0, levels, (n, V)).astype(np.float32)
+
+
+@pytest.mark.parametrize("V", [1500, 5003, 50257])
+@pytest.mark.parametrize("top,step,levels,t", [
+    (1e6, 0.0625, 100, 1.0), (1.5e6, 0.125, 2, 0.7), (1.5e7, 1.0, 5, 1.0), (2.0 ** 24, 1.0, 5, 3.0),
+    (-1e6, 0.0625, 5, 0.1), (1e9, 64.0, 5, 100.0), (1e9, 64.0, 5, 1.0)])
+def test_logits_far_from_zero(top, step, levels, t, V):
+    """fp32 logits whose spacing is of the size of the cuts' bounds (scores with a large
+    common part): lists of more than 512 ids, bounded by a logit that is rounded by
+    more than the ids differ."""
+    rng = np.random.default_rng(V)
+    n = 6
+    x = far_rows(rng, n, V, top, step, levels)
+    u = uniform(rng, n, V)
+    ps = [0.3, 0.6, 0.9, 0.9759, 0.99, 0.999]
+    check(x, t, u, p=ps)
+    check(x, t, u, p=0.9999, m=[0.95, 0.9, 0.714, 0.5, 0.2, 0.02])
+    check(x, t, u, m=[0.95, 0.9, 0.714, 0.5, 0.2, 0.02])
+    check(x, t, u, k=[700, 1, 600, V // 2, 1200, V - 1])
+    check(x, t, u, k=[700, 2, 600, V // 2, 1200, V - 1], p=ps)
+    check(x, t, u, k=[700, 2, 600, V // 2, 1200, V - 1], p=0.97, m=[0.95, 0.9, 0.714, 0.5, 0.2, 0.02])

@@ -78,7 +78,9 @@ struct Scale {
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-f));
         return y * __int_as_float((127 - int(n)) << 23);
     }
-    // the same, the exponent rounded as a whole: off by 2^-24 t ln 2 more, for sums (where t is
+    // the same for any t
+    __device__ __forceinline__ float weight_or_0(float l) const { return t(l) < 125.f ? weight(l) : 0.f; }
+    // the same for any t, the exponent rounded as a whole: off by 2^-24 t ln 2 more, for sums (where t is
     // large enough to show, there are many of them or they weigh nothing)
     static __device__ __forceinline__ float rough(float t)
     {
@@ -239,7 +241,7 @@ struct Row {
     const T *share;                       // this CTA's ids lo .. lo + n - 1
     int lo, n, rank;
     Scale c;
-    float t_max, l_min;                   // ids with t above, or logits below, are not kept
+    float t_max, l_min;                   // ids with t above are not kept; those with logits below are not looked at
     bool listed;                          // the others are in s.cand, else the whole share is looked at
     int round = 0;                        // histograms so far
     float t_lo = 0.f, t_hi = INFINITY;    // only ids with t in this range are looked at
@@ -378,8 +380,9 @@ __device__ u64 find_cut(Row<T> &r, bool by_mass, u64 want, u64 last)
     Range range{};
     u64 before = 0;                       // ids, or mass, before the range
     r.t_lo = 0.f, r.t_hi = INFINITY;
-    // the first digit: 256 to 512 bins up to the largest t that is left
-    const int top = 32 - __clz(fixed(r.t_max * 1.0001f) | 1);
+    // the first digit: 256 to 512 bins up to the largest t that is left, which is l_min's (t is
+    // monotone) and not t_max, since l_min is rounded to the logits' spacing
+    const int top = 32 - __clz(fixed(r.c.t(r.l_min)) | 1);
     for (Digit digit{0, max(top - 9, 0), min(top, 9)};; digit.next()) {
         const int k = r.round++ & 1;
         s.count[k][tid] = s.lo[k][tid] = s.hi[k][tid] = 0;
@@ -487,7 +490,7 @@ __device__ u64 find_cut(Row<T> &r, bool by_mass, u64 want, u64 last)
         if (r.rank == 0) {
             const int m = int(min(inside, uint32_t(kList)));
             const u64 key = sorted(s, m);
-            u64 own = tid < m ? (by_mass ? mass_of(r.c.weight(logit_at(key))) : 1) : 0, to = own;
+            u64 own = tid < m ? (by_mass ? mass_of(r.c.weight_or_0(logit_at(key))) : 1) : 0, to = own;
             uint32_t none = 0;
             block_scan(s, none, to);
             // kept are those with fewer ids, or less mass, before them than wanted
@@ -771,13 +774,14 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                     // this thread's id in the race, and the number of ids and the mass before it
                     const bool mine = tid < int(m);
                     const u64 my = mine ? s.list[tid] : ~0ull;
-                    const float e = mine ? u[uint32_t(my)] : 0.5f, w = mine ? r.c.weight(logit_at(my)) : 0.f;
+                    // (l_min may let some of no weight through)
+                    const float e = mine ? u[uint32_t(my)] : 0.5f, w = mine ? r.c.weight_or_0(logit_at(my)) : 0.f;
                     const u64 own = mine ? mass_of(w) : 0;
                     uint32_t ahead = 0;
                     u64 before = 0, sum_k = 0;
                     settle(s, int(m), my, own, top_k, ahead, before, sum_k);
                     const u64 up_to = top_k > 0 ? u64(double(top_p) * double(sum_k)) : want;
-                    const bool keep = mine && (top_k == 0 || ahead < uint32_t(top_k)) && w >= min_p &&
+                    const bool keep = w > 0.f && (top_k == 0 || ahead < uint32_t(top_k)) && w >= min_p &&
                                       (top_p >= 1.f || before < up_to || ahead == 0);
                     z = block_sum(s, keep ? own : 0);
                     const u64 key = keep ? argmax_key(__fdividef(w, -logf(e)), uint32_t(my)) : 0, high = block_max(s, key);
