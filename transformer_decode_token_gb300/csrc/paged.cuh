@@ -5,7 +5,7 @@
 // one unit after another, are one list, and every warp takes an equal share of
 // it, whatever the lengths: no warp waits for a longer row, none meets a barrier.
 // A unit that lies in one warp's share is written by that warp.  Of a unit that is
-// cut, each warp writes its part (maximum, sum of the weights, weighted sum, in
+// cut, each warp writes its part (maximum, sum of the weights, weighted mean, in
 // fp32) to the workspace, and a second kernel joins the parts in the order of the
 // list, so every call gives the same bits.  (It costs 2 to 3 us.  Joins by the warp
 // that comes last, through tickets, took 10 us more for one request's 63 parts, and
@@ -347,16 +347,19 @@ __device__ __forceinline__ void put(const PagedArgs &a, size_t at, const float *
     }
 }
 
-// One result row (query head h of the unit's tile) by its definition, by a warp in
-// fp32: the maximum and the sum of the weights, a key per lane, then the weighted
-// values, D / 32 dimensions per lane.  For results that are not finite where the
-// kernel's products in parts make a NaN of an infinity.
+// One result row (query head h of the unit's tile), or a part of it (keys j_from .. j_to - 1,
+// to `part`), by its definition, by a warp in fp32: the maximum and the sum of the
+// weights, a key per lane, then the weighted values, D / 32 dimensions per lane.  For
+// what is not finite: the kernels sum values times weights of up to 2^8 and divide in
+// the end (and the matrix instructions' products in parts make a NaN of an infinity), so
+// that large values can pass fp32's range where those of the formula, whose weights
+// add up to one, do not.
 template <int KIND, int D, int R>
-__device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int h)
+__device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int h, int j_from, int j_to, float *part)
 {
     constexpr bool kScaled = KIND == GPT2_INT8 || KIND == GPT2_E4M3;
     constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31, len = seen(a, row), head = unit / a.row_tiles;
+    const int lane = threadIdx.x & 31, head = unit / a.row_tiles;
     const int32_t *table = table_of(a, row);
     const size_t q_at = row_at<D, R>(a, row, unit, a.q_stride) + size_t(h) * D;
     auto score = [&](uint32_t j, uint32_t r) {       // -infinity where it is not seen
@@ -372,10 +375,10 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
         }
         return x;
     };
-    auto at = [&](int j) { return j < len ? cache_row(a, table, uint32_t(j), head) : kNone; };
+    auto at = [&](int j) { return j < j_to ? cache_row(a, table, uint32_t(j), head) : kNone; };
     float m = -INFINITY, l = 0.f, out[N];
     bool nan = false;
-    for (int j0 = 0; j0 < len && !nan; j0 += 32) {
+    for (int j0 = j_from; j0 < j_to && !nan; j0 += 32) {
         const float s = score(j0 + lane, at(j0 + lane)), top = fmaxf(m, s), safe = top == -INFINITY ? 0.f : top;
         nan = __any_sync(0xffffffffu, s != s || s == INFINITY);
         l = l * exp2_approx(m - safe) + exp2_approx(s - safe);
@@ -386,7 +389,7 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
     for (int i = 0; i < N; ++i) out[i] = nan ? __int_as_float(0x7fc00000) : 0.f;
     if (!nan && top != -INFINITY) {
         l = warp_sum(l * exp2_approx(m - top));
-        for (int j0 = 0; j0 < len; j0 += 32) {
+        for (int j0 = j_from; j0 < j_to; j0 += 32) {
             const uint32_t r = at(j0 + lane);
             const float p = exp2_approx(score(j0 + lane, r) - top) / l;
             for (int t = 0; t < 32; ++t) {
@@ -402,9 +405,37 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
     const size_t o = row_at<D, R>(a, row, unit, a.out_stride) + size_t(h) * D + lane * N;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (a.q_dtype == GPT2_F32) static_cast<float *>(a.out)[o + i] = out[i];
+        if (part) part[lane * N + i] = out[i];
+        else if (a.q_dtype == GPT2_F32) static_cast<float *>(a.out)[o + i] = out[i];
         else if (a.q_dtype == GPT2_F16) static_cast<__half *>(a.out)[o + i] = __float2half_rn(out[i]);
         else static_cast<__nv_bfloat16 *>(a.out)[o + i] = __float2bfloat16_rn(out[i]);
+    }
+}
+
+// What a warp has written of its share and is not finite, computed anew: its share w goes
+// from tile `tile` of the unit (row, unit) to tile last_tile of (last_row, last_unit).
+template <int KIND, int D, int R, int KS>
+__device__ __noinline__ void share_anew(const PagedArgs &a, uint32_t w, int row, int unit, int tile, int last_row,
+                                        int last_unit, int last_tile)
+{
+    const int lane = threadIdx.x & 31, units = a.kv.n_head * a.row_tiles;
+    for (; row <= last_row; ++row, unit = 0) {
+        const int len = seen(a, row), tiles = int((uint32_t(len) + KS - 1) / KS);
+        if (len == 0) continue;
+        for (const int end = row == last_row ? last_unit + 1 : units; unit < end; ++unit, tile = 0) {
+            const bool last = row == last_row && unit == last_unit;
+            const bool whole = tile == 0 && (!last || last_tile + 1 == tiles);
+            const int to = last && last_tile + 1 < tiles ? (last_tile + 1) * KS : len;
+            for (int r = 0; r < heads_of<R>(a, unit); ++r) {
+                float *part = a.sums + ((size_t(w) * 2 + (tile == 0)) * R + r) * D;
+                const size_t at = row_at<D, R>(a, row, unit, a.out_stride) + size_t(r) * D + lane;
+                bool odd = false;
+#pragma unroll
+                for (int i = 0; i < D; i += 32)
+                    odd = odd || !is_finite(whole ? row_value(a.out, at + i, a.q_dtype) : part[lane + i]);
+                if (__any_sync(0xffffffffu, odd)) row_anew<KIND, D, R>(a, row, unit, r, tile * KS, to, whole ? nullptr : part);
+            }
+        }
     }
 }
 
@@ -412,9 +443,10 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
 // the beginnings of the others'.
 __device__ __forceinline__ size_t part_of(uint32_t w, uint32_t i) { return i == 0 ? size_t(w) * 2 + 1 : size_t(w + i) * 2; }
 
-// Joins the n parts (from warp w on) of query head r of a unit, by a warp.  KIND: the
-// cache's type where the parts come from the matrix instructions, whose results
-// that are not finite are computed anew; -1 otherwise.
+// Joins the n parts (from warp w on) of query head r of a unit, by a warp: their means,
+// each times its share of the weights, so that nothing grows past the largest mean.
+// KIND: the cache's type where the parts come from the matrix instructions, whose results
+// that are not finite are computed anew here; -1 where that has been done for the parts.
 template <int KIND, int D, int R>
 __device__ __forceinline__ void join_row(const PagedArgs &a, int row, int unit, uint32_t w, uint32_t n, int r)
 {
@@ -434,9 +466,12 @@ __device__ __forceinline__ void join_row(const PagedArgs &a, int row, int unit, 
                             : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         const float mn = fmaxf(top, warp_max(ml.x)), safe = mn == -INFINITY ? 0.f : mn;
-        const float keep = exp2_approx(top - safe), f = exp2_approx(ml.x - safe);
+        float keep = exp2_approx(top - safe), f = ml.y * exp2_approx(ml.x - safe);
         top = mn;
-        l = l * keep + ml.y * f;
+        keep *= l;
+        l = keep + warp_sum(f);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        keep *= inv, f *= inv;
         v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
         for (uint32_t j = 0; j < here; j += kBatch * kSide) {
             if (j)
@@ -455,17 +490,15 @@ __device__ __forceinline__ void join_row(const PagedArgs &a, int row, int unit, 
             }
         }
     }
-    l = warp_sum(l);
 #pragma unroll
     for (int d = kLanes; d < 32; d *= 2) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, d), v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
         v.z += __shfl_xor_sync(0xffffffffu, v.z, d), v.w += __shfl_xor_sync(0xffffffffu, v.w, d);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
     if (side == 0) put4(a, row_at<D, R>(a, row, unit, a.out_stride) + size_t(r) * D + e, v.x, v.y, v.z, v.w);
     if constexpr (KIND >= 0)
-        if (__any_sync(0xffffffffu, !is_finite(v.x + v.y + v.z + v.w))) row_anew<KIND, D, R>(a, row, unit, r);
+        if (__any_sync(0xffffffffu, !(is_finite(v.x) && is_finite(v.y) && is_finite(v.z) && is_finite(v.w))))
+            row_anew<KIND, D, R>(a, row, unit, r, 0, seen(a, row), nullptr);
 }
 
 }  // namespace paged

@@ -9,7 +9,7 @@ namespace paged {
 namespace {
 
 // Joins the parts of the units that were cut: a warp per unit whose parts begin with
-// that warp of the attention's kernel, or, for four or eight query heads, a CTA.
+// that warp of the attention's kernel, or, for four or more query heads, a CTA.
 template <int KIND, int D, int R>
 __global__ void __launch_bounds__(kThreads) k_paged_join(const __grid_constant__ PagedArgs a)
 {

@@ -58,6 +58,9 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, D, R>::kCtas) k_paged_few(
     Share<KS> sh;
     find_share<KS, D>(a, sh);
     Place<KS> at = sh.at;
+    __shared__ int began[kNW][3];                        // where the warp's share begins: row, unit, tile
+    if (lane == 0) began[warp][0] = at.row, began[warp][1] = at.unit, began[warp][2] = int(at.tile);
+    float sane = 0.f;                                    // NaN once something that was written is not finite
     const uint32_t w = sh.w, x0 = sh.x0, x1 = sh.x1;
     int4 head = make_int4(0, 0, 0, 0);                   // the unit whose parts begin with this warp's: row, unit, parts
     uint8_t *ring = dyn + warp * (S * F::kStage) + lane * 16;
@@ -267,13 +270,15 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, D, R>::kCtas) k_paged_few(
                 }
                 if (r < heads) {
                     const int dim = (c + first / EP * LPR) * EP + first % EP;
+                    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) sane = fmaf(v[i] * inv, 0.f, sane);
                     if (whole) {
-                        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
                         put<N>(a, row_at<D, R>(a, at.row, at.unit, a.out_stride) + size_t(r) * D + dim, v, inv);
                     } else {
                         float *to = a.sums + (size_t(part) * R + r) * D + dim;
 #pragma unroll
-                        for (int i = 0; i < N; ++i) to[i] = v[i];
+                        for (int i = 0; i < N; ++i) to[i] = v[i] * inv;
                         if (lane == 0) a.ml[size_t(part) * R + r] = make_float2(m[r], l[r]);
                     }
                 }
@@ -287,6 +292,11 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, D, R>::kCtas) k_paged_few(
         }
     }
     if (lane == 0) a.heads[w] = head;
+    // (here and not where it is written: a call from the loop takes registers of the loop's)
+    if (__any_sync(0xffffffffu, sane != 0.f)) {
+        __syncwarp();
+        share_anew<KIND, D, R, KS>(a, w, began[warp][0], began[warp][1], began[warp][2], at.row, at.unit, int(at.tile));
+    }
 }
 
 template <int KIND, int D, int R>

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
                 const int r = g + 8 * h;
-                const float inv = !whole ? 1.f : l[h] == 0.f ? 0.f : 1.f / l[h];
+                const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
                 float sane = 0.f;                        // NaN once a result is not finite
                 if (r < heads) {
                     const size_t to = row_at<D, R>(a, at.row, at.unit, a.out_stride) + size_t(r) * D;
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
                     uint32_t odd = __ballot_sync(0xffffffffu, sane != 0.f);
                     while (odd) {
                         const int k = (__ffs(odd) - 1) >> 2;
-                        row_anew<KIND, D, R>(a, at.row, at.unit, k + 8 * h);
+                        row_anew<KIND, D, R>(a, at.row, at.unit, k + 8 * h, 0, int(at.len), nullptr);
                         odd &= ~(0xfu << (k * 4));
                     }
                 }
