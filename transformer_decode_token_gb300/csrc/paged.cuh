@@ -403,6 +403,7 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
         }
     }
     const size_t o = row_at<D, R>(a, row, unit, a.out_stride) + size_t(h) * D + lane * N;
+    __syncwarp();                                        // (what other lanes have written there comes first)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         if (part) part[lane * N + i] = out[i];
