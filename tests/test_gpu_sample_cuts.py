@@ -111,3 +111,20 @@ def test_logits_far_from_zero(top, step, levels, t, V):
     check(x, t, u, k=[700, 1, 600, V // 2, 1200, V - 1])
     check(x, t, u, k=[700, 2, 600, V // 2, 1200, V - 1], p=ps)
     check(x, t, u, k=[700, 2, 600, V // 2, 1200, V - 1], p=0.97, m=[0.95, 0.9, 0.714, 0.5, 0.2, 0.02])
+
+
+@pytest.mark.parametrize("t", [0.9, 1.0, 0.37])
+def test_min_p_next_to_a_weight(t):
+    """min-p within some roundings of the weight of thousands of ids, which are a good part
+    of the whole: they are drawn from if the distribution has them."""
+    rng = np.random.default_rng(3)
+    n, V = 400, 8000
+    x = np.full((n, V), -80.0, np.float32)
+    t = np.float32(t)
+    l0 = np.repeat(rng.uniform(-12, -4, n // 8) * t, 8).astype(np.float32)
+    x[:, rng.permutation(V)[:4000]] = l0[:, None]
+    x[:, 77] = 0
+    m = (np.exp(l0.astype(np.float64) / float(t)) * (1 + (np.arange(n) % 8 - 3.5) * 2.0 ** -23)).astype(np.float32)
+    for u in (uniform(rng, n, V), np.where(x > -80, 0.9, 0.5)):
+        check(x, t, u, m=m)
+        check(x, t, u, m=m, p=0.99999)

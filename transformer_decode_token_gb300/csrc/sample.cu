@@ -846,7 +846,8 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
                         if (id[k] < 0) continue;
                         const float t = r.c.t(l[k]);
                         float w = Scale::rough(t);
-                        if (w < min_p) continue;
+                        // (next to min_p by the exact weight, as the distribution has it)
+                        if (w < min_p * 1.0001f && r.c.weight_or_0(l[k]) < min_p) continue;
                         mass += mass_of(w);
                         if (!(w > bound * (1.f - e[k]))) continue;
                         w = r.c.weight(l[k]);
