@@ -427,7 +427,9 @@ int gpt2_decode_batch_greedy(gpt2_batch *m, int32_t n_steps);
  * for gpt2_argmax_batch, gpt2_batch_ids and the next gpt2_decode_batch_greedy.  A sequence that
  * took no part in the last step, or whose nodes the last tree step ran, keeps what it has
  * and gets -1.  Synchronises.  Errors: NOT_READY (no such sequence among them), INVALID_ARG,
- * DEVICE_STATE (logits without a choice: -1, and that sequence has none), CUDA. */
+ * DEVICE_STATE (logits without a choice: -1, and that sequence has none), CUDA; DEVICE_STATE or
+ * TIMEOUT where a step before has failed on the device: the sequences of the last step then have no
+ * choice.  Where the call fails for another reason than want of a choice, host_ids are all -1. */
 int gpt2_sample_batch(gpt2_batch *m, int32_t n, const float *temperature, const int32_t *top_k, const float *top_p,
                       const float *min_p, const float *u, int32_t *host_ids);
 

@@ -500,7 +500,7 @@ class BatchModel:
         uniform numbers u [n][vocab], as op_sample; see gpt2_sample_batch.
         Returns the ids, -1 for a sequence that took no part in that step.  Where some
         sequence's logits leave no choice, the GPT2Error (DEVICE_STATE) has
-        them as `tokens`."""
+        them as `tokens` (all -1 where a step before has failed)."""
         import torch
         n, V = int(n), self.cfg.vocab_size
         given = [(name, t, shape, dtype) for name, t, shape, dtype in
@@ -512,7 +512,7 @@ class BatchModel:
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self._device}")
         if given:
             self._wait_for_tensors()
-        out, op = _i32(np.zeros(max(n, 0)))
+        out, op = _i32(np.full(max(n, 0), -1))
         status = lib().gpt2_sample_batch(self._h, n, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
                                          op)
         if STATUS.get(status) == "DEVICE_STATE":

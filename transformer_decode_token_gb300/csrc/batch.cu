@@ -1625,6 +1625,7 @@ int gpt2_sample_batch(gpt2_batch *m, int32_t n, const float *temperature, const 
                       const float *min_p, const float *u, int32_t *host_ids)
 {
     if (!m || !host_ids || n < 1 || n > m->max_batch) return GPT2_ERR_INVALID_ARG;
+    std::fill(host_ids, host_ids + n, -1);         // (until the new ones are known)
     DrawnAt d;
     bool any = false;
     for (int b = 0; b < kTcMaxRows; ++b) {
@@ -1636,7 +1637,7 @@ int gpt2_sample_batch(gpt2_batch *m, int32_t n, const float *temperature, const 
     int rc = gpt2_op_sample(m->logits, GPT2_F32, m->cfg.vocab_size, n, m->cfg.vocab_size, temperature, top_k, top_p,
                             min_p, u, m->tok, nullptr, nullptr, m->stream);
     if (rc != GPT2_OK) return rc;
-    for (int b = 0; b < n; ++b)                    // (until the new ones are known)
+    for (int b = 0; b < n; ++b)
         if (d.at[b] >= 0) m->choice[b] = 0;
     k_b_set_drawn<<<1, kTcMaxRows, 0, m->stream>>>(m->next_tok, m->out_ids, m->tok, d, m->max_batch);
     BTRY(cudaGetLastError());
@@ -1646,8 +1647,8 @@ int gpt2_sample_batch(gpt2_batch *m, int32_t n, const float *temperature, const 
     rc = read_batch_state(m);
     if (rc != GPT2_OK) return rc;
     for (int b = 0; b < n; ++b) {
-        host_ids[b] = d.at[b] >= 0 ? drawn[b] : -1;
         if (d.at[b] < 0) continue;
+        host_ids[b] = drawn[b];
         m->choice[b] = drawn[b] >= 0;
         if (drawn[b] < 0) rc = GPT2_ERR_DEVICE_STATE;
     }
