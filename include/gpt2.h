@@ -706,8 +706,9 @@ int gpt2_op_page_map(const int32_t *cached, const int32_t *grow, int32_t n_seqs,
  * query heads on a cache head the weights meet the values in two parts of 16 bits: in
  * fp16 those below 2^-37 of the largest may vanish; and bf16 queries meet 8-bit keys
  * to within 2^-40 of a head's largest element).  n_slots * n_head * n_positions of
- * the cache < 2^32 - 1, max_blocks * n_positions < 2^31, n_rows < 2^30, and n_rows * n_head * max_blocks *
- * n_positions / 8 < 4e9.
+ * the cache < 2^32 - 1, max_blocks * n_positions < 2^31, n_rows < 2^30, n_head <= 2^16, and n_rows * n_head *
+ * T < 4e9 with T = max_blocks * n_positions / 8, rounded up (the table's width counts, whatever the
+ * positions are).
  * workspace: 16-byte aligned DEVICE memory of gpt2_op_paged_attention_workspace
  * bytes (which depends on the current device, not on the number of rows), not used by another call in
  * flight.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
@@ -743,7 +744,7 @@ int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, i
  * zeros), as gpt2_op_verify_tree takes it for draft_probs, may be NULL.  Weights
  * and sums are fp32 or more: a cut or a draw can differ from the exact one within 1e-6 of its
  * border.
- * vocab <= GPT2_SAMPLE_MAX_VOCAB.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
+ * vocab <= GPT2_SAMPLE_MAX_VOCAB, n_rows < 2^27.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
 #define GPT2_SAMPLE_MAX_VOCAB 524288
 int gpt2_op_sample(const void *logits, int32_t dtype, int64_t row_stride, int32_t n_rows, int32_t vocab,
                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
