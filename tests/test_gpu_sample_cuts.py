@@ -128,3 +128,20 @@ def test_min_p_next_to_a_weight(t):
     for u in (uniform(rng, n, V), np.where(x > -80, 0.9, 0.5)):
         check(x, t, u, m=m)
         check(x, t, u, m=m, p=0.99999)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [900, 20011])
+@pytest.mark.parametrize("t", [1e30, 1e36, 2e37, 1e38, 3.4e38, math.inf])
+def test_differences_past_the_largest_number(t, V, dtype):
+    """Logits next to the largest of both signs, whose differences fp32 does not hold, at
+    temperatures that make ordinary weights of them."""
+    rng = np.random.default_rng(V)
+    n = 4
+    x = 3.3e38 * rng.uniform(-1, 1, (n, V))
+    x[1] = np.where(rng.random(V) < 0.5, 3.3e38, -3.3e38)
+    x[2] = -3.3e38
+    x[2, 11] = 3.3e38
+    u = uniform(rng, n, V)
+    for arg in ({}, dict(p=0.9), dict(p=0.3), dict(k=20), dict(k=700), dict(k=700, p=0.8), dict(m=0.4), dict(m=0.02, p=0.95)):
+        check(x, t, u, dtype=dtype, **arg)

@@ -65,13 +65,16 @@ struct SampleArgs {
     int32_t V, per, split;                // ids of a row, of a CTA's share; CTAs of a row
 };
 
-// 1 / (T ln 2) in two parts, and the row's largest logit.
+// 1 / (T ln 2) in two parts, and the row's largest logit; with a temperature near fp32's
+// largest the logits are taken in units of 2^8 (pre = 2^-8), so that their differences,
+// which it makes ordinary, stay in fp32's range.
 struct Scale {
-    float hi, lo, m;
-    __device__ __forceinline__ float t(float l) const { return (m - l) * hi; }   // -log2 of the weight (monotone)
+    float hi, lo, m, pre;                 // (m in these units, hi and lo per unit)
+    __device__ __forceinline__ float t(float l) const { return fmaf(-l, pre, m) * hi; }   // -log2 of the weight (monotone)
     // exp((l - m) / T) for t(l) < 126
     __device__ __forceinline__ float weight(float l) const
     {
+        l *= pre;
         const float d = m - l, v = d - m, rest = (m - (d - v)) - (l + v);
         const float n = rintf(d * hi), f = fmaf(d, hi, -n) + fmaf(rest, hi, d * lo);
         float y;
@@ -585,11 +588,12 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
     };
     Row<T> r{a, s, share, lo, n, rank};
     {
-        const float c = 1.4426950408889634f / temperature;
+        const float unit = temperature >= 0x1p100f ? 256.f : 1.f, c = 1.4426950408889634f * unit / temperature;
+        r.c.pre = 1.f / unit;
         r.c.hi = fminf(fmaxf(c, FLT_TRUE_MIN), FLT_MAX);   // (above 0: a logit of -infinity has t = infinity)
         r.c.lo = 0.f;
         if (c > 0.f && c <= FLT_MAX)
-            r.c.lo = (fmaf(-c, temperature, 1.4426950216293335f) + 1.9259629911e-8f) / temperature;
+            r.c.lo = (fmaf(-c, temperature, 1.4426950216293335f * unit) + 1.9259629911e-8f * unit) / temperature;
     }
     int32_t token = -1;
     float prob = 0.f;
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
 
     if (!greedy && !cut) {
         // ---- the race over all ids, by this CTA's own maximum ----
-        r.c.m = cta_top;
+        r.c.m = cta_top * r.c.pre;
         float won = 0.f, won_w = 0.f;
         int who = -1;
         u64 mass = 0;
@@ -646,14 +650,13 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
         cl.sync();
         const Exchange x = told(s.ex[0], a.split);
         const bool any_bad = __any_sync(0xffffffffu, x.bad);
-        const float m = warp_max(x.m), t = (m - x.m) * r.c.hi;
-        const float f = x.best && t < 125.f ? Scale{r.c.hi, r.c.lo, m}.weight(x.m) : 0.f;
+        r.c.m = warp_max(x.m) * r.c.pre;
+        const float f = x.best ? r.c.weight_or_0(x.m) : 0.f;
         const float total = warp_sum(f * (float(x.z) * (1.f / kUnit)));
         const u64 mine = f > 0.f ? argmax_key(f * logit_of(x.best), uint32_t(argmax_key_index(x.best))) : 0;
         const u64 win = warp_max_u64(mine);
         const float w = __shfl_sync(0xffffffffu, f * x.w, win ? __ffs(__ballot_sync(0xffffffffu, mine == win)) - 1 : 0);
         if (win && !any_bad) token = argmax_key_index(win), prob = w / total;
-        r.c.m = m;
         r.listed = false;
         r.t_max = 124.9f;
         z = token >= 0 ? u64(double(total) * double(kUnit)) : 0;
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
             const u64 best = warp_max_u64(x.m > -INFINITY ? x.best : 0);
             if (best) token = argmax_key_index(best), prob = 1.f;
         } else if (row_top > -INFINITY && !any_bad) {
-            r.c.m = row_top;
+            r.c.m = row_top * r.c.pre;
             // ---- what can be kept ----
             r.t_max = 124.9f;
             u64 all = 0;                  // the row's mass (top-p alone)
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(const __grid_constant__ Sampl
             }
             // ---- their list, and a common one in the first CTA, as far as it goes ----
             // (by the logits, a little below the bound, and above those of no weight)
-            r.l_min = fmaxf(r.c.m - r.t_max / r.c.hi * 1.00001f, -FLT_MAX);
+            r.l_min = fmaxf((r.c.m - r.t_max / r.c.hi * 1.00001f) * (1.f / r.c.pre), -FLT_MAX);
             Shared *first = cl.map_shared_rank(&s, 0);
             const int lane = tid & 31;
             bool at_edge = tid < edges && float(share[edge]) >= r.l_min;   // an id before or behind the whole pieces
