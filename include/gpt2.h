@@ -742,8 +742,9 @@ int gpt2_op_paged_attention(const gpt2_kv *kv, const void *q, int32_t q_dtype, i
  * drawn token had among the kept ones (greedy 1; token -1: 0), may be NULL; dist fp32
  * [n_rows][vocab], the whole distribution drawn from (greedy: 1 at the token; token -1:
  * zeros), as gpt2_op_verify_tree takes it for draft_probs, may be NULL.  Weights
- * and sums are fp32 or more: a cut or a draw can differ from the exact one within 1e-6 of its
- * border.
+ * and sums are fp32 or more: a cut or a draw can differ from the exact one within 2e-6 of its
+ * border (of the sum of the weights; of the highest weight), and prob and dist are off by at most
+ * 4e-6 of themselves.
  * vocab <= GPT2_SAMPLE_MAX_VOCAB, n_rows < 2^27.  Errors: INVALID_ARG, CUDA, UNSUPPORTED_DEVICE. */
 #define GPT2_SAMPLE_MAX_VOCAB 524288
 int gpt2_op_sample(const void *logits, int32_t dtype, int64_t row_stride, int32_t n_rows, int32_t vocab,

@@ -13,6 +13,18 @@ from test_gpu_spec import dt, i32, uniform
 
 pytestmark = pytest.mark.gpu
 
+# How far a probability is off relatively, where its sum is that of a whole row or of a long
+# list (of at most 2^15.62 = 50257 weights, the largest of them 1):
+#   7e-7     the sum's exponents, rounded as a whole: t = d * hi is off by 2^-24 t (the product) and
+#            2^-25 t (hi), so a weight of 2^-t by ln 2 times that; such weights are at most the share
+#            s = V 2^-t / (1 + V 2^-t) of the sum, and 1.5 * 2^-24 ln 2 t s is at most 7e-7 (t = 13)
+#   2^-22    ex2
+#   7 2^-24  a thread's weights, eight at a time in fp32
+#   2^-22 + 2^-25 + 6 2^-24   CTAs' sums: the factor of each, its conversion and product, additions
+#   2^-22 + 2^-25 + 3 2^-24   the id's own weight; conversion, product, quotient
+# (a list of up to 512 ids is settled more exactly: OFF)
+WHOLE = 7e-7 + 3 * 2.0 ** -22 + 2 * 2.0 ** -25 + 16 * 2.0 ** -24
+
 
 class Cut:
     """A row by the definition in gpt2.h (temperature above 0, finite logits): its ids in
@@ -47,15 +59,15 @@ class Cut:
         with np.errstate(divide="ignore"):
             score = r[:n] / -np.log(u[ids[:n]].astype(np.float64))
         assert score[at] >= score.max() * (1 - NEAR), (token, at, int(score.argmax()))
-        assert least[at] * (1 - OFF) <= prob <= most[at] * (1 + OFF) + 1e-30, (prob, least[at], most[at])
+        assert least[at] * (1 - WHOLE) <= prob <= most[at] * (1 + WHOLE) + 1e-30, (prob, least[at], most[at])
         if dist is None:
             return
         d = dist[ids].astype(np.float64)
         assert np.all(d[hi:] == 0)
-        assert np.all(d[:hi] <= most[:hi] * (1 + OFF) + 1e-34)
-        assert np.all(d[:lo] >= least[:lo] * (1 - OFF) - 1e-34)
+        assert np.all(d[:hi] <= most[:hi] * (1 + WHOLE) + 1e-34)
+        assert np.all(d[:lo] >= least[:lo] * (1 - WHOLE) - 1e-34)
         open_ = d[lo:hi]
-        assert np.all((open_ == 0) | (open_ >= least[lo:hi] * (1 - OFF) - 1e-34))
+        assert np.all((open_ == 0) | (open_ >= least[lo:hi] * (1 - WHOLE) - 1e-34))
         # the draw and the distribution are of the same ids: the probability is the one
         # that the distribution has (each off by OFF)
         assert abs(d[at] - prob) <= 2 * OFF * prob + 1e-34, (d[at], prob)
@@ -145,3 +157,40 @@ def test_differences_past_the_largest_number(t, V, dtype):
     u = uniform(rng, n, V)
     for arg in ({}, dict(p=0.9), dict(p=0.3), dict(k=20), dict(k=700), dict(k=700, p=0.8), dict(m=0.4), dict(m=0.02, p=0.95)):
         check(x, t, u, dtype=dtype, **arg)
+
+
+def flat(rng, n, V):
+    return 0.02 * peaked(rng, n, V)
+
+
+def tails(rng, n, V):
+    x = 0.01 * rng.standard_normal((n, V))
+    x[:, 77] = 12.0
+    x[-1] = -np.arange(V) * 0.001
+    return x
+
+
+def two_values(rng, n, V):
+    return rng.integers(0, 2, (n, V)) * 0.5
+
+
+def wide(rng, n, V):
+    return 4.0 * rng.standard_normal((n, V))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [3001, 50257])
+@pytest.mark.parametrize("rows", [peaked, flat, tails, two_values, wide])
+def test_every_row_between_its_borders(rows, V, dtype):
+    """Rows whose cuts lie among few ids and among thousands, with neighbours next to the
+    border or not.  With 8 of the settings 6 rows each, the first of them uncut or by count,
+    a third at least leaves one set only."""
+    rng = np.random.default_rng(V)
+    n = 6
+    x, u = rows(rng, n, V), uniform(rng, n, V)
+    one = 0
+    for arg in (dict(), dict(k=[1, 50, 700, 3000, V - 1, V]), dict(k=V // 3), dict(p=[0.0, 0.3, 0.5, 0.9, 0.999, 0.99999]),
+                dict(m=[1.0, 0.9, 0.5, 0.1, 1e-3, 1e-6]), dict(p=0.9, m=0.05), dict(k=900, p=[0.2, 0.5, 0.8, 0.95, 0.99, 1.0]),
+                dict(k=2000, p=0.97, m=[1.0, 0.9, 0.5, 0.1, 1e-3, 1e-6])):
+        one += check(x, 0.8, u, dtype=dtype, **arg)[1]
+    assert one >= 16

@@ -28,10 +28,13 @@
 // among thousands of ids, takes 56 us: two passes of two shared-memory atomics per id,
 // two of lists, and the race.
 //
-// Rounding: a weight is off by some 2^-22 of itself (the exponent's integer part
-// is taken off exactly before the exponential), so a cut by mass can differ from
-// the exact one where it falls within about 1e-7 of its border, and a race where
-// its two best are within 1e-6 of each other.
+// Rounding: a weight is off by some 2^-22 of itself (the exponent's integer part is
+// taken off exactly before the exponential), those of a row's or a long list's sum, whose
+// exponents are rounded as a whole, by up to 1e-6 of the sum together, and up to eight of a
+// thread are added in fp32.  So a cut by mass can differ from the exact one where it
+// falls within 2e-6 of its border (usually 1e-7), and a race where its two best are
+// within 1e-6 of each other; probabilities are off by at most 4e-6 (lists of up to 512
+// ids: 6e-7).
 #include <cooperative_groups.h>
 
 #include <cfloat>
