@@ -52,8 +52,9 @@ using namespace tree;
 constexpr int kThreads = kNW * 32;
 constexpr uint32_t kNone = 0xffffffffu;      // no cache row
 
-// Cache rows that query row i sees.
-__device__ __forceinline__ int seen(const PagedArgs &a, int i)
+// Cache rows that query row i sees, below 2^31 (counts and places of rows and tiles are
+// unsigned: rounded up to whole tiles they may pass it).
+__device__ __forceinline__ uint32_t seen(const PagedArgs &a, int i)
 {
     const long long cap = (long long)a.max_blocks * a.kv.n_positions;
     const long long n = (long long)a.position[i] + 1;
@@ -62,7 +63,7 @@ __device__ __forceinline__ int seen(const PagedArgs &a, int i)
         const int b = a.seq[i];
         if (b < 0 || b >= a.n_seqs) return 0;
     }
-    return int(n < cap ? n : cap);
+    return uint32_t(n < cap ? n : cap);
 }
 __device__ __forceinline__ const int32_t *table_of(const PagedArgs &a, int i)
 {
@@ -109,7 +110,7 @@ struct Place {
     __device__ __forceinline__ void enter(const PagedArgs &a, int i)
     {
         row = i;
-        len = uint32_t(seen(a, i));
+        len = seen(a, i);
         tiles = (len + KS - 1) / KS;
         table = len ? table_of(a, i) : nullptr;
     }
@@ -355,7 +356,8 @@ __device__ __forceinline__ void put(const PagedArgs &a, size_t at, const float *
 // that large values can pass fp32's range where those of the formula, whose weights
 // add up to one, do not.
 template <int KIND, int D, int R>
-__device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int h, int j_from, int j_to, float *part)
+__device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int h, uint32_t j_from, uint32_t j_to,
+                                      float *part)
 {
     constexpr bool kScaled = KIND == GPT2_INT8 || KIND == GPT2_E4M3;
     constexpr int N = D / 32;
@@ -375,10 +377,10 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
         }
         return x;
     };
-    auto at = [&](int j) { return j < j_to ? cache_row(a, table, uint32_t(j), head) : kNone; };
+    auto at = [&](uint32_t j) { return j < j_to ? cache_row(a, table, j, head) : kNone; };
     float m = -INFINITY, l = 0.f, out[N];
     bool nan = false;
-    for (int j0 = j_from; j0 < j_to && !nan; j0 += 32) {
+    for (uint32_t j0 = j_from; j0 < j_to && !nan; j0 += 32) {
         const float s = score(j0 + lane, at(j0 + lane)), top = fmaxf(m, s), safe = top == -INFINITY ? 0.f : top;
         nan = __any_sync(0xffffffffu, s != s || s == INFINITY);
         l = l * exp2_approx(m - safe) + exp2_approx(s - safe);
@@ -389,7 +391,7 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
     for (int i = 0; i < N; ++i) out[i] = nan ? __int_as_float(0x7fc00000) : 0.f;
     if (!nan && top != -INFINITY) {
         l = warp_sum(l * exp2_approx(m - top));
-        for (int j0 = j_from; j0 < j_to; j0 += 32) {
+        for (uint32_t j0 = j_from; j0 < j_to; j0 += 32) {
             const uint32_t r = at(j0 + lane);
             const float p = exp2_approx(score(j0 + lane, r) - top) / l;
             for (int t = 0; t < 32; ++t) {
@@ -416,17 +418,17 @@ __device__ __noinline__ void row_anew(const PagedArgs &a, int row, int unit, int
 // What a warp has written of its share and is not finite, computed anew: its share w goes
 // from tile `tile` of the unit (row, unit) to tile last_tile of (last_row, last_unit).
 template <int KIND, int D, int R, int KS>
-__device__ __noinline__ void share_anew(const PagedArgs &a, uint32_t w, int row, int unit, int tile, int last_row,
-                                        int last_unit, int last_tile)
+__device__ __noinline__ void share_anew(const PagedArgs &a, uint32_t w, int row, int unit, uint32_t tile, int last_row,
+                                        int last_unit, uint32_t last_tile)
 {
     const int lane = threadIdx.x & 31, units = a.kv.n_head * a.row_tiles;
     for (; row <= last_row; ++row, unit = 0) {
-        const int len = seen(a, row), tiles = int((uint32_t(len) + KS - 1) / KS);
+        const uint32_t len = seen(a, row), tiles = (len + KS - 1) / KS;
         if (len == 0) continue;
         for (const int end = row == last_row ? last_unit + 1 : units; unit < end; ++unit, tile = 0) {
             const bool last = row == last_row && unit == last_unit;
             const bool whole = tile == 0 && (!last || last_tile + 1 == tiles);
-            const int to = last && last_tile + 1 < tiles ? (last_tile + 1) * KS : len;
+            const uint32_t to = last && last_tile + 1 < tiles ? (last_tile + 1) * KS : len;
             for (int r = 0; r < heads_of<R>(a, unit); ++r) {
                 float *part = a.sums + ((size_t(w) * 2 + (tile == 0)) * R + r) * D;
                 const size_t at = row_at<D, R>(a, row, unit, a.out_stride) + size_t(r) * D + lane;

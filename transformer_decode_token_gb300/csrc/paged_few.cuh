@@ -58,8 +58,9 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, D, R>::kCtas) k_paged_few(
     Share<KS> sh;
     find_share<KS, D>(a, sh);
     Place<KS> at = sh.at;
-    __shared__ int began[kNW][3];                        // where the warp's share begins: row, unit, tile
-    if (lane == 0) began[warp][0] = at.row, began[warp][1] = at.unit, began[warp][2] = int(at.tile);
+    __shared__ int began[kNW][2];                        // where the warp's share begins: row, unit
+    __shared__ uint32_t began_tile[kNW];
+    if (lane == 0) began[warp][0] = at.row, began[warp][1] = at.unit, began_tile[warp] = at.tile;
     float sane = 0.f;                                    // NaN once something that was written is not finite
     const uint32_t w = sh.w, x0 = sh.x0, x1 = sh.x1;
     int4 head = make_int4(0, 0, 0, 0);                   // the unit whose parts begin with this warp's: row, unit, parts
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, Few<KIND, D, R>::kCtas) k_paged_few(
     // (here and not where it is written: a call from the loop takes registers of the loop's)
     if (__any_sync(0xffffffffu, sane != 0.f)) {
         __syncwarp();
-        share_anew<KIND, D, R, KS>(a, w, began[warp][0], began[warp][1], began[warp][2], at.row, at.unit, int(at.tile));
+        share_anew<KIND, D, R, KS>(a, w, began[warp][0], began[warp][1], began_tile[warp], at.row, at.unit, at.tile);
     }
 }
 

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, MmaRing<KIND, D>::kCtas) k_paged_mma
                     uint32_t odd = __ballot_sync(0xffffffffu, sane != 0.f);
                     while (odd) {
                         const int k = (__ffs(odd) - 1) >> 2;
-                        row_anew<KIND, D, R>(a, at.row, at.unit, k + 8 * h, 0, int(at.len), nullptr);
+                        row_anew<KIND, D, R>(a, at.row, at.unit, k + 8 * h, 0, at.len, nullptr);
                         odd &= ~(0xfu << (k * 4));
                     }
                 }
