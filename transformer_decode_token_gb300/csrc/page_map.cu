@@ -11,7 +11,7 @@
 // read of them and the first write; blocks are taken from one end of the ring and given
 // back at the other, and tables grow behind what is read, so nothing else is
 // both read and written.  What bounds it is latency: a launch, one load of the
-// lengths, three scans, a search and one dependent load per row (64 rows 4.3 us, 16,384 rows 5.4,
+// lengths, three scans, a search and one dependent load per row (64 rows 4.5 us, 16,384 rows 5.5,
 // whose bytes would take 0.04).
 #include <cooperative_groups.h>
 

@@ -9,11 +9,11 @@
 // weighted sum takes the weights from the lanes that hold them.  The weights are
 // taken relative to a maximum that is only raised when a score passes it by more
 // than kSlack (a vote instead of a reduction per tile; fp32 holds 2^kSlack as well as
-// 1).  Lane l looks up the place of the tile's row l in the block table, so that pages
+// 1, but for values near its largest: row_anew).  Lane l looks up the place of the tile's row l in the block table, so that pages
 // may have any size and end anywhere in a tile.
 //
 // Long caches run at the memory's rate (64 sequences of 2,000 to 4,000 rows, 12 heads
-// of 64: fp32 172 us, 1.0 of the copy rate, bf16 91, 0.95; int8 57.5, 0.8, where the
+// of 64: fp32 175 us, 0.99 of the copy rate, bf16 92, 0.94; int8 58.2, 0.8, where the
 // conversion of the codes takes as long as they take to arrive).
 #pragma once
 

@@ -23,7 +23,7 @@
 //
 // What bounds it is latency: the load of a share, two or three exchanges over the
 // cluster, and barriers around the list, its order and the race, most of them the same
-// for one row (8.7 us with top-p) as for 64 (12.8 with top-k and top-p, 11.5 uncut; the
+// for one row (8.8 us with top-p) as for 64 (12.8 with top-k and top-p, 11.5 uncut; the
 // logits alone would take 1.9, with the random numbers 3.8).  A flat row, whose cut lies
 // among thousands of ids, takes 56 us: two passes of two shared-memory atomics per id,
 // two of lists, and the race.
